@@ -414,6 +414,244 @@ mtp_status mtp_tree_commit(mtp_ctx* ctx, void* stream, const mtp_kv* kv, const m
 mtp_status mtp_tree_loop(mtp_ctx* ctx, void* stream, const mtp_kv* kv, const mtp_loop* loop, const mtp_tree* tree,
                          int iters);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, the 8-bit KV cache and logit processing: the verifier's
+ * side of a draft-and-verify step.  A caller that runs the target model next
+ * to the head rotates and appends the K + 1 rows of each request
+ * (mtp_kv8_append), attends with them over the request's cache
+ * (mtp_kv8_attention: causal, or with a packed tree's ancestor mask), applies
+ * penalties, biases and grammar masks to the target rows
+ * (mtp_logits_process), verifies (mtp_verify), and keeps what was accepted
+ * (mtp_kv8_commit_accepted).  ("Speculative Decoding", "Overview" and "Tree
+ * Drafting": the target scores the drafted rows in one pass over its cache,
+ * and the cache keeps the accepted prefix.)
+ *
+ * These calls take their head counts, head_dim, block size (16), vocabulary
+ * and dtype from the context, which needs no weights.  They allocate nothing
+ * and can be captured into graphs.  Calls on one cache, one workspace or one
+ * output must be ordered by the caller (one stream, or events).
+ * ---------------------------------------------------------------------- */
+
+/* Which elements of a rotated head form a pair: HALF (i, i + rotary_dim/2),
+ * INTERLEAVED (2i, 2i + 1). */
+typedef enum { MTP_ROPE_HALF = 0, MTP_ROPE_INTERLEAVED = 1 } mtp_rope_layout;
+
+/* How the angle per position f_i = theta^(-2i/rotary_dim) is changed for
+ * contexts longer than trained, with s = factor, L0 = original_max_pos:
+ *   NONE    f_i
+ *   LINEAR  f_i / s
+ *   PARTS   w f_i + (1 - w) f_i / s with w = clamp((r - low_freq_factor) /
+ *           (high_freq_factor - low_freq_factor), 0, 1), r = L0 f_i / 2pi the
+ *           pair's turns over the original context
+ *   YARN    (1 - w) f_i + w f_i / s with w = clamp((i - lo) / (hi - lo), 0, 1),
+ *           lo = max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)),
+ *           rotary_dim - 1), c(b) = rotary_dim ln(L0 / (2pi b)) / (2 ln theta)
+ *           (hi - lo at least 0.001), and the rotated elements are multiplied
+ *           by 0.1 ln s + 1 (1 for s <= 1)
+ * magnitude, if not 0, replaces the factor on the rotated elements. */
+typedef enum { MTP_ROPE_SCALE_NONE = 0, MTP_ROPE_SCALE_LINEAR = 1, MTP_ROPE_SCALE_PARTS = 2,
+               MTP_ROPE_SCALE_YARN = 3 } mtp_rope_scaling;
+
+typedef struct {
+  int layout;             /* mtp_rope_layout                                   */
+  int rotary_dim;         /* leading elements of a head that turn: even, 2..128 */
+  int scaling;            /* mtp_rope_scaling                                  */
+  float theta;            /* > 1                                               */
+  float factor;           /* s > 0                                             */
+  float low_freq_factor, high_freq_factor;   /* PARTS: low < high              */
+  float beta_fast, beta_slow;                /* YARN: fast > slow > 0          */
+  int original_max_pos;   /* L0 > 0 (PARTS, YARN)                              */
+  float magnitude;        /* 0: as the scaling gives it                        */
+} mtp_rope_params;
+
+/* A rotary table: host memory, filled by mtp_rope_table_make and passed by
+ * value to the kernels; it holds no pointer and may be copied and shared.
+ * turns[i]: the pair's angle per position as a fraction of a turn, times
+ * 2^64, so that position * turns[i] modulo 2^64 is the exact phase of any
+ * int32 position (negative ones turn the other way). */
+typedef struct {
+  int layout;
+  int rotary_dim;
+  float magnitude;
+  int reserved;
+  uint64_t turns[64];
+} mtp_rope_table;
+
+/* Fill *out from *params (host only, no GPU work).  MTP_ERR_INVALID for NULL
+ * pointers or parameters outside the ranges above. */
+mtp_status mtp_rope_table_make(const mtp_rope_params* params, mtp_rope_table* out);
+
+/* Rotate x [T, heads, head_dim] (dtype; rows of heads * head_dim contiguous
+ * elements, x_stride elements apart) to the positions [T] and write out
+ * (out_stride): the pair (a, b) becomes magnitude * (a cos - b sin,
+ * b cos + a sin), elements from rotary_dim on are copied.  Computed in
+ * float32 from exact phases, rounded once.  out may be x itself (with the
+ * same stride) but not overlap it otherwise.  T = 0 is a no-op.  Host errors:
+ * T < 0, heads < 1, rotary_dim > head_dim, a stride below
+ * heads * head_dim, NULL pointers. */
+mtp_status mtp_rope(mtp_ctx* ctx, void* stream, int T, int heads, const void* x, int64_t x_stride,
+                    const int32_t* positions, const mtp_rope_table* rope, void* out, int64_t out_stride);
+
+/* The paged 8-bit KV cache (device pointers, borrowed).
+ *   k_pool, v_pool:   [num_blocks, n_kv, 16, head_dim] e4m3 codes (1 byte;
+ *                     4 exponent bits, 3 mantissa bits, 0x7f = NaN), 16-byte
+ *                     aligned.
+ *   k_scale, v_scale: [num_blocks, n_kv] float32, one scale for a block of 16
+ *                     tokens and a head: 0 or a power of two of at least
+ *                     2^-126; an entry's value is code * scale, which bf16
+ *                     holds exactly.
+ *   block_table, seq_len, pending: as in mtp_kv.
+ *   arrive:           [B] int32, zeroed once by the caller and left zero by
+ *                     every call (the calls count their thread blocks in it).
+ * Every block belongs to one request at a time.  The calls keep the invariant
+ * of mtp_kv (slots that no request holds are zero bits) and, with it, a scale
+ * of 0 for blocks that hold no entry. */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  int32_t* block_table;
+  int32_t* seq_len;
+  int32_t* pending;
+  int32_t* arrive;
+  int num_blocks;
+  int max_blocks;
+} mtp_kv8;
+
+/* Append rows row_offsets[b] .. row_offsets[b+1]-1 of k and v ([T, n_kv,
+ * head_dim], dtype, strides in elements between rows) to request b as pending
+ * entries: slots seq_len[b] + pending[b] on, then pending[b] grows by the row
+ * count.  With rope (and positions [T]) k is rotated first, in float32,
+ * without rounding in between; q [T, n_q, head_dim], if not NULL, is rotated
+ * by the same table into q_out (dtype; may be q itself).  rope NULL: k is
+ * stored as given, and q must be NULL.
+ *   Quantization, per (block, kv head), K and V apart: the scale becomes the
+ * smallest power of two s with max|x| <= 448 s over the new finite values, or
+ * stays if it was larger and the block held entries; entries it held are
+ * requantized when it grows (exact but for values that fall below the
+ * format's smallest normal number); code = x / s rounded to nearest even.
+ * Values that are not finite are stored as NaN and do not count in max|x|.
+ *   row_offsets [B+1] int32, ascending from >= 0 to <= T; rows outside are not
+ * read.  Device errors: MTP_ERR_DEVICE_ARGS for bad offsets or lengths,
+ * MTP_ERR_CAPACITY for slots beyond max_blocks (the request is then left as
+ * it was) or a block id outside the pool (that block is skipped).  T = 0 is a
+ * no-op.  Host errors: B outside 1..max_batch, T < 0, strides below the row,
+ * NULL pointers. */
+mtp_status mtp_kv8_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                          const mtp_rope_table* rope, const void* q, int64_t q_stride, void* q_out,
+                          int64_t q_out_stride, const mtp_kv8* kv);
+
+/* Read entries back: row row_offsets[b] + i of k_out and v_out ([T, n_kv,
+ * head_dim] bf16, whatever the dtype: bf16 holds every entry) receives slot
+ * start[b] + i.  The slots must be held (below seq_len[b] + pending[b]; else
+ * MTP_ERR_DEVICE_ARGS and that request's rows are left as they were).  Rows
+ * outside row_offsets are left as they were. */
+mtp_status mtp_kv8_read(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* start, int T,
+                        const int32_t* row_offsets, void* k_out, void* v_out);
+
+/* Commits and edits as mtp_kv_commit, mtp_kv_commit_accepted, mtp_kv_rollback
+ * and mtp_kv_truncate; dropped slots are zeroed, and the scale of a block that
+ * is left without an entry becomes 0.  A block that keeps an entry keeps its
+ * scale. */
+mtp_status mtp_kv8_commit(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* n_keep);
+mtp_status mtp_kv8_commit_accepted(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* accepted,
+                                   int extra);
+mtp_status mtp_kv8_rollback(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv);
+mtp_status mtp_kv8_truncate(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* new_len);
+
+/* Commit the pending entries keep[b * keep_stride + j], j < n_keep[b] (their
+ * places among the pending ones, strictly ascending: an accepted path of a
+ * packed tree): they move to slots seq_len[b] + j, are requantized to the
+ * scales of the blocks they enter (as in mtp_kv8_append), and the other
+ * pending entries are dropped.  At most 256 pending entries
+ * (MTP_ERR_DEVICE_ARGS, as for a bad list; the request is then unchanged). */
+mtp_status mtp_kv8_commit_path(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* keep,
+                               int keep_stride, const int32_t* n_keep);
+
+/* Bytes of a workspace of mtp_kv8_attention for this context's device; 0 for
+ * a NULL context.  The caller zeroes it once; every call leaves it ready for
+ * the next.  Calls that may run at the same time need workspaces of their
+ * own, graphs that contain such calls included. */
+size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx);
+
+/* Attention of new rows over an 8-bit cache.  Request b's rows r =
+ * row_offsets[b] + i, i < n_b = row_offsets[b+1] - row_offsets[b], belong to
+ * its last n_b entries (base_b = seq_len[b] + pending[b] - n_b >= 0 entries
+ * come before them).  With q [T, n_q, head_dim] (dtype, q_stride elements
+ * between rows), head h and its kv head g = h / (n_q / n_kv):
+ *   out[r, h] = sum_t p_t V[t, g],  p = softmax over the slots t that row i
+ *   sees of scale * q[r, h] . K[t, g].
+ * Row i sees the slots below base_b, and of the n_b last ones: those up to
+ * itself (mask NULL), or the slot base_b + j for each bit j set in its mask
+ * words (mask [T, mask_words] int32, bit j of word j / 32; bits from n_b on
+ * are ignored).  A row that sees nothing gives zeros and lse = -inf.  NaN
+ * entries reach only the rows that see them.  out [T, n_q, head_dim]
+ * contiguous, dtype; lse [T, n_q] float32 or NULL: the natural logarithm of
+ * the softmax sum.  Sums, maxima and products are held in float32.
+ *   max_rows: at least every n_b (1..256); mask_words >= ceil(max_rows / 32)
+ * with a mask.  scale: finite, > 0.  Rows outside row_offsets are left as
+ * they were.  Device errors: MTP_ERR_DEVICE_ARGS (bad offsets, n_b >
+ * max_rows, base_b < 0), MTP_ERR_CAPACITY (more entries than max_blocks
+ * blocks hold): that request's rows are left as they were; a block id outside
+ * the pool sets MTP_ERR_CAPACITY and its entries count as zeros.
+ * T = 0 is a no-op. */
+mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
+                             const void* q, int64_t q_stride, const mtp_kv8* kv, const int32_t* mask, int mask_words,
+                             float scale, void* out, float* lse, void* ws, size_t ws_bytes);
+
+/* Add tokens to the per-request counts [B, vocab] int32: tokens[b * stride +
+ * i], i < n_tokens[b].  in_prompt = 0: the token's count grows by one for
+ * each time it is named; 1: its top bit (bit 31: the token occurs in the
+ * prompt) is set.  Device errors (MTP_ERR_DEVICE_ARGS): n_tokens[b] outside
+ * 0..stride (that request is skipped), a token outside the vocabulary (that
+ * token is skipped). */
+mtp_status mtp_token_counts_add(mtp_ctx* ctx, void* stream, int B, const int32_t* tokens, int stride,
+                                const int32_t* n_tokens, int in_prompt, int32_t* counts);
+
+/* Penalties, biases and masks on logits rows (host struct of device
+ * pointers; NULL leaves the part out).  Rows row_offsets[b] + j, j < n_b, are
+ * request b's; row j follows its history and the first j of drafts[b *
+ * drafts_stride ...].  For vocabulary entry v with c = the count in
+ * counts[b, v] (low 31 bits) plus the number of those drafts equal to v:
+ *   z1 = z / repetition[b] if z > 0, z * repetition[b] otherwise, where c > 0
+ *        or the prompt bit of counts[b, v] is set; z elsewhere
+ *   z2 = z1 - frequency[b] * c - presence[b] * (c > 0)
+ *   z3 = z2 + the sum of bias_values[e], bias_offsets[b] <= e <
+ *        bias_offsets[b+1], bias_tokens[e] = v (in order of e)
+ *   out = z3, or -inf where mask row mask_index[row] (-1: none) has bit
+ *        v % 32 of word v / 32 clear.
+ * Computed in float32 and rounded once; NaN logits stay NaN unless masked. */
+typedef struct {
+  int B;                       /* 1..max_batch                                 */
+  int num_rows;                /* rows of logits and out                       */
+  const int32_t* row_offsets;  /* [B + 1]                                      */
+  const void* logits;          /* [num_rows, vocab], dtype                     */
+  void* out;                   /* [num_rows, vocab], dtype; may be logits      */
+  const int32_t* counts;       /* [B, vocab] (mtp_token_counts_add), or NULL   */
+  const int32_t* drafts;       /* [B, drafts_stride] or NULL; needs counts     */
+  int drafts_stride;           /* n_b - 1 <= drafts_stride with drafts         */
+  const float* repetition;     /* [B] finite, > 0, or NULL (1); needs counts   */
+  const float* frequency;      /* [B] finite, or NULL (0); needs counts        */
+  const float* presence;       /* [B] finite, or NULL (0); needs counts        */
+  const int32_t* bias_offsets; /* [B + 1] into the next two, or NULL           */
+  const int32_t* bias_tokens;  /* [num_bias]                                   */
+  const float* bias_values;    /* [num_bias]                                   */
+  int num_bias;
+  const int32_t* mask;         /* [num_masks, ceil(vocab / 32)] or NULL        */
+  const int32_t* mask_index;   /* [num_rows], -1..num_masks-1; with mask       */
+  int num_masks;
+} mtp_logits_args;
+
+/* Rows outside row_offsets are left as they were.  Host errors:
+ * MTP_ERR_INVALID for a part given without what it needs.  Device errors
+ * (MTP_ERR_DEVICE_ARGS): bad offsets or parameters (that request's rows are
+ * left as they were), a bias token outside the vocabulary (skipped) or a bad
+ * mask index (that row is left as it was); a draft outside the vocabulary
+ * (-1: none) counts for nothing. */
+mtp_status mtp_logits_process(mtp_ctx* ctx, void* stream, const mtp_logits_args* args);
+
 /* Failure-detection diagnostic.  Runs one of the library's bounded waits on
  * a condition that never becomes true, so that the wait runs out as it would
  * for a lost arrival in a real launch: which = 0, the shared-memory barrier

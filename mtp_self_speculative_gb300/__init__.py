@@ -21,7 +21,9 @@ from ._lib import (  # noqa: F401
     MTP_ERR_INVALID, MTP_ERR_OOM, MTP_ERR_TIMEOUT, MTP_KERNEL_ATTENTION, MTP_KERNEL_DOWN, MTP_KERNEL_EH_PROJ,
     MTP_KERNEL_GATE_UP, MTP_KERNEL_KV_EDIT, MTP_KERNEL_LM_HEAD, MTP_KERNEL_O_PROJ, MTP_KERNEL_QKV_ROPE,
     MTP_KERNEL_VERIFY, MTP_KERNEL_DRAFT_PERSISTENT, MTP_OK, MTP_WEIGHTS_DENSE, MTP_WEIGHTS_INT4_G64, MTPConfig, MTPKV,
-    MTPLoop, MTPTree, MTPWeights, WEIGHT_FIELDS,
+    MTPKV8, MTPLogitsArgs, MTPLoop, MTPRopeParams, MTPRopeTable, MTPTree, MTPWeights, MTP_ROPE_HALF,
+    MTP_ROPE_INTERLEAVED, MTP_ROPE_SCALE_LINEAR, MTP_ROPE_SCALE_NONE, MTP_ROPE_SCALE_PARTS, MTP_ROPE_SCALE_YARN,
+    WEIGHT_FIELDS,
 )
 
 _clib = L.load()
@@ -79,10 +81,12 @@ class KVCache:
 class Context:
     """Owns an mtp_ctx handle and keeps the borrowed weight tensors alive."""
 
-    def __init__(self, handle: int, cfg: MTPConfig, weights: Optional[Dict[str, torch.Tensor]]):
+    def __init__(self, handle: int, cfg: MTPConfig, weights: Optional[Dict[str, torch.Tensor]],
+                 device: Optional[int] = None):
         self.handle = handle
         self.cfg = cfg
         self.weights = weights
+        self.device = device
 
     def close(self):
         if self.handle:
@@ -120,7 +124,7 @@ def mtp_init(cfg: MTPConfig, weights: Optional[Dict[str, torch.Tensor]] = None, 
     out = ctypes.c_void_p()
     _check(_clib.mtp_init(ctypes.byref(cfg), ctypes.byref(wst) if wst is not None else None, int(device),
                          ctypes.byref(out)), "mtp_init")
-    return Context(out.value, cfg, weights)
+    return Context(out.value, cfg, weights, int(device))
 
 
 def mtp_draft(ctx: Context, hidden: torch.Tensor, embeds: torch.Tensor, positions: torch.Tensor, kv: KVCache, K: int,
@@ -387,6 +391,291 @@ def mtp_kv_truncate(ctx: Context, kv: KVCache, new_len: torch.Tensor, stream=Non
     kvs = kv.struct()
     _check(_clib.mtp_kv_truncate(ctx.handle, _stream(stream), int(kv.seq_len.shape[0]), ctypes.byref(kvs),
                                 _ptr(new_len, torch.int32, "new_len")), "mtp_kv_truncate")
+
+
+# -------------------- rotary positions, the 8-bit KV cache, logit processing
+
+def _dev_ptr(ctx: Context, t: Optional[torch.Tensor], dtype, name: str, shape=None) -> Optional[int]:
+    """_ptr with the context's device and a shape (None entries: any size)."""
+    if t is None:
+        return None
+    p = _ptr(t, dtype, name)
+    if ctx.device is not None and t.device.index != ctx.device:
+        raise ValueError("%s must be on the context's device cuda:%d, got %s" % (name, ctx.device, t.device))
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and int(s) != w
+                                                           for s, w in zip(t.shape, shape))):
+        raise ValueError("%s must be %s, got %s"
+                         % (name, ["any" if w is None else w for w in shape], tuple(t.shape)))
+    return p
+
+
+def _row_ptr(ctx: Context, t: torch.Tensor, name: str, rows: int, heads: int):
+    """Pointer and row stride of a [rows, heads, head_dim] tensor in the
+    context's dtype whose rows are contiguous (a slice of a packed [rows,
+    width] projection, say)."""
+    hd, dt = ctx.cfg.head_dim, torch_dtype(ctx.cfg.dtype)
+    if t.dim() != 3 or tuple(t.shape) != (rows, heads, hd):
+        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, hd, tuple(t.shape)))
+    if t.dtype != dt:
+        raise ValueError("%s must be %s, got %s" % (name, dt, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if ctx.device is not None and t.device.index != ctx.device:
+        raise ValueError("%s must be on the context's device cuda:%d, got %s" % (name, ctx.device, t.device))
+    st = t.stride()
+    if rows and (st[2] != 1 or (heads > 1 and st[1] != hd) or (rows > 1 and st[0] < heads * hd)):
+        raise ValueError("%s must have contiguous, non-overlapping rows, got strides %s" % (name, st))
+    return t.data_ptr(), (st[0] if rows > 1 else heads * hd)
+
+
+def _ctx_stream(ctx: Context, stream) -> int:
+    if stream is None:
+        stream = torch.cuda.current_stream(ctx.device)
+    return stream.cuda_stream
+
+
+class RopeTable(MTPRopeTable):
+    """Rotary table (host memory) for mtp_rope and mtp_kv8_append: ``layout``
+    "half" or "interleaved", ``scaling`` "none", "linear", "parts" or "yarn"
+    (include/mtp.h gives each formula)."""
+
+    LAYOUTS = {"half": MTP_ROPE_HALF, "interleaved": MTP_ROPE_INTERLEAVED}
+    SCALINGS = {"none": MTP_ROPE_SCALE_NONE, "linear": MTP_ROPE_SCALE_LINEAR, "parts": MTP_ROPE_SCALE_PARTS,
+                "yarn": MTP_ROPE_SCALE_YARN}
+
+    def __init__(self, rotary_dim: int, theta: float = 1e6, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original_max_pos: int = 0, low_freq_factor: float = 1.0,
+                 high_freq_factor: float = 4.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 magnitude: float = 0.0):
+        super().__init__()
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            raise ValueError("RopeTable: layout %r, scaling %r" % (layout, scaling))
+        p = MTPRopeParams(self.LAYOUTS[layout], int(rotary_dim), self.SCALINGS[scaling], theta, factor,
+                          low_freq_factor, high_freq_factor, beta_fast, beta_slow, int(original_max_pos), magnitude)
+        _check(_clib.mtp_rope_table_make(ctypes.byref(p), ctypes.byref(self)), "mtp_rope_table_make")
+
+
+def mtp_rope(ctx: Context, x: torch.Tensor, positions: torch.Tensor, rope: RopeTable,
+             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotate x [T, heads, head_dim] to ``positions`` [T] into ``out`` (None:
+    in place); rows may be strided.  Returns out."""
+    out = x if out is None else out
+    if x.dim() != 3:
+        raise ValueError("x must be [T, heads, head_dim], got %s" % (tuple(x.shape),))
+    T, heads = int(x.shape[0]), int(x.shape[1])
+    xp, xs = _row_ptr(ctx, x, "x", T, heads)
+    op, os_ = (xp, xs) if out is x else _row_ptr(ctx, out, "out", T, heads)
+    if T == 0:
+        return out
+    _check(_clib.mtp_rope(ctx.handle, _ctx_stream(ctx, stream), T, heads, xp, xs,
+                          _dev_ptr(ctx, positions, torch.int32, "positions", (T,)), ctypes.byref(rope), op, os_),
+           "mtp_rope")
+    return out
+
+
+@dataclass
+class KVCache8:
+    """Caller-owned paged 8-bit KV cache (device tensors; mtp_kv8)."""
+    k_pool: torch.Tensor        # [num_blocks, n_kv, 16, head_dim] e4m3 codes (uint8 or float8_e4m3fn)
+    v_pool: torch.Tensor
+    k_scale: torch.Tensor       # [num_blocks, n_kv] float32
+    v_scale: torch.Tensor
+    block_table: torch.Tensor   # [B, max_blocks] int32
+    seq_len: torch.Tensor       # [B] int32
+    pending: torch.Tensor       # [B] int32
+    arrive: torch.Tensor        # [B] int32, zeroed once
+
+    @classmethod
+    def empty(cls, ctx: Context, num_blocks: int, block_table: torch.Tensor) -> "KVCache8":
+        """An empty cache of num_blocks blocks for the requests of block_table."""
+        c, dev, B = ctx.cfg, block_table.device, int(block_table.shape[0])
+        pools = [torch.zeros((num_blocks, c.n_kv_heads, 16, c.head_dim), dtype=torch.uint8, device=dev)
+                 for _ in range(2)]
+        scales = [torch.zeros((num_blocks, c.n_kv_heads), dtype=torch.float32, device=dev) for _ in range(2)]
+        ints = [torch.zeros(B, dtype=torch.int32, device=dev) for _ in range(3)]
+        return cls(pools[0], pools[1], scales[0], scales[1], block_table, ints[0], ints[1], ints[2])
+
+    def struct(self, ctx: Context) -> MTPKV8:
+        c = ctx.cfg
+        nb, B = int(self.k_pool.shape[0]), int(self.seq_len.shape[0])
+        if self.block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_blocks]")
+        pool, per = (nb, c.n_kv_heads, 16, c.head_dim), (nb, c.n_kv_heads)
+        for t, name in ((self.k_pool, "k_pool"), (self.v_pool, "v_pool")):
+            if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+                raise ValueError("%s must be uint8 or float8_e4m3fn, got %s" % (name, t.dtype))
+        i32, f32 = torch.int32, torch.float32
+        return MTPKV8(_dev_ptr(ctx, self.k_pool, None, "k_pool", pool), _dev_ptr(ctx, self.v_pool, None, "v_pool", pool),
+                      _dev_ptr(ctx, self.k_scale, f32, "k_scale", per),
+                      _dev_ptr(ctx, self.v_scale, f32, "v_scale", per),
+                      _dev_ptr(ctx, self.block_table, i32, "block_table", (B, None)),
+                      _dev_ptr(ctx, self.seq_len, i32, "seq_len", (B,)),
+                      _dev_ptr(ctx, self.pending, i32, "pending", (B,)),
+                      _dev_ptr(ctx, self.arrive, i32, "arrive", (B,)), nb, int(self.block_table.shape[1]))
+
+
+def mtp_kv8_append(ctx: Context, kv: KVCache8, k: torch.Tensor, v: torch.Tensor, row_offsets: torch.Tensor,
+                   q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                   positions: Optional[torch.Tensor] = None, rope: Optional[RopeTable] = None, stream=None) -> None:
+    """Append the rows of k and v [T, n_kv, head_dim] to the requests' caches
+    as pending entries, k rotated by ``rope`` at ``positions`` if given; q
+    [T, n_q, head_dim] is rotated by the same table into q_out (None: in
+    place).  Rows may be strided."""
+    B, T, c = int(kv.seq_len.shape[0]), int(k.shape[0]), ctx.cfg
+    st = kv.struct(ctx)
+    kp, ks = _row_ptr(ctx, k, "k", T, c.n_kv_heads)
+    vp, vs = _row_ptr(ctx, v, "v", T, c.n_kv_heads)
+    qp, qs, qop, qos = None, 0, None, 0
+    if q is not None:
+        qp, qs = _row_ptr(ctx, q, "q", T, c.n_q_heads)
+        qop, qos = (qp, qs) if q_out is None or q_out is q else _row_ptr(ctx, q_out, "q_out", T, c.n_q_heads)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if T == 0:
+        return
+    _check(_clib.mtp_kv8_append(ctx.handle, _ctx_stream(ctx, stream), B, T,
+                                _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), kp, ks, vp, vs,
+                                _dev_ptr(ctx, positions, torch.int32, "positions", (T,)),
+                                ctypes.byref(rope) if rope is not None else None, qp, qs, qop, qos,
+                                ctypes.byref(st)), "mtp_kv8_append")
+
+
+def mtp_kv8_read(ctx: Context, kv: KVCache8, start: torch.Tensor, row_offsets: torch.Tensor, k_out: torch.Tensor,
+                 v_out: torch.Tensor, stream=None) -> None:
+    """Entries start[b] .. of each request, as many as it has rows in
+    row_offsets, into k_out and v_out [T, n_kv, head_dim] bf16."""
+    B, T, c = int(kv.seq_len.shape[0]), int(k_out.shape[0]), ctx.cfg
+    st, shape = kv.struct(ctx), (T, c.n_kv_heads, c.head_dim)
+    kp = _dev_ptr(ctx, k_out, torch.bfloat16, "k_out", shape)
+    vp = _dev_ptr(ctx, v_out, torch.bfloat16, "v_out", shape)
+    if T == 0:
+        return
+    _check(_clib.mtp_kv8_read(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+                              _dev_ptr(ctx, start, torch.int32, "start", (B,)), T,
+                              _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), kp, vp),
+           "mtp_kv8_read")
+
+
+def mtp_kv8_commit(ctx: Context, kv: KVCache8, n_keep: torch.Tensor, stream=None) -> None:
+    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
+    _check(_clib.mtp_kv8_commit(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+                                _dev_ptr(ctx, n_keep, torch.int32, "n_keep", (B,))), "mtp_kv8_commit")
+
+
+def mtp_kv8_commit_accepted(ctx: Context, kv: KVCache8, accepted: torch.Tensor, extra: int = 1, stream=None) -> None:
+    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
+    _check(_clib.mtp_kv8_commit_accepted(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+                                         _dev_ptr(ctx, accepted, torch.int32, "accepted", (B,)), int(extra)),
+           "mtp_kv8_commit_accepted")
+
+
+def mtp_kv8_rollback(ctx: Context, kv: KVCache8, stream=None) -> None:
+    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
+    _check(_clib.mtp_kv8_rollback(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st)), "mtp_kv8_rollback")
+
+
+def mtp_kv8_truncate(ctx: Context, kv: KVCache8, new_len: torch.Tensor, stream=None) -> None:
+    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
+    _check(_clib.mtp_kv8_truncate(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+                                  _dev_ptr(ctx, new_len, torch.int32, "new_len", (B,))), "mtp_kv8_truncate")
+
+
+def mtp_kv8_commit_path(ctx: Context, kv: KVCache8, keep: torch.Tensor, n_keep: torch.Tensor, stream=None) -> None:
+    """Keep the pending entries keep[b, :n_keep[b]] (ascending), drop the rest."""
+    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
+    kp = _dev_ptr(ctx, keep, torch.int32, "keep", (B, None))
+    _check(_clib.mtp_kv8_commit_path(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st), kp,
+                                     int(keep.shape[1]), _dev_ptr(ctx, n_keep, torch.int32, "n_keep", (B,))),
+           "mtp_kv8_commit_path")
+
+
+class Attention8Workspace:
+    """Scratch of mtp_kv8_attention; calls that may run at the same time need
+    one each (graphs that contain such calls included)."""
+
+    def __init__(self, ctx: Context):
+        n = int(_clib.mtp_kv8_attention_workspace_bytes(ctx.handle))
+        if n == 0:
+            raise MTPError(MTP_ERR_INVALID, "mtp_kv8_attention_workspace_bytes")
+        self.device = ctx.device
+        self.ws = torch.zeros(n, dtype=torch.uint8, device="cuda:%d" % ctx.device)
+
+
+def mtp_kv8_attention(ctx: Context, kv: KVCache8, q: torch.Tensor, row_offsets: torch.Tensor, out: torch.Tensor,
+                      ws: Attention8Workspace, max_rows: int, mask: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None) -> None:
+    """out [T, n_q, head_dim] = attention of the rows q (may be strided) over
+    the requests' caches: the rows of request b are its last entries; causal
+    among them, or as the bits of mask [T, words] say.  ``max_rows``: at least
+    the rows of any request; lse [T, n_q] float32; scale: 1 / sqrt(head_dim)."""
+    B, T, c = int(kv.seq_len.shape[0]), int(q.shape[0]), ctx.cfg
+    st = kv.struct(ctx)
+    qp, qs = _row_ptr(ctx, q, "q", T, c.n_q_heads)
+    op = _dev_ptr(ctx, out, torch_dtype(c.dtype), "out", (T, c.n_q_heads, c.head_dim))
+    lp = _dev_ptr(ctx, lse, torch.float32, "lse", (T, c.n_q_heads))
+    mp = _dev_ptr(ctx, mask, torch.int32, "mask", (T, None))
+    if ws.device != ctx.device:
+        raise ValueError("the workspace belongs to cuda:%s" % ws.device)
+    if T == 0:
+        return
+    _check(_clib.mtp_kv8_attention(ctx.handle, _ctx_stream(ctx, stream), B, T,
+                                   _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), int(max_rows),
+                                   qp, qs, ctypes.byref(st), mp, int(mask.shape[1]) if mask is not None else 0,
+                                   c.head_dim ** -0.5 if scale is None else float(scale), op, lp,
+                                   ws.ws.data_ptr(), int(ws.ws.numel())), "mtp_kv8_attention")
+
+
+def mtp_token_counts_add(ctx: Context, counts: torch.Tensor, tokens: torch.Tensor, n_tokens: torch.Tensor,
+                         in_prompt: bool = False, stream=None) -> None:
+    """Count tokens[b, :n_tokens[b]] in counts [B, vocab] int32 (in_prompt:
+    mark them as occurring in the prompt instead)."""
+    B = int(n_tokens.shape[0])
+    tp = _dev_ptr(ctx, tokens, torch.int32, "tokens", (B, None))
+    if int(tokens.shape[1]) == 0:
+        return
+    _check(_clib.mtp_token_counts_add(ctx.handle, _ctx_stream(ctx, stream), B, tp, int(tokens.shape[1]),
+                                      _dev_ptr(ctx, n_tokens, torch.int32, "n_tokens", (B,)), int(bool(in_prompt)),
+                                      _dev_ptr(ctx, counts, torch.int32, "counts", (B, ctx.cfg.vocab))),
+           "mtp_token_counts_add")
+
+
+def mtp_logits_process(ctx: Context, logits: torch.Tensor, row_offsets: torch.Tensor,
+                       out: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                       drafts: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                       frequency: Optional[torch.Tensor] = None, presence: Optional[torch.Tensor] = None,
+                       bias_offsets: Optional[torch.Tensor] = None, bias_tokens: Optional[torch.Tensor] = None,
+                       bias_values: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                       mask_index: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Penalties (counts [B, vocab], repetition / frequency / presence [B],
+    drafts [B, stride]), biases (bias_offsets [B + 1] into bias_tokens and
+    bias_values) and bit masks (mask [masks, ceil(vocab / 32)], mask_index
+    [rows]) on logits [rows, vocab] into out (None: in place).  Returns out."""
+    V, dt = ctx.cfg.vocab, torch_dtype(ctx.cfg.dtype)
+    out = logits if out is None else out
+    if row_offsets.dim() != 1 or int(row_offsets.shape[0]) < 2:
+        raise ValueError("row_offsets must be [B + 1]")
+    if (bias_offsets is None) != (bias_tokens is None) or (bias_offsets is None) != (bias_values is None):
+        raise ValueError("bias_offsets, bias_tokens and bias_values go together")
+    if (mask is None) != (mask_index is None):
+        raise ValueError("mask and mask_index go together")
+    B, i32, f32 = int(row_offsets.shape[0]) - 1, torch.int32, torch.float32
+    lp = _dev_ptr(ctx, logits, dt, "logits", (None, V))
+    rows = int(logits.shape[0])
+    op = lp if out is logits else _dev_ptr(ctx, out, dt, "out", (rows, V))
+    num_bias = int(bias_tokens.numel()) if bias_tokens is not None else 0
+    a = MTPLogitsArgs(
+        B, rows, _dev_ptr(ctx, row_offsets, i32, "row_offsets"), lp, op, _dev_ptr(ctx, counts, i32, "counts", (B, V)),
+        _dev_ptr(ctx, drafts, i32, "drafts", (B, None)), int(drafts.shape[1]) if drafts is not None else 0,
+        _dev_ptr(ctx, repetition, f32, "repetition", (B,)), _dev_ptr(ctx, frequency, f32, "frequency", (B,)),
+        _dev_ptr(ctx, presence, f32, "presence", (B,)), _dev_ptr(ctx, bias_offsets, i32, "bias_offsets", (B + 1,)),
+        _dev_ptr(ctx, bias_tokens, i32, "bias_tokens", (num_bias,)),
+        _dev_ptr(ctx, bias_values, f32, "bias_values", (num_bias,)), num_bias,
+        _dev_ptr(ctx, mask, i32, "mask", (None, (V + 31) // 32)), _dev_ptr(ctx, mask_index, i32, "mask_index", (rows,)),
+        int(mask.shape[0]) if mask is not None else 0)
+    if rows == 0:
+        return out
+    _check(_clib.mtp_logits_process(ctx.handle, _ctx_stream(ctx, stream), ctypes.byref(a)), "mtp_logits_process")
+    return out
 
 
 def mtp_selftest_wait_timeout(ctx: Context, which: int, stream=None) -> None:

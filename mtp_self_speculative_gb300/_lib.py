@@ -62,6 +62,38 @@ class MTPTree(ctypes.Structure):
                 ("parents", c_void_p), ("depths", c_void_p)]
 
 
+MTP_ROPE_HALF, MTP_ROPE_INTERLEAVED = 0, 1
+MTP_ROPE_SCALE_NONE, MTP_ROPE_SCALE_LINEAR, MTP_ROPE_SCALE_PARTS, MTP_ROPE_SCALE_YARN = range(4)
+
+
+class MTPRopeParams(ctypes.Structure):
+    _fields_ = [("layout", c_int), ("rotary_dim", c_int), ("scaling", c_int), ("theta", c_float),
+                ("factor", c_float), ("low_freq_factor", c_float), ("high_freq_factor", c_float),
+                ("beta_fast", c_float), ("beta_slow", c_float), ("original_max_pos", c_int),
+                ("magnitude", c_float)]
+
+
+class MTPRopeTable(ctypes.Structure):
+    _fields_ = [("layout", c_int), ("rotary_dim", c_int), ("magnitude", c_float), ("reserved", c_int),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
+class MTPKV8(ctypes.Structure):
+    _fields_ = [("k_pool", c_void_p), ("v_pool", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("block_table", c_void_p), ("seq_len", c_void_p), ("pending", c_void_p), ("arrive", c_void_p),
+                ("num_blocks", c_int), ("max_blocks", c_int)]
+
+
+class MTPLogitsArgs(ctypes.Structure):
+    _fields_ = [("B", c_int), ("num_rows", c_int), ("row_offsets", c_void_p), ("logits", c_void_p),
+                ("out", c_void_p), ("counts", c_void_p), ("drafts", c_void_p), ("drafts_stride", c_int),
+                ("repetition", c_void_p), ("frequency", c_void_p), ("presence", c_void_p),
+                ("bias_offsets", c_void_p), ("bias_tokens", c_void_p), ("bias_values", c_void_p),
+                ("num_bias", c_int), ("mask", c_void_p), ("mask_index", c_void_p), ("num_masks", c_int)]
+
+
+P_kv8 = ctypes.POINTER(MTPKV8)
+
 # name -> (restype, argtypes); every symbol declared in include/mtp.h
 SIGNATURES = {
     "mtp_init": (c_int, [ctypes.POINTER(MTPConfig), ctypes.POINTER(MTPWeights), c_int, ctypes.POINTER(c_void_p)]),
@@ -92,6 +124,22 @@ SIGNATURES = {
     "mtp_tree_commit": (c_int, [c_void_p, c_void_p, ctypes.POINTER(MTPKV), ctypes.POINTER(MTPTree), P_i32]),
     "mtp_tree_loop": (c_int, [c_void_p, c_void_p, ctypes.POINTER(MTPKV), ctypes.POINTER(MTPLoop),
                               ctypes.POINTER(MTPTree), c_int]),
+    "mtp_rope_table_make": (c_int, [ctypes.POINTER(MTPRopeParams), ctypes.POINTER(MTPRopeTable)]),
+    "mtp_rope": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int64, P_i32, ctypes.POINTER(MTPRopeTable),
+                         c_void_p, c_int64]),
+    "mtp_kv8_append": (c_int, [c_void_p, c_void_p, c_int, c_int, P_i32, c_void_p, c_int64, c_void_p, c_int64, P_i32,
+                               ctypes.POINTER(MTPRopeTable), c_void_p, c_int64, c_void_p, c_int64, P_kv8]),
+    "mtp_kv8_read": (c_int, [c_void_p, c_void_p, c_int, P_kv8, P_i32, c_int, P_i32, c_void_p, c_void_p]),
+    "mtp_kv8_commit": (c_int, [c_void_p, c_void_p, c_int, P_kv8, P_i32]),
+    "mtp_kv8_commit_accepted": (c_int, [c_void_p, c_void_p, c_int, P_kv8, P_i32, c_int]),
+    "mtp_kv8_rollback": (c_int, [c_void_p, c_void_p, c_int, P_kv8]),
+    "mtp_kv8_truncate": (c_int, [c_void_p, c_void_p, c_int, P_kv8, P_i32]),
+    "mtp_kv8_commit_path": (c_int, [c_void_p, c_void_p, c_int, P_kv8, P_i32, c_int, P_i32]),
+    "mtp_kv8_attention_workspace_bytes": (c_size_t, [c_void_p]),
+    "mtp_kv8_attention": (c_int, [c_void_p, c_void_p, c_int, c_int, P_i32, c_int, c_void_p, c_int64, P_kv8, P_i32,
+                                  c_int, c_float, c_void_p, c_void_p, c_void_p, c_size_t]),
+    "mtp_token_counts_add": (c_int, [c_void_p, c_void_p, c_int, P_i32, c_int, P_i32, c_int, P_i32]),
+    "mtp_logits_process": (c_int, [c_void_p, c_void_p, ctypes.POINTER(MTPLogitsArgs)]),
     "mtp_selftest_wait_timeout": (c_int, [c_void_p, c_void_p, c_int]),
     "mtp_get_device_error": (c_int, [c_void_p]),
     "mtp_destroy": (None, [c_void_p]),
