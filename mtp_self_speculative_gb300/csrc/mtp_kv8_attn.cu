@@ -4,13 +4,40 @@
 //   out[r, h] = sum_t p_t V[t, g] / sum_t p_t,  p_t = 2^(c s_t - m),
 //   s_t = q[r, h] . K[t, g], c = scale * log2 e, m the running maximum.
 //
-// A warp owns one (row, query head): lanes hold head_dim / 32 dimensions,
-// scores are summed across the lanes, and the softmax is online.
+// The (row, query head) pairs that share a kv head are the columns of a tile
+// (n_b * G of them, 8 NT per tile); both products run on the tensor cores with
+// the cache as the A operand, so that a single decoding row wastes half of an
+// 8-wide tile at most:
+//   S^T[16 tokens, 8 cols] = K[16, d] Q^T          m16n8k16, fp16 in, fp32 out
+//   O^T[16 dims, 8 cols]  += V^T[16, 16 tokens] P^T
+// e4m3 codes convert to fp16 exactly; the block scales multiply the float32
+// accumulators.  Queries are scaled per column by a power of two into fp16's
+// range (bf16 queries are then exact), P is held as 2^14 p (11 bits).  Float32
+// heads split both Q and P into a high and a low half (22 bits) and issue each
+// product twice.  P^T comes out of the S^T accumulators with one movmatrix per
+// 8 x 8; V is read 4 tokens x 16 dims per lane and its bytes are interleaved
+// in registers, so no transposed copy of V exists anywhere.
+//
+// Work is split over the flattened sequence (request, kv head, tile, step of
+// 32 tokens): every thread block takes an equal contiguous share, whatever
+// the lengths are (they are only known on the device), so ragged batches and
+// a single long context both fill the machine.  Each warp streams every
+// fourth step of its block's share through its own ring of shared memory
+// (cp.async, 16 bytes a lane, swizzled so that the fragment reads are free of
+// bank conflicts).  Pieces of a segment that spans blocks meet in the
+// workspace; the last block to arrive joins them in a fixed order.
 #include <math.h>
 
 #include "mtp_kv8.cuh"
 
 namespace mtp {
+
+constexpr int kA8Warps = 4;
+constexpr int kA8Threads = kA8Warps * 32;
+constexpr int kA8Step = 32;        // tokens of a step (two cache blocks)
+constexpr int kA8MaxB = 1024;      // requests of a call (prefix sums in shared memory)
+constexpr int kA8MinShare = 4;     // steps of a thread block's share at least
+constexpr int kA8MaxCols = 32;     // columns of a tile
 
 struct Attn8Args {
   const void* q;
@@ -20,74 +47,626 @@ struct Attn8Args {
   const int32_t* mask;
   mtp_kv8 kv;
   int* err;
+  float* part;     // [2 * grid][32][HD + 4]: o, then maximum and sum
+  int* cnt;        // [grid]
   long long q_stride;
-  int B, T, max_rows, mask_words, n_kv, n_q;
-  float qscale;  // scale * log2(e)
+  int B, T, max_rows, mask_words, n_kv, g_shift;
+  float qscale;    // scale * log2(e)
 };
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) kv8_attn_kernel(const Attn8Args a) {
-  constexpr int DPL = HD / 32;
-  __shared__ int sh[3];
-  const int r = blockIdx.x;
-  if (!find_request(a.row_offsets, a.B, a.T, r, a.err, sh, [](int o, int) { return o; })) return;
-  const int b = sh[0], o0 = sh[1], n = sh[2] - o0;
-  const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const long long L = (long long)a.kv.seq_len[b] + a.kv.pending[b];
-  if (n > a.max_rows || L < n || a.kv.seq_len[b] < 0 || a.kv.pending[b] < 0) {
-    if (threadIdx.x == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
-    return;
-  }
-  if (L > (long long)a.kv.max_blocks * kBlk) {
-    if (threadIdx.x == 0) set_error(a.err, MTP_ERR_CAPACITY);
-    return;
-  }
-  if (h >= a.n_q) return;
-  const int g = h / (a.n_q / a.n_kv), base = (int)L - n, i = r - o0;
-  const int32_t* bits = a.mask ? a.mask + (long long)r * a.mask_words : nullptr;
-  float q[DPL], o[DPL], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < DPL; ++e) {
-    q[e] = Elem<T>::load1((const T*)a.q + (long long)r * a.q_stride + h * HD + lane * DPL + e);
-    o[e] = 0.0f;
-  }
-  for (int t = 0; t < (int)L; ++t) {
-    const int j = t - base;
-    if (j >= 0 && (bits ? !((uint32_t)bits[j >> 5] >> (j & 31) & 1u) : j > i)) continue;
-    const int blk = a.kv.block_table[(long long)b * a.kv.max_blocks + (t >> 4)];
-    float kx[DPL], vx[DPL];
-#pragma unroll
-    for (int e = 0; e < DPL; ++e) kx[e] = vx[e] = 0.0f;
-    if (blk < 0 || blk >= a.kv.num_blocks) {
-      if (lane == 0) set_error(a.err, MTP_ERR_CAPACITY);
-    } else {
-      const long long tile = (long long)blk * a.n_kv + g, at = (tile * kBlk + (t & 15)) * HD + lane * DPL;
-      const float ks = a.kv.k_scale[tile], vs = a.kv.v_scale[tile];
-#pragma unroll
-      for (int e = 0; e < DPL; e += 2) {
-        const float2 kk = e4m3_to_float2(*(const uint16_t*)((const uint8_t*)a.kv.k_pool + at + e));
-        const float2 vv = e4m3_to_float2(*(const uint16_t*)((const uint8_t*)a.kv.v_pool + at + e));
-        kx[e] = kk.x * ks; kx[e + 1] = kk.y * ks;
-        vx[e] = vv.x * vs; vx[e + 1] = vv.y * vs;
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// 16 (or 4) bytes global -> shared; bytes = 0 fills zeros.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ float lds32f(uint32_t a) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
+  return r;
+}
+// 2^x to 2^-22 of its value; results below 2^-126 are zero.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+// One bit (0x80 of the byte) per NaN code of a word.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Byte offset of 16-byte chunk c of token row r (0..31) within a staged K or
+// V tile.  Rows of 128 (64) bytes; K: the two rows that eight lanes read
+// together swap halves; V: the four rows that eight lanes read together are
+// spread over the banks.
+template <int HD>
+__device__ __forceinline__ uint32_t k_at(int r, int c) {
+  if constexpr (HD == 128) return (uint32_t)(r * 128 + ((c ^ ((r & 1) << 2)) << 4));
+  return (uint32_t)(r * 64 + (c << 4));
+}
+template <int HD>
+__device__ __forceinline__ uint32_t v_at(int r, int c) {
+  if constexpr (HD == 128) return (uint32_t)(r * 128 + ((c ^ (r & 6)) << 4));
+  return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4));
+}
+
+template <int HD, int NT, int SPLIT>
+struct Attn8Shape {
+  static constexpr int kTile = kA8Step * HD;               // bytes of a staged K (or V) tile
+  static constexpr int kStage = 2 * kTile + 16;            // K, V, two scales each
+  static constexpr int kStages = SPLIT == 2 && NT >= 3 ? 2 : 3;   // two blocks per SM fit their shared memory
+  static constexpr int kRing = kA8Warps * kStages * kStage;
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kPitch = HD + 4;                    // floats of a merged row
+  static constexpr int kMerge = kA8Warps * kCols * kPitch * 4;
+  static constexpr int kMain = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kQ = NT * (HD / 16) * 32 * 8 * SPLIT;
+  static constexpr int kBytes = kMain + kQ;
+};
+
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args a) {
+  constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
+  using S = Attn8Shape<HD, NT, SPLIT>;
+  constexpr int KS = HD / 16;                 // k-steps of Q K^T
+  constexpr int MT = HD / 16;                 // m-tiles of V^T P^T
+  constexpr int STEP = kA8Step;
+  constexpr bool kQReg = NT * SPLIT <= 2;     // query fragments stay in registers
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int pre[kA8MaxB + 1];            // units before each request
+  __shared__ long long wsum[kA8Warps];
+  __shared__ float qfac_s[S::kCols];
+  __shared__ float wm[kA8Warps][S::kCols], wl[kA8Warps][S::kCols];
+  __shared__ int last_s;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
+  const int G = 1 << a.g_shift;
+
+  // ---- the call's work: units (steps) before each request
+  auto request = [&](int b, int& o0, int& n, int& L) -> bool {
+    o0 = a.row_offsets[b];
+    const int o1 = a.row_offsets[b + 1], sl = a.kv.seq_len[b], pe = a.kv.pending[b];
+    n = o1 - o0;
+    const long long len = (long long)sl + pe;
+    L = (int)len;
+    return n > 0 && n <= a.max_rows && sl >= 0 && pe >= 0 && len >= n && len <= (long long)a.kv.max_blocks * kBlk;
+  };
+  long long carry = 0;
+  int bad = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kA8Threads) {
+    const int b = b0 + tid;
+    long long units = 0;
+    if (b < a.B) {
+      const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1];
+      if (o0 < 0 || o1 < o0 || o1 > a.T) {
+        bad = 1;
+      } else if (o1 > o0) {
+        int oo, n, L;
+        if (request(b, oo, n, L)) {
+          const int tiles = (n * G + S::kCols - 1) / S::kCols;
+          units = (long long)((L + STEP - 1) / STEP) * tiles * a.n_kv;
+        } else if (blockIdx.x == 0) {
+          set_error(a.err, n <= a.max_rows && (long long)a.kv.seq_len[b] + a.kv.pending[b] > (long long)a.kv.max_blocks * kBlk
+                               ? MTP_ERR_CAPACITY : MTP_ERR_DEVICE_ARGS);
+        }
       }
     }
-    float s = 0.0f;
+    long long x = units;  // inclusive scan over the block
 #pragma unroll
-    for (int e = 0; e < DPL; ++e) s = fmaf(q[e], kx[e], s);
-    s = warp_sum(s) * a.qscale;
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.0f : exp2f(m - mn), p = exp2f(s - mn);
-    l = l * f + p;
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    long long add = carry, all = 0;
 #pragma unroll
-    for (int e = 0; e < DPL; ++e) o[e] = o[e] * f + p * vx[e];
-    m = mn;
+    for (int w = 0; w < kA8Warps; ++w) {
+      if (w < warp) add += wsum[w];
+      all += wsum[w];
+    }
+    if (b < a.B) pre[b + 1] = (int)(add + x);
+    carry += all;
+    __syncthreads();
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (tid == 0) pre[0] = 0;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0 && blockIdx.x == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
+    return;
+  }
+  const long long total = carry;
+  if (total > INT32_MAX) {  // more steps than a call can count (16 TB of cache read)
+    if (tid == 0 && blockIdx.x == 0) set_error(a.err, MTP_ERR_CAPACITY);
+    return;
+  }
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < kA8MinShare) share = kA8MinShare;
+  long long u = (long long)blockIdx.x * share;
+  const long long u_end = min(total, u + share);
+
+  const uint32_t ring = smem_addr(smem) + warp * (S::kStages * S::kStage);
+  float* merge = reinterpret_cast<float*>(smem);
+  unsigned char* qf = smem + S::kMain;
+
+  while (u < u_end) {
+    // ---- the piece: request b, kv head g, tile, steps [s_lo, s_hi)
+    int b = 0;
+    {
+      int lo = 0, hi = a.B - 1;  // the request with pre[b] <= u < pre[b + 1]
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+    }
+    int o0, n, L;
+    request(b, o0, n, L);
+    const int base = L - n;
+    const int steps = (L + STEP - 1) / STEP, tiles = (n * G + S::kCols - 1) / S::kCols;
+    const long long in = u - pre[b];
+    const int seg = (int)(in / steps), s_lo = (int)(in - (long long)seg * steps);
+    const int g = seg / tiles, tile = seg - g * tiles;
+    const int s_hi = (int)min((long long)steps, s_lo + (u_end - u));
+    const long long seg_u0 = pre[b] + (long long)seg * steps;   // the segment's first unit
+    const int col0 = tile * S::kCols, ncols = min(S::kCols, n * G - col0);
+
+    // ---- queries: per column a power of two that brings them into fp16's
+    // range, then fragments in the order the lanes read them
+    __syncthreads();  // the last piece's shared memory is free
+    for (int c = warp; c < S::kCols; c += kA8Warps) {
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const bool lane_on = lane < HD / 4;
+      if (c < ncols && lane_on) {
+        const int cc = col0 + c;
+        const T* qp = (const T*)a.q + (long long)(o0 + (cc >> a.g_shift)) * a.q_stride +
+                      ((long long)g * G + (cc & (G - 1))) * HD + lane * 4;
 #pragma unroll
-  for (int e = 0; e < DPL; ++e)
-    Elem<T>::store1((T*)a.out + ((long long)r * a.n_q + h) * HD + lane * DPL + e, o[e] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(long long)r * a.n_q + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        for (int e = 0; e < 4; ++e) x[e] = Elem<T>::loads(qp + e);
+      }
+      float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+      m = warp_max(m);
+      int sh = 0;  // largest element to [2^14, 2^15)
+      if (m > 0.0f && finite_f(m)) sh = min(126, 141 - (int)(__float_as_uint(m) >> 23));
+      const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+      if (lane == 0) qfac_s[c] = a.qscale * (1.0f / up);
+      if (lane_on) {
+        // element d = 4 lane: half d / 64, lane group (d % 64) / 16, word (d % 16) / 4
+        const int ks = (lane >> 4) * 4 + (lane & 3), fl = (c & 7) * 4 + ((lane & 15) >> 2);
+        uint2 hi;
+        hi.x = pack_half2(x[0] * up, x[1] * up);
+        hi.y = pack_half2(x[2] * up, x[3] * up);
+        uint2* dst = reinterpret_cast<uint2*>(qf) + ((size_t)(c >> 3) * KS + ks) * 32 + fl;
+        *dst = hi;
+        if constexpr (SPLIT == 2) {
+          const float2 h0 = unpack_half2(hi.x), h1 = unpack_half2(hi.y);
+          dst[(size_t)NT * KS * 32] = make_uint2(pack_half2(x[0] * up - h0.x, x[1] * up - h0.y),
+                                                 pack_half2(x[2] * up - h1.x, x[3] * up - h1.y));
+        }
+      }
+    }
+    __syncthreads();
+    uint2 qreg[kQReg ? SPLIT : 1][kQReg ? NT : 1][kQReg ? KS : 1];
+    if constexpr (kQReg) {
+#pragma unroll
+      for (int sp = 0; sp < SPLIT; ++sp)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            qreg[sp][nt][ks] = reinterpret_cast<const uint2*>(qf)[((size_t)(sp * NT + nt) * KS + ks) * 32 + lane];
+    }
+    float qfac[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      qfac[nt][0] = qfac_s[nt * 8 + 2 * ti];
+      qfac[nt][1] = qfac_s[nt * 8 + 2 * ti + 1];
+    }
+
+    // ---- this warp's steps: s_lo + warp, + 4, ...
+    const int n_my = s_hi - s_lo > warp ? (s_hi - s_lo - warp + kA8Warps - 1) / kA8Warps : 0;
+    const int32_t* trow = a.kv.block_table + (long long)b * a.kv.max_blocks;
+    // table entries of 16 steps at a time: lane 2 i + j holds block j of step i
+    auto load_table = [&](int batch) -> int {
+      const int i = batch * 16 + (lane >> 1);
+      const int bi = 2 * (s_lo + warp + kA8Warps * i) + (lane & 1);
+      int id = -1;
+      if (i < n_my && (long long)bi * kBlk < L) {
+        id = trow[bi];
+        if (id < 0 || id >= a.kv.num_blocks) {
+          set_error(a.err, MTP_ERR_CAPACITY);
+          id = -1;
+        }
+      }
+      return id;
+    };
+    int tbl = -1, tnext = load_table(0);
+    auto issue = [&](int i) {
+      if (i < n_my) {
+        if ((i & 15) == 0) {
+          tbl = tnext;
+          tnext = load_table((i >> 4) + 1);
+        }
+        const int tok0 = (s_lo + warp + kA8Warps * i) * STEP;
+        const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStage;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int id = __shfl_sync(0xffffffffu, tbl, 2 * (i & 15) + j);
+          const long long t = (long long)max(id, 0) * a.n_kv + g;
+          const unsigned char* kp = (const unsigned char*)a.kv.k_pool + t * (kBlk * HD);
+          const unsigned char* vp = (const unsigned char*)a.kv.v_pool + t * (kBlk * HD);
+#pragma unroll
+          for (int x = 0; x < HD / 32; ++x) {
+            const int idx = x * 32 + lane, r = idx / (HD / 16), c = idx % (HD / 16);
+            const int bytes = id >= 0 && tok0 + 16 * j + r < L ? 16 : 0;
+            cp16(st + k_at<HD>(16 * j + r, c), kp + idx * 16, bytes);
+            cp16(st + S::kTile + v_at<HD>(16 * j + r, c), vp + idx * 16, bytes);
+          }
+          if (lane < 2) cp4(st + 2 * S::kTile + (lane * 2 + j) * 4, (lane ? a.kv.v_scale : a.kv.k_scale) + t, id >= 0 ? 4 : 0);
+        }
+      }
+      cp_commit();
+    };
+
+    float o[NT][MT][4], m_run[NT][2], l_run[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
+      m_run[nt][0] = m_run[nt][1] = -INFINITY;
+      l_run[nt][0] = l_run[nt][1] = 0.0f;
+    }
+
+    // whether column c (of the tile) sees token t >= base
+    auto sees = [&](int c, int t) -> bool {
+      const int i = (col0 + c) >> a.g_shift, j = t - base;
+      if (i >= n || j >= n) return false;
+      if (!a.mask) return j <= i;
+      return (uint32_t)a.mask[(long long)(o0 + i) * a.mask_words + (j >> 5)] >> (j & 31) & 1u;
+    };
+
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+    for (int it = 0; it < n_my; ++it) {
+      cp_wait<S::kStages - 2>();
+      __syncwarp();
+      issue(it + S::kStages - 1);
+      const uint32_t st = ring + (uint32_t)(it % S::kStages) * S::kStage;
+      const int tok0 = (s_lo + warp + kA8Warps * it) * STEP;
+      const bool edge = tok0 + STEP > base;   // some tokens are not seen by every column
+      // ---- scores
+      float sc[2][NT][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[j][nt][0] = sc[j][nt][1] = sc[j][nt][2] = sc[j][nt][3] = 0.0f;
+#pragma unroll
+        for (int hh = 0; hh < HD / 64; ++hh) {
+          const uint4 lo = lds128(st + k_at<HD>(16 * j + gi, hh * 4 + ti));
+          const uint4 hi = lds128(st + k_at<HD>(16 * j + gi + 8, hh * 4 + ti));
+          const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = e4m3_unpack2(lw[w] & 0xFFFFu), a2 = e4m3_unpack2(lw[w] >> 16);
+            const uint32_t a1 = e4m3_unpack2(hw[w] & 0xFFFFu), a3 = e4m3_unpack2(hw[w] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int sp = 0; sp < SPLIT; ++sp) {
+                uint2 qq;
+                if constexpr (kQReg) qq = qreg[sp][nt][hh * 4 + w];
+                else qq = reinterpret_cast<const uint2*>(qf)[((size_t)(sp * NT + nt) * KS + hh * 4 + w) * 32 + lane];
+                mma_f16(sc[j][nt], a0, a1, a2, a3, qq.x, qq.y);
+              }
+          }
+        }
+      }
+      // ---- online softmax over the step's 32 tokens
+      const float ks0 = lds32f(st + 2 * S::kTile), ks1 = lds32f(st + 2 * S::kTile + 4);
+      const float vs0 = lds32f(st + 2 * S::kTile + 8), vs1 = lds32f(st + 2 * S::kTile + 12);
+      float alpha[NT][2];
+      bool moved = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // a zero scale stands for zero entries: a factor above zero keeps
+          // -inf * f from becoming NaN
+          const float f0 = fmaxf(ks0 * qfac[nt][e], 1e-37f), f1 = fmaxf(ks1 * qfac[nt][e], 1e-37f);
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int t = tok0 + 16 * j + 8 * h + gi;
+                if (t >= L || (t >= base && !sees(nt * 8 + 2 * ti + e, t))) sc[j][nt][2 * h + e] = -INFINITY;
+              }
+          }
+          float mx = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]) * f0, fmaxf(sc[1][nt][e], sc[1][nt][2 + e]) * f1);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          // the reference r: a whole number, so that it moves rarely, 14 below
+          // the maximum, so that fp16 keeps 11 bits of weights down to 2^-28
+          // of the largest.  Beyond 2^20 that sum would round: r = maximum.
+          const float ref = fabsf(mx) > 1048576.0f ? mx : ceilf(mx) - 14.0f;
+          const float rn = fmaxf(m_run[nt][e], ref);
+          const float ru = rn == -INFINITY ? 0.0f : rn;
+          alpha[nt][e] = ex2(m_run[nt][e] - ru);
+          moved |= rn != m_run[nt][e];
+          m_run[nt][e] = rn;
+          float sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float p = ex2(fmaf(sc[j][nt][2 * h + e], j ? f1 : f0, -ru));
+              sc[j][nt][2 * h + e] = p;
+              sum += p;
+            }
+          l_run[nt][e] = l_run[nt][e] * alpha[nt][e] + sum;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            o[nt][mt][0] *= alpha[nt][0];
+            o[nt][mt][1] *= alpha[nt][1];
+            o[nt][mt][2] *= alpha[nt][0];
+            o[nt][mt][3] *= alpha[nt][1];
+          }
+      }
+      // ---- values
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t pb[SPLIT][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t h0 = pack_half2(sc[j][nt][0], sc[j][nt][1]), h1 = pack_half2(sc[j][nt][2], sc[j][nt][3]);
+          pb[0][nt][0] = movmatrix(h0);
+          pb[0][nt][1] = movmatrix(h1);
+          if constexpr (SPLIT == 2) {
+            const float2 f0 = unpack_half2(h0), f1 = unpack_half2(h1);
+            pb[1][nt][0] = movmatrix(pack_half2(sc[j][nt][0] - f0.x, sc[j][nt][1] - f0.y));
+            pb[1][nt][1] = movmatrix(pack_half2(sc[j][nt][2] - f1.x, sc[j][nt][3] - f1.y));
+          }
+        }
+        // tokens 2 ti, 2 ti + 1, 2 ti + 8, 2 ti + 9; dims (HD / 8) gi ..
+        constexpr int WD = HD / 32;  // words of a token per lane
+        uint32_t v[4][WD];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = 16 * j + 2 * ti + (x & 1) + (x >> 1) * 8;
+          if constexpr (HD == 128) {
+            const uint4 y = lds128(st + S::kTile + v_at<HD>(r, gi));
+            v[x][0] = y.x; v[x][1] = y.y; v[x][2] = y.z; v[x][3] = y.w;
+          } else {
+            const uint2 y = lds64(st + S::kTile + v_at<HD>(r, gi >> 1) + (gi & 1) * 8);
+            v[x][0] = y.x; v[x][1] = y.y;
+          }
+        }
+        if (edge) {
+          // a NaN entry must not reach columns that do not see it through
+          // 0 * NaN: take it out of the product and put it in by hand
+          uint32_t any = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int w = 0; w < WD; ++w) {
+              const uint32_t nb = nan_bytes(v[x][w]);
+              any |= nb;
+              v[x][w] &= ~((nb >> 7) * 0xFFu);
+            }
+          if (__any_sync(0xffffffffu, any != 0)) {
+            for (int t = 0; t < 16; ++t) {
+              uint32_t nb[WD];
+#pragma unroll
+              for (int w = 0; w < WD; ++w) {
+                uint32_t y;
+                const uint32_t at = st + S::kTile + (HD == 128 ? v_at<HD>(16 * j + t, gi) : v_at<HD>(16 * j + t, gi >> 1) + (gi & 1) * 8);
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(y) : "r"(at + 4 * w));
+                nb[w] = nan_bytes(y);
+              }
+              const int tok = tok0 + 16 * j + t;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  if (!(tok < L && (tok < base || sees(nt * 8 + 2 * ti + e, tok)))) continue;
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                      if (nb[mt >> 1] >> (8 * (2 * (mt & 1) + h)) & 0x80u)
+                        o[nt][mt][2 * h + e] = __uint_as_float(0x7FC00000u);
+                }
+            }
+          }
+        }
+        const float vs = j ? vs1 : vs0;
+#pragma unroll
+        for (int w = 0; w < WD; ++w) {
+          const uint32_t p01 = __byte_perm(v[0][w], v[1][w], 0x5140), q01 = __byte_perm(v[0][w], v[1][w], 0x7362);
+          const uint32_t p23 = __byte_perm(v[2][w], v[3][w], 0x5140), q23 = __byte_perm(v[2][w], v[3][w], 0x7362);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int mt = 2 * w + h;
+            const uint32_t x01 = h ? q01 : p01, x23 = h ? q23 : p23;
+            const uint32_t a0 = e4m3_unpack2(x01 & 0xFFFFu), a1 = e4m3_unpack2(x01 >> 16);
+            const uint32_t a2 = e4m3_unpack2(x23 & 0xFFFFu), a3 = e4m3_unpack2(x23 >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float pv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int sp = 0; sp < SPLIT; ++sp) mma_f16(pv, a0, a1, a2, a3, pb[sp][nt][0], pb[sp][nt][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][mt][e] = fmaf(pv[e], vs, o[nt][mt][e]);
+            }
+          }
+        }
+      }
+    }
+
+    // ---- join the warps: the ring becomes [warp][column][HD + 4]
+    cp_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = l_run[nt][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int c = nt * 8 + 2 * ti + e;
+        if (gi == 0) {
+          wm[warp][c] = m_run[nt][e];
+          wl[warp][c] = l;
+        }
+        float* row = merge + (warp * S::kCols + c) * S::kPitch + gi * (HD / 8);
+#pragma unroll
+        for (int mt = 0; mt < MT; mt += 2)
+          *reinterpret_cast<float4*>(row + 2 * mt) =
+              make_float4(o[nt][mt][e], o[nt][mt][2 + e], o[nt][mt + 1][e], o[nt][mt + 1][2 + e]);
+      }
+    __syncthreads();
+    const long long c_first = seg_u0 / share, c_last = (seg_u0 + steps - 1) / share;
+    const bool whole = c_first == c_last;
+    const int slot = (long long)blockIdx.x == c_first ? 1 : 0;
+    auto finish = [&](int c, int d4, float4 x, float M, float Ls) {
+      const int cc = col0 + c;
+      const long long row = (long long)(o0 + (cc >> a.g_shift)) * (a.n_kv << a.g_shift) + (long long)g * G + (cc & (G - 1));
+      const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+      T* op = (T*)a.out + row * HD + d4 * 4;
+      if (!MTP_IN_BOUNDS(a.err, row * HD + d4 * 4 + 3, (long long)a.T * (a.n_kv << a.g_shift) * HD)) return;
+      Elem<T>::store1(op, x.x * inv);
+      Elem<T>::store1(op + 1, x.y * inv);
+      Elem<T>::store1(op + 2, x.z * inv);
+      Elem<T>::store1(op + 3, x.w * inv);
+      if (a.lse && d4 == 0) a.lse[row] = Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
+    };
+    for (int i = tid; i < ncols * (HD / 4); i += kA8Threads) {
+      const int c = i / (HD / 4), d4 = i - c * (HD / 4);
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kA8Warps; ++w) M = fmaxf(M, wm[w][c]);
+      const float mu = M == -INFINITY ? 0.0f : M;
+      float Ls = 0.0f;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kA8Warps; ++w) {
+        const float f = ex2(wm[w][c] - mu);
+        const float4 y = *reinterpret_cast<const float4*>(merge + (w * S::kCols + c) * S::kPitch + d4 * 4);
+        Ls += wl[w][c] * f;
+        x.x = fmaf(y.x, f, x.x);
+        x.y = fmaf(y.y, f, x.y);
+        x.z = fmaf(y.z, f, x.z);
+        x.w = fmaf(y.w, f, x.w);
+      }
+      if (whole) {
+        finish(c, d4, x, M, Ls);
+      } else {
+        float* pr = a.part + ((2ll * blockIdx.x + slot) * kA8MaxCols + c) * (HD + 4);
+        *reinterpret_cast<float4*>(pr + d4 * 4) = x;
+        if (d4 == 0) *reinterpret_cast<float2*>(pr + HD) = make_float2(M, Ls);
+      }
+    }
+    if (!whole) {
+      __syncthreads();
+      if (tid == 0) last_s = arrive_last(a.cnt + c_first, (int)(c_last - c_first + 1));
+      __syncthreads();
+      if (last_s) {
+        for (int i = tid; i < ncols * (HD / 4); i += kA8Threads) {
+          const int c = i / (HD / 4), d4 = i - c * (HD / 4);
+          float M = -INFINITY, Ls = 0.0f;
+          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          constexpr int kAhead = 8;
+          for (long long k0 = c_first; k0 <= c_last; k0 += kAhead) {
+            float2 ml[kAhead];
+            float4 y[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+              ml[k] = make_float2(-INFINITY, 0.0f);
+              y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (k0 + k <= c_last) {
+                const float* pr = a.part + ((2 * (k0 + k) + (k0 + k == c_first ? 1 : 0)) * kA8MaxCols + c) * (HD + 4);
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(pr + HD));
+                y[k] = __ldcg(reinterpret_cast<const float4*>(pr) + d4);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+              const float mn = fmaxf(M, ml[k].x), mu = mn == -INFINITY ? 0.0f : mn;
+              const float f0 = ex2(M - mu), f1 = ex2(ml[k].x - mu);
+              Ls = Ls * f0 + ml[k].y * f1;
+              x.x = x.x * f0 + y[k].x * f1;
+              x.y = x.y * f0 + y[k].y * f1;
+              x.z = x.z * f0 + y[k].z * f1;
+              x.w = x.w * f0 + y[k].w * f1;
+              M = mn;
+            }
+          }
+          finish(c, d4, x, M, Ls);
+        }
+      }
+    }
+    u += s_hi - s_lo;
+  }
+}
+
+static int a8_grid(const mtp_ctx* ctx) { return 2 * ctx->num_sms; }
+
+// counters, then the partials
+static size_t a8_counter_bytes(const mtp_ctx* ctx) { return ((size_t)a8_grid(ctx) * 4 + 255) & ~(size_t)255; }
+
+template <typename T, int HD, int NT>
+static cudaError_t attn8_launch(mtp_ctx* ctx, cudaStream_t s, const Attn8Args& a) {
+  using S = Attn8Shape<HD, NT, sizeof(T) == 4 ? 2 : 1>;
+  cudaError_t e = ensure_smem((const void*)kv8_attn_kernel<T, HD, NT>, S::kBytes);
+  if (e != cudaSuccess) return e;
+  kv8_attn_kernel<T, HD, NT><<<a8_grid(ctx), kA8Threads, S::kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD>
+static cudaError_t attn8_pick(mtp_ctx* ctx, cudaStream_t s, const Attn8Args& a, int nt) {
+  switch (nt) {
+    case 1: return attn8_launch<T, HD, 1>(ctx, s, a);
+    case 2: return attn8_launch<T, HD, 2>(ctx, s, a);
+    case 3: return attn8_launch<T, HD, 3>(ctx, s, a);
+    default: return attn8_launch<T, HD, 4>(ctx, s, a);
+  }
 }
 
 }  // namespace mtp
@@ -96,12 +675,15 @@ using namespace mtp;
 
 extern "C" {
 
-size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx) { return ctx ? 256 : 0; }
+size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx) {
+  if (!ctx) return 0;
+  return a8_counter_bytes(ctx) + (size_t)2 * a8_grid(ctx) * kA8MaxCols * (ctx->cfg.head_dim + 4) * 4;
+}
 
 mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
                              const void* q, int64_t q_stride, const mtp_kv8* kv, const int32_t* mask, int mask_words,
                              float scale, void* out, float* lse, void* ws, size_t ws_bytes) {
-  if (!ctx || B < 1 || B > ctx->cfg.max_batch || T < 0 || !row_offsets || !q || !out || !kv8_ok(kv))
+  if (!ctx || B < 1 || B > ctx->cfg.max_batch || B > kA8MaxB || T < 0 || !row_offsets || !q || !out || !kv8_ok(kv))
     return MTP_ERR_INVALID;
   const mtp_config& c = ctx->cfg;
   if (max_rows < 1 || max_rows > 256 || q_stride < (int64_t)c.n_q_heads * c.head_dim) return MTP_ERR_INVALID;
@@ -111,20 +693,35 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
   if (T == 0) return MTP_OK;
   DeviceGuard dev(ctx->device);
   if (!dev.ok) return MTP_ERR_CUDA;
-  Attn8Args a{q, out, lse, row_offsets, mask, *kv, ctx->err, q_stride, B, T, max_rows, mask_words, c.n_kv_heads,
-              c.n_q_heads, scale * 1.4426950408889634f};
-  const dim3 grid(T, (c.n_q_heads + 3) / 4);
+  Attn8Args a{};
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.row_offsets = row_offsets;
+  a.mask = mask;
+  a.kv = *kv;
+  a.err = ctx->err;
+  a.cnt = (int*)ws;
+  a.part = (float*)((char*)ws + a8_counter_bytes(ctx));
+  a.q_stride = q_stride;
+  a.B = B;
+  a.T = T;
+  a.max_rows = max_rows;
+  a.mask_words = mask_words;
+  a.n_kv = c.n_kv_heads;
+  const int G = c.n_q_heads / c.n_kv_heads;
+  for (a.g_shift = 0; (1 << a.g_shift) < G; ++a.g_shift) {
+  }
+  a.qscale = scale * 1.4426950408889634f;
+  // columns per tile: the fewest tiles of at most 32 columns, evenly filled
+  const int cols = max_rows * G, tiles = (cols + kA8MaxCols - 1) / kA8MaxCols;
+  const int nt = (cols + 8 * tiles - 1) / (8 * tiles);
   cudaStream_t s = (cudaStream_t)stream;
   const bool bf = c.dtype == MTP_DTYPE_BF16;
-  if (c.head_dim == 128) {
-    if (bf) kv8_attn_kernel<uint16_t, 128><<<grid, 128, 0, s>>>(a);
-    else kv8_attn_kernel<float, 128><<<grid, 128, 0, s>>>(a);
-  } else {
-    if (bf) kv8_attn_kernel<uint16_t, 64><<<grid, 128, 0, s>>>(a);
-    else kv8_attn_kernel<float, 64><<<grid, 128, 0, s>>>(a);
-  }
+  const cudaError_t e = c.head_dim == 128 ? (bf ? attn8_pick<uint16_t, 128>(ctx, s, a, nt) : attn8_pick<float, 128>(ctx, s, a, nt))
+                                          : (bf ? attn8_pick<uint16_t, 64>(ctx, s, a, nt) : attn8_pick<float, 64>(ctx, s, a, nt));
   ctx->launches++;
-  return launch_status(cudaGetLastError());
+  return launch_status(e);
 }
 
 }  // extern "C"
