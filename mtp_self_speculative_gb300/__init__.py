@@ -87,6 +87,7 @@ class Context:
         self.cfg = cfg
         self.weights = weights
         self.device = device
+        self.dtype, self.head_dim = torch_dtype(cfg.dtype), int(cfg.head_dim)
 
     def close(self):
         if self.handle:
@@ -395,10 +396,16 @@ def mtp_kv_truncate(ctx: Context, kv: KVCache, new_len: torch.Tensor, stream=Non
 
 # -------------------- rotary positions, the 8-bit KV cache, logit processing
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _dev_ptr(ctx: Context, t: Optional[torch.Tensor], dtype, name: str, shape=None) -> Optional[int]:
     """_ptr with the context's device and a shape (None entries: any size)."""
     if t is None:
         return None
+    if (t.get_device() == ctx.device and (dtype is None or t.dtype is dtype) and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     p = _ptr(t, dtype, name)
     if ctx.device is not None and t.device.index != ctx.device:
         raise ValueError("%s must be on the context's device cuda:%d, got %s" % (name, ctx.device, t.device))
@@ -413,25 +420,27 @@ def _row_ptr(ctx: Context, t: torch.Tensor, name: str, rows: int, heads: int):
     """Pointer and row stride of a [rows, heads, head_dim] tensor in the
     context's dtype whose rows are contiguous (a slice of a packed [rows,
     width] projection, say)."""
-    hd, dt = ctx.cfg.head_dim, torch_dtype(ctx.cfg.dtype)
-    if t.dim() != 3 or tuple(t.shape) != (rows, heads, hd):
+    hd, dt = ctx.head_dim, ctx.dtype
+    if t.shape != (rows, heads, hd):
         raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, hd, tuple(t.shape)))
-    if t.dtype != dt:
+    if t.dtype is not dt:
         raise ValueError("%s must be %s, got %s" % (name, dt, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if ctx.device is not None and t.device.index != ctx.device:
-        raise ValueError("%s must be on the context's device cuda:%d, got %s" % (name, ctx.device, t.device))
-    st = t.stride()
-    if rows and (st[2] != 1 or (heads > 1 and st[1] != hd) or (rows > 1 and st[0] < heads * hd)):
-        raise ValueError("%s must have contiguous, non-overlapping rows, got strides %s" % (name, st))
-    return t.data_ptr(), (st[0] if rows > 1 else heads * hd)
+    if t.get_device() != ctx.device:
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        raise ValueError("%s must be on the context's device cuda:%s, got %s" % (name, ctx.device, t.device))
+    s0, s1, s2 = t.stride()
+    if rows and (s2 != 1 or (heads > 1 and s1 != hd) or (rows > 1 and s0 < heads * hd)):
+        raise ValueError("%s must have contiguous, non-overlapping rows, got strides %s" % (name, (s0, s1, s2)))
+    return t.data_ptr(), (s0 if rows > 1 else heads * hd)
 
 
 def _ctx_stream(ctx: Context, stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream(ctx.device)
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(ctx.device)
+    return torch.cuda.current_stream(ctx.device).cuda_stream
 
 
 class RopeTable(MTPRopeTable):
@@ -496,6 +505,13 @@ class KVCache8:
         return cls(pools[0], pools[1], scales[0], scales[1], block_table, ints[0], ints[1], ints[2])
 
     def struct(self, ctx: Context) -> MTPKV8:
+        # the checks run again when a field has become another tensor
+        ptrs = (ctx.cfg, self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.k_scale.data_ptr(),
+                self.v_scale.data_ptr(), self.block_table.data_ptr(), self.seq_len.data_ptr(),
+                self.pending.data_ptr(), self.arrive.data_ptr(), self.k_pool.shape, self.block_table.shape)
+        done = self.__dict__.get("_checked")
+        if done is not None and done[0] == ptrs:
+            return done[1]
         c = ctx.cfg
         nb, B = int(self.k_pool.shape[0]), int(self.seq_len.shape[0])
         if self.block_table.dim() != 2:
@@ -505,13 +521,14 @@ class KVCache8:
             if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
                 raise ValueError("%s must be uint8 or float8_e4m3fn, got %s" % (name, t.dtype))
         i32, f32 = torch.int32, torch.float32
-        return MTPKV8(_dev_ptr(ctx, self.k_pool, None, "k_pool", pool), _dev_ptr(ctx, self.v_pool, None, "v_pool", pool),
-                      _dev_ptr(ctx, self.k_scale, f32, "k_scale", per),
-                      _dev_ptr(ctx, self.v_scale, f32, "v_scale", per),
-                      _dev_ptr(ctx, self.block_table, i32, "block_table", (B, None)),
-                      _dev_ptr(ctx, self.seq_len, i32, "seq_len", (B,)),
-                      _dev_ptr(ctx, self.pending, i32, "pending", (B,)),
-                      _dev_ptr(ctx, self.arrive, i32, "arrive", (B,)), nb, int(self.block_table.shape[1]))
+        st = MTPKV8(_dev_ptr(ctx, self.k_pool, None, "k_pool", pool), _dev_ptr(ctx, self.v_pool, None, "v_pool", pool),
+                    _dev_ptr(ctx, self.k_scale, f32, "k_scale", per), _dev_ptr(ctx, self.v_scale, f32, "v_scale", per),
+                    _dev_ptr(ctx, self.block_table, i32, "block_table", (B, None)),
+                    _dev_ptr(ctx, self.seq_len, i32, "seq_len", (B,)),
+                    _dev_ptr(ctx, self.pending, i32, "pending", (B,)),
+                    _dev_ptr(ctx, self.arrive, i32, "arrive", (B,)), nb, int(self.block_table.shape[1]))
+        self.__dict__["_checked"] = (ptrs, st)
+        return st
 
 
 def mtp_kv8_append(ctx: Context, kv: KVCache8, k: torch.Tensor, v: torch.Tensor, row_offsets: torch.Tensor,
