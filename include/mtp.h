@@ -571,9 +571,9 @@ mtp_status mtp_kv8_commit_path(mtp_ctx* ctx, void* stream, int B, const mtp_kv8*
                                int keep_stride, const int32_t* n_keep);
 
 /* Bytes of a workspace of mtp_kv8_attention for this context's device; 0 for
- * a NULL context.  The caller zeroes it once; every call leaves it ready for
- * the next.  Calls that may run at the same time need workspaces of their
- * own, graphs that contain such calls included. */
+ * a NULL context.  It needs no initialisation and carries nothing from one
+ * call to the next.  Calls that may run at the same time need workspaces of
+ * their own, graphs that contain such calls included. */
 size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx);
 
 /* Attention of new rows over an 8-bit cache.  Request b's rows r =

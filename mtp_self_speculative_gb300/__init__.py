@@ -615,7 +615,7 @@ class Attention8Workspace:
         if n == 0:
             raise MTPError(MTP_ERR_INVALID, "mtp_kv8_attention_workspace_bytes")
         self.device = ctx.device
-        self.ws = torch.zeros(n, dtype=torch.uint8, device="cuda:%d" % ctx.device)
+        self.ws = torch.empty(n, dtype=torch.uint8, device="cuda:%d" % ctx.device)
 
 
 def mtp_kv8_attention(ctx: Context, kv: KVCache8, q: torch.Tensor, row_offsets: torch.Tensor, out: torch.Tensor,

@@ -24,8 +24,12 @@
 // a single long context both fill the machine.  Each warp streams every
 // fourth step of its block's share through its own ring of shared memory
 // (cp.async, 16 bytes a lane, swizzled so that the fragment reads are free of
-// bank conflicts).  Pieces of a segment that spans blocks meet in the
-// workspace; the last block to arrive joins them in a fixed order.
+// bank conflicts).  A segment (request, kv head, tile) costs a start and an end
+// besides its steps, so it counts kA8Lead steps more.  Pieces of a segment
+// that spans blocks meet in the workspace, and a second, small kernel joins
+// them in a fixed order: the joining of a long context (a piece from every
+// block) is spread over the machine, where the last block to arrive took
+// three quarters of the call.
 #include <math.h>
 
 #include "mtp_kv8.cuh"
@@ -36,7 +40,8 @@ constexpr int kA8Warps = 4;
 constexpr int kA8Threads = kA8Warps * 32;
 constexpr int kA8Step = 32;        // tokens of a step (two cache blocks)
 constexpr int kA8MaxB = 1024;      // requests of a call (prefix sums in shared memory)
-constexpr int kA8MinShare = 4;     // steps of a thread block's share at least
+constexpr int kA8MinShare = 8;     // units of a thread block's share at least
+constexpr int kA8Lead = 4;         // units that a segment's start and end count for
 constexpr int kA8MaxCols = 32;     // columns of a tile
 
 struct Attn8Args {
@@ -47,8 +52,8 @@ struct Attn8Args {
   const int32_t* mask;
   mtp_kv8 kv;
   int* err;
-  float* part;     // [2 * grid][32][HD + 4]: o, then maximum and sum
-  int* cnt;        // [grid]
+  float* part;     // [2 * grid][32][HD + 4]: o, then reference and sum
+  int4* meta;      // [2 * grid]: the segment that begins in a block and goes on in others
   long long q_stride;
   int B, T, max_rows, mask_words, n_kv, g_shift;
   float qscale;    // scale * log2(e)
@@ -125,7 +130,9 @@ template <int HD, int NT, int SPLIT>
 struct Attn8Shape {
   static constexpr int kTile = kA8Step * HD;               // bytes of a staged K (or V) tile
   static constexpr int kStage = 2 * kTile + 16;            // K, V, two scales each
-  static constexpr int kStages = SPLIT == 2 && NT >= 3 ? 2 : 3;   // two blocks per SM fit their shared memory
+  static constexpr int kBlocks = SPLIT == 1 && NT == 1 ? 3 : 2;   // thread blocks per SM (registers)
+  // stages of a warp's ring: what the shared memory of an SM holds for them
+  static constexpr int kStages = kBlocks == 3 || (SPLIT == 2 && NT >= 3) ? 2 : 3;
   static constexpr int kRing = kA8Warps * kStages * kStage;
   static constexpr int kCols = 8 * NT;
   static constexpr int kPitch = HD + 4;                    // floats of a merged row
@@ -135,8 +142,36 @@ struct Attn8Shape {
   static constexpr int kBytes = kMain + kQ;
 };
 
+// Write four elements of a column's result and its lse.
+template <typename T, int HD>
+__device__ __forceinline__ void attn8_finish(const Attn8Args& a, int o0, int col, int g, int d4, float4 x, float ref,
+                                             float sum) {
+  const int G = 1 << a.g_shift;
+  const long long row = (long long)(o0 + (col >> a.g_shift)) * (a.n_kv << a.g_shift) + (long long)g * G + (col & (G - 1));
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (!MTP_IN_BOUNDS(a.err, row * HD + d4 * 4 + 3, (long long)a.T * (a.n_kv << a.g_shift) * HD)) return;
+  T* op = (T*)a.out + row * HD + d4 * 4;
+  Elem<T>::store1(op, x.x * inv);
+  Elem<T>::store1(op + 1, x.y * inv);
+  Elem<T>::store1(op + 2, x.z * inv);
+  Elem<T>::store1(op + 3, x.w * inv);
+  if (a.lse && d4 == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
+// Take a partial result (reference m, sum l, o) into another.
+__device__ __forceinline__ void attn8_take(float& M, float& Ls, float4& x, float m, float l, const float4& y) {
+  const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.0f : mn;
+  const float f0 = ex2(M - mu), f1 = ex2(m - mu);
+  Ls = Ls * f0 + l * f1;
+  x.x = x.x * f0 + y.x * f1;
+  x.y = x.y * f0 + y.y * f1;
+  x.z = x.z * f0 + y.z * f1;
+  x.w = x.w * f0 + y.w * f1;
+  M = mn;
+}
+
 template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args a) {
+__global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4 ? 2 : 1>::kBlocks)) kv8_attn_kernel(const Attn8Args a) {
   constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
   using S = Attn8Shape<HD, NT, SPLIT>;
   constexpr int KS = HD / 16;                 // k-steps of Q K^T
@@ -148,8 +183,9 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
   __shared__ long long wsum[kA8Warps];
   __shared__ float qfac_s[S::kCols];
   __shared__ float wm[kA8Warps][S::kCols], wl[kA8Warps][S::kCols];
-  __shared__ int last_s;
 
+  pdl_wait();
+  pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
   const int G = 1 << a.g_shift;
 
@@ -160,7 +196,8 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
     n = o1 - o0;
     const long long len = (long long)sl + pe;
     L = (int)len;
-    return n > 0 && n <= a.max_rows && sl >= 0 && pe >= 0 && len >= n && len <= (long long)a.kv.max_blocks * kBlk;
+    return n > 0 && n <= a.max_rows && sl >= 0 && pe >= 0 && len >= n &&
+           len <= min((long long)a.kv.max_blocks * kBlk, 1ll << 30);
   };
   long long carry = 0;
   int bad = 0;
@@ -175,7 +212,7 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
         int oo, n, L;
         if (request(b, oo, n, L)) {
           const int tiles = (n * G + S::kCols - 1) / S::kCols;
-          units = (long long)((L + STEP - 1) / STEP) * tiles * a.n_kv;
+          units = (long long)((L + STEP - 1) / STEP + kA8Lead) * tiles * a.n_kv;
         } else if (blockIdx.x == 0) {
           set_error(a.err, n <= a.max_rows && (long long)a.kv.seq_len[b] + a.kv.pending[b] > (long long)a.kv.max_blocks * kBlk
                                ? MTP_ERR_CAPACITY : MTP_ERR_DEVICE_ARGS);
@@ -200,7 +237,10 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
     carry += all;
     __syncthreads();
   }
-  if (tid == 0) pre[0] = 0;
+  if (tid == 0) {
+    pre[0] = 0;
+    a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
   if (__syncthreads_or(bad)) {
     if (tid == 0 && blockIdx.x == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
     return;
@@ -235,15 +275,63 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
     const int base = L - n;
     const int steps = (L + STEP - 1) / STEP, tiles = (n * G + S::kCols - 1) / S::kCols;
     const long long in = u - pre[b];
-    const int seg = (int)(in / steps), s_lo = (int)(in - (long long)seg * steps);
+    const int seg = (int)(in / (steps + kA8Lead));
     const int g = seg / tiles, tile = seg - g * tiles;
-    const int s_hi = (int)min((long long)steps, s_lo + (u_end - u));
-    const long long seg_u0 = pre[b] + (long long)seg * steps;   // the segment's first unit
+    const long long seg_u0 = pre[b] + (long long)seg * (steps + kA8Lead) + kA8Lead;   // the segment's first step
+    const int s_lo = (int)max(0ll, u - seg_u0), s_hi = (int)min((long long)steps, u_end - seg_u0);
+    if (s_hi <= s_lo) break;   // the share ends before the segment's first step
     const int col0 = tile * S::kCols, ncols = min(S::kCols, n * G - col0);
+
+    // ---- this warp's steps: s_lo + warp, + 4, ...
+    __syncthreads();  // the last piece's shared memory is free
+    const int n_my = s_hi - s_lo > warp ? (s_hi - s_lo - warp + kA8Warps - 1) / kA8Warps : 0;
+    const int32_t* trow = a.kv.block_table + (long long)b * a.kv.max_blocks;
+    // table entries of 16 steps at a time: lane 2 i + j holds block j of step i
+    auto load_table = [&](int batch) -> int {
+      const int i = batch * 16 + (lane >> 1);
+      const int bi = 2 * (s_lo + warp + kA8Warps * i) + (lane & 1);
+      int id = -1;
+      if (i < n_my && (long long)bi * kBlk < L) {
+        id = trow[bi];
+        if (id < 0 || id >= a.kv.num_blocks) {
+          set_error(a.err, MTP_ERR_CAPACITY);
+          id = -1;
+        }
+      }
+      return id;
+    };
+    int tbl = -1, tnext = load_table(0);
+    auto issue = [&](int i) {
+      if (i < n_my) {
+        if ((i & 15) == 0) {
+          tbl = tnext;
+          tnext = load_table((i >> 4) + 1);
+        }
+        const int tok0 = (s_lo + warp + kA8Warps * i) * STEP;
+        const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStage;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int id = __shfl_sync(0xffffffffu, tbl, 2 * (i & 15) + j);
+          const long long t = (long long)max(id, 0) * a.n_kv + g;
+          const unsigned char* kp = (const unsigned char*)a.kv.k_pool + t * (kBlk * HD);
+          const unsigned char* vp = (const unsigned char*)a.kv.v_pool + t * (kBlk * HD);
+#pragma unroll
+          for (int x = 0; x < HD / 32; ++x) {
+            const int idx = x * 32 + lane, r = idx / (HD / 16), c = idx % (HD / 16);
+            const int bytes = id >= 0 && tok0 + 16 * j + r < L ? 16 : 0;
+            cp16(st + k_at<HD>(16 * j + r, c), kp + idx * 16, bytes);
+            cp16(st + S::kTile + v_at<HD>(16 * j + r, c), vp + idx * 16, bytes);
+          }
+          if (lane < 2) cp4(st + 2 * S::kTile + (lane * 2 + j) * 4, (lane ? a.kv.v_scale : a.kv.k_scale) + t, id >= 0 ? 4 : 0);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
 
     // ---- queries: per column a power of two that brings them into fp16's
     // range, then fragments in the order the lanes read them
-    __syncthreads();  // the last piece's shared memory is free
     for (int c = warp; c < S::kCols; c += kA8Warps) {
       float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       const bool lane_on = lane < HD / 4;
@@ -293,51 +381,6 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
       qfac[nt][1] = qfac_s[nt * 8 + 2 * ti + 1];
     }
 
-    // ---- this warp's steps: s_lo + warp, + 4, ...
-    const int n_my = s_hi - s_lo > warp ? (s_hi - s_lo - warp + kA8Warps - 1) / kA8Warps : 0;
-    const int32_t* trow = a.kv.block_table + (long long)b * a.kv.max_blocks;
-    // table entries of 16 steps at a time: lane 2 i + j holds block j of step i
-    auto load_table = [&](int batch) -> int {
-      const int i = batch * 16 + (lane >> 1);
-      const int bi = 2 * (s_lo + warp + kA8Warps * i) + (lane & 1);
-      int id = -1;
-      if (i < n_my && (long long)bi * kBlk < L) {
-        id = trow[bi];
-        if (id < 0 || id >= a.kv.num_blocks) {
-          set_error(a.err, MTP_ERR_CAPACITY);
-          id = -1;
-        }
-      }
-      return id;
-    };
-    int tbl = -1, tnext = load_table(0);
-    auto issue = [&](int i) {
-      if (i < n_my) {
-        if ((i & 15) == 0) {
-          tbl = tnext;
-          tnext = load_table((i >> 4) + 1);
-        }
-        const int tok0 = (s_lo + warp + kA8Warps * i) * STEP;
-        const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStage;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int id = __shfl_sync(0xffffffffu, tbl, 2 * (i & 15) + j);
-          const long long t = (long long)max(id, 0) * a.n_kv + g;
-          const unsigned char* kp = (const unsigned char*)a.kv.k_pool + t * (kBlk * HD);
-          const unsigned char* vp = (const unsigned char*)a.kv.v_pool + t * (kBlk * HD);
-#pragma unroll
-          for (int x = 0; x < HD / 32; ++x) {
-            const int idx = x * 32 + lane, r = idx / (HD / 16), c = idx % (HD / 16);
-            const int bytes = id >= 0 && tok0 + 16 * j + r < L ? 16 : 0;
-            cp16(st + k_at<HD>(16 * j + r, c), kp + idx * 16, bytes);
-            cp16(st + S::kTile + v_at<HD>(16 * j + r, c), vp + idx * 16, bytes);
-          }
-          if (lane < 2) cp4(st + 2 * S::kTile + (lane * 2 + j) * 4, (lane ? a.kv.v_scale : a.kv.k_scale) + t, id >= 0 ? 4 : 0);
-        }
-      }
-      cp_commit();
-    };
-
     float o[NT][MT][4], m_run[NT][2], l_run[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -355,8 +398,6 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
       return (uint32_t)a.mask[(long long)(o0 + i) * a.mask_words + (j >> 5)] >> (j & 31) & 1u;
     };
 
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
     for (int it = 0; it < n_my; ++it) {
       cp_wait<S::kStages - 2>();
       __syncwarp();
@@ -564,18 +605,6 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
     const long long c_first = seg_u0 / share, c_last = (seg_u0 + steps - 1) / share;
     const bool whole = c_first == c_last;
     const int slot = (long long)blockIdx.x == c_first ? 1 : 0;
-    auto finish = [&](int c, int d4, float4 x, float M, float Ls) {
-      const int cc = col0 + c;
-      const long long row = (long long)(o0 + (cc >> a.g_shift)) * (a.n_kv << a.g_shift) + (long long)g * G + (cc & (G - 1));
-      const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
-      T* op = (T*)a.out + row * HD + d4 * 4;
-      if (!MTP_IN_BOUNDS(a.err, row * HD + d4 * 4 + 3, (long long)a.T * (a.n_kv << a.g_shift) * HD)) return;
-      Elem<T>::store1(op, x.x * inv);
-      Elem<T>::store1(op + 1, x.y * inv);
-      Elem<T>::store1(op + 2, x.z * inv);
-      Elem<T>::store1(op + 3, x.w * inv);
-      if (a.lse && d4 == 0) a.lse[row] = Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
-    };
     for (int i = tid; i < ncols * (HD / 4); i += kA8Threads) {
       const int c = i / (HD / 4), d4 = i - c * (HD / 4);
       float M = -INFINITY;
@@ -595,68 +624,90 @@ __global__ void __launch_bounds__(kA8Threads, 2) kv8_attn_kernel(const Attn8Args
         x.w = fmaf(y.w, f, x.w);
       }
       if (whole) {
-        finish(c, d4, x, M, Ls);
+        attn8_finish<T, HD>(a, o0, col0 + c, g, d4, x, M, Ls);
       } else {
         float* pr = a.part + ((2ll * blockIdx.x + slot) * kA8MaxCols + c) * (HD + 4);
         *reinterpret_cast<float4*>(pr + d4 * 4) = x;
         if (d4 == 0) *reinterpret_cast<float2*>(pr + HD) = make_float2(M, Ls);
       }
     }
-    if (!whole) {
-      __syncthreads();
-      if (tid == 0) last_s = arrive_last(a.cnt + c_first, (int)(c_last - c_first + 1));
-      __syncthreads();
-      if (last_s) {
-        for (int i = tid; i < ncols * (HD / 4); i += kA8Threads) {
-          const int c = i / (HD / 4), d4 = i - c * (HD / 4);
-          float M = -INFINITY, Ls = 0.0f;
-          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          constexpr int kAhead = 8;
-          for (long long k0 = c_first; k0 <= c_last; k0 += kAhead) {
-            float2 ml[kAhead];
-            float4 y[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-              ml[k] = make_float2(-INFINITY, 0.0f);
-              y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (k0 + k <= c_last) {
-                const float* pr = a.part + ((2 * (k0 + k) + (k0 + k == c_first ? 1 : 0)) * kA8MaxCols + c) * (HD + 4);
-                ml[k] = __ldcg(reinterpret_cast<const float2*>(pr + HD));
-                y[k] = __ldcg(reinterpret_cast<const float4*>(pr) + d4);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-              const float mn = fmaxf(M, ml[k].x), mu = mn == -INFINITY ? 0.0f : mn;
-              const float f0 = ex2(M - mu), f1 = ex2(ml[k].x - mu);
-              Ls = Ls * f0 + ml[k].y * f1;
-              x.x = x.x * f0 + y[k].x * f1;
-              x.y = x.y * f0 + y[k].y * f1;
-              x.z = x.z * f0 + y[k].z * f1;
-              x.w = x.w * f0 + y[k].w * f1;
-              M = mn;
-            }
-          }
-          finish(c, d4, x, M, Ls);
-        }
-      }
+    if (tid == 0 && !whole && slot == 1) {
+      a.meta[2 * blockIdx.x + 1] = make_int4(o0, col0, ncols, g);
+      a.meta[2 * blockIdx.x] = make_int4((int)(c_last - c_first + 1), 0, 0, 0);
     }
-    u += s_hi - s_lo;
+    u = seg_u0 + s_hi;
   }
 }
 
-static int a8_grid(const mtp_ctx* ctx) { return 2 * ctx->num_sms; }
+// Joins the pieces of the segment that begins in thread block blockIdx.x of
+// the first kernel: block (x, y) takes the column pairs y, y + gridDim.y, ...;
+// kWays threads share an element's pieces, four loads in flight each.
+constexpr int kJoinThreads = 256;
 
-// counters, then the partials
-static size_t a8_counter_bytes(const mtp_ctx* ctx) { return ((size_t)a8_grid(ctx) * 4 + 255) & ~(size_t)255; }
+template <typename T, int HD>
+__global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8Args a) {
+  constexpr int kItems = 2 * (HD / 4), kWays = kJoinThreads / kItems;
+  __shared__ float4 xs[kWays][kItems];
+  __shared__ float2 ms[kWays][kItems];
+  pdl_wait();
+  const int c_first = blockIdx.x, count = a.meta[2 * c_first].x;
+  if (count == 0) return;
+  const int4 seg = a.meta[2 * c_first + 1];
+  const int item = threadIdx.x % kItems, way = threadIdx.x / kItems;
+  const int d4 = item % (HD / 4);
+  for (int c0 = 2 * blockIdx.y; c0 < seg.z; c0 += 2 * gridDim.y) {
+    const int c = c0 + item / (HD / 4);
+    float M = -INFINITY, Ls = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < seg.z) {
+      for (int k0 = way; k0 < count; k0 += 4 * kWays) {
+        float2 ml[4];
+        float4 y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int kk = k0 + k * kWays;
+          ml[k] = make_float2(-INFINITY, 0.0f);
+          y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (kk < count) {
+            const float* pr = a.part + ((2ll * (c_first + kk) + (kk == 0 ? 1 : 0)) * kA8MaxCols + c) * (HD + 4);
+            ml[k] = __ldcg(reinterpret_cast<const float2*>(pr + HD));
+            y[k] = __ldcg(reinterpret_cast<const float4*>(pr) + d4);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) attn8_take(M, Ls, x, ml[k].x, ml[k].y, y[k]);
+      }
+    }
+    __syncthreads();
+    xs[way][item] = x;
+    ms[way][item] = make_float2(M, Ls);
+    __syncthreads();
+    if (way == 0 && c < seg.z) {
+#pragma unroll
+      for (int w = 1; w < kWays; ++w) attn8_take(M, Ls, x, ms[w][item].x, ms[w][item].y, xs[w][item]);
+      attn8_finish<T, HD>(a, seg.x, seg.y + c, seg.w, d4, x, M, Ls);
+    }
+  }
+}
+
+// Blocks per SM of the widest grid: the workspace serves every tile width.
+constexpr int kA8MaxBlocks = 3;
+static size_t a8_meta_bytes(const mtp_ctx* ctx) { return (size_t)kA8MaxBlocks * ctx->num_sms * 2 * sizeof(int4); }
 
 template <typename T, int HD, int NT>
 static cudaError_t attn8_launch(mtp_ctx* ctx, cudaStream_t s, const Attn8Args& a) {
   using S = Attn8Shape<HD, NT, sizeof(T) == 4 ? 2 : 1>;
+  static_assert(S::kBlocks <= kA8MaxBlocks, "workspace");
   cudaError_t e = ensure_smem((const void*)kv8_attn_kernel<T, HD, NT>, S::kBytes);
   if (e != cudaSuccess) return e;
-  kv8_attn_kernel<T, HD, NT><<<a8_grid(ctx), kA8Threads, S::kBytes, s>>>(a);
-  return cudaGetLastError();
+  const int grid = S::kBlocks * ctx->num_sms;
+  e = launch_pdl(kv8_attn_kernel<T, HD, NT>, dim3(grid), dim3(kA8Threads), S::kBytes, s, a);
+  if (e != cudaSuccess) return e;
+  // few segments: many pieces each, so columns in parallel; many segments:
+  // two or three pieces each, so one block for all columns
+  const long long tiles = ((long long)a.max_rows << a.g_shift) / S::kCols + 1;
+  const int gy = (long long)a.B * a.n_kv * tiles * 2 >= grid ? 1 : S::kCols / 2;
+  return launch_pdl(kv8_attn_join_kernel<T, HD>, dim3(grid, gy), dim3(kJoinThreads), 0, s, a);
 }
 
 template <typename T, int HD>
@@ -677,7 +728,7 @@ extern "C" {
 
 size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx) {
   if (!ctx) return 0;
-  return a8_counter_bytes(ctx) + (size_t)2 * a8_grid(ctx) * kA8MaxCols * (ctx->cfg.head_dim + 4) * 4;
+  return a8_meta_bytes(ctx) + (size_t)2 * kA8MaxBlocks * ctx->num_sms * kA8MaxCols * (ctx->cfg.head_dim + 4) * 4;
 }
 
 mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
@@ -701,8 +752,8 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
   a.mask = mask;
   a.kv = *kv;
   a.err = ctx->err;
-  a.cnt = (int*)ws;
-  a.part = (float*)((char*)ws + a8_counter_bytes(ctx));
+  a.meta = (int4*)ws;
+  a.part = (float*)((char*)ws + a8_meta_bytes(ctx));
   a.q_stride = q_stride;
   a.B = B;
   a.T = T;
@@ -720,7 +771,7 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
   const bool bf = c.dtype == MTP_DTYPE_BF16;
   const cudaError_t e = c.head_dim == 128 ? (bf ? attn8_pick<uint16_t, 128>(ctx, s, a, nt) : attn8_pick<float, 128>(ctx, s, a, nt))
                                           : (bf ? attn8_pick<uint16_t, 64>(ctx, s, a, nt) : attn8_pick<float, 64>(ctx, s, a, nt));
-  ctx->launches++;
+  ctx->launches += 2;
   return launch_status(e);
 }
 
