@@ -57,6 +57,7 @@ struct Attn8Args {
   long long q_stride;
   int B, T, max_rows, mask_words, n_kv, g_shift;
   float qscale;    // scale * log2(e)
+  int q_vec;       // query rows allow four elements per load
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -124,6 +125,27 @@ template <int HD>
 __device__ __forceinline__ uint32_t v_at(int r, int c) {
   if constexpr (HD == 128) return (uint32_t)(r * 128 + ((c ^ (r & 6)) << 4));
   return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4));
+}
+
+// Four consecutive elements, in one load where the alignment allows it.
+template <typename T> __device__ __forceinline__ void load_q4(const T* p, int vec, float (&x)[4]);
+template <> __device__ __forceinline__ void load_q4<float>(const float* p, int vec, float (&x)[4]) {
+  if (vec) {
+    const float4 y = *reinterpret_cast<const float4*>(p);
+    x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = p[e];
+  }
+}
+template <> __device__ __forceinline__ void load_q4<uint16_t>(const uint16_t* p, int vec, float (&x)[4]) {
+  if (vec) {
+    const uint2 y = *reinterpret_cast<const uint2*>(p);
+    x[0] = bf16_lo(y.x); x[1] = bf16_hi(y.x); x[2] = bf16_lo(y.y); x[3] = bf16_hi(y.y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = Elem<uint16_t>::loads(p + e);
+  }
 }
 
 template <int HD, int NT, int SPLIT>
@@ -250,10 +272,10 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
     if (tid == 0 && blockIdx.x == 0) set_error(a.err, MTP_ERR_CAPACITY);
     return;
   }
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < kA8MinShare) share = kA8MinShare;
-  long long u = (long long)blockIdx.x * share;
-  const long long u_end = min(total, u + share);
+  // units fit 31 bits, so the divisions below are 32-bit ones
+  const uint32_t units = (uint32_t)total, share = max((units + gridDim.x - 1) / gridDim.x, (uint32_t)kA8MinShare);
+  uint32_t u = min((unsigned long long)blockIdx.x * share, (unsigned long long)units);
+  const uint32_t u_end = min(units - u, share) + u;
 
   const uint32_t ring = smem_addr(smem) + warp * (S::kStages * S::kStage);
   float* merge = reinterpret_cast<float*>(smem);
@@ -266,7 +288,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       int lo = 0, hi = a.B - 1;  // the request with pre[b] <= u < pre[b + 1]
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+        if ((uint32_t)pre[mid] <= u) lo = mid; else hi = mid - 1;
       }
       b = lo;
     }
@@ -274,12 +296,11 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
     request(b, o0, n, L);
     const int base = L - n;
     const int steps = (L + STEP - 1) / STEP, tiles = (n * G + S::kCols - 1) / S::kCols;
-    const long long in = u - pre[b];
-    const int seg = (int)(in / (steps + kA8Lead));
-    const int g = seg / tiles, tile = seg - g * tiles;
-    const long long seg_u0 = pre[b] + (long long)seg * (steps + kA8Lead) + kA8Lead;   // the segment's first step
-    const int s_lo = (int)max(0ll, u - seg_u0), s_hi = (int)min((long long)steps, u_end - seg_u0);
-    if (s_hi <= s_lo) break;   // the share ends before the segment's first step
+    const uint32_t seg = (u - (uint32_t)pre[b]) / (uint32_t)(steps + kA8Lead);
+    const int g = (int)(seg / (uint32_t)tiles), tile = (int)seg - g * tiles;
+    const uint32_t seg_u0 = (uint32_t)pre[b] + seg * (uint32_t)(steps + kA8Lead) + kA8Lead;   // the segment's first step
+    if (u_end <= seg_u0) break;   // the share ends before it
+    const int s_lo = u > seg_u0 ? (int)(u - seg_u0) : 0, s_hi = min(steps, (int)(u_end - seg_u0));
     const int col0 = tile * S::kCols, ncols = min(S::kCols, n * G - col0);
 
     // ---- this warp's steps: s_lo + warp, + 4, ...
@@ -332,16 +353,22 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
 
     // ---- queries: per column a power of two that brings them into fp16's
     // range, then fragments in the order the lanes read them
-    for (int c = warp; c < S::kCols; c += kA8Warps) {
-      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const bool lane_on = lane < HD / 4;
-      if (c < ncols && lane_on) {
-        const int cc = col0 + c;
-        const T* qp = (const T*)a.q + (long long)(o0 + (cc >> a.g_shift)) * a.q_stride +
-                      ((long long)g * G + (cc & (G - 1))) * HD + lane * 4;
+    const bool lane_on = lane < HD / 4;
+    float xq[2 * NT][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = Elem<T>::loads(qp + e);
-      }
+    for (int k = 0; k < 2 * NT; ++k) {
+      const int c = warp + kA8Warps * k, cc = col0 + c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) xq[k][e] = 0.0f;
+      if (c < ncols && lane_on)
+        load_q4<T>((const T*)a.q + (long long)(o0 + (cc >> a.g_shift)) * a.q_stride +
+                       ((long long)g * G + (cc & (G - 1))) * HD + lane * 4,
+                   a.q_vec, xq[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) {
+      const int c = warp + kA8Warps * k;
+      const float (&x)[4] = xq[k];
       float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
       m = warp_max(m);
       int sh = 0;  // largest element to [2^14, 2^15)
@@ -602,9 +629,9 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
               make_float4(o[nt][mt][e], o[nt][mt][2 + e], o[nt][mt + 1][e], o[nt][mt + 1][2 + e]);
       }
     __syncthreads();
-    const long long c_first = seg_u0 / share, c_last = (seg_u0 + steps - 1) / share;
+    const uint32_t c_first = seg_u0 / share, c_last = (seg_u0 + (uint32_t)steps - 1) / share;
     const bool whole = c_first == c_last;
-    const int slot = (long long)blockIdx.x == c_first ? 1 : 0;
+    const int slot = blockIdx.x == c_first ? 1 : 0;
     for (int i = tid; i < ncols * (HD / 4); i += kA8Threads) {
       const int c = i / (HD / 4), d4 = i - c * (HD / 4);
       float M = -INFINITY;
@@ -635,37 +662,41 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       a.meta[2 * blockIdx.x + 1] = make_int4(o0, col0, ncols, g);
       a.meta[2 * blockIdx.x] = make_int4((int)(c_last - c_first + 1), 0, 0, 0);
     }
-    u = seg_u0 + s_hi;
+    u = seg_u0 + (uint32_t)s_hi;
   }
 }
 
 // Joins the pieces of the segment that begins in thread block blockIdx.x of
-// the first kernel: block (x, y) takes the column pairs y, y + gridDim.y, ...;
-// kWays threads share an element's pieces, four loads in flight each.
+// the first kernel.  A thread owns four elements of a column, or shares them
+// with `ways - 1` others where there are many pieces; block (x, y) takes the
+// y-th group of columns and every gridDim.y-th after it.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 8;   // pieces in flight per thread
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8Args a) {
-  constexpr int kItems = 2 * (HD / 4), kWays = kJoinThreads / kItems;
-  __shared__ float4 xs[kWays][kItems];
-  __shared__ float2 ms[kWays][kItems];
+  __shared__ float4 xs[kJoinThreads];
+  __shared__ float2 ms[kJoinThreads];
   pdl_wait();
+  pdl_trigger();
   const int c_first = blockIdx.x, count = a.meta[2 * c_first].x;
   if (count == 0) return;
   const int4 seg = a.meta[2 * c_first + 1];
-  const int item = threadIdx.x % kItems, way = threadIdx.x / kItems;
+  const int ways = count <= kJoinAhead ? 1 : 4;
+  const int items = kJoinThreads / ways, cols = items / (HD / 4);
+  const int item = threadIdx.x % items, way = threadIdx.x / items;
   const int d4 = item % (HD / 4);
-  for (int c0 = 2 * blockIdx.y; c0 < seg.z; c0 += 2 * gridDim.y) {
+  for (int c0 = cols * blockIdx.y; c0 < seg.z; c0 += cols * gridDim.y) {
     const int c = c0 + item / (HD / 4);
     float M = -INFINITY, Ls = 0.0f;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < seg.z) {
-      for (int k0 = way; k0 < count; k0 += 4 * kWays) {
-        float2 ml[4];
-        float4 y[4];
+      for (int k0 = way; k0 < count; k0 += kJoinAhead * ways) {
+        float2 ml[kJoinAhead];
+        float4 y[kJoinAhead];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int kk = k0 + k * kWays;
+        for (int k = 0; k < kJoinAhead; ++k) {
+          const int kk = k0 + k * ways;
           ml[k] = make_float2(-INFINITY, 0.0f);
           y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (kk < count) {
@@ -675,18 +706,18 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8
           }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) attn8_take(M, Ls, x, ml[k].x, ml[k].y, y[k]);
+        for (int k = 0; k < kJoinAhead; ++k) attn8_take(M, Ls, x, ml[k].x, ml[k].y, y[k]);
       }
     }
-    __syncthreads();
-    xs[way][item] = x;
-    ms[way][item] = make_float2(M, Ls);
-    __syncthreads();
-    if (way == 0 && c < seg.z) {
-#pragma unroll
-      for (int w = 1; w < kWays; ++w) attn8_take(M, Ls, x, ms[w][item].x, ms[w][item].y, xs[w][item]);
-      attn8_finish<T, HD>(a, seg.x, seg.y + c, seg.w, d4, x, M, Ls);
+    if (ways > 1) {
+      __syncthreads();
+      xs[threadIdx.x] = x;
+      ms[threadIdx.x] = make_float2(M, Ls);
+      __syncthreads();
+      for (int w = 1; way == 0 && w < ways; ++w)
+        attn8_take(M, Ls, x, ms[w * items + item].x, ms[w * items + item].y, xs[w * items + item]);
     }
+    if (way == 0 && c < seg.z) attn8_finish<T, HD>(a, seg.x, seg.y + c, seg.w, d4, x, M, Ls);
   }
 }
 
@@ -703,10 +734,12 @@ static cudaError_t attn8_launch(mtp_ctx* ctx, cudaStream_t s, const Attn8Args& a
   const int grid = S::kBlocks * ctx->num_sms;
   e = launch_pdl(kv8_attn_kernel<T, HD, NT>, dim3(grid), dim3(kA8Threads), S::kBytes, s, a);
   if (e != cudaSuccess) return e;
-  // few segments: many pieces each, so columns in parallel; many segments:
-  // two or three pieces each, so one block for all columns
+  // few segments have many pieces each, and the join takes 64 / (HD / 4)
+  // columns at a time; many segments have a few, and it takes 256 / (HD / 4)
+  const int cols = min(S::kCols, a.max_rows << a.g_shift);
   const long long tiles = ((long long)a.max_rows << a.g_shift) / S::kCols + 1;
-  const int gy = (long long)a.B * a.n_kv * tiles * 2 >= grid ? 1 : S::kCols / 2;
+  const int per = (long long)a.B * a.n_kv * tiles * kJoinAhead < grid ? 64 / (HD / 4) : 256 / (HD / 4);
+  const int gy = (cols + per - 1) / per;
   return launch_pdl(kv8_attn_join_kernel<T, HD>, dim3(grid, gy), dim3(kJoinThreads), 0, s, a);
 }
 
@@ -764,6 +797,8 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
   for (a.g_shift = 0; (1 << a.g_shift) < G; ++a.g_shift) {
   }
   a.qscale = scale * 1.4426950408889634f;
+  const size_t q4 = 4 * (c.dtype == MTP_DTYPE_BF16 ? 2 : 4);
+  a.q_vec = (uintptr_t)q % q4 == 0 && q_stride % 4 == 0;
   // columns per tile: the fewest tiles of at most 32 columns, evenly filled
   const int cols = max_rows * G, tiles = (cols + kA8MaxCols - 1) / kA8MaxCols;
   const int nt = (cols + 8 * tiles - 1) / (8 * tiles);
