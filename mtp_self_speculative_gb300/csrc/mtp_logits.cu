@@ -43,9 +43,63 @@ __device__ __forceinline__ void gather_biases(const int32_t* tok, const float* v
   }
 }
 
-template <typename T>
+// A thread's eight entries of a row: consecutive ones in 16-byte vectors
+// (VEC: rows and outputs start on 16 bytes), else every 128th, which keeps a
+// warp's accesses together whatever the row's alignment.
+template <typename T, bool VEC>
+struct LogitRow {
+  float z[kLogitPer];
+  __device__ static __forceinline__ int at(int v0, int tid, int e) {
+    return VEC ? v0 + tid * kLogitPer + e : v0 + e * kLogitThreads + tid;
+  }
+  __device__ __forceinline__ void load(const T* row, int v0, int tid, int V) {
+    if constexpr (VEC) {
+      if (at(v0, tid, 0) >= V) return;  // V is a multiple of 8 here
+      const uint4* p = reinterpret_cast<const uint4*>(row + at(v0, tid, 0));
+      if constexpr (sizeof(T) == 2) {
+        const uint4 x = *p;
+        z[0] = bf16_lo(x.x); z[1] = bf16_hi(x.x); z[2] = bf16_lo(x.y); z[3] = bf16_hi(x.y);
+        z[4] = bf16_lo(x.z); z[5] = bf16_hi(x.z); z[6] = bf16_lo(x.w); z[7] = bf16_hi(x.w);
+      } else {
+        const uint4 x = p[0], y = p[1];
+        z[0] = __uint_as_float(x.x); z[1] = __uint_as_float(x.y); z[2] = __uint_as_float(x.z);
+        z[3] = __uint_as_float(x.w); z[4] = __uint_as_float(y.x); z[5] = __uint_as_float(y.y);
+        z[6] = __uint_as_float(y.z); z[7] = __uint_as_float(y.w);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLogitPer; ++e)
+        if (at(v0, tid, e) < V) z[e] = Elem<T>::loads(row + at(v0, tid, e));
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int v0, int tid, int V) const {
+    if constexpr (VEC) {
+      if (at(v0, tid, 0) >= V) return;
+      uint4* p = reinterpret_cast<uint4*>(row + at(v0, tid, 0));
+      if constexpr (sizeof(T) == 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = (uint32_t)f32_to_bf16_rne(z[2 * i]) | ((uint32_t)f32_to_bf16_rne(z[2 * i + 1]) << 16);
+        *p = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        p[0] = make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
+        p[1] = make_uint4(__float_as_uint(z[4]), __float_as_uint(z[5]), __float_as_uint(z[6]), __float_as_uint(z[7]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLogitPer; ++e)
+        if (at(v0, tid, e) < V) Elem<T>::store1(row + at(v0, tid, e), z[e]);
+    }
+  }
+};
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const mtp_logits_args a, int V, int* err) {
-  __shared__ float bias[kLogitRange];
+  using Row = LogitRow<T, VEC>;
+  __shared__ float bias_s[kLogitRange];
+  pdl_wait();
+  pdl_trigger();
   const int b = blockIdx.y, v0 = blockIdx.x * kLogitRange, tid = threadIdx.x;
   const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1];
   float rep = 1.0f, freq = 0.0f, pres = 0.0f;
@@ -63,50 +117,94 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const mtp_logits_
     return;
   }
   if (o0 == o1) return;
-  if (e1 > e0) {
-    for (int i = tid; i < kLogitRange; i += kLogitThreads) bias[i] = 0.0f;
-    __syncthreads();
-    if (tid < 32) gather_biases(a.bias_tokens, a.bias_values, e0, e1, v0, V, bias, err);
-    __syncthreads();
+  const T* x = (const T*)a.logits;
+  T* out = (T*)a.out;
+  Row next;
+  next.load(x + (long long)o0 * V, v0, tid, V);
+  uint32_t cnt[kLogitPer], any = 0;
+#pragma unroll
+  for (int e = 0; e < kLogitPer; ++e) cnt[e] = 0;
+  if (a.counts) {
+    const int32_t* c = a.counts + (long long)b * V;
+    if (VEC && !((uintptr_t)a.counts & 15)) {
+      if (Row::at(v0, tid, 0) < V) {
+        const uint4* p = reinterpret_cast<const uint4*>(c + Row::at(v0, tid, 0));
+        const uint4 y = __ldg(p), w = __ldg(p + 1);
+        cnt[0] = y.x; cnt[1] = y.y; cnt[2] = y.z; cnt[3] = y.w;
+        cnt[4] = w.x; cnt[5] = w.y; cnt[6] = w.z; cnt[7] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLogitPer; ++e)
+        if (Row::at(v0, tid, e) < V) cnt[e] = (uint32_t)__ldg(c + Row::at(v0, tid, e));
+    }
   }
-  const int base = v0 + tid * kLogitPer;
-  if (base >= V) return;
-  const int n = min(kLogitPer, V - base);
+  float bias[kLogitPer];
+#pragma unroll
+  for (int e = 0; e < kLogitPer; ++e) bias[e] = 0.0f;
+  if (e1 > e0) {
+    for (int i = tid; i < kLogitRange; i += kLogitThreads) bias_s[i] = 0.0f;
+    __syncthreads();
+    if (tid < 32) gather_biases(a.bias_tokens, a.bias_values, e0, e1, v0, V, bias_s, err);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kLogitPer; ++e) bias[e] = bias_s[Row::at(0, tid, e)];
+  }
+#pragma unroll
+  for (int e = 0; e < kLogitPer; ++e) any |= cnt[e];
   const float inv = 1.0f / rep;
   const int words = (V + 31) / 32;
-  uint32_t cnt[kLogitPer];
-#pragma unroll
-  for (int e = 0; e < kLogitPer; ++e)
-    cnt[e] = a.counts && e < n ? (uint32_t)a.counts[(long long)b * V + base + e] : 0u;
   for (int j = 0; j < o1 - o0; ++j) {
     const long long row = o0 + j;
+    Row z = next;
+    if (j + 1 < o1 - o0) next.load(x + (row + 1) * V, v0, tid, V);
     if (j > 0 && a.drafts) {
-      const int d = a.drafts[(long long)b * a.drafts_stride + j - 1] - base;
+      const int d = a.drafts[(long long)b * a.drafts_stride + j - 1];
+      if (d >= v0 && d < v0 + kLogitRange) {
 #pragma unroll
-      for (int e = 0; e < kLogitPer; ++e) cnt[e] += e == d ? 1u : 0u;
+        for (int e = 0; e < kLogitPer; ++e)
+          if (Row::at(v0, tid, e) == d) {
+            cnt[e] += 1u;
+            any |= 1u;
+          }
+      }
     }
-    uint32_t allow = 0xFFu;
+    if (any) {
+#pragma unroll
+      for (int e = 0; e < kLogitPer; ++e) {
+        const uint32_t c = cnt[e] & 0x7FFFFFFFu;
+        const float met = z.z[e] * (z.z[e] > 0.0f ? inv : rep) - freq * (float)c;
+        if (cnt[e]) z.z[e] = c ? met - pres : met;
+      }
+    }
+    if (e1 > e0) {
+#pragma unroll
+      for (int e = 0; e < kLogitPer; ++e) z.z[e] += bias[e];
+    }
     if (a.mask) {
       const int mi = a.mask_index[row];
       if (mi < -1 || mi >= a.num_masks) {
         set_error(err, MTP_ERR_DEVICE_ARGS);
         continue;
       }
-      if (mi >= 0) allow = (uint32_t)a.mask[(long long)mi * words + (base >> 5)] >> (base & 31);
-    }
+      if (mi >= 0) {
+        const int32_t* m = a.mask + (long long)mi * words;
+        if constexpr (VEC) {
+          const int v = Row::at(v0, tid, 0);
+          const uint32_t ok = v < V ? (uint32_t)__ldg(m + (v >> 5)) >> (v & 31) : 0u;
 #pragma unroll
-    for (int e = 0; e < kLogitPer; ++e) {
-      if (e >= n) break;
-      float z = Elem<T>::loads((const T*)a.logits + row * V + base + e);
-      const uint32_t c = cnt[e] & 0x7FFFFFFFu;
-      if (cnt[e]) {
-        z = z > 0.0f ? z * inv : z * rep;
-        z = z - freq * (float)c - (c ? pres : 0.0f);
+          for (int e = 0; e < kLogitPer; ++e)
+            if (!(ok >> e & 1u)) z.z[e] = -INFINITY;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kLogitPer; ++e) {
+            const int v = Row::at(v0, tid, e);
+            if (v < V && !((uint32_t)__ldg(m + (v >> 5)) >> (v & 31) & 1u)) z.z[e] = -INFINITY;
+          }
+        }
       }
-      if (e1 > e0) z += bias[tid * kLogitPer + e];
-      if (!(allow >> e & 1u)) z = -INFINITY;
-      Elem<T>::store1((T*)a.out + row * V + base + e, z);
     }
+    if (MTP_IN_BOUNDS(err, row, a.num_rows)) z.store(out + row * V, v0, tid, V);
   }
 }
 
@@ -163,12 +261,17 @@ mtp_status mtp_logits_process(mtp_ctx* ctx, void* stream, const mtp_logits_args*
   if (!dev.ok) return MTP_ERR_CUDA;
   const int V = ctx->cfg.vocab;
   const dim3 grid((V + kLogitRange - 1) / kLogitRange, a.B);
+  const bool vec = V % 8 == 0 && !(((uintptr_t)a.logits | (uintptr_t)a.out) & 15);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
   if (ctx->cfg.dtype == MTP_DTYPE_BF16)
-    logits_kernel<uint16_t><<<grid, kLogitThreads, 0, (cudaStream_t)stream>>>(a, V, ctx->err);
+    e = vec ? launch_pdl(logits_kernel<uint16_t, true>, grid, dim3(kLogitThreads), 0, s, a, V, ctx->err)
+            : launch_pdl(logits_kernel<uint16_t, false>, grid, dim3(kLogitThreads), 0, s, a, V, ctx->err);
   else
-    logits_kernel<float><<<grid, kLogitThreads, 0, (cudaStream_t)stream>>>(a, V, ctx->err);
+    e = vec ? launch_pdl(logits_kernel<float, true>, grid, dim3(kLogitThreads), 0, s, a, V, ctx->err)
+            : launch_pdl(logits_kernel<float, false>, grid, dim3(kLogitThreads), 0, s, a, V, ctx->err);
   ctx->launches++;
-  return launch_status(cudaGetLastError());
+  return launch_status(e);
 }
 
 }  // extern "C"

@@ -6,9 +6,8 @@
 //
 // The work is a copy with a few multiplications per element, so memory bounds
 // it: each element is read and written once, 16 bytes at a time where rows
-// and pairs allow.  A thread owns one unit of a token's head -- the two
-// vectors (half layout) or the one vector (interleaved) that hold its pairs --
-// computes that unit's cosines and sines once, and walks over the heads.
+// and pairs allow.  A thread owns one unit of a token's head, computes that
+// unit's cosines and sines once, and walks over the heads.
 #include <math.h>
 
 #include "mtp_kv8.cuh"
@@ -21,7 +20,7 @@ struct RopeArgs {
   const int32_t* positions;
   long long x_stride, out_stride;
   int T, heads, hd;
-  int rot_units, units;   // rotating units of a head, and those plus the copied ones
+  int rot_units, units;   // rotating units of a head, and those with the copied ones
   int heads_per_block;
 };
 
@@ -31,8 +30,80 @@ template <> __device__ __forceinline__ float rope_get<uint16_t>(const uint16_t* 
   return __uint_as_float((uint32_t)*p << 16);
 }
 
+// A thread's unit of 2 N elements of a head: N = 8 (bf16) or 4 (float32)
+// elements at two places (half layout) or the 2 N next to one another, in
+// 16-byte vectors, when the rows, the rotated part and the halves start on
+// 16 bytes.
 template <typename T>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a, const __grid_constant__ mtp_rope_table tab) {
+__device__ __forceinline__ void rope_load(const T* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  if constexpr (sizeof(T) == 2) {
+    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+  } else {
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void rope_store(T* p, const float* x) {
+  uint4 u;
+  if constexpr (sizeof(T) == 2) {
+    u.x = (uint32_t)f32_to_bf16_rne(x[0]) | ((uint32_t)f32_to_bf16_rne(x[1]) << 16);
+    u.y = (uint32_t)f32_to_bf16_rne(x[2]) | ((uint32_t)f32_to_bf16_rne(x[3]) << 16);
+    u.z = (uint32_t)f32_to_bf16_rne(x[4]) | ((uint32_t)f32_to_bf16_rne(x[5]) << 16);
+    u.w = (uint32_t)f32_to_bf16_rne(x[6]) | ((uint32_t)f32_to_bf16_rne(x[7]) << 16);
+  } else {
+    u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+  *reinterpret_cast<uint4*>(p) = u;
+}
+
+template <typename T, int LAYOUT>
+__global__ void __launch_bounds__(128) rope_vec_kernel(const RopeArgs a, const __grid_constant__ mtp_rope_table tab) {
+  constexpr int N = 16 / sizeof(T);
+  pdl_wait();
+  pdl_trigger();
+  const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (item >= (long long)a.T * a.units) return;
+  const int t = (int)(item / a.units), u = (int)(item - (long long)t * a.units);
+  const int h0 = blockIdx.y * a.heads_per_block, h1 = min(a.heads, h0 + a.heads_per_block);
+  const T* x = (const T*)a.x + (long long)t * a.x_stride;
+  T* o = (T*)a.out + (long long)t * a.out_stride;
+  if (u >= a.rot_units) {  // N elements past the rotated part
+    const int e = tab.rotary_dim + (u - a.rot_units) * N;
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h)
+      *reinterpret_cast<uint4*>(o + h * a.hd + e) = *reinterpret_cast<const uint4*>(x + h * a.hd + e);
+    return;
+  }
+  const int pos = a.positions[t];
+  const int ea = LAYOUT == MTP_ROPE_HALF ? u * N : u * 2 * N;
+  const int eb = LAYOUT == MTP_ROPE_HALF ? ea + tab.rotary_dim / 2 : ea + N;
+  float2 cs[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) cs[i] = rope_cos_sin(pos, tab.turns[u * N + i], tab.magnitude);
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+    float p[2 * N], r[2 * N];
+    rope_load(x + h * a.hd + ea, p);
+    rope_load(x + h * a.hd + eb, p + N);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int ia = LAYOUT == MTP_ROPE_HALF ? i : 2 * i, ib = LAYOUT == MTP_ROPE_HALF ? i + N : 2 * i + 1;
+      r[ia] = p[ia] * cs[i].x - p[ib] * cs[i].y;
+      r[ib] = p[ib] * cs[i].x + p[ia] * cs[i].y;
+    }
+    rope_store(o + h * a.hd + ea, r);
+    rope_store(o + h * a.hd + eb, r + N);
+  }
+}
+
+// Any alignment and rotated part: a thread owns one pair, or one element past
+// the rotated part, of a token's heads.
+template <typename T>
+__global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a, const __grid_constant__ mtp_rope_table tab) {
+  pdl_wait();
+  pdl_trigger();
   const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= (long long)a.T * a.units) return;
   const int t = (int)(item / a.units), u = (int)(item - (long long)t * a.units);
@@ -52,6 +123,32 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a, const __gri
     Elem<T>::store1(o + h * a.hd + ia, p * cs.x - q * cs.y);
     Elem<T>::store1(o + h * a.hd + ib, q * cs.x + p * cs.y);
   }
+}
+
+template <typename T>
+static cudaError_t rope_launch(mtp_ctx* ctx, cudaStream_t s, RopeArgs a, const mtp_rope_table& tab) {
+  constexpr int N = 16 / sizeof(T);
+  const bool half = tab.layout == MTP_ROPE_HALF;
+  // the half layout wants its second half on 16 bytes too
+  const bool vec = !(((uintptr_t)a.x | (uintptr_t)a.out) & 15) && a.x_stride % N == 0 && a.out_stride % N == 0 &&
+                   tab.rotary_dim % (2 * N) == 0;
+  const int per = vec ? N : 1;
+  a.rot_units = tab.rotary_dim / 2 / per;
+  a.units = a.rot_units + (a.x == a.out ? 0 : (a.hd - tab.rotary_dim) / per);
+  const long long items = (long long)a.T * a.units, gx = (items + 127) / 128;
+  if (gx > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  // a thread computes its unit's cosines once for all its heads; few tokens
+  // split the heads over more threads until there are about 16 blocks per SM
+  const long long want = 16ll * ctx->num_sms;
+  int gy = gx >= want ? 1 : (int)((want + gx - 1) / gx);
+  gy = gy < a.heads ? gy : a.heads;
+  gy = gy < 65535 ? gy : 65535;
+  a.heads_per_block = (a.heads + gy - 1) / gy;
+  gy = (a.heads + a.heads_per_block - 1) / a.heads_per_block;
+  const dim3 grid((unsigned)gx, gy);
+  if (!vec) return launch_pdl(rope_kernel<T>, grid, dim3(128), 0, s, a, tab);
+  return half ? launch_pdl(rope_vec_kernel<T, MTP_ROPE_HALF>, grid, dim3(128), 0, s, a, tab)
+              : launch_pdl(rope_vec_kernel<T, MTP_ROPE_INTERLEAVED>, grid, dim3(128), 0, s, a, tab);
 }
 
 }  // namespace mtp
@@ -137,18 +234,11 @@ mtp_status mtp_rope(mtp_ctx* ctx, void* stream, int T, int heads, const void* x,
   a.T = T;
   a.heads = heads;
   a.hd = hd;
-  a.rot_units = rope->rotary_dim / 2;
-  a.units = a.rot_units + (x == out ? 0 : hd - rope->rotary_dim);
-  a.heads_per_block = heads;
-  const long long items = (long long)T * a.units;
-  const long long gx = (items + 255) / 256;
-  if (gx > 0x7FFFFFFFll) return MTP_ERR_INVALID;
-  if (ctx->cfg.dtype == MTP_DTYPE_BF16)
-    rope_kernel<uint16_t><<<dim3((unsigned)gx, 1), 256, 0, (cudaStream_t)stream>>>(a, *rope);
-  else
-    rope_kernel<float><<<dim3((unsigned)gx, 1), 256, 0, (cudaStream_t)stream>>>(a, *rope);
+  const cudaError_t e = ctx->cfg.dtype == MTP_DTYPE_BF16 ? rope_launch<uint16_t>(ctx, (cudaStream_t)stream, a, *rope)
+                                                         : rope_launch<float>(ctx, (cudaStream_t)stream, a, *rope);
+  if (e == cudaErrorInvalidValue) return MTP_ERR_INVALID;
   ctx->launches++;
-  return launch_status(cudaGetLastError());
+  return launch_status(e);
 }
 
 }  // extern "C"
