@@ -18,90 +18,82 @@ constexpr int kLogitThreads = 128;
 constexpr int kLogitPer = 8;                                // consecutive entries per thread
 constexpr int kLogitRange = kLogitThreads * kLogitPer;
 
-// Sum the biases that fall into [v0, v0 + kLogitRange) into acc.  One warp
-// walks the list 32 entries at a time; entries of one step that name the same
-// token are added by its first lane in list order, so the sum does not depend
-// on timing.
-__device__ __forceinline__ void gather_biases(const int32_t* tok, const float* val, int e0, int e1, int v0, int V,
-                                              float* acc, int* err) {
-  const int lane = threadIdx.x & 31;
-  for (int e = e0; e < e1; e += 32) {
-    const bool in = e + lane < e1;
-    const int t = in ? tok[e + lane] : -1;
-    const float x = in ? val[e + lane] : 0.0f;
-    if (in && (t < 0 || t >= V) && v0 == 0) set_error(err, MTP_ERR_DEVICE_ARGS);
-    const bool mine = in && t >= v0 && t < V && t < v0 + kLogitRange;
-    if (!__any_sync(0xffffffffu, mine)) continue;
-    const unsigned same = __match_any_sync(0xffffffffu, mine ? t : -1 - lane);
-    float sum = 0.0f;
-    for (int l = 0; l < 32; ++l) {
-      const float y = __shfl_sync(0xffffffffu, x, l);
-      if (same >> l & 1u) sum = (l == __ffs(same) - 1) ? (mine ? acc[t - v0] + y : 0.0f) : sum + y;
-    }
-    if (mine && lane == __ffs(same) - 1) acc[t - v0] = sum;
-    __syncwarp();
-  }
-}
-
-// A thread's eight entries of a row: consecutive ones in 16-byte vectors
-// (VEC: rows and outputs start on 16 bytes), else every 128th, which keeps a
-// warp's accesses together whatever the row's alignment.
+// A thread's eight entries of a row, as loaded: consecutive ones in 16-byte
+// vectors (VEC: rows and outputs start on 16 bytes and V is a multiple of 8),
+// else every 32nd of its warp's 256, which keeps a warp's accesses together
+// whatever the row's alignment.
 template <typename T, bool VEC>
 struct LogitRow {
-  float z[kLogitPer];
-  __device__ static __forceinline__ int at(int v0, int tid, int e) {
-    return VEC ? v0 + tid * kLogitPer + e : v0 + e * kLogitThreads + tid;
-  }
-  __device__ __forceinline__ void load(const T* row, int v0, int tid, int V) {
+  static constexpr int kWords = VEC && sizeof(T) == 2 ? 4 : 8;
+  uint32_t w[kWords];
+  // entry e of a lane, within the warp's 256
+  __device__ static __forceinline__ int at(int lane, int e) { return VEC ? lane * kLogitPer + e : e * 32 + lane; }
+  __device__ __forceinline__ void load(const T* row, int lane, int left) {
     if constexpr (VEC) {
-      if (at(v0, tid, 0) >= V) return;  // V is a multiple of 8 here
-      const uint4* p = reinterpret_cast<const uint4*>(row + at(v0, tid, 0));
-      if constexpr (sizeof(T) == 2) {
-        const uint4 x = *p;
-        z[0] = bf16_lo(x.x); z[1] = bf16_hi(x.x); z[2] = bf16_lo(x.y); z[3] = bf16_hi(x.y);
-        z[4] = bf16_lo(x.z); z[5] = bf16_hi(x.z); z[6] = bf16_lo(x.w); z[7] = bf16_hi(x.w);
-      } else {
-        const uint4 x = p[0], y = p[1];
-        z[0] = __uint_as_float(x.x); z[1] = __uint_as_float(x.y); z[2] = __uint_as_float(x.z);
-        z[3] = __uint_as_float(x.w); z[4] = __uint_as_float(y.x); z[5] = __uint_as_float(y.y);
-        z[6] = __uint_as_float(y.z); z[7] = __uint_as_float(y.w);
+      if (at(lane, 0) >= left) return;
+      const uint4* p = reinterpret_cast<const uint4*>(row + at(lane, 0));
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 x = p[i / 4];
+        w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
       }
     } else {
 #pragma unroll
       for (int e = 0; e < kLogitPer; ++e)
-        if (at(v0, tid, e) < V) z[e] = Elem<T>::loads(row + at(v0, tid, e));
+        if (at(lane, e) < left) w[e] = __float_as_uint(Elem<T>::loads(row + at(lane, e)));
     }
   }
-  __device__ __forceinline__ void store(T* row, int v0, int tid, int V) const {
+  __device__ __forceinline__ float value(int e) const {
+    return kWords == 8 ? __uint_as_float(w[e]) : (e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+  }
+  __device__ static __forceinline__ void store(T* row, const float (&z)[kLogitPer], int lane, int left) {
     if constexpr (VEC) {
-      if (at(v0, tid, 0) >= V) return;
-      uint4* p = reinterpret_cast<uint4*>(row + at(v0, tid, 0));
-      if constexpr (sizeof(T) == 2) {
-        uint32_t w[4];
+      if (at(lane, 0) >= left) return;
+      uint4* p = reinterpret_cast<uint4*>(row + at(lane, 0));
+      uint32_t w[kWords];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = (uint32_t)f32_to_bf16_rne(z[2 * i]) | ((uint32_t)f32_to_bf16_rne(z[2 * i + 1]) << 16);
-        *p = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        p[0] = make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
-        p[1] = make_uint4(__float_as_uint(z[4]), __float_as_uint(z[5]), __float_as_uint(z[6]), __float_as_uint(z[7]));
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (kWords == 4) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(z[2 * i + 1]), "f"(z[2 * i]));
+        else w[i] = __float_as_uint(z[i]);
       }
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) p[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     } else {
 #pragma unroll
       for (int e = 0; e < kLogitPer; ++e)
-        if (at(v0, tid, e) < V) Elem<T>::store1(row + at(v0, tid, e), z[e]);
+        if (at(lane, e) < left) Elem<T>::store1(row + at(lane, e), z[e]);
     }
   }
 };
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kLogitThreads) logits_kernel(const mtp_logits_args a, int V, int* err) {
+__global__ void __launch_bounds__(kLogitThreads, (VEC && sizeof(T) == 2 ? 8 : 6)) logits_kernel(const mtp_logits_args a, int V, int* err) {
   using Row = LogitRow<T, VEC>;
-  __shared__ float bias_s[kLogitRange];
+  constexpr int kWarpRange = 32 * kLogitPer;
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.y, v0 = blockIdx.x * kLogitRange, tid = threadIdx.x;
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int v0 = blockIdx.x * kLogitRange + warp * kWarpRange;     // the warp's first entry
+  const int left = V - v0;                                         // entries from there on
   const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1];
+  uint32_t cnt[kLogitPer];
+#pragma unroll
+  for (int e = 0; e < kLogitPer; ++e) cnt[e] = 0;
+  if (a.counts) {
+    const int32_t* counts = a.counts + (long long)b * V + v0;
+    if (VEC && !((uintptr_t)a.counts & 15)) {
+      if (Row::at(lane, 0) < left) {
+        const uint4* p = reinterpret_cast<const uint4*>(counts + Row::at(lane, 0));
+        const uint4 y = __ldg(p), w = __ldg(p + 1);
+        cnt[0] = y.x; cnt[1] = y.y; cnt[2] = y.z; cnt[3] = y.w;
+        cnt[4] = w.x; cnt[5] = w.y; cnt[6] = w.z; cnt[7] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLogitPer; ++e)
+        if (Row::at(lane, e) < left) cnt[e] = (uint32_t)__ldg(counts + Row::at(lane, e));
+    }
+  }
   float rep = 1.0f, freq = 0.0f, pres = 0.0f;
   if (a.repetition) rep = a.repetition[b];
   if (a.frequency) freq = a.frequency[b];
@@ -111,100 +103,110 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const mtp_logits_
     e0 = a.bias_offsets[b];
     e1 = a.bias_offsets[b + 1];
   }
-  if (o0 < 0 || o1 < o0 || o1 > a.num_rows || (a.drafts && o1 - o0 > a.drafts_stride + 1) || !(rep > 0.0f) ||
+  const int n = o1 - o0;
+  if (o0 < 0 || o1 < o0 || o1 > a.num_rows || (a.drafts && n > a.drafts_stride + 1) || !(rep > 0.0f) ||
       !finite_f(rep) || !finite_f(freq) || !finite_f(pres) || e0 < 0 || e1 < e0 || e1 > a.num_bias) {
-    if (tid == 0) set_error(err, MTP_ERR_DEVICE_ARGS);
+    if (threadIdx.x == 0) set_error(err, MTP_ERR_DEVICE_ARGS);
     return;
   }
-  if (o0 == o1) return;
-  const T* x = (const T*)a.logits;
-  T* out = (T*)a.out;
-  Row next;
-  next.load(x + (long long)o0 * V, v0, tid, V);
-  uint32_t cnt[kLogitPer], any = 0;
-#pragma unroll
-  for (int e = 0; e < kLogitPer; ++e) cnt[e] = 0;
-  if (a.counts) {
-    const int32_t* c = a.counts + (long long)b * V;
-    if (VEC && !((uintptr_t)a.counts & 15)) {
-      if (Row::at(v0, tid, 0) < V) {
-        const uint4* p = reinterpret_cast<const uint4*>(c + Row::at(v0, tid, 0));
-        const uint4 y = __ldg(p), w = __ldg(p + 1);
-        cnt[0] = y.x; cnt[1] = y.y; cnt[2] = y.z; cnt[3] = y.w;
-        cnt[4] = w.x; cnt[5] = w.y; cnt[6] = w.z; cnt[7] = w.w;
-      }
+  if (n == 0 || left <= 0) return;
+  const T* x = (const T*)a.logits + (long long)o0 * V + v0;
+  T* out = (T*)a.out + (long long)o0 * V + v0;
+  const int32_t* drafts = a.drafts ? a.drafts + (long long)b * a.drafts_stride : nullptr;
+  // the first two rows, and the first one's mask, on their way
+  Row cur, next;
+  cur.load(x, lane, left);
+  if (n > 1) next.load(x + V, lane, left);
+  const int words = (V + 31) / 32;
+  const int32_t* mask = a.mask + (v0 >> 5);
+  // the mask bits of the thread's entries in row j; 0x100: a bad index, the row is left as it was
+  auto allowed = [&](int j) -> uint32_t {
+    const int mi = a.mask_index[o0 + j];
+    if (mi == -1) return 0xFFu;
+    if (mi < -1 || mi >= a.num_masks) {
+      set_error(err, MTP_ERR_DEVICE_ARGS);
+      return 0x100u;
+    }
+    const int32_t* m = mask + (long long)mi * words;
+    if constexpr (VEC) {
+      return Row::at(lane, 0) < left ? (uint32_t)__ldg(m + (lane >> 2)) >> (8 * (lane & 3)) & 0xFFu : 0u;
     } else {
+      uint32_t ok = 0;
 #pragma unroll
       for (int e = 0; e < kLogitPer; ++e)
-        if (Row::at(v0, tid, e) < V) cnt[e] = (uint32_t)__ldg(c + Row::at(v0, tid, e));
+        if (Row::at(lane, e) < left) ok |= ((uint32_t)__ldg(m + e) >> lane & 1u) << e;
+      return ok;
+    }
+  };
+  uint32_t ok = a.mask ? allowed(0) : 0xFFu;
+  // z <- z * (z > 0 ? up : down) - sub, sub = f c + p [c > 0] - bias.  Each warp
+  // looks through the biases for its own entries; one that falls among them
+  // is added by the thread that owns it, in the list's order.
+  float up[kLogitPer], down[kLogitPer], sub[kLogitPer];
+  bool any = false;
+#pragma unroll
+  for (int e = 0; e < kLogitPer; ++e) sub[e] = 0.0f;
+  for (int at = e0; at < e1; at += 32) {
+    const int t = at + lane < e1 ? a.bias_tokens[at + lane] : -1;
+    if (v0 == 0 && at + lane < e1 && (t < 0 || t >= V)) set_error(err, MTP_ERR_DEVICE_ARGS);
+    for (unsigned hit = __ballot_sync(0xffffffffu, t >= v0 && t < V && t - v0 < kWarpRange); hit; hit &= hit - 1) {
+      const int l = __ffs(hit) - 1, k = __shfl_sync(0xffffffffu, t, l) - v0;
+      const float y = a.bias_values[at + l];
+#pragma unroll
+      for (int e = 0; e < kLogitPer; ++e)
+        if (Row::at(lane, e) == k) {
+          sub[e] -= y;
+          any = true;
+        }
     }
   }
-  float bias[kLogitPer];
-#pragma unroll
-  for (int e = 0; e < kLogitPer; ++e) bias[e] = 0.0f;
-  if (e1 > e0) {
-    for (int i = tid; i < kLogitRange; i += kLogitThreads) bias_s[i] = 0.0f;
-    __syncthreads();
-    if (tid < 32) gather_biases(a.bias_tokens, a.bias_values, e0, e1, v0, V, bias_s, err);
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kLogitPer; ++e) bias[e] = bias_s[Row::at(0, tid, e)];
-  }
-#pragma unroll
-  for (int e = 0; e < kLogitPer; ++e) any |= cnt[e];
   const float inv = 1.0f / rep;
-  const int words = (V + 31) / 32;
-  for (int j = 0; j < o1 - o0; ++j) {
-    const long long row = o0 + j;
-    Row z = next;
-    if (j + 1 < o1 - o0) next.load(x + (row + 1) * V, v0, tid, V);
-    if (j > 0 && a.drafts) {
-      const int d = a.drafts[(long long)b * a.drafts_stride + j - 1];
-      if (d >= v0 && d < v0 + kLogitRange) {
 #pragma unroll
-        for (int e = 0; e < kLogitPer; ++e)
-          if (Row::at(v0, tid, e) == d) {
-            cnt[e] += 1u;
-            any |= 1u;
-          }
-      }
-    }
+  for (int e = 0; e < kLogitPer; ++e) {
+    const uint32_t c = cnt[e] & 0x7FFFFFFFu;
+    up[e] = cnt[e] ? inv : 1.0f;
+    down[e] = cnt[e] ? rep : 1.0f;
+    sub[e] += fmaf(freq, (float)(int)c, c ? pres : 0.0f);
+    any |= cnt[e] != 0;
+  }
+  int d_next = drafts && n > 1 ? drafts[0] : -1;
+#pragma unroll 2
+  for (int j = 0; j < n; ++j) {
+    float z[kLogitPer];
+#pragma unroll
+    for (int e = 0; e < kLogitPer; ++e) z[e] = cur.value(e);
+    cur = next;
+    if (j + 2 < n) next.load(x + 2 * (long long)V, lane, left);
+    x += V;
+    const uint32_t ok_now = ok;
+    if (a.mask && j + 1 < n) ok = allowed(j + 1);
     if (any) {
 #pragma unroll
-      for (int e = 0; e < kLogitPer; ++e) {
-        const uint32_t c = cnt[e] & 0x7FFFFFFFu;
-        const float met = z.z[e] * (z.z[e] > 0.0f ? inv : rep) - freq * (float)c;
-        if (cnt[e]) z.z[e] = c ? met - pres : met;
-      }
+      for (int e = 0; e < kLogitPer; ++e) z[e] = fmaf(z[e], z[e] > 0.0f ? up[e] : down[e], -sub[e]);
     }
-    if (e1 > e0) {
+    if (ok_now != 0xFFu) {
 #pragma unroll
-      for (int e = 0; e < kLogitPer; ++e) z.z[e] += bias[e];
+      for (int e = 0; e < kLogitPer; ++e)
+        if (!(ok_now & (1u << e))) z[e] = -INFINITY;
     }
-    if (a.mask) {
-      const int mi = a.mask_index[row];
-      if (mi < -1 || mi >= a.num_masks) {
-        set_error(err, MTP_ERR_DEVICE_ARGS);
-        continue;
-      }
-      if (mi >= 0) {
-        const int32_t* m = a.mask + (long long)mi * words;
-        if constexpr (VEC) {
-          const int v = Row::at(v0, tid, 0);
-          const uint32_t ok = v < V ? (uint32_t)__ldg(m + (v >> 5)) >> (v & 31) : 0u;
+    if (ok_now != 0x100u && MTP_IN_BOUNDS(err, o0 + j, a.num_rows)) Row::store(out, z, lane, left);
+    out += V;
+    // the draft between row j and row j + 1 counts from there on
+    const int d = d_next - v0;
+    if (drafts && j + 2 < n) d_next = drafts[j + 1];
+    if (drafts && j + 1 < n && d >= 0 && d < kWarpRange && d < left) {
+      const int32_t* counts = a.counts + (long long)b * V + v0;
+      uint32_t c = (uint32_t)__ldg(counts + d) & 0x7FFFFFFFu;   // the token's count before this draft
+      for (int k = 0; k < j; ++k) c += drafts[k] - v0 == d ? 1u : 0u;
 #pragma unroll
-          for (int e = 0; e < kLogitPer; ++e)
-            if (!(ok >> e & 1u)) z.z[e] = -INFINITY;
-        } else {
-#pragma unroll
-          for (int e = 0; e < kLogitPer; ++e) {
-            const int v = Row::at(v0, tid, e);
-            if (v < V && !((uint32_t)__ldg(m + (v >> 5)) >> (v & 31) & 1u)) z.z[e] = -INFINITY;
-          }
+      for (int e = 0; e < kLogitPer; ++e)
+        if (Row::at(lane, e) == d) {
+          up[e] = inv;
+          down[e] = rep;
+          sub[e] += c ? freq : freq + pres;
+          any = true;
         }
-      }
     }
-    if (MTP_IN_BOUNDS(err, row, a.num_rows)) z.store(out + row * V, v0, tid, V);
   }
 }
 
