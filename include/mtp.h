@@ -547,7 +547,8 @@ mtp_status mtp_kv8_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_
  * head_dim] bf16, whatever the dtype: bf16 holds every entry) receives slot
  * start[b] + i.  The slots must be held (below seq_len[b] + pending[b]; else
  * MTP_ERR_DEVICE_ARGS and that request's rows are left as they were).  Rows
- * outside row_offsets are left as they were. */
+ * outside row_offsets are left as they were.  k_out and v_out: 16-byte
+ * aligned. */
 mtp_status mtp_kv8_read(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* start, int T,
                         const int32_t* row_offsets, void* k_out, void* v_out);
 

@@ -23,16 +23,16 @@ struct Append8Args {
   const int32_t* positions;
   mtp_kv8 kv;
   int* err;
-  int B, T, n_kv, n_q;
-  int rope;
+  int B, T, n_kv, g_shift;
+  int rope;    // rotate k (and q)
+  int vec;     // k and v: rows on 16 bytes, rotary_dim a multiple of 8
+  int q_vec;   // q and q_out: rows on 16 bytes, rotary_dim a multiple of 16
 };
 
 // A unit is one cache block that takes new rows.  Request b's units start at
 // floor(off_b / 16) + 2 b, which leaves it floor(n_b / 16) + 2 at least: as
 // many as n_b rows can touch.
-struct UnitFirst {
-  __device__ int operator()(int o, int b) const { return (o >> 4) + 2 * b; }
-};
+__device__ __forceinline__ int append_unit(int o, int b) { return (o >> 4) + 2 * b; }
 
 template <typename T> __device__ __forceinline__ float get1(const T* p);
 template <> __device__ __forceinline__ float get1<float>(const float* p) { return *p; }
@@ -40,155 +40,287 @@ template <> __device__ __forceinline__ float get1<uint16_t>(const uint16_t* p) {
   return __uint_as_float((uint32_t)*p << 16);
 }
 
-// One rotated element e of a head row (cs: the row's cosines and sines, or
-// null for no rotation).
-template <typename T>
-__device__ __forceinline__ float rotated(const T* row, int e, const float2* cs, int rd, int layout) {
-  const float x = get1<T>(row + e);
-  if (!cs || e >= rd) return x;
-  if (layout == MTP_ROPE_HALF) {
-    const int h = rd >> 1;
-    if (e < h) return x * cs[e].x - get1<T>(row + e + h) * cs[e].y;
-    return x * cs[e - h].x + get1<T>(row + e - h) * cs[e - h].y;
+// N elements (4, or 8 on 16 bytes) as floats, and back.
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, float* x) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p + i);
+      x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
+    }
+  } else if constexpr (N == 4) {
+    const uint2 y = *reinterpret_cast<const uint2*>(p);
+    x[0] = bf16_lo(y.x); x[1] = bf16_hi(y.x); x[2] = bf16_lo(y.y); x[3] = bf16_hi(y.y);
+  } else {
+    const uint4 y = *reinterpret_cast<const uint4*>(p);
+    x[0] = bf16_lo(y.x); x[1] = bf16_hi(y.x); x[2] = bf16_lo(y.y); x[3] = bf16_hi(y.y);
+    x[4] = bf16_lo(y.z); x[5] = bf16_hi(y.z); x[6] = bf16_lo(y.w); x[7] = bf16_hi(y.w);
   }
-  const float2 c = cs[e >> 1];
-  if (!(e & 1)) return x * c.x - get1<T>(row + e + 1) * c.y;
-  return x * c.x + get1<T>(row + e - 1) * c.y;
+}
+template <typename T>
+__device__ __forceinline__ void store_8(T* p, const float* x) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
+__device__ __forceinline__ uint32_t e4m3_pack4(const float* x, float inv) {
+  return e4m3_pack2(e4m3_in(x[0], inv), e4m3_in(x[1], inv)) |
+         (e4m3_pack2(e4m3_in(x[2], inv), e4m3_in(x[3], inv)) << 16);
+}
+
+// Thread block (unit, kv head): the unit's new rows of k and v, and of the
+// head's queries.  16 (HD = 128) or 8 threads share a row, each with 8
+// elements: two fours half the rotated part apart (half layout, aligned) or
+// eight next to one another, so that a thread has both members of its pairs,
+// computes their cosine once, and nothing goes through shared memory but the
+// two maxima.  What bounds a decoding step is the chain of dependent loads:
+// lengths, then rows, positions and block id together, then the old scale.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append8Args a,
                                                                     const __grid_constant__ mtp_rope_table tab) {
   constexpr int W = kAppendThreads / 32;
-  constexpr int RPW = kBlk / W;          // rows of a block per warp
-  constexpr int DPL = HD / 32;           // elements of a row per lane
-  __shared__ float2 cs[kBlk][HD / 2];
+  constexpr int LPR = HD / 8;                          // threads of a row
+  constexpr int PASS = kBlk * LPR / kAppendThreads;    // rows per thread
+  constexpr int STEP = kAppendThreads / LPR;
   __shared__ float red[2][W];
-  __shared__ int sh[3], live_blk[3];
+  __shared__ int sh[5];
+  pdl_wait();
+  pdl_trigger();
   const int u = blockIdx.x, g = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (!find_request(a.row_offsets, a.B, a.T, u, a.err, sh, UnitFirst())) return;
-  const int b = sh[0], o0 = sh[1], n_new = sh[2] - o0;
-  if (tid == 0) {
-    const int L0 = a.kv.seq_len[b], P = a.kv.pending[b];
-    int bi = -1, blk = -1, start = 0;
-    if (L0 < 0 || P < 0 || L0 > INT32_MAX - P) {
-      set_error(a.err, MTP_ERR_DEVICE_ARGS);
-    } else if ((long long)L0 + P + n_new > (long long)a.kv.max_blocks * kBlk) {
-      set_error(a.err, MTP_ERR_CAPACITY);
-    } else {
-      start = L0 + P;
-      const int first = start >> 4, last = (start + n_new - 1) >> 4;
-      bi = first + (u - UnitFirst()(o0, b));
-      if (bi > last) {
-        bi = -1;
-      } else {
-        blk = a.kv.block_table[(long long)b * a.kv.max_blocks + bi];
-        if (blk < 0 || blk >= a.kv.num_blocks) {
-          set_error(a.err, MTP_ERR_CAPACITY);
-          blk = -1;
-        }
-        // the last of the request's thread blocks publishes the new length:
-        // all have read the old one by then
-        if (arrive_last(a.kv.arrive + b, (last - first + 1) * a.n_kv)) a.kv.pending[b] = P + n_new;
-      }
-    }
-    live_blk[0] = bi;
-    live_blk[1] = blk;
-    live_blk[2] = start;
-  }
+  // ---- the unit's request; every thread checks some of the offsets
+  if (tid == 0) sh[0] = -1;
   __syncthreads();
-  const int bi = live_blk[0], blk = live_blk[1], start = live_blk[2];
-  if (bi < 0) return;
+  int bad = 0;
+  for (int b = tid; b < a.B; b += kAppendThreads) {
+    const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1], sl = a.kv.seq_len[b], pe = a.kv.pending[b];
+    if (o0 < 0 || o1 < o0 || o1 > a.T) {
+      bad = 1;
+    } else if (o1 > o0 && append_unit(o0, b) <= u && u < append_unit(o1, b + 1)) {
+      sh[0] = b; sh[1] = o0; sh[2] = o1; sh[3] = sl; sh[4] = pe;
+    }
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
+    return;
+  }
+  const int b = sh[0];
+  if (b < 0) return;
+  const int o0 = sh[1], n_new = sh[2] - o0, P = sh[4];
+  if (sh[3] < 0 || P < 0 || sh[3] > INT32_MAX - P) {
+    if (tid == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
+    return;
+  }
+  const int start = sh[3] + P;
+  if ((long long)start + n_new > (long long)a.kv.max_blocks * kBlk) {
+    if (tid == 0) set_error(a.err, MTP_ERR_CAPACITY);
+    return;
+  }
+  const int first = start >> 4, last = (start + n_new - 1) >> 4, bi = first + (u - append_unit(o0, b));
+  if (bi > last) return;
   const int s0 = max(start - bi * kBlk, 0);                  // first new slot within the block
   const int s1 = min(start + n_new - bi * kBlk, kBlk);       // one past the last
   const int r0 = o0 + bi * kBlk + s0 - start;                // input row of slot s0
-  const int rd = a.rope ? tab.rotary_dim : 0, half = rd >> 1;
-  for (int i = tid; i < (s1 - s0) * half; i += kAppendThreads) {
-    const int r = i / half, p = i - r * half;
-    cs[r][p] = rope_cos_sin(a.positions[r0 + r], tab.turns[p], tab.magnitude);
+  const int blk = a.kv.block_table[(long long)b * a.kv.max_blocks + bi];
+  const int rd = a.rope ? tab.rotary_dim : 0;
+  // ---- rows: slot s0 + tid / LPR, + STEP, ...
+  const int e8 = tid % LPR;
+  const bool split = a.vec && tab.layout == MTP_ROPE_HALF && e8 < rd / 8;   // elements 4 e8 .., rd / 2 + 4 e8 ..
+  const int ea = split ? 4 * e8 : 8 * e8, eb = split ? rd / 2 + 4 * e8 : 8 * e8 + 4;
+  float kx[PASS][8], vx[PASS][8];
+  float amax[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < PASS; ++j) {
+    const int i = tid / LPR + j * STEP;
+    if (i >= s1 - s0) continue;
+    const T* kr = (const T*)a.k + (long long)(r0 + i) * a.k_stride + g * HD;
+    const T* vr = (const T*)a.v + (long long)(r0 + i) * a.v_stride + g * HD;
+    if (a.vec) {
+      load_n<T, 4>(kr + ea, kx[j]);
+      load_n<T, 4>(kr + eb, kx[j] + 4);
+      load_n<T, 8>(vr + 8 * e8, vx[j]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        kx[j][e] = get1<T>(kr + 8 * e8 + e);
+        vx[j][e] = get1<T>(vr + 8 * e8 + e);
+      }
+    }
   }
-  __syncthreads();
-  if (blk >= 0) {
-    float val[2][RPW][DPL];
-    float amax[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < RPW; ++j) {
-      const int s = warp + j * W;  // slot within the block
-      if (s < s0 || s >= s1) continue;
-      const int r = r0 + s - s0;
-      const T* kr = (const T*)a.k + (long long)r * a.k_stride + g * HD;
-      const T* vr = (const T*)a.v + (long long)r * a.v_stride + g * HD;
+  for (int j = 0; j < PASS; ++j) {
+    const int i = tid / LPR + j * STEP;
+    if (i >= s1 - s0) continue;
+    if (rd) {
+      const int pos = a.positions[r0 + i];
+      if (split) {
 #pragma unroll
-      for (int e = 0; e < DPL; ++e) {
-        val[0][j][e] = rotated<T>(kr, lane * DPL + e, rd ? cs[s - s0] : nullptr, rd, tab.layout);
-        val[1][j][e] = get1<T>(vr + lane * DPL + e);
+        for (int e = 0; e < 4; ++e) {
+          const float2 c = rope_cos_sin(pos, tab.turns[ea + e], tab.magnitude);
+          const float x = kx[j][e], y = kx[j][4 + e];
+          kx[j][e] = x * c.x - y * c.y;
+          kx[j][4 + e] = y * c.x + x * c.y;
+        }
+      } else if (tab.layout == MTP_ROPE_INTERLEAVED) {   // a pair lies within a thread's eight
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (finite_f(val[w][j][e])) amax[w] = fmaxf(amax[w], fabsf(val[w][j][e]));
+        for (int e = 0; e < 8; e += 2) {
+          if (8 * e8 + e >= rd) continue;
+          const float2 c = rope_cos_sin(pos, tab.turns[4 * e8 + e / 2], tab.magnitude);
+          const float x = kx[j][e], y = kx[j][e + 1];
+          kx[j][e] = x * c.x - y * c.y;
+          kx[j][e + 1] = y * c.x + x * c.y;
+        }
+      } else if (!a.vec) {                               // halves that do not fall on fours: partners one by one
+        const T* kr = (const T*)a.k + (long long)(r0 + i) * a.k_stride + g * HD;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = 8 * e8 + e;
+          if (d >= rd) continue;
+          const bool low = d < rd / 2;
+          const float2 c = rope_cos_sin(pos, tab.turns[low ? d : d - rd / 2], tab.magnitude);
+          const float y = get1<T>(kr + (low ? d + rd / 2 : d - rd / 2));
+          kx[j][e] = low ? kx[j][e] * c.x - y * c.y : kx[j][e] * c.x + y * c.y;
+        }
       }
     }
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const float m = warp_max(amax[w]);
-      if (lane == 0) red[w][warp] = m;
+    for (int e = 0; e < 8; ++e) {
+      if (finite_f(kx[j][e])) amax[0] = fmaxf(amax[0], fabsf(kx[j][e]));
+      if (finite_f(vx[j][e])) amax[1] = fmaxf(amax[1], fabsf(vx[j][e]));
     }
-    __syncthreads();
+  }
+  const bool good = blk >= 0 && blk < a.kv.num_blocks;
+  const long long t = (long long)(good ? blk : 0) * a.n_kv + g;
+  float was[2] = {0.0f, 0.0f};
+  if (s0 > 0 && good) {
+    was[0] = a.kv.k_scale[t];
+    was[1] = a.kv.v_scale[t];
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float m = warp_max(amax[w]);
+    if (lane == 0) red[w][warp] = m;
+  }
+  __syncthreads();   // (also: all have read the old scales)
+  if (!good) {
+    if (tid == 0) set_error(a.err, MTP_ERR_CAPACITY);
+  } else {
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      float m = 0.0f;
+      float m = red[w][0];
 #pragma unroll
-      for (int i = 0; i < W; ++i) m = fmaxf(m, red[w][i]);
-      float* scale = (w ? a.kv.v_scale : a.kv.k_scale) + (long long)blk * a.n_kv + g;
-      uint8_t* tile = (uint8_t*)(w ? a.kv.v_pool : a.kv.k_pool) + ((long long)blk * a.n_kv + g) * (kBlk * HD);
-      const float was = s0 > 0 ? *scale : 0.0f;
-      const float need = e4m3_scale(m);
-      const float now = fmaxf(was, need);
+      for (int i = 1; i < W; ++i) m = fmaxf(m, red[w][i]);
+      uint8_t* tile = (uint8_t*)(w ? a.kv.v_pool : a.kv.k_pool) + t * (kBlk * HD);
+      const float now = fmaxf(was[w], e4m3_scale(m));
       const float inv = now > 0.0f ? 1.0f / now : 0.0f;
       // entries of a block whose scale grows
-      if (was > 0.0f && now > was) {
-        const float f = was * inv;
-        for (int i = tid; i < s0 * (HD / 2); i += kAppendThreads) {
-          uint16_t* p = (uint16_t*)tile + i;
-          const float2 x = e4m3_to_float2(*p);
-          *p = (uint16_t)e4m3_pack2(x.x * f, x.y * f);
+      if (was[w] > 0.0f && now > was[w]) {
+        const float f = was[w] * inv;
+        for (int i = tid; i < s0 * (HD / 4); i += kAppendThreads) {
+          uint32_t* p = (uint32_t*)tile + i;
+          const uint32_t c = *p;
+          const float2 x = e4m3_to_float2(c & 0xFFFFu), y = e4m3_to_float2(c >> 16);
+          *p = e4m3_pack2(x.x * f, x.y * f) | (e4m3_pack2(y.x * f, y.y * f) << 16);
         }
       }
 #pragma unroll
-      for (int j = 0; j < RPW; ++j) {
-        const int s = warp + j * W;
-        if (s < s0 || s >= s1) continue;
-        uint16_t* p = (uint16_t*)(tile + s * HD + lane * DPL);
-#pragma unroll
-        for (int e = 0; e < DPL; e += 2)
-          p[e / 2] = (uint16_t)e4m3_pack2(e4m3_in(val[w][j][e], inv), e4m3_in(val[w][j][e + 1], inv));
+      for (int j = 0; j < PASS; ++j) {
+        const int i = tid / LPR + j * STEP;
+        if (i >= s1 - s0) continue;
+        const float* x = w ? vx[j] : kx[j];
+        uint8_t* row = tile + (s0 + i) * HD;
+        if (!MTP_IN_BOUNDS(a.err, t * (kBlk * HD) + (s0 + i) * HD + HD - 1, (long long)a.kv.num_blocks * a.n_kv * kBlk * HD)) continue;
+        *(uint32_t*)(row + (w ? 8 * e8 : ea)) = e4m3_pack4(x, inv);
+        *(uint32_t*)(row + (w ? 8 * e8 + 4 : eb)) = e4m3_pack4(x + 4, inv);
       }
-      __syncthreads();  // all have read the old scale
-      if (tid == 0) *scale = now;
+      if (tid == 0) (w ? a.kv.v_scale : a.kv.k_scale)[t] = now;
     }
   }
+  // ---- the head's queries
   if (a.q) {
-    const int G = a.n_q / a.n_kv;
-    const int width = G * HD;
-    for (int i = tid; i < (s1 - s0) * (width / 2); i += kAppendThreads) {
-      const int r = i / (width / 2), p = i - r * (width / 2);
-      const int h = p / (HD / 2), pe = p - h * (HD / 2);
-      const T* x = (const T*)a.q + (long long)(r0 + r) * a.q_stride + (g * G + h) * HD;
-      T* o = (T*)a.q_out + (long long)(r0 + r) * a.q_out_stride + (g * G + h) * HD;
-      // pe < half: a rotated pair; then the rest, two at a time
-      const int ia = pe < half ? (tab.layout == MTP_ROPE_HALF ? pe : 2 * pe) : 2 * pe;
-      const int ib = pe < half && tab.layout == MTP_ROPE_HALF ? pe + half : ia + 1;
-      const float xa = get1<T>(x + ia), xb = get1<T>(x + ib);
-      if (pe < half) {
-        const float2 c = cs[r][pe];
-        Elem<T>::store1(o + ia, xa * c.x - xb * c.y);
-        Elem<T>::store1(o + ib, xb * c.x + xa * c.y);
-      } else if (x != o) {
-        o[ia] = x[ia];
-        o[ib] = x[ib];
+    const int G = 1 << a.g_shift, rows = s1 - s0;
+    const T* q0 = (const T*)a.q + (long long)r0 * a.q_stride + (long long)g * G * HD;
+    T* w0 = (T*)a.q_out + (long long)r0 * a.q_out_stride + (long long)g * G * HD;
+    if (a.q_vec) {
+      // a thread owns 8 pairs (or 8 elements past the rotated part) of a
+      // row and walks over heads; few rows share the heads among threads
+      const int turning = rd / 16, units = turning + (a.q == a.q_out ? 0 : (HD - rd) / 8);
+      int hs = 1;
+      while (hs < G && 2 * hs * rows * units <= kAppendThreads) hs *= 2;
+      for (int i = tid; i < rows * units * hs; i += kAppendThreads) {
+        const int h0 = i % hs, x = i / hs, r = x / units, un = x - r * units;
+        const T* qr = q0 + (long long)r * a.q_stride;
+        T* wr = w0 + (long long)r * a.q_out_stride;
+        if (un >= turning) {
+          const int e = rd + 8 * (un - turning);
+          for (int h = h0; h < G; h += hs) {
+            float y[8];
+            load_n<T, 8>(qr + h * HD + e, y);
+            store_8(wr + h * HD + e, y);
+          }
+          continue;
+        }
+        const bool hf = tab.layout == MTP_ROPE_HALF;
+        const int xa = hf ? 8 * un : 16 * un, xb = hf ? 8 * un + rd / 2 : 16 * un + 8;
+        const int pos = a.positions[r0 + r];
+        float2 cs[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cs[e] = rope_cos_sin(pos, tab.turns[8 * un + e], tab.magnitude);
+        for (int h = h0; h < G; h += hs) {
+          float p[16], y[16];
+          load_n<T, 8>(qr + h * HD + xa, p);
+          load_n<T, 8>(qr + h * HD + xb, p + 8);
+          if (hf) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              y[e] = p[e] * cs[e].x - p[8 + e] * cs[e].y;
+              y[8 + e] = p[8 + e] * cs[e].x + p[e] * cs[e].y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              y[2 * e] = p[2 * e] * cs[e].x - p[2 * e + 1] * cs[e].y;
+              y[2 * e + 1] = p[2 * e + 1] * cs[e].x + p[2 * e] * cs[e].y;
+            }
+          }
+          store_8(wr + h * HD + xa, y);
+          store_8(wr + h * HD + xb, y + 8);
+        }
+      }
+    } else {
+      for (int i = tid; i < rows * (HD / 2); i += kAppendThreads) {
+        const int r = i / (HD / 2), pe = i - r * (HD / 2);
+        const T* qr = q0 + (long long)r * a.q_stride;
+        T* wr = w0 + (long long)r * a.q_out_stride;
+        const bool turn = pe < rd / 2, hf = turn && tab.layout == MTP_ROPE_HALF;
+        const int ia = hf ? pe : 2 * pe, ib = hf ? pe + rd / 2 : 2 * pe + 1;
+        float2 c = make_float2(0.0f, 0.0f);
+        if (turn) c = rope_cos_sin(a.positions[r0 + r], tab.turns[pe], tab.magnitude);
+        for (int h = 0; h < G; ++h) {
+          if (turn) {
+            const float x = get1<T>(qr + h * HD + ia), y = get1<T>(qr + h * HD + ib);
+            Elem<T>::store1(wr + h * HD + ia, x * c.x - y * c.y);
+            Elem<T>::store1(wr + h * HD + ib, y * c.x + x * c.y);
+          } else if (a.q != a.q_out) {
+            wr[h * HD + ia] = qr[h * HD + ia];
+            wr[h * HD + ib] = qr[h * HD + ib];
+          }
+        }
       }
     }
   }
+  // the last of the request's thread blocks publishes the new length: all
+  // have read the old one by then
+  if (tid == 0 && arrive_last(a.kv.arrive + b, (last - first + 1) * a.n_kv)) a.kv.pending[b] = P + n_new;
 }
 
 // -------------------------------------------------------------------- read
@@ -202,42 +334,59 @@ struct Read8Args {
   int B, T, n_kv;
 };
 
+// Thread block: one row, all kv heads; a thread turns 8 codes into 16 bytes.
 template <int HD>
 __global__ void __launch_bounds__(128) kv8_read_kernel(const Read8Args a) {
   const int r = blockIdx.x;
-  __shared__ int sh[3], at[2];
-  if (!find_request(a.row_offsets, a.B, a.T, r, a.err, sh, [](int o, int) { return o; })) return;
-  if (threadIdx.x == 0) {
-    const int b = sh[0], s = a.start[b];
-    const long long L = (long long)a.kv.seq_len[b] + a.kv.pending[b];
-    int blk = -1, slot = 0;
-    if (s < 0 || (long long)s + (sh[2] - sh[1]) > L) {
-      set_error(a.err, MTP_ERR_DEVICE_ARGS);
-    } else {
-      slot = s + (r - sh[1]);
-      const int bi = slot >> 4;
-      blk = bi < a.kv.max_blocks ? a.kv.block_table[(long long)b * a.kv.max_blocks + bi] : -1;
-      if (blk < 0 || blk >= a.kv.num_blocks) {
-        set_error(a.err, MTP_ERR_CAPACITY);
-        blk = -1;
-      }
-    }
-    at[0] = blk;
-    at[1] = slot & 15;
-  }
+  __shared__ int sh[5];
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) sh[0] = -1;
   __syncthreads();
-  const int blk = at[0], off = at[1];
-  if (blk < 0) return;
-  const int per = a.n_kv * (HD / 2);
+  int bad = 0;
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1], s = a.start[b];
+    const long long L = (long long)a.kv.seq_len[b] + a.kv.pending[b];
+    if (o0 < 0 || o1 < o0 || o1 > a.T) {
+      bad = 1;
+    } else if (o0 <= r && r < o1) {
+      sh[0] = b;
+      sh[1] = s < 0 || (long long)s + (o1 - o0) > L ? -1 : s + (r - o0);
+    }
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
+    return;
+  }
+  const int b = sh[0], slot = sh[1];
+  if (b < 0) return;
+  if (slot < 0) {
+    if (threadIdx.x == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
+    return;
+  }
+  const int bi = slot >> 4, off = slot & 15;
+  const int blk = bi < a.kv.max_blocks ? a.kv.block_table[(long long)b * a.kv.max_blocks + bi] : -1;
+  if (blk < 0 || blk >= a.kv.num_blocks) {
+    if (threadIdx.x == 0) set_error(a.err, MTP_ERR_CAPACITY);
+    return;
+  }
+  constexpr int VEC = HD / 8;
+  const int per = a.n_kv * VEC;
   for (int i = threadIdx.x; i < 2 * per; i += blockDim.x) {
     const int w = i >= per;
-    const int j = i - w * per, g = j / (HD / 2), e = j - g * (HD / 2);
+    const int j = i - w * per, g = j / VEC, e = j - g * VEC;
     const long long tile = (long long)blk * a.n_kv + g;
-    const uint16_t c = ((const uint16_t*)(w ? a.kv.v_pool : a.kv.k_pool))[(tile * kBlk + off) * (HD / 2) + e];
+    const uint2 c = *((const uint2*)(w ? a.kv.v_pool : a.kv.k_pool) + (tile * kBlk + off) * VEC + e);
     const float s = (w ? a.kv.v_scale : a.kv.k_scale)[tile];
-    const float2 x = e4m3_to_float2(c);
-    ((uint32_t*)(w ? a.v_out : a.k_out))[((long long)r * a.n_kv + g) * (HD / 2) + e] =
-        (uint32_t)f32_to_bf16_rne(x.x * s) | ((uint32_t)f32_to_bf16_rne(x.y * s) << 16);
+    uint32_t o[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float2 y = e4m3_to_float2((x < 2 ? c.x : c.y) >> (16 * (x & 1)) & 0xFFFFu);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[x]) : "f"(y.y * s), "f"(y.x * s));
+    }
+    const long long at = ((long long)r * a.n_kv + g) * HD + 8 * e;
+    if (!MTP_IN_BOUNDS(a.err, at + 7, (long long)a.T * a.n_kv * HD)) continue;
+    *reinterpret_cast<uint4*>((w ? a.v_out : a.k_out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -261,6 +410,8 @@ __global__ void __launch_bounds__(kEditThreads) kv8_edit_kernel(const Edit8Args 
   __shared__ float kept_scale[kPathMax];
   __shared__ float red[kEditThreads / 32];
   __shared__ int sh[4];
+  pdl_wait();
+  pdl_trigger();
   const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int32_t* keep = a.keep ? a.keep + (long long)b * a.keep_stride : nullptr;
   if (tid == 0) {
@@ -373,6 +524,7 @@ __global__ void __launch_bounds__(kEditThreads) kv8_edit_kernel(const Edit8Args 
         set_error(a.err, MTP_ERR_CAPACITY);
         continue;
       }
+      if (!MTP_IN_BOUNDS(a.err, (t * kBlk + (slot & 15)) * vec + e, (long long)a.kv.num_blocks * a.n_kv * kBlk * vec)) continue;
       pool[(t * kBlk + (slot & 15)) * vec + e] = make_uint4(0, 0, 0, 0);
       if (e == 0 && (slot & 15) == 0) scale[t] = 0.0f;
     }
@@ -418,36 +570,42 @@ mtp_status mtp_kv8_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_
   a.B = B;
   a.T = T;
   a.n_kv = c.n_kv_heads;
-  a.n_q = c.n_q_heads;
+  for (a.g_shift = 0; (1 << a.g_shift) < c.n_q_heads / c.n_kv_heads; ++a.g_shift) {
+  }
   a.rope = rope != nullptr;
   mtp_rope_table tab = {};
   if (rope) tab = *rope;
-  const dim3 grid(T / 16 + 2 * B, c.n_kv_heads);
-  cudaStream_t s = (cudaStream_t)stream;
   const bool bf = c.dtype == MTP_DTYPE_BF16;
-  if (c.head_dim == 128) {
-    if (bf) kv8_append_kernel<uint16_t, 128><<<grid, kAppendThreads, 0, s>>>(a, tab);
-    else kv8_append_kernel<float, 128><<<grid, kAppendThreads, 0, s>>>(a, tab);
-  } else {
-    if (bf) kv8_append_kernel<uint16_t, 64><<<grid, kAppendThreads, 0, s>>>(a, tab);
-    else kv8_append_kernel<float, 64><<<grid, kAppendThreads, 0, s>>>(a, tab);
-  }
+  const int per16 = bf ? 8 : 4;   // elements of 16 bytes
+  a.vec = !(((uintptr_t)k | (uintptr_t)v) & 15) && k_stride % per16 == 0 && v_stride % per16 == 0 &&
+          tab.rotary_dim % 8 == 0;
+  a.q_vec = !(((uintptr_t)q | (uintptr_t)q_out) & 15) && q_stride % per16 == 0 && q_out_stride % per16 == 0 &&
+            tab.rotary_dim % 16 == 0;
+  const dim3 grid(T / 16 + 2 * B, c.n_kv_heads), block(kAppendThreads);
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e =
+      c.head_dim == 128 ? (bf ? launch_pdl(kv8_append_kernel<uint16_t, 128>, grid, block, 0, s, a, tab)
+                              : launch_pdl(kv8_append_kernel<float, 128>, grid, block, 0, s, a, tab))
+                        : (bf ? launch_pdl(kv8_append_kernel<uint16_t, 64>, grid, block, 0, s, a, tab)
+                              : launch_pdl(kv8_append_kernel<float, 64>, grid, block, 0, s, a, tab));
   ctx->launches++;
-  return launch_status(cudaGetLastError());
+  return launch_status(e);
 }
 
 mtp_status mtp_kv8_read(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* start, int T,
                         const int32_t* row_offsets, void* k_out, void* v_out) {
-  if (!ctx || B < 1 || B > ctx->cfg.max_batch || T < 0 || !start || !row_offsets || !k_out || !v_out || !kv8_ok(kv))
+  if (!ctx || B < 1 || B > ctx->cfg.max_batch || T < 0 || !start || !row_offsets || !k_out || !v_out || !kv8_ok(kv) ||
+      (((uintptr_t)k_out | (uintptr_t)v_out) & 15))
     return MTP_ERR_INVALID;
   if (T == 0) return MTP_OK;
   DeviceGuard dev(ctx->device);
   if (!dev.ok) return MTP_ERR_CUDA;
   Read8Args a{*kv, start, row_offsets, (uint16_t*)k_out, (uint16_t*)v_out, ctx->err, B, T, ctx->cfg.n_kv_heads};
-  if (ctx->cfg.head_dim == 128) kv8_read_kernel<128><<<T, 128, 0, (cudaStream_t)stream>>>(a);
-  else kv8_read_kernel<64><<<T, 128, 0, (cudaStream_t)stream>>>(a);
+  const cudaError_t e = ctx->cfg.head_dim == 128
+                            ? launch_pdl(kv8_read_kernel<128>, dim3(T), dim3(128), 0, (cudaStream_t)stream, a)
+                            : launch_pdl(kv8_read_kernel<64>, dim3(T), dim3(128), 0, (cudaStream_t)stream, a);
   ctx->launches++;
-  return launch_status(cudaGetLastError());
+  return launch_status(e);
 }
 
 static mtp_status kv8_edit(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, int mode, const int32_t* arg,
@@ -458,9 +616,10 @@ static mtp_status kv8_edit(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv,
   if (!dev.ok) return MTP_ERR_CUDA;
   Edit8Args a{*kv, arg, keep, ctx->err, keep_stride, mode, extra, ctx->cfg.n_kv_heads, ctx->cfg.head_dim};
   const size_t smem = keep ? (size_t)kPathMax * ctx->cfg.head_dim : 0;  // at most 32 KB
-  kv8_edit_kernel<<<dim3(ctx->cfg.n_kv_heads, B), kEditThreads, smem, (cudaStream_t)stream>>>(a);
+  const cudaError_t e = launch_pdl(kv8_edit_kernel, dim3(ctx->cfg.n_kv_heads, B), dim3(kEditThreads), smem,
+                                   (cudaStream_t)stream, a);
   ctx->launches++;
-  return launch_status(cudaGetLastError());
+  return launch_status(e);
 }
 
 mtp_status mtp_kv8_commit(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* n_keep) {

@@ -101,34 +101,6 @@ __device__ __forceinline__ float2 rope_cos_sin(int32_t pos, uint64_t turns, floa
   return cs;
 }
 
-// The request of one unit of work, found by the whole thread block: request
-// b's units are [first(o, b), first(o', b + 1)) for its rows [o, o').  All
-// offsets are checked on the way; with a bad one (descending, or outside
-// 0..T) the call does nothing.  sh receives b, o and o'.  False (the same in
-// every thread) if the unit is nobody's.
-template <typename First>
-__device__ __forceinline__ bool find_request(const int32_t* off, int B, int T, int unit, int* err, int* sh,
-                                             First first) {
-  if (threadIdx.x == 0) sh[0] = -1;
-  __syncthreads();
-  int bad = 0;
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const int o0 = off[b], o1 = off[b + 1];
-    if (o0 < 0 || o1 < o0 || o1 > T) {
-      bad = 1;
-    } else if (o1 > o0 && first(o0, b) <= unit && unit < first(o1, b + 1)) {
-      sh[0] = b;
-      sh[1] = o0;
-      sh[2] = o1;
-    }
-  }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) set_error(err, MTP_ERR_DEVICE_ARGS);
-    return false;
-  }
-  return sh[0] >= 0;
-}
-
 // Counts thread blocks that share a request in *arrive; true, and the count
 // zero again, for the last of `total`.  Acquire-release: what the others read
 // before arriving was read before the last one goes on.
