@@ -47,6 +47,13 @@ __device__ __forceinline__ uint32_t e4m3_unpack2(uint32_t two) {
   return r;
 }
 
+// Four codes to two pairs of halves.
+__device__ __forceinline__ void e4m3_unpack4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+
 __device__ __forceinline__ float2 e4m3_to_float2(uint32_t two) {
   const uint32_t h = e4m3_unpack2(two);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));

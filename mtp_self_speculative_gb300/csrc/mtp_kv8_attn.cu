@@ -2,7 +2,8 @@
 // verification, packed trees).
 //
 //   out[r, h] = sum_t p_t V[t, g] / sum_t p_t,  p_t = 2^(c s_t - m),
-//   s_t = q[r, h] . K[t, g], c = scale * log2 e, m the running maximum.
+//   s_t = q[r, h] . K[t, g], c = scale * log2 e, m a running
+// reference near the maximum.
 //
 // The (row, query head) pairs that share a kv head are the columns of a tile
 // (n_b * G of them, 8 NT per tile); both products run on the tensor cores with
@@ -43,6 +44,7 @@ constexpr int kA8MaxB = 1024;      // requests of a call (prefix sums in shared 
 constexpr int kA8MinShare = 8;     // units of a thread block's share at least
 constexpr int kA8Lead = 4;         // units that a segment's start and end count for
 constexpr int kA8MaxCols = 32;     // columns of a tile
+constexpr float kA8Least = -3.4028235e38f;   // the reference of a column that has seen nothing
 
 struct Attn8Args {
   const void* q;
@@ -66,6 +68,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same onto zero.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
@@ -182,8 +192,8 @@ __device__ __forceinline__ void attn8_finish(const Attn8Args& a, int o0, int col
 
 // Take a partial result (reference m, sum l, o) into another.
 __device__ __forceinline__ void attn8_take(float& M, float& Ls, float4& x, float m, float l, const float4& y) {
-  const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.0f : mn;
-  const float f0 = ex2(M - mu), f1 = ex2(m - mu);
+  const float mn = fmaxf(M, m);
+  const float f0 = ex2(M - mn), f1 = ex2(m - mn);
   Ls = Ls * f0 + l * f1;
   x.x = x.x * f0 + y.x * f1;
   x.y = x.y * f0 + y.y * f1;
@@ -377,29 +387,33 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       if (lane == 0) qfac_s[c] = a.qscale * (1.0f / up);
       if (lane_on) {
         // element d = 4 lane: half d / 64, lane group (d % 64) / 16, word (d % 16) / 4
+        // (two words' fragments, 16 bytes, lie together)
         const int ks = (lane >> 4) * 4 + (lane & 3), fl = (c & 7) * 4 + ((lane & 15) >> 2);
         uint2 hi;
         hi.x = pack_half2(x[0] * up, x[1] * up);
         hi.y = pack_half2(x[2] * up, x[3] * up);
-        uint2* dst = reinterpret_cast<uint2*>(qf) + ((size_t)(c >> 3) * KS + ks) * 32 + fl;
+        uint2* dst = reinterpret_cast<uint2*>(qf) + ((c >> 3) * KS + (ks & ~1)) * 32 + fl * 2 + (ks & 1);
         *dst = hi;
         if constexpr (SPLIT == 2) {
           const float2 h0 = unpack_half2(hi.x), h1 = unpack_half2(hi.y);
-          dst[(size_t)NT * KS * 32] = make_uint2(pack_half2(x[0] * up - h0.x, x[1] * up - h0.y),
+          dst[NT * KS * 32] = make_uint2(pack_half2(x[0] * up - h0.x, x[1] * up - h0.y),
                                                  pack_half2(x[2] * up - h1.x, x[3] * up - h1.y));
         }
       }
     }
     __syncthreads();
-    uint2 qreg[kQReg ? SPLIT : 1][kQReg ? NT : 1][kQReg ? KS : 1];
+    // fragments of k-steps 2 i and 2 i + 1
+    auto q_frag = [&](int sp, int nt, int i) -> uint4 {
+      return lds128(smem_addr(qf) + (uint32_t)(((sp * NT + nt) * KS + 2 * i) * 256 + lane * 16));
+    };
+    uint4 qreg[kQReg ? SPLIT : 1][kQReg ? NT : 1][kQReg ? KS / 2 : 1];
     if constexpr (kQReg) {
 #pragma unroll
       for (int sp = 0; sp < SPLIT; ++sp)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-            qreg[sp][nt][ks] = reinterpret_cast<const uint2*>(qf)[((size_t)(sp * NT + nt) * KS + ks) * 32 + lane];
+          for (int i = 0; i < KS / 2; ++i) qreg[sp][nt][i] = q_frag(sp, nt, i);
     }
     float qfac[NT][2];
 #pragma unroll
@@ -413,7 +427,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
-      m_run[nt][0] = m_run[nt][1] = -INFINITY;
+      m_run[nt][0] = m_run[nt][1] = kA8Least;
       l_run[nt][0] = l_run[nt][1] = 0.0f;
     }
 
@@ -437,24 +451,28 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[j][nt][0] = sc[j][nt][1] = sc[j][nt][2] = sc[j][nt][3] = 0.0f;
-#pragma unroll
         for (int hh = 0; hh < HD / 64; ++hh) {
           const uint4 lo = lds128(st + k_at<HD>(16 * j + gi, hh * 4 + ti));
           const uint4 hi = lds128(st + k_at<HD>(16 * j + gi + 8, hh * 4 + ti));
           const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = e4m3_unpack2(lw[w] & 0xFFFFu), a2 = e4m3_unpack2(lw[w] >> 16);
-            const uint32_t a1 = e4m3_unpack2(hw[w] & 0xFFFFu), a3 = e4m3_unpack2(hw[w] >> 16);
+          for (int w = 0; w < 4; w += 2) {
+            uint32_t f[2][4];   // the A fragments of two k-steps
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              e4m3_unpack4(lw[w + x], f[x][0], f[x][2]);
+              e4m3_unpack4(hw[w + x], f[x][1], f[x][3]);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int sp = 0; sp < SPLIT; ++sp) {
-                uint2 qq;
-                if constexpr (kQReg) qq = qreg[sp][nt][hh * 4 + w];
-                else qq = reinterpret_cast<const uint2*>(qf)[((size_t)(sp * NT + nt) * KS + hh * 4 + w) * 32 + lane];
-                mma_f16(sc[j][nt], a0, a1, a2, a3, qq.x, qq.y);
+                uint4 qq;
+                if constexpr (kQReg) qq = qreg[sp][nt][hh * 2 + w / 2];
+                else qq = q_frag(sp, nt, hh * 2 + w / 2);
+                if (hh == 0 && w == 0 && sp == 0) mma_f16_zero(sc[j][nt], f[0][0], f[0][1], f[0][2], f[0][3], qq.x, qq.y);
+                else mma_f16(sc[j][nt], f[0][0], f[0][1], f[0][2], f[0][3], qq.x, qq.y);
+                mma_f16(sc[j][nt], f[1][0], f[1][1], f[1][2], f[1][3], qq.z, qq.w);
               }
           }
         }
@@ -462,59 +480,71 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       // ---- online softmax over the step's 32 tokens
       const float ks0 = lds32f(st + 2 * S::kTile), ks1 = lds32f(st + 2 * S::kTile + 4);
       const float vs0 = lds32f(st + 2 * S::kTile + 8), vs1 = lds32f(st + 2 * S::kTile + 12);
-      float alpha[NT][2];
-      bool moved = false;
+      // Weights are 2^(s - r).  The reference r of a column stays while every
+      // score is at most r + 15 (fp16 holds 2^15.9), so most steps need no
+      // maximum across the lanes and no rescaling.  When one is above, r
+      // becomes 14 below the maximum, a whole number: fp16 then keeps 11 bits
+      // of weights down to 2^-28 of the largest.  (Beyond 2^20 that sum would
+      // round, and r is the maximum itself.)
+      float fac[2][NT][2];
+      bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // a zero scale stands for zero entries: a factor above zero keeps
-          // -inf * f from becoming NaN
-          const float f0 = fmaxf(ks0 * qfac[nt][e], 1e-37f), f1 = fmaxf(ks1 * qfac[nt][e], 1e-37f);
-          if (edge) {
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j) {
+            // a zero scale stands for zero entries: a factor above zero keeps
+            // -inf * f from becoming NaN
+            const float f = fmaxf((j ? ks1 : ks0) * qfac[nt][e], 1e-37f);
+            fac[j][nt][e] = f;
+            if (edge) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int t = tok0 + 16 * j + 8 * h + gi;
                 if (t >= L || (t >= base && !sees(nt * 8 + 2 * ti + e, t))) sc[j][nt][2 * h + e] = -INFINITY;
               }
+            }
+            above |= fmaf(fmaxf(sc[j][nt][e], sc[j][nt][2 + e]), f, -m_run[nt][e]) > 15.0f;
           }
-          float mx = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]) * f0, fmaxf(sc[1][nt][e], sc[1][nt][2 + e]) * f1);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          // the reference r: a whole number, so that it moves rarely, 14 below
-          // the maximum, so that fp16 keeps 11 bits of weights down to 2^-28
-          // of the largest.  Beyond 2^20 that sum would round: r = maximum.
-          const float ref = fabsf(mx) > 1048576.0f ? mx : ceilf(mx) - 14.0f;
-          const float rn = fmaxf(m_run[nt][e], ref);
-          const float ru = rn == -INFINITY ? 0.0f : rn;
-          alpha[nt][e] = ex2(m_run[nt][e] - ru);
-          moved |= rn != m_run[nt][e];
-          m_run[nt][e] = rn;
-          float sum = 0.0f;
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]) * fac[0][nt][e],
+                             fmaxf(sc[1][nt][e], sc[1][nt][2 + e]) * fac[1][nt][e]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float ref = fabsf(mx) > 1048576.0f ? mx : ceilf(mx) - 14.0f;
+            const float rn = fmaxf(m_run[nt][e], ref);
+            alpha[e] = ex2(m_run[nt][e] - rn);
+            m_run[nt][e] = rn;
+            l_run[nt][e] *= alpha[e];
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            o[nt][mt][0] *= alpha[0];
+            o[nt][mt][1] *= alpha[1];
+            o[nt][mt][2] *= alpha[0];
+            o[nt][mt][3] *= alpha[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float p = ex2(fmaf(sc[j][nt][2 * h + e], j ? f1 : f0, -ru));
+              const float p = ex2(fmaf(sc[j][nt][2 * h + e], fac[j][nt][e], -m_run[nt][e]));
               sc[j][nt][2 * h + e] = p;
-              sum += p;
+              l_run[nt][e] += p;
             }
-          l_run[nt][e] = l_run[nt][e] * alpha[nt][e] + sum;
-        }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            o[nt][mt][0] *= alpha[nt][0];
-            o[nt][mt][1] *= alpha[nt][1];
-            o[nt][mt][2] *= alpha[nt][0];
-            o[nt][mt][3] *= alpha[nt][1];
-          }
-      }
       // ---- values
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -591,13 +621,14 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
           for (int h = 0; h < 2; ++h) {
             const int mt = 2 * w + h;
             const uint32_t x01 = h ? q01 : p01, x23 = h ? q23 : p23;
-            const uint32_t a0 = e4m3_unpack2(x01 & 0xFFFFu), a1 = e4m3_unpack2(x01 >> 16);
-            const uint32_t a2 = e4m3_unpack2(x23 & 0xFFFFu), a3 = e4m3_unpack2(x23 >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3_unpack4(x01, a0, a1);
+            e4m3_unpack4(x23, a2, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float pv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int sp = 0; sp < SPLIT; ++sp) mma_f16(pv, a0, a1, a2, a3, pb[sp][nt][0], pb[sp][nt][1]);
+              float pv[4];
+              mma_f16_zero(pv, a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
+              if constexpr (SPLIT == 2) mma_f16(pv, a0, a1, a2, a3, pb[SPLIT - 1][nt][0], pb[SPLIT - 1][nt][1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[nt][mt][e] = fmaf(pv[e], vs, o[nt][mt][e]);
             }
@@ -634,15 +665,14 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
     const int slot = blockIdx.x == c_first ? 1 : 0;
     for (int i = tid; i < ncols * (HD / 4); i += kA8Threads) {
       const int c = i / (HD / 4), d4 = i - c * (HD / 4);
-      float M = -INFINITY;
+      float M = kA8Least;
 #pragma unroll
       for (int w = 0; w < kA8Warps; ++w) M = fmaxf(M, wm[w][c]);
-      const float mu = M == -INFINITY ? 0.0f : M;
       float Ls = 0.0f;
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kA8Warps; ++w) {
-        const float f = ex2(wm[w][c] - mu);
+        const float f = ex2(wm[w][c] - M);
         const float4 y = *reinterpret_cast<const float4*>(merge + (w * S::kCols + c) * S::kPitch + d4 * 4);
         Ls += wl[w][c] * f;
         x.x = fmaf(y.x, f, x.x);
@@ -688,7 +718,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8
   const int d4 = item % (HD / 4);
   for (int c0 = cols * blockIdx.y; c0 < seg.z; c0 += cols * gridDim.y) {
     const int c = c0 + item / (HD / 4);
-    float M = -INFINITY, Ls = 0.0f;
+    float M = kA8Least, Ls = 0.0f;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < seg.z) {
       for (int k0 = way; k0 < count; k0 += kJoinAhead * ways) {
@@ -697,7 +727,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) {
           const int kk = k0 + k * ways;
-          ml[k] = make_float2(-INFINITY, 0.0f);
+          ml[k] = make_float2(kA8Least, 0.0f);
           y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (kk < count) {
             const float* pr = a.part + ((2ll * (c_first + kk) + (kk == 0 ? 1 : 0)) * kA8MaxCols + c) * (HD + 4);
