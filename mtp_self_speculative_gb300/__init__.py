@@ -87,7 +87,7 @@ class Context:
         self.cfg = cfg
         self.weights = weights
         self.device = device
-        self.dtype, self.head_dim = torch_dtype(cfg.dtype), int(cfg.head_dim)
+        self.dtype, self.head_dim, self.vocab = torch_dtype(cfg.dtype), int(cfg.head_dim), int(cfg.vocab)
 
     def close(self):
         if self.handle:
@@ -477,7 +477,7 @@ def mtp_rope(ctx: Context, x: torch.Tensor, positions: torch.Tensor, rope: RopeT
     if T == 0:
         return out
     _check(_clib.mtp_rope(ctx.handle, _ctx_stream(ctx, stream), T, heads, xp, xs,
-                          _dev_ptr(ctx, positions, torch.int32, "positions", (T,)), ctypes.byref(rope), op, os_),
+                          _dev_ptr(ctx, positions, torch.int32, "positions", (T,)), rope, op, os_),
            "mtp_rope")
     return out
 
@@ -505,7 +505,11 @@ class KVCache8:
         return cls(pools[0], pools[1], scales[0], scales[1], block_table, ints[0], ints[1], ints[2])
 
     def struct(self, ctx: Context) -> MTPKV8:
-        # the checks run again when a field has become another tensor
+        return self._checked_struct(ctx)[0]
+
+    def _checked_struct(self, ctx: Context):
+        """(struct, B, n_q, n_kv, head_dim); the checks run again when a field
+        or the context's configuration has become another one."""
         ptrs = (ctx.cfg, self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.k_scale.data_ptr(),
                 self.v_scale.data_ptr(), self.block_table.data_ptr(), self.seq_len.data_ptr(),
                 self.pending.data_ptr(), self.arrive.data_ptr(), self.k_pool.shape, self.block_table.shape)
@@ -523,12 +527,13 @@ class KVCache8:
         i32, f32 = torch.int32, torch.float32
         st = MTPKV8(_dev_ptr(ctx, self.k_pool, None, "k_pool", pool), _dev_ptr(ctx, self.v_pool, None, "v_pool", pool),
                     _dev_ptr(ctx, self.k_scale, f32, "k_scale", per), _dev_ptr(ctx, self.v_scale, f32, "v_scale", per),
-                    _dev_ptr(ctx, self.block_table, i32, "block_table", (B, None)),
+                    _dev_ptr(ctx, self.block_table, i32, "block_table", (B, int(self.block_table.shape[1]))),
                     _dev_ptr(ctx, self.seq_len, i32, "seq_len", (B,)),
                     _dev_ptr(ctx, self.pending, i32, "pending", (B,)),
                     _dev_ptr(ctx, self.arrive, i32, "arrive", (B,)), nb, int(self.block_table.shape[1]))
-        self.__dict__["_checked"] = (ptrs, st)
-        return st
+        got = (st, B, int(c.n_q_heads), int(c.n_kv_heads), int(c.head_dim))
+        self.__dict__["_checked"] = (ptrs, got)
+        return got
 
 
 def mtp_kv8_append(ctx: Context, kv: KVCache8, k: torch.Tensor, v: torch.Tensor, row_offsets: torch.Tensor,
@@ -538,70 +543,69 @@ def mtp_kv8_append(ctx: Context, kv: KVCache8, k: torch.Tensor, v: torch.Tensor,
     as pending entries, k rotated by ``rope`` at ``positions`` if given; q
     [T, n_q, head_dim] is rotated by the same table into q_out (None: in
     place).  Rows may be strided."""
-    B, T, c = int(kv.seq_len.shape[0]), int(k.shape[0]), ctx.cfg
-    st = kv.struct(ctx)
-    kp, ks = _row_ptr(ctx, k, "k", T, c.n_kv_heads)
-    vp, vs = _row_ptr(ctx, v, "v", T, c.n_kv_heads)
+    st, B, n_q, n_kv, _ = kv._checked_struct(ctx)
+    T = k.shape[0]
+    kp, ks = _row_ptr(ctx, k, "k", T, n_kv)
+    vp, vs = _row_ptr(ctx, v, "v", T, n_kv)
     qp, qs, qop, qos = None, 0, None, 0
     if q is not None:
-        qp, qs = _row_ptr(ctx, q, "q", T, c.n_q_heads)
-        qop, qos = (qp, qs) if q_out is None or q_out is q else _row_ptr(ctx, q_out, "q_out", T, c.n_q_heads)
+        qp, qs = _row_ptr(ctx, q, "q", T, n_q)
+        qop, qos = (qp, qs) if q_out is None or q_out is q else _row_ptr(ctx, q_out, "q_out", T, n_q)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if T == 0:
         return
     _check(_clib.mtp_kv8_append(ctx.handle, _ctx_stream(ctx, stream), B, T,
                                 _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), kp, ks, vp, vs,
-                                _dev_ptr(ctx, positions, torch.int32, "positions", (T,)),
-                                ctypes.byref(rope) if rope is not None else None, qp, qs, qop, qos,
-                                ctypes.byref(st)), "mtp_kv8_append")
+                                _dev_ptr(ctx, positions, torch.int32, "positions", (T,)), rope, qp, qs, qop, qos,
+                                st), "mtp_kv8_append")
 
 
 def mtp_kv8_read(ctx: Context, kv: KVCache8, start: torch.Tensor, row_offsets: torch.Tensor, k_out: torch.Tensor,
                  v_out: torch.Tensor, stream=None) -> None:
     """Entries start[b] .. of each request, as many as it has rows in
     row_offsets, into k_out and v_out [T, n_kv, head_dim] bf16."""
-    B, T, c = int(kv.seq_len.shape[0]), int(k_out.shape[0]), ctx.cfg
-    st, shape = kv.struct(ctx), (T, c.n_kv_heads, c.head_dim)
-    kp = _dev_ptr(ctx, k_out, torch.bfloat16, "k_out", shape)
-    vp = _dev_ptr(ctx, v_out, torch.bfloat16, "v_out", shape)
+    st, B, _, n_kv, hd = kv._checked_struct(ctx)
+    T = k_out.shape[0]
+    kp = _dev_ptr(ctx, k_out, torch.bfloat16, "k_out", (T, n_kv, hd))
+    vp = _dev_ptr(ctx, v_out, torch.bfloat16, "v_out", (T, n_kv, hd))
     if T == 0:
         return
-    _check(_clib.mtp_kv8_read(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+    _check(_clib.mtp_kv8_read(ctx.handle, _ctx_stream(ctx, stream), B, st,
                               _dev_ptr(ctx, start, torch.int32, "start", (B,)), T,
                               _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), kp, vp),
            "mtp_kv8_read")
 
 
 def mtp_kv8_commit(ctx: Context, kv: KVCache8, n_keep: torch.Tensor, stream=None) -> None:
-    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
-    _check(_clib.mtp_kv8_commit(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+    st, B = kv._checked_struct(ctx)[:2]
+    _check(_clib.mtp_kv8_commit(ctx.handle, _ctx_stream(ctx, stream), B, st,
                                 _dev_ptr(ctx, n_keep, torch.int32, "n_keep", (B,))), "mtp_kv8_commit")
 
 
 def mtp_kv8_commit_accepted(ctx: Context, kv: KVCache8, accepted: torch.Tensor, extra: int = 1, stream=None) -> None:
-    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
-    _check(_clib.mtp_kv8_commit_accepted(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+    st, B = kv._checked_struct(ctx)[:2]
+    _check(_clib.mtp_kv8_commit_accepted(ctx.handle, _ctx_stream(ctx, stream), B, st,
                                          _dev_ptr(ctx, accepted, torch.int32, "accepted", (B,)), int(extra)),
            "mtp_kv8_commit_accepted")
 
 
 def mtp_kv8_rollback(ctx: Context, kv: KVCache8, stream=None) -> None:
-    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
-    _check(_clib.mtp_kv8_rollback(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st)), "mtp_kv8_rollback")
+    st, B = kv._checked_struct(ctx)[:2]
+    _check(_clib.mtp_kv8_rollback(ctx.handle, _ctx_stream(ctx, stream), B, st), "mtp_kv8_rollback")
 
 
 def mtp_kv8_truncate(ctx: Context, kv: KVCache8, new_len: torch.Tensor, stream=None) -> None:
-    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
-    _check(_clib.mtp_kv8_truncate(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st),
+    st, B = kv._checked_struct(ctx)[:2]
+    _check(_clib.mtp_kv8_truncate(ctx.handle, _ctx_stream(ctx, stream), B, st,
                                   _dev_ptr(ctx, new_len, torch.int32, "new_len", (B,))), "mtp_kv8_truncate")
 
 
 def mtp_kv8_commit_path(ctx: Context, kv: KVCache8, keep: torch.Tensor, n_keep: torch.Tensor, stream=None) -> None:
     """Keep the pending entries keep[b, :n_keep[b]] (ascending), drop the rest."""
-    B, st = int(kv.seq_len.shape[0]), kv.struct(ctx)
+    st, B = kv._checked_struct(ctx)[:2]
     kp = _dev_ptr(ctx, keep, torch.int32, "keep", (B, None))
-    _check(_clib.mtp_kv8_commit_path(ctx.handle, _ctx_stream(ctx, stream), B, ctypes.byref(st), kp,
+    _check(_clib.mtp_kv8_commit_path(ctx.handle, _ctx_stream(ctx, stream), B, st, kp,
                                      int(keep.shape[1]), _dev_ptr(ctx, n_keep, torch.int32, "n_keep", (B,))),
            "mtp_kv8_commit_path")
 
@@ -614,8 +618,9 @@ class Attention8Workspace:
         n = int(_clib.mtp_kv8_attention_workspace_bytes(ctx.handle))
         if n == 0:
             raise MTPError(MTP_ERR_INVALID, "mtp_kv8_attention_workspace_bytes")
-        self.device = ctx.device
+        self.device, self.bytes = ctx.device, n
         self.ws = torch.empty(n, dtype=torch.uint8, device="cuda:%d" % ctx.device)
+        self.ptr = self.ws.data_ptr()
 
 
 def mtp_kv8_attention(ctx: Context, kv: KVCache8, q: torch.Tensor, row_offsets: torch.Tensor, out: torch.Tensor,
@@ -625,21 +630,21 @@ def mtp_kv8_attention(ctx: Context, kv: KVCache8, q: torch.Tensor, row_offsets: 
     the requests' caches: the rows of request b are its last entries; causal
     among them, or as the bits of mask [T, words] say.  ``max_rows``: at least
     the rows of any request; lse [T, n_q] float32; scale: 1 / sqrt(head_dim)."""
-    B, T, c = int(kv.seq_len.shape[0]), int(q.shape[0]), ctx.cfg
-    st = kv.struct(ctx)
-    qp, qs = _row_ptr(ctx, q, "q", T, c.n_q_heads)
-    op = _dev_ptr(ctx, out, torch_dtype(c.dtype), "out", (T, c.n_q_heads, c.head_dim))
-    lp = _dev_ptr(ctx, lse, torch.float32, "lse", (T, c.n_q_heads))
-    mp = _dev_ptr(ctx, mask, torch.int32, "mask", (T, None))
+    st, B, n_q, _, hd = kv._checked_struct(ctx)
+    T = q.shape[0]
+    qp, qs = _row_ptr(ctx, q, "q", T, n_q)
+    op = _dev_ptr(ctx, out, ctx.dtype, "out", (T, n_q, hd))
+    lp = _dev_ptr(ctx, lse, torch.float32, "lse", (T, n_q))
+    words = mask.shape[-1] if mask is not None else 0
+    mp = _dev_ptr(ctx, mask, torch.int32, "mask", (T, words))
     if ws.device != ctx.device:
         raise ValueError("the workspace belongs to cuda:%s" % ws.device)
     if T == 0:
         return
     _check(_clib.mtp_kv8_attention(ctx.handle, _ctx_stream(ctx, stream), B, T,
-                                   _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), int(max_rows),
-                                   qp, qs, ctypes.byref(st), mp, int(mask.shape[1]) if mask is not None else 0,
-                                   c.head_dim ** -0.5 if scale is None else float(scale), op, lp,
-                                   ws.ws.data_ptr(), int(ws.ws.numel())), "mtp_kv8_attention")
+                                   _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), max_rows,
+                                   qp, qs, st, mp, words, hd ** -0.5 if scale is None else scale, op, lp, ws.ptr,
+                                   ws.bytes), "mtp_kv8_attention")
 
 
 def mtp_token_counts_add(ctx: Context, counts: torch.Tensor, tokens: torch.Tensor, n_tokens: torch.Tensor,
@@ -647,7 +652,7 @@ def mtp_token_counts_add(ctx: Context, counts: torch.Tensor, tokens: torch.Tenso
     """Count tokens[b, :n_tokens[b]] in counts [B, vocab] int32 (in_prompt:
     mark them as occurring in the prompt instead)."""
     B = int(n_tokens.shape[0])
-    tp = _dev_ptr(ctx, tokens, torch.int32, "tokens", (B, None))
+    tp = _dev_ptr(ctx, tokens, torch.int32, "tokens", (B, tokens.shape[-1]))
     if int(tokens.shape[1]) == 0:
         return
     _check(_clib.mtp_token_counts_add(ctx.handle, _ctx_stream(ctx, stream), B, tp, int(tokens.shape[1]),
@@ -667,31 +672,43 @@ def mtp_logits_process(ctx: Context, logits: torch.Tensor, row_offsets: torch.Te
     drafts [B, stride]), biases (bias_offsets [B + 1] into bias_tokens and
     bias_values) and bit masks (mask [masks, ceil(vocab / 32)], mask_index
     [rows]) on logits [rows, vocab] into out (None: in place).  Returns out."""
-    V, dt = ctx.cfg.vocab, torch_dtype(ctx.cfg.dtype)
-    out = logits if out is None else out
-    if row_offsets.dim() != 1 or int(row_offsets.shape[0]) < 2:
+    V, dt, i32, f32 = ctx.vocab, ctx.dtype, torch.int32, torch.float32
+    if row_offsets.dim() != 1 or row_offsets.shape[0] < 2:
         raise ValueError("row_offsets must be [B + 1]")
     if (bias_offsets is None) != (bias_tokens is None) or (bias_offsets is None) != (bias_values is None):
         raise ValueError("bias_offsets, bias_tokens and bias_values go together")
     if (mask is None) != (mask_index is None):
         raise ValueError("mask and mask_index go together")
-    B, i32, f32 = int(row_offsets.shape[0]) - 1, torch.int32, torch.float32
-    lp = _dev_ptr(ctx, logits, dt, "logits", (None, V))
-    rows = int(logits.shape[0])
+    B, rows = row_offsets.shape[0] - 1, logits.shape[0]
+    lp = _dev_ptr(ctx, logits, dt, "logits", (rows, V))
+    if out is None:
+        out = logits
     op = lp if out is logits else _dev_ptr(ctx, out, dt, "out", (rows, V))
-    num_bias = int(bias_tokens.numel()) if bias_tokens is not None else 0
-    a = MTPLogitsArgs(
-        B, rows, _dev_ptr(ctx, row_offsets, i32, "row_offsets"), lp, op, _dev_ptr(ctx, counts, i32, "counts", (B, V)),
-        _dev_ptr(ctx, drafts, i32, "drafts", (B, None)), int(drafts.shape[1]) if drafts is not None else 0,
-        _dev_ptr(ctx, repetition, f32, "repetition", (B,)), _dev_ptr(ctx, frequency, f32, "frequency", (B,)),
-        _dev_ptr(ctx, presence, f32, "presence", (B,)), _dev_ptr(ctx, bias_offsets, i32, "bias_offsets", (B + 1,)),
-        _dev_ptr(ctx, bias_tokens, i32, "bias_tokens", (num_bias,)),
-        _dev_ptr(ctx, bias_values, f32, "bias_values", (num_bias,)), num_bias,
-        _dev_ptr(ctx, mask, i32, "mask", (None, (V + 31) // 32)), _dev_ptr(ctx, mask_index, i32, "mask_index", (rows,)),
-        int(mask.shape[0]) if mask is not None else 0)
+    a = MTPLogitsArgs(B, rows, _dev_ptr(ctx, row_offsets, i32, "row_offsets"), lp, op)
+    if counts is not None:
+        a.counts = _dev_ptr(ctx, counts, i32, "counts", (B, V))
+    if drafts is not None:
+        a.drafts_stride = drafts.shape[-1]
+        a.drafts = _dev_ptr(ctx, drafts, i32, "drafts", (B, a.drafts_stride))
+    one = (B,)
+    if repetition is not None:
+        a.repetition = _dev_ptr(ctx, repetition, f32, "repetition", one)
+    if frequency is not None:
+        a.frequency = _dev_ptr(ctx, frequency, f32, "frequency", one)
+    if presence is not None:
+        a.presence = _dev_ptr(ctx, presence, f32, "presence", one)
+    if bias_offsets is not None:
+        a.num_bias = n = bias_tokens.numel()
+        a.bias_offsets = _dev_ptr(ctx, bias_offsets, i32, "bias_offsets", (B + 1,))
+        a.bias_tokens = _dev_ptr(ctx, bias_tokens, i32, "bias_tokens", (n,))
+        a.bias_values = _dev_ptr(ctx, bias_values, f32, "bias_values", (n,))
+    if mask is not None:
+        a.num_masks = n = mask.shape[0]
+        a.mask = _dev_ptr(ctx, mask, i32, "mask", (n, (V + 31) // 32))
+        a.mask_index = _dev_ptr(ctx, mask_index, i32, "mask_index", (rows,))
     if rows == 0:
         return out
-    _check(_clib.mtp_logits_process(ctx.handle, _ctx_stream(ctx, stream), ctypes.byref(a)), "mtp_logits_process")
+    _check(_clib.mtp_logits_process(ctx.handle, _ctx_stream(ctx, stream), a), "mtp_logits_process")
     return out
 
 

@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       // Weights are 2^(s - r).  The reference r of a column stays while every
       // score is at most r + 15 (fp16 holds 2^15.9), so most steps need no
       // maximum across the lanes and no rescaling.  When one is above, r
-      // becomes 14 below the maximum, a whole number: fp16 then keeps 11 bits
-      // of weights down to 2^-28 of the largest.  (Beyond 2^20 that sum would
+      // becomes 9 below the maximum, a whole number: fp16 then keeps 11 bits
+      // of weights down to 2^-23 of the largest.  (Beyond 2^20 that sum would
       // round, and r is the maximum itself.)
       float fac[2][NT][2];
       bool above = false;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float ref = fabsf(mx) > 1048576.0f ? mx : ceilf(mx) - 14.0f;
+            const float ref = fabsf(mx) > 1048576.0f ? mx : ceilf(mx) - 9.0f;
             const float rn = fmaxf(m_run[nt][e], ref);
             alpha[e] = ex2(m_run[nt][e] - rn);
             m_run[nt][e] = rn;
