@@ -20,13 +20,13 @@
 // in registers, so no transposed copy of V exists anywhere.
 //
 // Work is split over the flattened sequence (request, kv head, tile, step of
-// 32 tokens): every thread block takes an equal contiguous share, whatever
+// 16 or 32 tokens): every thread block takes an equal contiguous share, whatever
 // the lengths are (they are only known on the device), so ragged batches and
 // a single long context both fill the machine.  Each warp streams every
 // fourth step of its block's share through its own ring of shared memory
 // (cp.async, 16 bytes a lane, swizzled so that the fragment reads are free of
 // bank conflicts).  A segment (request, kv head, tile) costs a start and an end
-// besides its steps, so it counts kA8Lead steps more.  Pieces of a segment
+// besides its steps, so it counts kLead steps more.  Pieces of a segment
 // that spans blocks meet in the workspace, and a second, small kernel joins
 // them in a fixed order: the joining of a long context (a piece from every
 // block) is spread over the machine, where the last block to arrive took
@@ -39,10 +39,8 @@ namespace mtp {
 
 constexpr int kA8Warps = 4;
 constexpr int kA8Threads = kA8Warps * 32;
-constexpr int kA8Step = 32;        // tokens of a step (two cache blocks)
 constexpr int kA8MaxB = 1024;      // requests of a call (prefix sums in shared memory)
-constexpr int kA8MinShare = 8;     // units of a thread block's share at least
-constexpr int kA8Lead = 4;         // units that a segment's start and end count for
+constexpr int kA8MinShare = 16;    // cache blocks of a thread block's share at least
 constexpr int kA8MaxCols = 32;     // columns of a tile
 constexpr float kA8Least = -3.4028235e38f;   // the reference of a column that has seen nothing
 
@@ -137,34 +135,47 @@ __device__ __forceinline__ uint32_t v_at(int r, int c) {
   return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4));
 }
 
-// Four consecutive elements, in one load where the alignment allows it.
-template <typename T> __device__ __forceinline__ void load_q4(const T* p, int vec, float (&x)[4]);
-template <> __device__ __forceinline__ void load_q4<float>(const float* p, int vec, float (&x)[4]) {
-  if (vec) {
-    const float4 y = *reinterpret_cast<const float4*>(p);
-    x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = p[e];
+// Four consecutive elements as loaded, in one load where the alignment allows
+// it, and later as floats (so that nothing waits for the load before then).
+template <typename T> struct Quad;
+template <> struct Quad<float> {
+  float4 w;
+  __device__ __forceinline__ void zero() { w = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void load(const float* p, int vec) {
+    if (vec) w = *reinterpret_cast<const float4*>(p);
+    else w = make_float4(p[0], p[1], p[2], p[3]);
   }
-}
-template <> __device__ __forceinline__ void load_q4<uint16_t>(const uint16_t* p, int vec, float (&x)[4]) {
-  if (vec) {
-    const uint2 y = *reinterpret_cast<const uint2*>(p);
-    x[0] = bf16_lo(y.x); x[1] = bf16_hi(y.x); x[2] = bf16_lo(y.y); x[3] = bf16_hi(y.y);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = Elem<uint16_t>::loads(p + e);
+  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w; }
+};
+template <> struct Quad<uint16_t> {
+  uint2 w;
+  __device__ __forceinline__ void zero() { w = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void load(const uint16_t* p, int vec) {
+    if (vec) w = *reinterpret_cast<const uint2*>(p);
+    else w = make_uint2((uint32_t)p[0] | ((uint32_t)p[1] << 16), (uint32_t)p[2] | ((uint32_t)p[3] << 16));
   }
-}
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+  }
+};
 
 template <int HD, int NT, int SPLIT>
 struct Attn8Shape {
-  static constexpr int kTile = kA8Step * HD;               // bytes of a staged K (or V) tile
-  static constexpr int kStage = 2 * kTile + 16;            // K, V, two scales each
+  // Cache blocks of a step.  Wide tiles have the registers for one (two spill
+  // at NT = 3 and 4: 16 x 6 rows 52.6 -> 50.1 us); one column tile gains
+  // from the longer softmax step.
+  static constexpr int JB = NT == 1 ? 2 : 1;
+  static constexpr int kStep = kBlk * JB;                  // tokens of a step
+  static constexpr int kTile = kStep * HD;                 // bytes of a staged K (or V) tile
+  static constexpr int kStage = 2 * kTile + 16;            // K, V, the blocks' scales
+  // units that a segment's start and end count for: its queries, the first
+  // stages' latency, the join of the warps.  8, 16, 24, 32 blocks for each
+  // (one 16 x 6 call: 49.9, 42.6, 38.1, 38.4 us; 8 x 61: 211, 167, 139, 127;
+  // 48: 115), so it grows with the width.
+  static constexpr int kLead = (16 + 8 * NT) / JB, kMinShare = kA8MinShare / JB;
   static constexpr int kBlocks = SPLIT == 1 && NT == 1 ? 3 : 2;   // thread blocks per SM (registers)
   // stages of a warp's ring: what the shared memory of an SM holds for them
-  static constexpr int kStages = kBlocks == 3 || (SPLIT == 2 && NT >= 3) ? 2 : 3;
+  static constexpr int kStages = (kBlocks == 3 || (SPLIT == 2 && NT >= 3) ? 2 : 3) * 2 / JB;
   static constexpr int kRing = kA8Warps * kStages * kStage;
   static constexpr int kCols = 8 * NT;
   static constexpr int kPitch = HD + 4;                    // floats of a merged row
@@ -208,11 +219,12 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
   using S = Attn8Shape<HD, NT, SPLIT>;
   constexpr int KS = HD / 16;                 // k-steps of Q K^T
   constexpr int MT = HD / 16;                 // m-tiles of V^T P^T
-  constexpr int STEP = kA8Step;
+  constexpr int STEP = S::kStep, JB = S::JB, PER = 32 / JB;   // PER: steps whose blocks a warp looks up at a time
   constexpr bool kQReg = NT * SPLIT <= 2;     // query fragments stay in registers
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int pre[kA8MaxB + 1];            // units before each request
   __shared__ long long wsum[kA8Warps];
+  __shared__ int piece_s[4];
   __shared__ float qfac_s[S::kCols];
   __shared__ float wm[kA8Warps][S::kCols], wl[kA8Warps][S::kCols];
 
@@ -233,6 +245,8 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
   };
   long long carry = 0;
   int bad = 0;
+  int my_o0 = 0, my_n = 0, my_len = 0;              // request tid of a batch of at most kA8Threads:
+  uint32_t my_first = 0, my_units = 0;              // its rows, length and units
   for (int b0 = 0; b0 < a.B; b0 += kA8Threads) {
     const int b = b0 + tid;
     long long units = 0;
@@ -241,12 +255,11 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       if (o0 < 0 || o1 < o0 || o1 > a.T) {
         bad = 1;
       } else if (o1 > o0) {
-        int oo, n, L;
-        if (request(b, oo, n, L)) {
-          const int tiles = (n * G + S::kCols - 1) / S::kCols;
-          units = (long long)((L + STEP - 1) / STEP + kA8Lead) * tiles * a.n_kv;
+        if (request(b, my_o0, my_n, my_len)) {
+          const int tiles = (my_n * G + S::kCols - 1) / S::kCols;
+          units = (long long)((my_len + STEP - 1) / STEP + S::kLead) * tiles * a.n_kv;
         } else if (blockIdx.x == 0) {
-          set_error(a.err, n <= a.max_rows && (long long)a.kv.seq_len[b] + a.kv.pending[b] > (long long)a.kv.max_blocks * kBlk
+          set_error(a.err, my_n <= a.max_rows && (long long)a.kv.seq_len[b] + a.kv.pending[b] > (long long)a.kv.max_blocks * kBlk
                                ? MTP_ERR_CAPACITY : MTP_ERR_DEVICE_ARGS);
         }
       }
@@ -266,6 +279,8 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       all += wsum[w];
     }
     if (b < a.B) pre[b + 1] = (int)(add + x);
+    my_first = (uint32_t)(add + x - units);
+    my_units = (uint32_t)units;
     carry += all;
     __syncthreads();
   }
@@ -283,7 +298,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
     return;
   }
   // units fit 31 bits, so the divisions below are 32-bit ones
-  const uint32_t units = (uint32_t)total, share = max((units + gridDim.x - 1) / gridDim.x, (uint32_t)kA8MinShare);
+  const uint32_t units = (uint32_t)total, share = max((units + gridDim.x - 1) / gridDim.x, (uint32_t)S::kMinShare);
   uint32_t u = min((unsigned long long)blockIdx.x * share, (unsigned long long)units);
   const uint32_t u_end = min(units - u, share) + u;
 
@@ -293,34 +308,53 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
 
   while (u < u_end) {
     // ---- the piece: request b, kv head g, tile, steps [s_lo, s_hi)
-    int b = 0;
-    {
+    int b, o0, n, L;
+    if (a.B <= kA8Threads) {
+      // the thread that holds the request says so
+      if (u - my_first < my_units) {
+        piece_s[0] = tid; piece_s[1] = my_o0; piece_s[2] = my_n; piece_s[3] = my_len;
+      }
+      __syncthreads();  // (the last piece's shared memory is free, too)
+      b = piece_s[0]; o0 = piece_s[1]; n = piece_s[2]; L = piece_s[3];
+    } else {
       int lo = 0, hi = a.B - 1;  // the request with pre[b] <= u < pre[b + 1]
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if ((uint32_t)pre[mid] <= u) lo = mid; else hi = mid - 1;
       }
       b = lo;
+      request(b, o0, n, L);
+      __syncthreads();
     }
-    int o0, n, L;
-    request(b, o0, n, L);
     const int base = L - n;
     const int steps = (L + STEP - 1) / STEP, tiles = (n * G + S::kCols - 1) / S::kCols;
-    const uint32_t seg = (u - (uint32_t)pre[b]) / (uint32_t)(steps + kA8Lead);
+    const uint32_t seg = (u - (uint32_t)pre[b]) / (uint32_t)(steps + S::kLead);
     const int g = (int)(seg / (uint32_t)tiles), tile = (int)seg - g * tiles;
-    const uint32_t seg_u0 = (uint32_t)pre[b] + seg * (uint32_t)(steps + kA8Lead) + kA8Lead;   // the segment's first step
+    const uint32_t seg_u0 = (uint32_t)pre[b] + seg * (uint32_t)(steps + S::kLead) + S::kLead;   // the segment's first step
     if (u_end <= seg_u0) break;   // the share ends before it
     const int s_lo = u > seg_u0 ? (int)(u - seg_u0) : 0, s_hi = min(steps, (int)(u_end - seg_u0));
     const int col0 = tile * S::kCols, ncols = min(S::kCols, n * G - col0);
 
+    // the queries' loads go first: behind the first stages' they would wait
+    // for all of those
+    const bool lane_on = lane < HD / 4;
+    Quad<T> xq[2 * NT];
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) {
+      const int c = warp + kA8Warps * k, cc = col0 + c;
+      xq[k].zero();
+      if (c < ncols && lane_on)
+        xq[k].load((const T*)a.q + (long long)(o0 + (cc >> a.g_shift)) * a.q_stride +
+                       ((long long)g * G + (cc & (G - 1))) * HD + lane * 4,
+                   a.q_vec);
+    }
     // ---- this warp's steps: s_lo + warp, + 4, ...
-    __syncthreads();  // the last piece's shared memory is free
     const int n_my = s_hi - s_lo > warp ? (s_hi - s_lo - warp + kA8Warps - 1) / kA8Warps : 0;
     const int32_t* trow = a.kv.block_table + (long long)b * a.kv.max_blocks;
-    // table entries of 16 steps at a time: lane 2 i + j holds block j of step i
+    // table entries of PER steps at a time: lane JB i + j holds block j of step i
     auto load_table = [&](int batch) -> int {
-      const int i = batch * 16 + (lane >> 1);
-      const int bi = 2 * (s_lo + warp + kA8Warps * i) + (lane & 1);
+      const int i = batch * PER + lane / JB;
+      const int bi = JB * (s_lo + warp + kA8Warps * i) + lane % JB;
       int id = -1;
       if (i < n_my && (long long)bi * kBlk < L) {
         id = trow[bi];
@@ -334,15 +368,15 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
     int tbl = -1, tnext = load_table(0);
     auto issue = [&](int i) {
       if (i < n_my) {
-        if ((i & 15) == 0) {
+        if (i % PER == 0) {
           tbl = tnext;
-          tnext = load_table((i >> 4) + 1);
+          tnext = load_table(i / PER + 1);
         }
         const int tok0 = (s_lo + warp + kA8Warps * i) * STEP;
         const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStage;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int id = __shfl_sync(0xffffffffu, tbl, 2 * (i & 15) + j);
+        for (int j = 0; j < JB; ++j) {
+          const int id = __shfl_sync(0xffffffffu, tbl, JB * (i % PER) + j);
           const long long t = (long long)max(id, 0) * a.n_kv + g;
           const unsigned char* kp = (const unsigned char*)a.kv.k_pool + t * (kBlk * HD);
           const unsigned char* vp = (const unsigned char*)a.kv.v_pool + t * (kBlk * HD);
@@ -353,7 +387,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
             cp16(st + k_at<HD>(16 * j + r, c), kp + idx * 16, bytes);
             cp16(st + S::kTile + v_at<HD>(16 * j + r, c), vp + idx * 16, bytes);
           }
-          if (lane < 2) cp4(st + 2 * S::kTile + (lane * 2 + j) * 4, (lane ? a.kv.v_scale : a.kv.k_scale) + t, id >= 0 ? 4 : 0);
+          if (lane < 2) cp4(st + 2 * S::kTile + (lane * JB + j) * 4, (lane ? a.kv.v_scale : a.kv.k_scale) + t, id >= 0 ? 4 : 0);
         }
       }
       cp_commit();
@@ -363,22 +397,11 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
 
     // ---- queries: per column a power of two that brings them into fp16's
     // range, then fragments in the order the lanes read them
-    const bool lane_on = lane < HD / 4;
-    float xq[2 * NT][4];
-#pragma unroll
-    for (int k = 0; k < 2 * NT; ++k) {
-      const int c = warp + kA8Warps * k, cc = col0 + c;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) xq[k][e] = 0.0f;
-      if (c < ncols && lane_on)
-        load_q4<T>((const T*)a.q + (long long)(o0 + (cc >> a.g_shift)) * a.q_stride +
-                       ((long long)g * G + (cc & (G - 1))) * HD + lane * 4,
-                   a.q_vec, xq[k]);
-    }
 #pragma unroll
     for (int k = 0; k < 2 * NT; ++k) {
       const int c = warp + kA8Warps * k;
-      const float (&x)[4] = xq[k];
+      float x[4];
+      xq[k].get(x);
       float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
       m = warp_max(m);
       int sh = 0;  // largest element to [2^14, 2^15)
@@ -447,9 +470,9 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       const int tok0 = (s_lo + warp + kA8Warps * it) * STEP;
       const bool edge = tok0 + STEP > base;   // some tokens are not seen by every column
       // ---- scores
-      float sc[2][NT][4];
+      float sc[JB][NT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < JB; ++j) {
 #pragma unroll
         for (int hh = 0; hh < HD / 64; ++hh) {
           const uint4 lo = lds128(st + k_at<HD>(16 * j + gi, hh * 4 + ti));
@@ -477,26 +500,30 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
           }
         }
       }
-      // ---- online softmax over the step's 32 tokens
-      const float ks0 = lds32f(st + 2 * S::kTile), ks1 = lds32f(st + 2 * S::kTile + 4);
-      const float vs0 = lds32f(st + 2 * S::kTile + 8), vs1 = lds32f(st + 2 * S::kTile + 12);
+      // ---- online softmax over the step's tokens
+      float kscale[JB], vscale[JB];
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        kscale[j] = lds32f(st + 2 * S::kTile + 4 * j);
+        vscale[j] = lds32f(st + 2 * S::kTile + 4 * (JB + j));
+      }
       // Weights are 2^(s - r).  The reference r of a column stays while every
       // score is at most r + 15 (fp16 holds 2^15.9), so most steps need no
       // maximum across the lanes and no rescaling.  When one is above, r
       // becomes 9 below the maximum, a whole number: fp16 then keeps 11 bits
       // of weights down to 2^-23 of the largest.  (Beyond 2^20 that sum would
       // round, and r is the maximum itself.)
-      float fac[2][NT][2];
+      float fac[JB][NT][2];
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < JB; ++j) {
             // a zero scale stands for zero entries: a factor above zero keeps
             // -inf * f from becoming NaN
-            const float f = fmaxf((j ? ks1 : ks0) * qfac[nt][e], 1e-37f);
+            const float f = fmaxf(kscale[j] * qfac[nt][e], 1e-37f);
             fac[j][nt][e] = f;
             if (edge) {
 #pragma unroll
@@ -513,8 +540,8 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]) * fac[0][nt][e],
-                             fmaxf(sc[1][nt][e], sc[1][nt][2 + e]) * fac[1][nt][e]);
+            float mx = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]) * fac[0][nt][e];
+            if constexpr (JB == 2) mx = fmaxf(mx, fmaxf(sc[JB - 1][nt][e], sc[JB - 1][nt][2 + e]) * fac[JB - 1][nt][e]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -538,7 +565,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < JB; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float p = ex2(fmaf(sc[j][nt][2 * h + e], fac[j][nt][e], -m_run[nt][e]));
@@ -547,7 +574,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
             }
       // ---- values
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < JB; ++j) {
         uint32_t pb[SPLIT][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -612,7 +639,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
             }
           }
         }
-        const float vs = j ? vs1 : vs0;
+        const float vs = vscale[j];
 #pragma unroll
         for (int w = 0; w < WD; ++w) {
           const uint32_t p01 = __byte_perm(v[0][w], v[1][w], 0x5140), q01 = __byte_perm(v[0][w], v[1][w], 0x7362);
