@@ -592,8 +592,8 @@ size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx);
  * contiguous, dtype; lse [T, n_q] float32 or NULL: the natural logarithm of
  * the softmax sum.  Sums, maxima and products are held in float32.
  *   max_rows: at least every n_b (1..256); mask_words >= ceil(max_rows / 32)
- * with a mask.  scale: finite, > 0.  Rows outside row_offsets are left as
- * they were.  Device errors: MTP_ERR_DEVICE_ARGS (bad offsets, n_b >
+ * with a mask.  scale: finite, > 0.  B: at most 1024.  Rows outside
+ * row_offsets are left as they were.  Device errors: MTP_ERR_DEVICE_ARGS (bad offsets, n_b >
  * max_rows, base_b < 0), MTP_ERR_CAPACITY (more entries than max_blocks
  * blocks hold): that request's rows are left as they were; a block id outside
  * the pool sets MTP_ERR_CAPACITY and its entries count as zeros.
@@ -629,7 +629,8 @@ typedef struct {
   int num_rows;                /* rows of logits and out                       */
   const int32_t* row_offsets;  /* [B + 1]                                      */
   const void* logits;          /* [num_rows, vocab], dtype                     */
-  void* out;                   /* [num_rows, vocab], dtype; may be logits      */
+  void* out;                   /* [num_rows, vocab], dtype; may be logits, but
+                                  not overlap them otherwise                   */
   const int32_t* counts;       /* [B, vocab] (mtp_token_counts_add), or NULL   */
   const int32_t* drafts;       /* [B, drafts_stride] or NULL; needs counts     */
   int drafts_stride;           /* n_b - 1 <= drafts_stride with drafts         */

@@ -18,7 +18,7 @@ struct Append8Args {
   const void* v;
   const void* q;
   void* q_out;
-  long long k_stride, v_stride, q_stride, q_out_stride;
+  long long k_stride, v_stride, q_stride, q_out_stride, q_extent;
   const int32_t* row_offsets;
   const int32_t* positions;
   mtp_kv8 kv;
@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     const int G = 1 << a.g_shift, rows = s1 - s0;
     const T* q0 = (const T*)a.q + (long long)r0 * a.q_stride + (long long)g * G * HD;
     T* w0 = (T*)a.q_out + (long long)r0 * a.q_out_stride + (long long)g * G * HD;
+    auto q_at = [&](int r, int h) -> long long { return (long long)(r0 + r) * a.q_out_stride + ((long long)g * G + h) * HD; };
+    (void)q_at;   // bounds-checked builds only
     if (a.q_vec) {
       // a thread owns 8 pairs (or 8 elements past the rotated part) of a
       // row and walks over heads; few rows share the heads among threads
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         if (un >= turning) {
           const int e = rd + 8 * (un - turning);
           for (int h = h0; h < G; h += hs) {
+            if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + e + 7, a.q_extent)) continue;
             float y[8];
             load_n<T, 8>(qr + h * HD + e, y);
             store_8(wr + h * HD + e, y);
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
               y[2 * e + 1] = p[2 * e + 1] * cs[e].x + p[2 * e] * cs[e].y;
             }
           }
+          if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + xb + 7, a.q_extent)) continue;
           store_8(wr + h * HD + xa, y);
           store_8(wr + h * HD + xb, y + 8);
         }
@@ -306,6 +310,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         float2 c = make_float2(0.0f, 0.0f);
         if (turn) c = rope_cos_sin(a.positions[r0 + r], tab.turns[pe], tab.magnitude);
         for (int h = 0; h < G; ++h) {
+          if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + ib, a.q_extent)) continue;
           if (turn) {
             const float x = get1<T>(qr + h * HD + ia), y = get1<T>(qr + h * HD + ib);
             Elem<T>::store1(wr + h * HD + ia, x * c.x - y * c.y);
@@ -563,6 +568,7 @@ mtp_status mtp_kv8_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_
   a.v_stride = v_stride;
   a.q_stride = q_stride;
   a.q_out_stride = q_out_stride;
+  a.q_extent = (int64_t)(T - 1) * q_out_stride + qw;
   a.row_offsets = row_offsets;
   a.positions = positions;
   a.kv = *kv;

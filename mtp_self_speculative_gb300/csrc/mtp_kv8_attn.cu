@@ -710,7 +710,9 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       if (whole) {
         attn8_finish<T, HD>(a, o0, col0 + c, g, d4, x, M, Ls);
       } else {
-        float* pr = a.part + ((2ll * blockIdx.x + slot) * kA8MaxCols + c) * (HD + 4);
+        const long long at = ((2ll * blockIdx.x + slot) * kA8MaxCols + c) * (HD + 4);
+        if (!MTP_IN_BOUNDS(a.err, at + HD + 1, 2ll * gridDim.x * kA8MaxCols * (HD + 4))) continue;
+        float* pr = a.part + at;
         *reinterpret_cast<float4*>(pr + d4 * 4) = x;
         if (d4 == 0) *reinterpret_cast<float2*>(pr + HD) = make_float2(M, Ls);
       }

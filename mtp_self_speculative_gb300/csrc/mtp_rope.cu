@@ -18,7 +18,8 @@ struct RopeArgs {
   const void* x;
   void* out;
   const int32_t* positions;
-  long long x_stride, out_stride;
+  int* err;
+  long long x_stride, out_stride, out_extent;   // elements; the extent for bounds-checked builds
   int T, heads, hd;
   int rot_units, units;   // rotating units of a head, and those with the copied ones
   int heads_per_block;
@@ -73,7 +74,8 @@ __global__ void __launch_bounds__(128) rope_vec_kernel(const RopeArgs a, const _
     const int e = tab.rotary_dim + (u - a.rot_units) * N;
 #pragma unroll 4
     for (int h = h0; h < h1; ++h)
-      *reinterpret_cast<uint4*>(o + h * a.hd + e) = *reinterpret_cast<const uint4*>(x + h * a.hd + e);
+      if (MTP_IN_BOUNDS(a.err, (long long)t * a.out_stride + h * a.hd + e + N - 1, a.out_extent))
+        *reinterpret_cast<uint4*>(o + h * a.hd + e) = *reinterpret_cast<const uint4*>(x + h * a.hd + e);
     return;
   }
   const int pos = a.positions[t];
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(128) rope_vec_kernel(const RopeArgs a, const _
       r[ia] = p[ia] * cs[i].x - p[ib] * cs[i].y;
       r[ib] = p[ib] * cs[i].x + p[ia] * cs[i].y;
     }
+    if (!MTP_IN_BOUNDS(a.err, (long long)t * a.out_stride + h * a.hd + eb + N - 1, a.out_extent)) continue;
     rope_store(o + h * a.hd + ea, r);
     rope_store(o + h * a.hd + eb, r + N);
   }
@@ -112,7 +115,8 @@ __global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a, const __gri
   T* o = (T*)a.out + (long long)t * a.out_stride;
   if (u >= a.rot_units) {  // an element past the rotated part
     const int e = tab.rotary_dim + (u - a.rot_units);
-    for (int h = h0; h < h1; ++h) o[h * a.hd + e] = x[h * a.hd + e];
+    for (int h = h0; h < h1; ++h)
+      if (MTP_IN_BOUNDS(a.err, (long long)t * a.out_stride + h * a.hd + e, a.out_extent)) o[h * a.hd + e] = x[h * a.hd + e];
     return;
   }
   const float2 cs = rope_cos_sin(a.positions[t], tab.turns[u], tab.magnitude);
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a, const __gri
   const int ib = tab.layout == MTP_ROPE_HALF ? u + tab.rotary_dim / 2 : 2 * u + 1;
   for (int h = h0; h < h1; ++h) {
     const float p = rope_get<T>(x + h * a.hd + ia), q = rope_get<T>(x + h * a.hd + ib);
+    if (!MTP_IN_BOUNDS(a.err, (long long)t * a.out_stride + h * a.hd + ib, a.out_extent)) continue;
     Elem<T>::store1(o + h * a.hd + ia, p * cs.x - q * cs.y);
     Elem<T>::store1(o + h * a.hd + ib, q * cs.x + p * cs.y);
   }
@@ -229,6 +234,8 @@ mtp_status mtp_rope(mtp_ctx* ctx, void* stream, int T, int heads, const void* x,
   a.x = x;
   a.out = out;
   a.positions = positions;
+  a.err = ctx->err;
+  a.out_extent = (int64_t)(T - 1) * out_stride + row;
   a.x_stride = x_stride;
   a.out_stride = out_stride;
   a.T = T;
