@@ -534,9 +534,10 @@ typedef struct {
  * Values that are not finite are stored as NaN and do not count in max|x|.
  *   row_offsets [B+1] int32, ascending from >= 0 to <= T; rows outside are not
  * read.  Device errors: MTP_ERR_DEVICE_ARGS for bad offsets or lengths,
- * MTP_ERR_CAPACITY for slots beyond max_blocks (the request is then left as
- * it was) or a block id outside the pool (that block is skipped).  T = 0 is a
- * no-op.  Host errors: B outside 1..max_batch, T < 0, strides below the row,
+ * MTP_ERR_CAPACITY for slots beyond max_blocks (the request's cache is then
+ * left as it was) or a block id outside the pool (that block is skipped);
+ * with bad offsets the call does nothing, else q is rotated whatever becomes
+ * of the cache.  T = 0 is a no-op.  Host errors: B outside 1..max_batch, T < 0, strides below the row,
  * NULL pointers. */
 mtp_status mtp_kv8_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, const void* k,
                           int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,

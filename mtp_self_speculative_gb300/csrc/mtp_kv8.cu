@@ -77,8 +77,99 @@ __device__ __forceinline__ uint32_t e4m3_pack4(const float* x, float inv) {
          (e4m3_pack2(e4m3_in(x[2], inv), e4m3_in(x[3], inv)) << 16);
 }
 
-// Thread block (unit, kv head): the unit's new rows of k and v, and of the
-// head's queries.  16 (HD = 128) or 8 threads share a row, each with 8
+// The queries of 16 rows and one kv head's group: they need the rows' offsets
+// (which rows there are) and positions, but nothing of the cache.
+template <typename T, int HD>
+__device__ __forceinline__ void append_queries(const Append8Args& a, const mtp_rope_table& tab, int u, int g) {
+  const int G = 1 << a.g_shift, tid = threadIdx.x;
+  int bad = 0;
+  for (int b = tid; b < a.B; b += kAppendThreads) {
+    const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1];
+    bad |= o0 < 0 || o1 < o0 || o1 > a.T;
+  }
+  const int r0 = max(16 * u, a.row_offsets[0]), rows = min(16 * u + 16, a.row_offsets[a.B]) - r0;
+  if (__syncthreads_or(bad) || rows <= 0) return;   // (the cache's thread blocks report it)
+  const int rd = tab.rotary_dim;
+  const T* q0 = (const T*)a.q + (long long)r0 * a.q_stride + (long long)g * G * HD;
+  T* w0 = (T*)a.q_out + (long long)r0 * a.q_out_stride + (long long)g * G * HD;
+  auto q_at = [&](int r, int h) -> long long { return (long long)(r0 + r) * a.q_out_stride + ((long long)g * G + h) * HD; };
+  (void)q_at;   // bounds-checked builds only
+  if (a.q_vec) {
+    // a thread owns 8 pairs (or 8 elements past the rotated part) of a
+    // row and walks over heads; few rows share the heads among threads
+    const int turning = rd / 16, units = turning + (a.q == a.q_out ? 0 : (HD - rd) / 8);
+    int hs = 1;
+    while (hs < G && 2 * hs * rows * units <= kAppendThreads) hs *= 2;
+    for (int i = tid; i < rows * units * hs; i += kAppendThreads) {
+      const int h0 = i % hs, x = i / hs, r = x / units, un = x - r * units;
+      const T* qr = q0 + (long long)r * a.q_stride;
+      T* wr = w0 + (long long)r * a.q_out_stride;
+      if (un >= turning) {
+        const int e = rd + 8 * (un - turning);
+        for (int h = h0; h < G; h += hs) {
+          if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + e + 7, a.q_extent)) continue;
+          float y[8];
+          load_n<T, 8>(qr + h * HD + e, y);
+          store_8(wr + h * HD + e, y);
+        }
+        continue;
+      }
+      const bool hf = tab.layout == MTP_ROPE_HALF;
+      const int xa = hf ? 8 * un : 16 * un, xb = hf ? 8 * un + rd / 2 : 16 * un + 8;
+      const int pos = a.positions[r0 + r];
+      float2 cs[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cs[e] = rope_cos_sin(pos, tab.turns[8 * un + e], tab.magnitude);
+      for (int h = h0; h < G; h += hs) {
+        float p[16], y[16];
+        load_n<T, 8>(qr + h * HD + xa, p);
+        load_n<T, 8>(qr + h * HD + xb, p + 8);
+        if (hf) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y[e] = p[e] * cs[e].x - p[8 + e] * cs[e].y;
+            y[8 + e] = p[8 + e] * cs[e].x + p[e] * cs[e].y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y[2 * e] = p[2 * e] * cs[e].x - p[2 * e + 1] * cs[e].y;
+            y[2 * e + 1] = p[2 * e + 1] * cs[e].x + p[2 * e] * cs[e].y;
+          }
+        }
+        if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + xb + 7, a.q_extent)) continue;
+        store_8(wr + h * HD + xa, y);
+        store_8(wr + h * HD + xb, y + 8);
+      }
+    }
+  } else {
+    for (int i = tid; i < rows * (HD / 2); i += kAppendThreads) {
+      const int r = i / (HD / 2), pe = i - r * (HD / 2);
+      const T* qr = q0 + (long long)r * a.q_stride;
+      T* wr = w0 + (long long)r * a.q_out_stride;
+      const bool turn = pe < rd / 2, hf = turn && tab.layout == MTP_ROPE_HALF;
+      const int ia = hf ? pe : 2 * pe, ib = hf ? pe + rd / 2 : 2 * pe + 1;
+      float2 c = make_float2(0.0f, 0.0f);
+      if (turn) c = rope_cos_sin(a.positions[r0 + r], tab.turns[pe], tab.magnitude);
+      for (int h = 0; h < G; ++h) {
+        if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + ib, a.q_extent)) continue;
+        if (turn) {
+          const float x = get1<T>(qr + h * HD + ia), y = get1<T>(qr + h * HD + ib);
+          Elem<T>::store1(wr + h * HD + ia, x * c.x - y * c.y);
+          Elem<T>::store1(wr + h * HD + ib, y * c.x + x * c.y);
+        } else if (a.q != a.q_out) {
+          wr[h * HD + ia] = qr[h * HD + ia];
+          wr[h * HD + ib] = qr[h * HD + ib];
+        }
+      }
+    }
+  }
+}
+
+// Thread block (unit, kv head, 0): the unit's new rows of k and v; (16 rows, kv
+// head, 1): the head's queries, in blocks of their own so that neither waits
+// for the other (one after the other: 11.6 and 29.9 us for 32 x 6 rows and four
+// prompts).  16 (HD = 128) or 8 threads share a row, each with 8
 // elements: two fours half the rotated part apart (half layout, aligned) or
 // eight next to one another, so that a thread has both members of its pairs,
 // computes their cosine once, and nothing goes through shared memory but the
@@ -97,6 +188,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   pdl_trigger();
   const int u = blockIdx.x, g = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.z == 1) {
+    append_queries<T, HD>(a, tab, u, g);
+    return;
+  }
   // ---- the unit's request; every thread checks some of the offsets
   if (tid == 0) sh[0] = -1;
   __syncthreads();
@@ -243,84 +338,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         *(uint32_t*)(row + (w ? 8 * e8 + 4 : eb)) = e4m3_pack4(x + 4, inv);
       }
       if (tid == 0) (w ? a.kv.v_scale : a.kv.k_scale)[t] = now;
-    }
-  }
-  // ---- the head's queries
-  if (a.q) {
-    const int G = 1 << a.g_shift, rows = s1 - s0;
-    const T* q0 = (const T*)a.q + (long long)r0 * a.q_stride + (long long)g * G * HD;
-    T* w0 = (T*)a.q_out + (long long)r0 * a.q_out_stride + (long long)g * G * HD;
-    auto q_at = [&](int r, int h) -> long long { return (long long)(r0 + r) * a.q_out_stride + ((long long)g * G + h) * HD; };
-    (void)q_at;   // bounds-checked builds only
-    if (a.q_vec) {
-      // a thread owns 8 pairs (or 8 elements past the rotated part) of a
-      // row and walks over heads; few rows share the heads among threads
-      const int turning = rd / 16, units = turning + (a.q == a.q_out ? 0 : (HD - rd) / 8);
-      int hs = 1;
-      while (hs < G && 2 * hs * rows * units <= kAppendThreads) hs *= 2;
-      for (int i = tid; i < rows * units * hs; i += kAppendThreads) {
-        const int h0 = i % hs, x = i / hs, r = x / units, un = x - r * units;
-        const T* qr = q0 + (long long)r * a.q_stride;
-        T* wr = w0 + (long long)r * a.q_out_stride;
-        if (un >= turning) {
-          const int e = rd + 8 * (un - turning);
-          for (int h = h0; h < G; h += hs) {
-            if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + e + 7, a.q_extent)) continue;
-            float y[8];
-            load_n<T, 8>(qr + h * HD + e, y);
-            store_8(wr + h * HD + e, y);
-          }
-          continue;
-        }
-        const bool hf = tab.layout == MTP_ROPE_HALF;
-        const int xa = hf ? 8 * un : 16 * un, xb = hf ? 8 * un + rd / 2 : 16 * un + 8;
-        const int pos = a.positions[r0 + r];
-        float2 cs[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) cs[e] = rope_cos_sin(pos, tab.turns[8 * un + e], tab.magnitude);
-        for (int h = h0; h < G; h += hs) {
-          float p[16], y[16];
-          load_n<T, 8>(qr + h * HD + xa, p);
-          load_n<T, 8>(qr + h * HD + xb, p + 8);
-          if (hf) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              y[e] = p[e] * cs[e].x - p[8 + e] * cs[e].y;
-              y[8 + e] = p[8 + e] * cs[e].x + p[e] * cs[e].y;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              y[2 * e] = p[2 * e] * cs[e].x - p[2 * e + 1] * cs[e].y;
-              y[2 * e + 1] = p[2 * e + 1] * cs[e].x + p[2 * e] * cs[e].y;
-            }
-          }
-          if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + xb + 7, a.q_extent)) continue;
-          store_8(wr + h * HD + xa, y);
-          store_8(wr + h * HD + xb, y + 8);
-        }
-      }
-    } else {
-      for (int i = tid; i < rows * (HD / 2); i += kAppendThreads) {
-        const int r = i / (HD / 2), pe = i - r * (HD / 2);
-        const T* qr = q0 + (long long)r * a.q_stride;
-        T* wr = w0 + (long long)r * a.q_out_stride;
-        const bool turn = pe < rd / 2, hf = turn && tab.layout == MTP_ROPE_HALF;
-        const int ia = hf ? pe : 2 * pe, ib = hf ? pe + rd / 2 : 2 * pe + 1;
-        float2 c = make_float2(0.0f, 0.0f);
-        if (turn) c = rope_cos_sin(a.positions[r0 + r], tab.turns[pe], tab.magnitude);
-        for (int h = 0; h < G; ++h) {
-          if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + ib, a.q_extent)) continue;
-          if (turn) {
-            const float x = get1<T>(qr + h * HD + ia), y = get1<T>(qr + h * HD + ib);
-            Elem<T>::store1(wr + h * HD + ia, x * c.x - y * c.y);
-            Elem<T>::store1(wr + h * HD + ib, y * c.x + x * c.y);
-          } else if (a.q != a.q_out) {
-            wr[h * HD + ia] = qr[h * HD + ia];
-            wr[h * HD + ib] = qr[h * HD + ib];
-          }
-        }
-      }
     }
   }
   // the last of the request's thread blocks publishes the new length: all
@@ -587,7 +604,7 @@ mtp_status mtp_kv8_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_
           tab.rotary_dim % 8 == 0;
   a.q_vec = !(((uintptr_t)q | (uintptr_t)q_out) & 15) && q_stride % per16 == 0 && q_out_stride % per16 == 0 &&
             tab.rotary_dim % 16 == 0;
-  const dim3 grid(T / 16 + 2 * B, c.n_kv_heads), block(kAppendThreads);
+  const dim3 grid(T / 16 + 2 * B, c.n_kv_heads, q ? 2 : 1), block(kAppendThreads);
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e =
       c.head_dim == 128 ? (bf ? launch_pdl(kv8_append_kernel<uint16_t, 128>, grid, block, 0, s, a, tab)
