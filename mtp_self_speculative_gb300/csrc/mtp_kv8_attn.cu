@@ -53,7 +53,8 @@ struct Attn8Args {
   mtp_kv8 kv;
   int* err;
   float* part;     // [2 * grid][32][HD + 4]: o, then reference and sum
-  int4* meta;      // [2 * grid]: the segment that begins in a block and goes on in others
+  int4* meta;      // [2 * grid]: what the join kernel joins, per segment (by_segment) or per first block
+  int by_segment, max_tiles, tile_cols;   // few segments: the join kernel has a block for each; tiles of max_rows rows
   long long q_stride;
   int B, T, max_rows, mask_words, n_kv, g_shift;
   float qscale;    // scale * log2(e)
@@ -185,6 +186,17 @@ struct Attn8Shape {
   static constexpr int kBytes = kMain + kQ;
 };
 
+// Request b's first row, rows and entries; false if the call leaves it out.
+__device__ __forceinline__ bool attn8_request(const Attn8Args& a, int b, int& o0, int& n, int& L) {
+  o0 = a.row_offsets[b];
+  const int o1 = a.row_offsets[b + 1], sl = a.kv.seq_len[b], pe = a.kv.pending[b];
+  n = o1 - o0;
+  const long long len = (long long)sl + pe;
+  L = (int)len;
+  return o0 >= 0 && o1 <= a.T && n > 0 && n <= a.max_rows && sl >= 0 && pe >= 0 && len >= n &&
+         len <= min((long long)a.kv.max_blocks * kBlk, 1ll << 30);
+}
+
 // Write four elements of a column's result and its lse.
 template <typename T, int HD>
 __device__ __forceinline__ void attn8_finish(const Attn8Args& a, int o0, int col, int g, int d4, float4 x, float ref,
@@ -234,15 +246,6 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
   const int G = 1 << a.g_shift;
 
   // ---- the call's work: units (steps) before each request
-  auto request = [&](int b, int& o0, int& n, int& L) -> bool {
-    o0 = a.row_offsets[b];
-    const int o1 = a.row_offsets[b + 1], sl = a.kv.seq_len[b], pe = a.kv.pending[b];
-    n = o1 - o0;
-    const long long len = (long long)sl + pe;
-    L = (int)len;
-    return n > 0 && n <= a.max_rows && sl >= 0 && pe >= 0 && len >= n &&
-           len <= min((long long)a.kv.max_blocks * kBlk, 1ll << 30);
-  };
   long long carry = 0;
   int bad = 0;
   int my_o0 = 0, my_n = 0, my_len = 0;              // request tid of a batch of at most kA8Threads:
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
       if (o0 < 0 || o1 < o0 || o1 > a.T) {
         bad = 1;
       } else if (o1 > o0) {
-        if (request(b, my_o0, my_n, my_len)) {
+        if (attn8_request(a, b, my_o0, my_n, my_len)) {
           const int tiles = (my_n * G + S::kCols - 1) / S::kCols;
           units = (long long)((my_len + STEP - 1) / STEP + S::kLead) * tiles * a.n_kv;
         } else if (blockIdx.x == 0) {
@@ -286,15 +289,15 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
   }
   if (tid == 0) {
     pre[0] = 0;
-    a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!a.by_segment) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0 && blockIdx.x == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
-    return;
-  }
+  const bool refused = __syncthreads_or(bad);
   const long long total = carry;
-  if (total > INT32_MAX) {  // more steps than a call can count (16 TB of cache read)
-    if (tid == 0 && blockIdx.x == 0) set_error(a.err, MTP_ERR_CAPACITY);
+  if (refused || total > INT32_MAX) {  // (or more steps than a call can count: 16 TB of cache read)
+    if (tid == 0) {
+      a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);   // nothing to join, whichever way it looks
+      if (blockIdx.x == 0) set_error(a.err, refused ? MTP_ERR_DEVICE_ARGS : MTP_ERR_CAPACITY);
+    }
     return;
   }
   // units fit 31 bits, so the divisions below are 32-bit ones
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
         if ((uint32_t)pre[mid] <= u) lo = mid; else hi = mid - 1;
       }
       b = lo;
-      request(b, o0, n, L);
+      attn8_request(a, b, o0, n, L);
       __syncthreads();
     }
     const int base = L - n;
@@ -717,53 +720,70 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4
         if (d4 == 0) *reinterpret_cast<float2*>(pr + HD) = make_float2(M, Ls);
       }
     }
-    if (tid == 0 && !whole && slot == 1) {
-      a.meta[2 * blockIdx.x + 1] = make_int4(o0, col0, ncols, g);
-      a.meta[2 * blockIdx.x] = make_int4((int)(c_last - c_first + 1), 0, 0, 0);
+    if (tid == 0 && slot == 1 && (a.by_segment || !whole)) {
+      int4* m = a.meta + 2 * (a.by_segment ? (b * a.n_kv + g) * a.max_tiles + tile : (int)blockIdx.x);
+      m[0] = make_int4(whole ? 0 : (int)(c_last - c_first + 1), (int)c_first, ncols, g);
+      m[1] = make_int4(o0, col0, 0, 0);
     }
     u = seg_u0 + (uint32_t)s_hi;
   }
 }
 
-// Joins the pieces of the segment that begins in thread block blockIdx.x of
-// the first kernel.  A thread owns four elements of a column, or shares them
-// with `ways - 1` others where there are many pieces; block (x, y) takes the
-// y-th group of columns and every gridDim.y-th after it.
+// Joins the pieces of segments that span thread blocks.  Where a call has
+// fewer segments than the first kernel has blocks, block x takes segment x;
+// else the one that begins in the first kernel's block x.  A thread owns four
+// elements of a column, or shares them with `ways - 1` others where there are
+// many pieces; block (x, y) takes the y-th group of columns and every
+// gridDim.y-th after it.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinAhead = 8;   // pieces in flight per thread
+constexpr int kJoinAhead = 4;   // pieces in flight per thread
+// Threads that share an element's pieces.
+__host__ __device__ __forceinline__ int join_ways(int count) {
+  return count <= kJoinAhead ? 1 : count <= 2 * kJoinAhead ? 2 : count <= 4 * kJoinAhead ? 4 : 8;
+}
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8Args a) {
   __shared__ float4 xs[kJoinThreads];
   __shared__ float2 ms[kJoinThreads];
+  if (a.by_segment) {
+    // a request that the call leaves out has written nothing; its rows and
+    // lengths do not change during the call
+    const int b = blockIdx.x / (a.n_kv * a.max_tiles), tile = blockIdx.x % a.max_tiles;
+    int o0, n, L;
+    if (!attn8_request(a, b, o0, n, L) || tile * a.tile_cols >= n << a.g_shift) return;
+  }
   pdl_wait();
   pdl_trigger();
-  const int c_first = blockIdx.x, count = a.meta[2 * c_first].x;
+  const int4 seg = a.meta[2 * blockIdx.x], at = a.meta[2 * blockIdx.x + 1];
+  const int count = seg.x, c_first = seg.y, ncols = seg.z;
   if (count == 0) return;
-  const int4 seg = a.meta[2 * c_first + 1];
-  const int ways = count <= kJoinAhead ? 1 : 4;
+  const int ways = join_ways(count);
+  static_assert(kJoinThreads / 8 >= HD / 4, "a block must hold a column at least, or the loop below stands still");
   const int items = kJoinThreads / ways, cols = items / (HD / 4);
   const int item = threadIdx.x % items, way = threadIdx.x / items;
   const int d4 = item % (HD / 4);
-  for (int c0 = cols * blockIdx.y; c0 < seg.z; c0 += cols * gridDim.y) {
+  for (int c0 = cols * blockIdx.y; c0 < ncols; c0 += cols * gridDim.y) {
     const int c = c0 + item / (HD / 4);
     float M = kA8Least, Ls = 0.0f;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < seg.z) {
+    if (c < ncols) {
       for (int k0 = way; k0 < count; k0 += kJoinAhead * ways) {
         float2 ml[kJoinAhead];
         float4 y[kJoinAhead];
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {
-          const int kk = k0 + k * ways;
-          ml[k] = make_float2(kA8Least, 0.0f);
-          y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (kk < count) {
-            const float* pr = a.part + ((2ll * (c_first + kk) + (kk == 0 ? 1 : 0)) * kA8MaxCols + c) * (HD + 4);
-            ml[k] = __ldcg(reinterpret_cast<const float2*>(pr + HD));
-            y[k] = __ldcg(reinterpret_cast<const float4*>(pr) + d4);
-          }
+        for (int k = 0; k < kJoinAhead; ++k) {   // no branches: all loads go out together
+          const int kk = min(k0 + k * ways, count - 1);
+          const float* pr = a.part + ((2ll * (c_first + kk) + (kk == 0 ? 1 : 0)) * kA8MaxCols + c) * (HD + 4);
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(pr + HD));
+          y[k] = __ldcg(reinterpret_cast<const float4*>(pr) + d4);
         }
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+          if (k0 + k * ways >= count) {
+            ml[k] = make_float2(kA8Least, 0.0f);
+            y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) attn8_take(M, Ls, x, ml[k].x, ml[k].y, y[k]);
       }
@@ -776,7 +796,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8
       for (int w = 1; way == 0 && w < ways; ++w)
         attn8_take(M, Ls, x, ms[w * items + item].x, ms[w * items + item].y, xs[w * items + item]);
     }
-    if (way == 0 && c < seg.z) attn8_finish<T, HD>(a, seg.x, seg.y + c, seg.w, d4, x, M, Ls);
+    if (way == 0 && c < ncols) attn8_finish<T, HD>(a, at.x, at.y + c, seg.w, d4, x, M, Ls);
   }
 }
 
@@ -785,21 +805,24 @@ constexpr int kA8MaxBlocks = 3;
 static size_t a8_meta_bytes(const mtp_ctx* ctx) { return (size_t)kA8MaxBlocks * ctx->num_sms * 2 * sizeof(int4); }
 
 template <typename T, int HD, int NT>
-static cudaError_t attn8_launch(mtp_ctx* ctx, cudaStream_t s, const Attn8Args& a) {
+static cudaError_t attn8_launch(mtp_ctx* ctx, cudaStream_t s, Attn8Args a) {
   using S = Attn8Shape<HD, NT, sizeof(T) == 4 ? 2 : 1>;
   static_assert(S::kBlocks <= kA8MaxBlocks, "workspace");
   cudaError_t e = ensure_smem((const void*)kv8_attn_kernel<T, HD, NT>, S::kBytes);
   if (e != cudaSuccess) return e;
   const int grid = S::kBlocks * ctx->num_sms;
+  const int cols = a.max_rows << a.g_shift;   // of the longest request
+  a.tile_cols = S::kCols;
+  a.max_tiles = (cols + S::kCols - 1) / S::kCols;
+  const long long segments = (long long)a.B * a.n_kv * a.max_tiles;
+  a.by_segment = segments <= grid;
   e = launch_pdl(kv8_attn_kernel<T, HD, NT>, dim3(grid), dim3(kA8Threads), S::kBytes, s, a);
   if (e != cudaSuccess) return e;
-  // few segments have many pieces each, and the join takes 64 / (HD / 4)
-  // columns at a time; many segments have a few, and it takes 256 / (HD / 4)
-  const int cols = min(S::kCols, a.max_rows << a.g_shift);
-  const long long tiles = ((long long)a.max_rows << a.g_shift) / S::kCols + 1;
-  const int per = (long long)a.B * a.n_kv * tiles * kJoinAhead < grid ? 64 / (HD / 4) : 256 / (HD / 4);
-  const int gy = (cols + per - 1) / per;
-  return launch_pdl(kv8_attn_join_kernel<T, HD>, dim3(grid, gy), dim3(kJoinThreads), 0, s, a);
+  // columns that a block joins at a time, for twice the average of pieces
+  const int even = kJoinThreads / join_ways((int)(2 * grid / segments + 1)) / (HD / 4), per = even > 1 ? even : 1;
+  const int gy = ((cols < S::kCols ? cols : S::kCols) + per - 1) / per;
+  return launch_pdl(kv8_attn_join_kernel<T, HD>, dim3(a.by_segment ? (unsigned)segments : (unsigned)grid, gy),
+                    dim3(kJoinThreads), 0, s, a);
 }
 
 template <typename T, int HD>
