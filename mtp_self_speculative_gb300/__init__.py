@@ -508,14 +508,19 @@ class KVCache8:
         return self._checked_struct(ctx)[0]
 
     def _checked_struct(self, ctx: Context):
-        """(struct, B, n_q, n_kv, head_dim); the checks run again when a field
-        or the context's configuration has become another one."""
-        ptrs = (ctx.cfg, self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.k_scale.data_ptr(),
-                self.v_scale.data_ptr(), self.block_table.data_ptr(), self.seq_len.data_ptr(),
-                self.pending.data_ptr(), self.arrive.data_ptr(), self.k_pool.shape, self.block_table.shape)
+        """(struct, B, n_q, n_kv, head_dim).  The checks run again when a field
+        is another tensor, a tensor has other storage, or the context has
+        another configuration."""
+        kp, vp, ks, vs, bt, sl, pe, ar = fields = (self.k_pool, self.v_pool, self.k_scale, self.v_scale,
+                                                   self.block_table, self.seq_len, self.pending, self.arrive)
+        ptrs = (kp.data_ptr(), vp.data_ptr(), ks.data_ptr(), vs.data_ptr(), bt.data_ptr(), sl.data_ptr(),
+                pe.data_ptr(), ar.data_ptr())
         done = self.__dict__.get("_checked")
-        if done is not None and done[0] == ptrs:
-            return done[1]
+        if done is not None and done[0] == ptrs and done[3] is ctx.cfg:
+            f = done[1]
+            if (f[0] is kp and f[1] is vp and f[2] is ks and f[3] is vs and f[4] is bt and f[5] is sl and f[6] is pe
+                    and f[7] is ar):
+                return done[2]
         c = ctx.cfg
         nb, B = int(self.k_pool.shape[0]), int(self.seq_len.shape[0])
         if self.block_table.dim() != 2:
@@ -532,7 +537,7 @@ class KVCache8:
                     _dev_ptr(ctx, self.pending, i32, "pending", (B,)),
                     _dev_ptr(ctx, self.arrive, i32, "arrive", (B,)), nb, int(self.block_table.shape[1]))
         got = (st, B, int(c.n_q_heads), int(c.n_kv_heads), int(c.head_dim))
-        self.__dict__["_checked"] = (ptrs, got)
+        self.__dict__["_checked"] = (ptrs, fields, got, c)
         return got
 
 

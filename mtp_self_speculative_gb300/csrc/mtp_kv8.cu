@@ -127,14 +127,14 @@ __device__ __forceinline__ void append_queries(const Append8Args& a, const mtp_r
         if (hf) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            y[e] = p[e] * cs[e].x - p[8 + e] * cs[e].y;
-            y[8 + e] = p[8 + e] * cs[e].x + p[e] * cs[e].y;
+            y[e] = rope_first(p[e], p[8 + e], cs[e]);
+            y[8 + e] = rope_second(p[e], p[8 + e], cs[e]);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            y[2 * e] = p[2 * e] * cs[e].x - p[2 * e + 1] * cs[e].y;
-            y[2 * e + 1] = p[2 * e + 1] * cs[e].x + p[2 * e] * cs[e].y;
+            y[2 * e] = rope_first(p[2 * e], p[2 * e + 1], cs[e]);
+            y[2 * e + 1] = rope_second(p[2 * e], p[2 * e + 1], cs[e]);
           }
         }
         if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + xb + 7, a.q_extent)) continue;
@@ -155,8 +155,8 @@ __device__ __forceinline__ void append_queries(const Append8Args& a, const mtp_r
         if (!MTP_IN_BOUNDS(a.err, q_at(r, h) + ib, a.q_extent)) continue;
         if (turn) {
           const float x = get1<T>(qr + h * HD + ia), y = get1<T>(qr + h * HD + ib);
-          Elem<T>::store1(wr + h * HD + ia, x * c.x - y * c.y);
-          Elem<T>::store1(wr + h * HD + ib, y * c.x + x * c.y);
+          Elem<T>::store1(wr + h * HD + ia, rope_first(x, y, c));
+          Elem<T>::store1(wr + h * HD + ib, rope_second(x, y, c));
         } else if (a.q != a.q_out) {
           wr[h * HD + ia] = qr[h * HD + ia];
           wr[h * HD + ib] = qr[h * HD + ib];
@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         for (int e = 0; e < 4; ++e) {
           const float2 c = rope_cos_sin(pos, tab.turns[ea + e], tab.magnitude);
           const float x = kx[j][e], y = kx[j][4 + e];
-          kx[j][e] = x * c.x - y * c.y;
-          kx[j][4 + e] = y * c.x + x * c.y;
+          kx[j][e] = rope_first(x, y, c);
+          kx[j][4 + e] = rope_second(x, y, c);
         }
       } else if (tab.layout == MTP_ROPE_INTERLEAVED) {   // a pair lies within a thread's eight
 #pragma unroll
@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
           if (8 * e8 + e >= rd) continue;
           const float2 c = rope_cos_sin(pos, tab.turns[4 * e8 + e / 2], tab.magnitude);
           const float x = kx[j][e], y = kx[j][e + 1];
-          kx[j][e] = x * c.x - y * c.y;
-          kx[j][e + 1] = y * c.x + x * c.y;
+          kx[j][e] = rope_first(x, y, c);
+          kx[j][e + 1] = rope_second(x, y, c);
         }
       } else if (!a.vec) {                               // halves that do not fall on fours: partners one by one
         const T* kr = (const T*)a.k + (long long)(r0 + i) * a.k_stride + g * HD;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
           const bool low = d < rd / 2;
           const float2 c = rope_cos_sin(pos, tab.turns[low ? d : d - rd / 2], tab.magnitude);
           const float y = get1<T>(kr + (low ? d + rd / 2 : d - rd / 2));
-          kx[j][e] = low ? kx[j][e] * c.x - y * c.y : kx[j][e] * c.x + y * c.y;
+          kx[j][e] = low ? rope_first(kx[j][e], y, c) : rope_second(y, kx[j][e], c);
         }
       }
     }

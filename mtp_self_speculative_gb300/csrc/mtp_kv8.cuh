@@ -119,6 +119,11 @@ __device__ __forceinline__ bool arrive_last(int* arrive, int total) {
   return true;
 }
 
+// The rotated pair, rounded in one way wherever it is computed (the result
+// does not depend on the rows' alignment).
+__device__ __forceinline__ float rope_first(float a, float b, float2 c) { return fmaf(a, c.x, -__fmul_rn(b, c.y)); }
+__device__ __forceinline__ float rope_second(float a, float b, float2 c) { return fmaf(b, c.x, __fmul_rn(a, c.y)); }
+
 // Host check of a rotary table against a head width.
 inline bool rope_table_ok(const mtp_rope_table* r, int head_dim) {
   return r && (r->layout == MTP_ROPE_HALF || r->layout == MTP_ROPE_INTERLEAVED) && r->rotary_dim >= 2 &&

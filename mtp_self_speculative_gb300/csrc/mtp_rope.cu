@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(128) rope_vec_kernel(const RopeArgs a, const _
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int ia = LAYOUT == MTP_ROPE_HALF ? i : 2 * i, ib = LAYOUT == MTP_ROPE_HALF ? i + N : 2 * i + 1;
-      r[ia] = p[ia] * cs[i].x - p[ib] * cs[i].y;
-      r[ib] = p[ib] * cs[i].x + p[ia] * cs[i].y;
+      r[ia] = rope_first(p[ia], p[ib], cs[i]);
+      r[ib] = rope_second(p[ia], p[ib], cs[i]);
     }
     if (!MTP_IN_BOUNDS(a.err, (long long)t * a.out_stride + h * a.hd + eb + N - 1, a.out_extent)) continue;
     rope_store(o + h * a.hd + ea, r);
@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a, const __gri
   for (int h = h0; h < h1; ++h) {
     const float p = rope_get<T>(x + h * a.hd + ia), q = rope_get<T>(x + h * a.hd + ib);
     if (!MTP_IN_BOUNDS(a.err, (long long)t * a.out_stride + h * a.hd + ib, a.out_extent)) continue;
-    Elem<T>::store1(o + h * a.hd + ia, p * cs.x - q * cs.y);
-    Elem<T>::store1(o + h * a.hd + ib, q * cs.x + p * cs.y);
+    Elem<T>::store1(o + h * a.hd + ia, rope_first(p, q, cs));
+    Elem<T>::store1(o + h * a.hd + ib, rope_second(p, q, cs));
   }
 }
 

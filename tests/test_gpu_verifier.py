@@ -683,6 +683,103 @@ def test_pools_beyond_two_gigabytes():
     clean(ctx)
 
 
+def test_a_reused_workspace_carries_nothing_over():
+    """A call that split its segments, then calls that leave requests (or everything) out, on one workspace."""
+    M = M_()
+    rng = np.random.default_rng(61)
+    ctx = context(8, 2, 128, "bf16", max_batch=3)
+    kv, twin = filled(ctx, [2500, 40, 1800], [2, 2, 2], rng)
+    ws = M.Attention8Workspace(ctx)
+    q, q64 = normal(rng, (6, 8, 128), "bf16")
+    off = np.array([0, 2, 4, 6])
+    got, lse = attend(ctx, kv, q, off, 2, ws=ws)
+    compare_attention(ctx, twin, q64, off, got, lse, "bf16")
+    for bad in ([0, 5, 4, 6], [0, 2, 4, 7]):
+        out = torch.full((6, 8, 128), 5.0, device="cuda").bfloat16()
+        M.mtp_kv8_attention(ctx, kv, q, i32(bad), out, ws, 2)
+        assert M.mtp_get_device_error(ctx) == M.MTP_ERR_DEVICE_ARGS and bool((out == 5).all())
+    # requests 0 and 2 have no rows this time; request 1's are its last two entries as before
+    some = np.array([3, 3, 5, 5])
+    got, lse = attend(ctx, kv, q, some, 2, ws=ws)
+    compare_attention(ctx, twin, q64, some, got, lse, "bf16")
+    kv.pending[2] = -1                      # request 2 is left out, the others are served
+    out = torch.full((6, 8, 128), 5.0, device="cuda").bfloat16()
+    M.mtp_kv8_attention(ctx, kv, q, i32(off), out, ws, 2)
+    assert M.mtp_get_device_error(ctx) == M.MTP_ERR_DEVICE_ARGS
+    assert bool((out[4:] == 5).all()) and bool((out[:4] != 5).any(-1).all())
+
+
+def test_batches_above_the_limit_are_refused():
+    M = M_()
+    ctx = context(1, 1, 64, "bf16", max_batch=1025)
+    kv = M.KVCache8.empty(ctx, 1, i32(np.zeros((1025, 1))))
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(M.MTPError):
+        M.mtp_kv8_attention(ctx, kv, q, i32(np.zeros(1026)), torch.empty_like(q), M.Attention8Workspace(ctx), 1)
+    clean(ctx)
+
+
+def test_commit_of_the_pending_counts_themselves():
+    """n_keep may be the cache's own pending array (keep everything)."""
+    M = M_()
+    rng = np.random.default_rng(62)
+    ctx = context(8, 8, 64, "bf16", max_batch=3)
+    kv, twin = make_cache(ctx, 3, 4, rng)
+    for _ in range(3):
+        append_both(ctx, kv, twin, [5, 17, 0], rng)
+        M.mtp_kv8_commit(ctx, kv, kv.pending)
+        for b, n in enumerate([5, 17, 0]):
+            twin.commit(b, n)
+        check_cache(ctx, kv, twin)
+    clean(ctx)
+
+
+@pytest.mark.parametrize("dtype,hd,layout", [("bf16", 128, "half"), ("f32", 64, "interleaved"), ("bf16", 64, "half")])
+@pytest.mark.parametrize("shift", [1, 4])
+def test_append_of_unaligned_rows(dtype, hd, layout, shift):
+    """k, v and q as slices that start off a 16-byte boundary, against the same values in aligned tensors."""
+    M = M_()
+    rng = np.random.default_rng(shift + hd)
+    ctx = context(4, 2, hd, dtype, max_batch=2)
+    off, pos, tab = i32([0, 19, 22]), i32(rng.integers(0, 5000, 22)), M.RopeTable(hd, layout=layout)
+    wide, _ = normal(rng, (22, shift + 8 * hd + 3), dtype)
+    q, k, v = (wide[:, shift + a * hd:shift + e * hd].unflatten(1, (e - a, hd)) for a, e in ((0, 4), (4, 6), (6, 8)))
+    got = []
+    for parts in ((q, k, v), tuple(t.contiguous() for t in (q, k, v))):
+        kv, _ = make_cache(ctx, 2, 3, np.random.default_rng(1))
+        out = torch.empty(22, 4, hd, dtype=TORCH[dtype], device="cuda")
+        M.mtp_kv8_append(ctx, kv, parts[1], parts[2], off, q=parts[0], q_out=out, positions=pos, rope=tab)
+        got.append((out, kv.k_pool.clone(), kv.v_pool.clone(), kv.k_scale.clone(), kv.v_scale.clone(), kv.pending.clone()))
+    clean(ctx)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_rows_beyond_two_giga_elements():
+    """Rotation and logits in the last rows of tensors of more than 2^31 elements."""
+    M = M_()
+    rng = np.random.default_rng(63)
+    ctx = context(2, 2, 128, "bf16")
+    wide = torch.zeros(70000, 32768, dtype=torch.bfloat16, device="cuda")
+    x = wide[:, -256:].unflatten(1, (2, 128))
+    part, p64 = normal(rng, (5, 2, 128), "bf16")
+    x[-5:] = part
+    pos = np.arange(70000) % 9001
+    M.mtp_rope(ctx, x, i32(pos), M.RopeTable(128))
+    want = V.rope(p64, pos[-5:])
+    close(host(x[-5:]), want, rope_tol(p64, want, "bf16"), "rope")
+    assert not wide[:, :-256].any() and not wide[:-5].any()
+    del wide, x
+    V_ = 151936
+    ctx = context(vocab=V_, dtype="bf16", max_batch=1)
+    z = torch.zeros(14500, V_, dtype=torch.bfloat16, device="cuda")
+    z[-2:, -3:] = 1.0
+    M.mtp_logits_process(ctx, z, i32([14498, 14500]), bias_offsets=i32([0, 1]), bias_tokens=i32([V_ - 1]),
+                         bias_values=torch.tensor([2.0], device="cuda"))
+    assert z[-2:, -3:].tolist() == [[1.0, 1.0, 3.0]] * 2 and not z[:-2].any() and not z[-2:, :-3].any()
+    clean(ctx)
+
+
 # ------------------------------------------------------------------ logits
 
 def logits_case(rng, B, V_, dtype, rows, penalties=True, drafts=True, bias=0, masks=0):
