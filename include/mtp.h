@@ -603,6 +603,19 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
                              const void* q, int64_t q_stride, const mtp_kv8* kv, const int32_t* mask, int mask_words,
                              float scale, void* out, float* lse, void* ws, size_t ws_bytes);
 
+/* mtp_draft on an 8-bit cache of the head: the same steps, arguments and
+ * checks (pending[b] == 0 on entry, K afterwards; rotary, dtype and kernels of
+ * the projections as there), the cache's entries quantized as in
+ * mtp_kv8_append from keys and values of the context's dtype.  Commit or roll
+ * back with mtp_kv8_commit_accepted and the others.  B: at most 1024; the
+ * persistent kernel is not used.  ws: mtp_draft_kv8_workspace_bytes(ctx) bytes
+ * (0 for a NULL context or one without weights), 256-byte aligned, not
+ * initialised, one per call that may run at the same time. */
+size_t mtp_draft_kv8_workspace_bytes(const mtp_ctx* ctx);
+mtp_status mtp_draft_kv8(mtp_ctx* ctx, void* stream, int B, const void* hidden, const void* embeds,
+                         const int32_t* positions, const mtp_kv8* kv, int K, const int32_t* chain_ids,
+                         int32_t* draft_ids, float* logits, float* hidden_out, void* ws, size_t ws_bytes);
+
 /* Add tokens to the per-request counts [B, vocab] int32: tokens[b * stride +
  * i], i < n_tokens[b].  in_prompt = 0: the token's count grows by one for
  * each time it is named; 1: its top bit (bit 31: the token occurs in the

@@ -652,6 +652,38 @@ def mtp_kv8_attention(ctx: Context, kv: KVCache8, q: torch.Tensor, row_offsets: 
                                    ws.bytes), "mtp_kv8_attention")
 
 
+class Draft8Workspace:
+    """Scratch of mtp_draft_kv8; calls that may run at the same time need one
+    each."""
+
+    def __init__(self, ctx: Context):
+        n = int(_clib.mtp_draft_kv8_workspace_bytes(ctx.handle))
+        if n == 0:
+            raise MTPError(MTP_ERR_INVALID, "mtp_draft_kv8_workspace_bytes")
+        self.device, self.bytes = ctx.device, n
+        self.ws = torch.empty(n, dtype=torch.uint8, device="cuda:%d" % ctx.device)
+        self.ptr = self.ws.data_ptr()
+
+
+def mtp_draft_kv8(ctx: Context, hidden: torch.Tensor, embeds: torch.Tensor, positions: torch.Tensor, kv: KVCache8,
+                  K: int, draft_ids: torch.Tensor, ws: Draft8Workspace, logits: Optional[torch.Tensor] = None,
+                  hidden_out: Optional[torch.Tensor] = None, chain_ids: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """mtp_draft with the head's cache in 8 bits."""
+    st, B = kv._checked_struct(ctx)[:2]
+    H, V, dt, i32, f32 = int(ctx.cfg.hidden), ctx.vocab, ctx.dtype, torch.int32, torch.float32
+    if ws.device != ctx.device:
+        raise ValueError("the workspace belongs to cuda:%s" % ws.device)
+    _check(_clib.mtp_draft_kv8(ctx.handle, _ctx_stream(ctx, stream), B, _dev_ptr(ctx, hidden, dt, "hidden", (B, H)),
+                               _dev_ptr(ctx, embeds, dt, "embeds", (B, H)),
+                               _dev_ptr(ctx, positions, i32, "positions", (B,)), st, int(K),
+                               _dev_ptr(ctx, chain_ids, i32, "chain_ids", (B, K - 1)),
+                               _dev_ptr(ctx, draft_ids, i32, "draft_ids", (B, K)),
+                               _dev_ptr(ctx, logits, f32, "logits", (B, K, V)),
+                               _dev_ptr(ctx, hidden_out, f32, "hidden_out", (B, H)), ws.ptr, ws.bytes),
+           "mtp_draft_kv8")
+
+
 def mtp_token_counts_add(ctx: Context, counts: torch.Tensor, tokens: torch.Tensor, n_tokens: torch.Tensor,
                          in_prompt: bool = False, stream=None) -> None:
     """Count tokens[b, :n_tokens[b]] in counts [B, vocab] int32 (in_prompt:

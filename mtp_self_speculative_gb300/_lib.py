@@ -138,6 +138,9 @@ SIGNATURES = {
     "mtp_kv8_attention_workspace_bytes": (c_size_t, [c_void_p]),
     "mtp_kv8_attention": (c_int, [c_void_p, c_void_p, c_int, c_int, P_i32, c_int, c_void_p, c_int64, P_kv8, P_i32,
                                   c_int, c_float, c_void_p, c_void_p, c_void_p, c_size_t]),
+    "mtp_draft_kv8_workspace_bytes": (c_size_t, [c_void_p]),
+    "mtp_draft_kv8": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, P_i32, P_kv8, c_int, P_i32, P_i32,
+                              c_void_p, c_void_p, c_void_p, c_size_t]),
     "mtp_token_counts_add": (c_int, [c_void_p, c_void_p, c_int, P_i32, c_int, P_i32, c_int, P_i32]),
     "mtp_logits_process": (c_int, [c_void_p, c_void_p, ctypes.POINTER(MTPLogitsArgs)]),
     "mtp_selftest_wait_timeout": (c_int, [c_void_p, c_void_p, c_int]),

@@ -866,6 +866,11 @@ static cudaError_t attention_t(mtp_ctx* ctx, cudaStream_t s, int B, int k, const
 
 cudaError_t launch_attention(mtp_ctx* ctx, cudaStream_t s, int B, int k, const mtp_kv* kv) {
   prof_before(ctx, MTP_KERNEL_ATTENTION, s);
+  if (ctx->kv8_draft) {
+    const cudaError_t e8 = launch_attention_kv8(ctx, s, B, k);
+    prof_after(ctx, MTP_KERNEL_ATTENTION, s);
+    return e8;
+  }
   cudaError_t e = (ctx->cfg.dtype == MTP_DTYPE_BF16) ? attention_t<uint16_t>(ctx, s, B, k, kv)
                                                      : attention_t<float>(ctx, s, B, k, kv);
   prof_after(ctx, MTP_KERNEL_ATTENTION, s);

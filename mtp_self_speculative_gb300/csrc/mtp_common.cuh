@@ -309,6 +309,7 @@ struct mtp_ctx {
   uint16_t* qw_s8;               // fp16 row scales [V]
   uint16_t* qw_s8_lm;            // LM-head row scales (== qw_s8 when tied)
   float qw_lm_sigma;             // power-of-two input scale of the LM head's fp16 operand
+  const void* kv8_draft;         // mtp::Kv8Draft of the mtp_draft_kv8 call being enqueued, else null
   int p_nslots[3];               // launch plan per batch width 1, 2, 4 (0 = not yet made)
   int p_warps[3];
   size_t p_smem[3];
@@ -345,6 +346,9 @@ cudaError_t launch_draft_step(mtp_ctx* ctx, cudaStream_t s, int B, int k, int K,
                               const void* embeds, const int32_t* positions, const mtp_kv* kv,
                               const int32_t* chain_ids, int32_t* draft_ids, float* logits, float* hidden_out);
 cudaError_t launch_attention(mtp_ctx* ctx, cudaStream_t s, int B, int k, const mtp_kv* kv);
+// The attention of a draft step on an 8-bit cache (mtp_draft_kv8): the staged
+// entry into the cache, then attention over it.
+cudaError_t launch_attention_kv8(mtp_ctx* ctx, cudaStream_t s, int B, int k);
 cudaError_t launch_draft_step_q(mtp_ctx* ctx, cudaStream_t s, int B, int k, int K, const void* hidden,
                                 const void* embeds, const int32_t* positions, const mtp_kv* kv,
                                 const int32_t* chain_ids, int32_t* draft_ids, float* logits, float* hidden_out);

@@ -47,6 +47,7 @@ constexpr float kA8Least = -3.4028235e38f;   // the reference of a column that h
 struct Attn8Args {
   const void* q;
   void* out;
+  uint16_t* out_bf16;   // a bf16 copy of float32 results, or null
   float* lse;
   const int32_t* row_offsets;
   const int32_t* mask;
@@ -210,6 +211,10 @@ __device__ __forceinline__ void attn8_finish(const Attn8Args& a, int o0, int col
   Elem<T>::store1(op + 1, x.y * inv);
   Elem<T>::store1(op + 2, x.z * inv);
   Elem<T>::store1(op + 3, x.w * inv);
+  if (sizeof(T) == 4 && a.out_bf16)
+    *reinterpret_cast<uint2*>(a.out_bf16 + row * HD + d4 * 4) =
+        make_uint2((uint32_t)f32_to_bf16_rne(x.x * inv) | ((uint32_t)f32_to_bf16_rne(x.y * inv) << 16),
+                   (uint32_t)f32_to_bf16_rne(x.z * inv) | ((uint32_t)f32_to_bf16_rne(x.w * inv) << 16));
   if (a.lse && d4 == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
@@ -835,11 +840,198 @@ static cudaError_t attn8_pick(mtp_ctx* ctx, cudaStream_t s, const Attn8Args& a, 
   }
 }
 
+// Fills in what follows from the context and the queries' type, and launches.
+static cudaError_t attn8_run(mtp_ctx* ctx, cudaStream_t s, Attn8Args& a, bool bf16, float scale) {
+  const mtp_config& c = ctx->cfg;
+  a.n_kv = c.n_kv_heads;
+  const int G = c.n_q_heads / c.n_kv_heads;
+  for (a.g_shift = 0; (1 << a.g_shift) < G; ++a.g_shift) {
+  }
+  a.qscale = scale * 1.4426950408889634f;
+  const size_t q4 = 4 * (bf16 ? 2 : 4);
+  a.q_vec = (uintptr_t)a.q % q4 == 0 && a.q_stride % 4 == 0;
+  // columns per tile: the fewest tiles of at most 32 columns, evenly filled
+  const int cols = a.max_rows * G, tiles = (cols + kA8MaxCols - 1) / kA8MaxCols;
+  const int nt = (cols + 8 * tiles - 1) / (8 * tiles);
+  return c.head_dim == 128 ? (bf16 ? attn8_pick<uint16_t, 128>(ctx, s, a, nt) : attn8_pick<float, 128>(ctx, s, a, nt))
+                           : (bf16 ? attn8_pick<uint16_t, 64>(ctx, s, a, nt) : attn8_pick<float, 64>(ctx, s, a, nt));
+}
+
+// --------------------------------------------- draft steps on an 8-bit cache
+//
+// The draft step's projection kernels write a step's key and value rows where
+// they are told the cache is.  For an 8-bit cache that is a staging area of
+// the call's workspace (a cache of max_k slots a request that starts empty);
+// the kernel below quantizes the step's row into the request's real slot, and
+// the attention above runs on the context's float32 queries.
+struct Kv8Draft {
+  mtp_kv8 kv;
+  mtp_kv stage;
+  const int32_t* row_offsets;   // 0, 1, .. B
+  void* attn_ws;
+};
+
+__global__ void __launch_bounds__(128) kv8_stage_kernel(int B, int blocks, int32_t* table, int32_t* seq_len,
+                                                        int32_t* pending, int32_t* offsets,
+                                                        const int32_t* kv_pending) {
+  pdl_wait();
+  pdl_trigger();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i <= B; i += gridDim.x * blockDim.x) {
+    offsets[i] = i;
+    if (i == B) break;
+    for (int j = 0; j < blocks; ++j) table[i * blocks + j] = i * blocks + j;
+    seq_len[i] = 0;
+    // a request with pending entries is refused by the first step's check
+    pending[i] = kv_pending[i] != 0;
+  }
+}
+
+// Thread block (kv head, request): warp 0 the key, warp 1 the value row of
+// step k.
+template <typename T, int HD>
+__global__ void __launch_bounds__(64) kv8_stage_append_kernel(mtp_kv8 kv, mtp_kv stage, const int* req_bad, int* err,
+                                                              int n_kv, int k) {
+  constexpr int DPL = HD / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.x, b = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (__ldcg(req_bad + b)) return;
+  const long long slot = (long long)kv.seq_len[b] + k - 1;
+  if (slot < k - 1 || slot >= (long long)kv.max_blocks * kBlk) {
+    if (threadIdx.x == 0) set_error(err, slot < k - 1 ? MTP_ERR_DEVICE_ARGS : MTP_ERR_CAPACITY);
+    return;
+  }
+  if (g == 0 && threadIdx.x == 0) kv.pending[b] = k;
+  const int blk = kv.block_table[(long long)b * kv.max_blocks + (slot >> 4)], off = (int)(slot & 15);
+  if (blk < 0 || blk >= kv.num_blocks) {
+    if (threadIdx.x == 0) set_error(err, MTP_ERR_CAPACITY);
+    return;
+  }
+  const long long st = ((long long)b * stage.max_blocks + ((k - 1) >> 4)) * n_kv + g;
+  const T* src = (const T*)(w ? stage.v_pool : stage.k_pool) + (st * kBlk + ((k - 1) & 15)) * HD + lane * DPL;
+  float x[DPL], amax = 0.0f;
+#pragma unroll
+  for (int e = 0; e < DPL; ++e) {
+    x[e] = Elem<T>::loads(src + e);
+    if (finite_f(x[e])) amax = fmaxf(amax, fabsf(x[e]));
+  }
+  const long long t = (long long)blk * n_kv + g;
+  float* scale = (w ? kv.v_scale : kv.k_scale) + t;
+  uint8_t* tile = (uint8_t*)(w ? kv.v_pool : kv.k_pool) + t * (kBlk * HD);
+  const float was = off > 0 ? *scale : 0.0f, now = fmaxf(was, e4m3_scale(warp_max(amax)));
+  const float inv = now > 0.0f ? 1.0f / now : 0.0f;
+  if (was > 0.0f && now > was) {
+    for (int i = lane; i < off * (HD / 2); i += 32) {
+      uint16_t* p = (uint16_t*)tile + i;
+      const float2 y = e4m3_to_float2(*p);
+      *p = (uint16_t)e4m3_pack2(y.x * (was * inv), y.y * (was * inv));
+    }
+  }
+  if (!MTP_IN_BOUNDS(err, t * (kBlk * HD) + off * HD + HD - 1, (long long)kv.num_blocks * n_kv * kBlk * HD)) return;
+#pragma unroll
+  for (int e = 0; e < DPL; e += 2)
+    *(uint16_t*)(tile + off * HD + lane * DPL + e) = (uint16_t)e4m3_pack2(e4m3_in(x[e], inv), e4m3_in(x[e + 1], inv));
+  __syncwarp();   // all lanes have read the old scale
+  if (lane == 0) *scale = now;
+}
+
+cudaError_t launch_attention_kv8(mtp_ctx* ctx, cudaStream_t s, int B, int k) {
+  const Kv8Draft& d = *(const Kv8Draft*)ctx->kv8_draft;
+  const mtp_config& c = ctx->cfg;
+  const dim3 grid(c.n_kv_heads, B), block(64);
+  const bool bf = c.dtype == MTP_DTYPE_BF16;
+  cudaError_t e =
+      c.head_dim == 128
+          ? (bf ? launch_pdl(kv8_stage_append_kernel<uint16_t, 128>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k)
+                : launch_pdl(kv8_stage_append_kernel<float, 128>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k))
+          : (bf ? launch_pdl(kv8_stage_append_kernel<uint16_t, 64>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k)
+                : launch_pdl(kv8_stage_append_kernel<float, 64>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k));
+  if (e != cudaSuccess) return e;
+  Attn8Args a{};
+  a.q = ctx->q;
+  a.out = ctx->attn;
+  a.out_bf16 = tc_supported(ctx, B) ? ctx->tc_attn : nullptr;
+  a.row_offsets = d.row_offsets;
+  a.kv = d.kv;
+  a.err = ctx->err;
+  a.meta = (int4*)d.attn_ws;
+  a.part = (float*)((char*)d.attn_ws + a8_meta_bytes(ctx));
+  a.q_stride = ctx->q_dim;
+  a.B = B;
+  a.T = B;
+  a.max_rows = 1;
+  ctx->launches += 3;
+  return attn8_run(ctx, s, a, false, 1.0f / sqrtf((float)c.head_dim));
+}
+
+// Workspace of a draft call: the attention's, then the staging cache.
+struct DraftLayout {
+  size_t attn, k, v, table, seq_len, pending, offsets, bytes;
+  int blocks;
+};
+static DraftLayout draft_layout(const mtp_ctx* ctx) {
+  const mtp_config& c = ctx->cfg;
+  DraftLayout L{};
+  L.blocks = (c.max_k + kBlk - 1) / kBlk;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = (off + bytes + 255) & ~(size_t)255;
+    return o;
+  };
+  const size_t entries = (size_t)c.max_batch * L.blocks, pool = entries * kBlk * ctx->kv_dim * (c.dtype == MTP_DTYPE_BF16 ? 2 : 4);
+  L.attn = take(mtp_kv8_attention_workspace_bytes(ctx));
+  L.k = take(pool);
+  L.v = take(pool);
+  L.table = take(entries * 4);
+  L.seq_len = take((size_t)c.max_batch * 4);
+  L.pending = take((size_t)c.max_batch * 4);
+  L.offsets = take(((size_t)c.max_batch + 1) * 4);
+  L.bytes = off;
+  return L;
+}
+
 }  // namespace mtp
 
 using namespace mtp;
 
 extern "C" {
+
+size_t mtp_draft_kv8_workspace_bytes(const mtp_ctx* ctx) { return ctx && ctx->has_weights ? draft_layout(ctx).bytes : 0; }
+
+mtp_status mtp_draft_kv8(mtp_ctx* ctx, void* stream, int B, const void* hidden, const void* embeds,
+                         const int32_t* positions, const mtp_kv8* kv, int K, const int32_t* chain_ids,
+                         int32_t* draft_ids, float* logits, float* hidden_out, void* ws, size_t ws_bytes) {
+  if (!ctx || !ctx->has_weights) return MTP_ERR_INVALID;
+  if (B < 1 || B > ctx->cfg.max_batch || B > kA8MaxB || K < 1 || K > ctx->cfg.max_k) return MTP_ERR_INVALID;
+  if (!hidden || !embeds || !positions || !draft_ids || !kv8_ok(kv)) return MTP_ERR_INVALID;
+  const DraftLayout L = draft_layout(ctx);
+  if (!ws || ((uintptr_t)ws & 255) || ws_bytes < L.bytes) return MTP_ERR_INVALID;
+  DeviceGuard dev(ctx->device);
+  if (!dev.ok) return MTP_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* base = (char*)ws;
+  Kv8Draft d{};
+  d.kv = *kv;
+  d.stage.k_pool = base + L.k;
+  d.stage.v_pool = base + L.v;
+  d.stage.block_table = (int32_t*)(base + L.table);
+  d.stage.seq_len = (int32_t*)(base + L.seq_len);
+  d.stage.pending = (int32_t*)(base + L.pending);
+  d.stage.num_blocks = ctx->cfg.max_batch * L.blocks;
+  d.stage.max_blocks = L.blocks;
+  d.row_offsets = (const int32_t*)(base + L.offsets);
+  d.attn_ws = base + L.attn;
+  cudaError_t e = launch_pdl(kv8_stage_kernel, dim3((B + 128) / 128), dim3(128), 0, s, B, L.blocks, d.stage.block_table,
+                             d.stage.seq_len, d.stage.pending, (int32_t*)(base + L.offsets),
+                             (const int32_t*)kv->pending);
+  ctx->launches++;
+  ctx->kv8_draft = &d;
+  for (int k = 1; k <= K && e == cudaSuccess; ++k)
+    e = draft_one_step(ctx, s, B, k, K, hidden, embeds, positions, &d.stage, chain_ids, draft_ids, logits, hidden_out);
+  ctx->kv8_draft = nullptr;
+  return launch_status(e);
+}
 
 size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx) {
   if (!ctx) return 0;
@@ -874,20 +1066,7 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
   a.T = T;
   a.max_rows = max_rows;
   a.mask_words = mask_words;
-  a.n_kv = c.n_kv_heads;
-  const int G = c.n_q_heads / c.n_kv_heads;
-  for (a.g_shift = 0; (1 << a.g_shift) < G; ++a.g_shift) {
-  }
-  a.qscale = scale * 1.4426950408889634f;
-  const size_t q4 = 4 * (c.dtype == MTP_DTYPE_BF16 ? 2 : 4);
-  a.q_vec = (uintptr_t)q % q4 == 0 && q_stride % 4 == 0;
-  // columns per tile: the fewest tiles of at most 32 columns, evenly filled
-  const int cols = max_rows * G, tiles = (cols + kA8MaxCols - 1) / kA8MaxCols;
-  const int nt = (cols + 8 * tiles - 1) / (8 * tiles);
-  cudaStream_t s = (cudaStream_t)stream;
-  const bool bf = c.dtype == MTP_DTYPE_BF16;
-  const cudaError_t e = c.head_dim == 128 ? (bf ? attn8_pick<uint16_t, 128>(ctx, s, a, nt) : attn8_pick<float, 128>(ctx, s, a, nt))
-                                          : (bf ? attn8_pick<uint16_t, 64>(ctx, s, a, nt) : attn8_pick<float, 64>(ctx, s, a, nt));
+  const cudaError_t e = attn8_run(ctx, (cudaStream_t)stream, a, c.dtype == MTP_DTYPE_BF16, scale);
   ctx->launches += 2;
   return launch_status(e);
 }

@@ -1,0 +1,227 @@
+"""mtp_draft_kv8: the draft steps on an 8-bit cache, against the float64 oracle
+with its cache replaced by the 8-bit twin (oracle/verifier.py).
+
+Tolerances are those of mtp_draft (tests/gpu_util.py).  The twin quantizes the
+oracle's own keys and values; where the GPU's, good to 2^-8, fall on the other
+side of a rounding border, an element of one new entry moves by a step (2^-3 of
+its value at most).  At that rate (2^-8 / 2^-3, one element in 32) such an
+entry's score moves by about 2^-3 / sqrt(32) of an element's share of it, which
+is far below the 2e-2 that logits are held to."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import oracle.mtp_oracle as core
+import synth
+from gpu_util import F32_LOGIT_TOL, LOGIT_TOL, Guarded, check_ids_are_argmax_of_own_logits, check_logits, dev, host
+from oracle import verifier as V
+from test_gpu_draft import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def M_():
+    import mtp_self_speculative_gb300 as M
+    return M
+
+
+def small(name, batch, K=3, lo=1, hi=70, **kw):
+    base = dict(H=512, n_q=8, n_kv=2, head_dim=128, ffn=1536, vocab=5003, dtype="bf16")
+    base.update(kw)
+    return synth.MTPShape(name, batch=batch, K=K, ctx_lo=lo, ctx_hi=hi, seed_index=71, **base)
+
+
+class Case8(Case):
+    """A draft case whose initial cache is quantized, on the GPU and in the twin."""
+
+    def __init__(self, cfg, **kw):
+        super().__init__(cfg, norm="random", **kw)
+        M, kv0 = M_(), self.kv0
+        nb = kv0.k_pool.shape[0]
+        self.kv = M.KVCache8.empty(self.ctx, nb, dev(kv0.block_table))
+        self.twin = V.Cache8(nb, cfg.n_kv, cfg.head_dim, kv0.block_table)
+        off = np.concatenate([[0], np.cumsum(self.lens)]).astype(np.int32)
+        rows = [np.zeros((0, cfg.n_kv, cfg.head_dim), kv0.k_pool.dtype)] * 2
+        for b, L in enumerate(self.lens):
+            k, v = (np.stack([p[kv0.block_table[b, s // 16], :, s % 16] for s in range(int(L))]) if L else rows[0][:0]
+                    for p in (kv0.k_pool, kv0.v_pool))
+            rows = [np.concatenate([rows[0], k]), np.concatenate([rows[1], v])]
+            self.twin.append(b, O.widen(k, cfg.dtype), O.widen(v, cfg.dtype))
+            self.twin.commit(b, int(L))
+        M.mtp_kv8_append(self.ctx, self.kv, dev(rows[0]), dev(rows[1]), dev(off))
+        M.mtp_kv8_commit(self.ctx, self.kv, self.kv.pending)
+        self.ws = M.Draft8Workspace(self.ctx)
+        self.check_prefix()
+
+    def check_prefix(self, drafted=0, requests=None):
+        """Lengths, and the codes and scales of all whole blocks below them."""
+        np.testing.assert_array_equal(self.kv.seq_len.cpu().numpy(), self.twin.seq_len)
+        np.testing.assert_array_equal(self.kv.pending.cpu().numpy(), self.twin.pending)
+        for b in range(self.B):
+            for j in range(int(self.twin.seq_len[b]) // 16):
+                blk = self.twin.table[b, j]
+                for w, (pool, scale) in enumerate(((self.kv.k_pool, self.kv.k_scale), (self.kv.v_pool, self.kv.v_scale))):
+                    np.testing.assert_array_equal(pool[blk].cpu().numpy(), self.twin.codes[w][blk])
+                    np.testing.assert_array_equal(scale[blk].cpu().numpy(), self.twin.scale[w][blk])
+
+    def draft(self, forced=True, stream=None):
+        M, cfg, B, K = M_(), self.cfg, self.B, self.K
+        ids, logits = Guarded((B, K), torch.int32, fill=-7), Guarded((B, K, cfg.vocab), torch.float32)
+        hout = Guarded((B, cfg.H), torch.float32)
+        chain = dev(self.chain[:, :K - 1].copy()) if forced and K > 1 else None
+        M.mtp_draft_kv8(self.ctx, *self.inputs, self.kv, K, ids.t, self.ws, logits=logits.t, hidden_out=hout.t,
+                        chain_ids=chain, stream=stream)
+        torch.cuda.synchronize()
+        for g, name in ((ids, "draft_ids"), (logits, "logits"), (hout, "hidden_out")):
+            g.check(name)
+        return host(ids.t), host(logits.t), host(hout.t)
+
+    def expect(self, monkeypatch):
+        """The oracle's forced draft, its cache accesses sent to the twin."""
+        cfg, twin = self.cfg, self.twin
+
+        def write(kv, b, slot, k, v, dtype):
+            assert slot == twin.seq_len[b] + twin.pending[b]
+            twin.append(b, *(O.widen(core.store_kv_values(x, dtype), dtype)[None] for x in (k, v)))
+
+        with monkeypatch.context() as m:
+            m.setattr(core, "_kv_write_slot", write)
+            m.setattr(core, "kv_read_slots", lambda kv, b, n, dtype: tuple(twin.values(b, 0, n)))
+            return self.oracle(np.arange(self.B), forced=True)[0]
+
+
+CASES = [(synth.TINY_F32, {}, F32_LOGIT_TOL), (small("kv8_b1", 1), {}, LOGIT_TOL), (small("kv8_b3", 3), {}, LOGIT_TOL),
+         (small("kv8_b7", 7), {}, LOGIT_TOL),                                       # tensor-core projections
+         (small("kv8_d64", 2, head_dim=64), {}, LOGIT_TOL), (small("kv8_k18", 2, K=18, lo=5, hi=30), {}, LOGIT_TOL),
+         (small("kv8_f32", 3, n_q=4, n_kv=4, dtype="f32", lo=15, hi=33), {}, F32_LOGIT_TOL),
+         (small("kv8_q4", 2, H=1024, ffn=2048, vocab=4099), dict(weight_format="int4_g64"), LOGIT_TOL)]
+
+
+@pytest.mark.parametrize("cfg,kw,tol", CASES, ids=[c[0].name for c in CASES])
+def test_draft_on_the_8_bit_cache(cfg, kw, tol, monkeypatch):
+    """Forced-chain logits and hidden state against the oracle; the new entries; roll-back; the same draft again."""
+    M = M_()
+    case = Case8(cfg, **kw)
+    before = int(M.mtp_launch_count(case.ctx))
+    ids, logits, hout = case.draft()
+    assert M.mtp_get_device_error(case.ctx) == 0 and M.mtp_launch_count(case.ctx) > before
+    check_ids_are_argmax_of_own_logits(ids, logits)
+    res = case.expect(monkeypatch)
+    check_logits(logits, res.logits, tol)
+    err = np.max(np.abs(hout - res.hidden_out), -1) / np.max(np.abs(res.hidden_out), -1)
+    assert np.max(err) <= tol
+    case.check_prefix()
+    # the drafted entries: at most a step of the format, and what the head itself may be off, from the twin's
+    for b in range(case.B):
+        L = int(case.lens[b])
+        off = np.zeros(case.B + 1, np.int32)
+        off[b + 1:] = case.K
+        out = [torch.empty(case.K, cfg.n_kv, cfg.head_dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        start = np.zeros(case.B, np.int32)
+        start[b] = L
+        M.mtp_kv8_read(case.ctx, case.kv, dev(start), dev(off), *out)
+        for got, want in zip(out, case.twin.values(b, L, L + case.K)):
+            g = got.double().cpu().numpy()
+            assert np.all(np.abs(g - want) <= 2.0 ** -3 * np.abs(want) + (2.0 ** -9 + tol) * np.max(np.abs(want)))
+    M.mtp_kv8_rollback(case.ctx, case.kv)
+    for b in range(case.B):
+        case.twin.commit(b, 0)
+    case.check_prefix()
+    again = case.draft()
+    np.testing.assert_array_equal(again[0], ids)     # (tail blocks keep their grown scales: the values are the same)
+    assert M.mtp_get_device_error(case.ctx) == 0
+
+
+def test_draft_verify_commit_over_several_steps():
+    """Free-running drafts, synthetic verification, commit: lengths as on a bf16 cache, and a second run repeats the ids."""
+    M = M_()
+    cfg = small("kv8_loop", 2, K=4, lo=10, hi=40)
+    runs = []
+    for _ in range(2):
+        case = Case8(cfg)
+        B, K = case.B, case.K
+        hist = []
+        lens = case.lens.astype(np.int64).copy()
+        rng = np.random.default_rng(3)
+        for step in range(2):
+            ids, logits, _ = case.draft(forced=False)
+            hist.append(ids)
+            check_ids_are_argmax_of_own_logits(ids, logits)
+            acc = rng.integers(0, K + 1, B).astype(np.int32)
+            if step == 0:
+                acc[:] = 0       # the cache was made with room for K + 3 more entries
+            M.mtp_kv8_commit_accepted(case.ctx, case.kv, dev(acc), extra=1)
+            lens += np.minimum(acc + 1, K)
+            np.testing.assert_array_equal(case.kv.seq_len.cpu().numpy(), lens)
+            assert not case.kv.pending.any()
+            pos = case.di.positions + 1
+            case.inputs = case.inputs[:2] + (dev(pos.astype(np.int32)),)
+        assert M.mtp_get_device_error(case.ctx) == 0
+        runs.append(hist)
+    for a, b in zip(*runs):
+        np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("batch", [2, 7])
+def test_requests_with_pending_entries_are_refused(batch):
+    """Its cache and counts stay; the others draft as they would."""
+    M = M_()
+    cfg = small("kv8_pend", batch)
+    good = Case8(cfg).draft()
+    case = Case8(cfg)
+    case.kv.pending[1] = 1
+    pools = [t.clone() for t in (case.kv.k_pool, case.kv.v_pool, case.kv.k_scale, case.kv.v_scale)]
+    ids, logits, _ = case.draft()
+    assert M.mtp_get_device_error(case.ctx) == M.MTP_ERR_DEVICE_ARGS
+    assert case.kv.pending.tolist() == [1 if b == 1 else cfg.K for b in range(batch)]
+    for t, was in zip((case.kv.k_pool, case.kv.v_pool, case.kv.k_scale, case.kv.v_scale), pools):
+        for blk in case.twin.table[1]:
+            if blk >= 0:
+                assert torch.equal(t[int(blk)], was[int(blk)])
+    others = [b for b in range(batch) if b != 1]
+    np.testing.assert_array_equal(logits[others], good[1][others])
+
+
+def test_a_cache_that_is_full_and_bad_calls():
+    M = M_()
+    case = Case8(small("kv8_full", 2, lo=14, hi=14))
+    case.kv.block_table = case.kv.block_table[:, :1].contiguous()      # 16 slots, 14 + 3 wanted
+    case.draft()
+    assert M.mtp_get_device_error(case.ctx) == M.MTP_ERR_CAPACITY
+    assert case.kv.pending.tolist() == [2, 2]
+    ids = torch.empty(2, 3, dtype=torch.int32, device="cuda")
+    with pytest.raises(M.MTPError):
+        M.mtp_draft_kv8(case.ctx, *case.inputs, case.kv, 0, torch.empty(2, 0, dtype=torch.int32, device="cuda"), case.ws)
+    case.ws.bytes -= 1
+    with pytest.raises(M.MTPError):
+        M.mtp_draft_kv8(case.ctx, *case.inputs, case.kv, 3, ids, case.ws)
+    with pytest.raises(ValueError):
+        M.mtp_draft_kv8(case.ctx, *case.inputs, case.kv, 3, ids[:, :2], case.ws)
+    bare = M.mtp_init(M.make_config(hidden=512, n_q_heads=8, n_kv_heads=2, head_dim=128, ffn=1536, vocab=5003, max_batch=2))
+    with pytest.raises(M.MTPError):
+        M.Draft8Workspace(bare)
+
+
+def test_drafts_captured_and_replayed():
+    """A captured draft, replayed after a roll-back, gives the ids and logits of the called one."""
+    M = M_()
+    for batch in (1, 7):
+        case = Case8(small("kv8_graph", batch))
+        B, K = case.B, case.K
+        want = case.draft(forced=False)
+        M.mtp_kv8_rollback(case.ctx, case.kv)
+        ids, logits = torch.empty(B, K, dtype=torch.int32, device="cuda"), torch.empty(B, K, case.cfg.vocab, device="cuda")
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                M.mtp_draft_kv8(case.ctx, *case.inputs, case.kv, K, ids, case.ws, logits=logits)
+                M.mtp_kv8_rollback(case.ctx, case.kv)
+        for _ in range(3):
+            ids.fill_(-1)
+            g.replay()
+            torch.cuda.synchronize()
+            np.testing.assert_array_equal(host(ids), want[0])
+            np.testing.assert_array_equal(host(logits), want[1])
+        assert M.mtp_get_device_error(case.ctx) == 0
