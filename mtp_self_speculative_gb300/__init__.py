@@ -464,6 +464,12 @@ class RopeTable(MTPRopeTable):
         _check(_clib.mtp_rope_table_make(ctypes.byref(p), ctypes.byref(self)), "mtp_rope_table_make")
 
 
+def mtp_set_rope(ctx: Context, rope: RopeTable) -> None:
+    """Use the table (half layout, the whole head) for the head's own rotary
+    embedding in every later draft; waits for the device's work."""
+    _check(_clib.mtp_set_rope(ctx.handle, rope), "mtp_set_rope")
+
+
 def mtp_rope(ctx: Context, x: torch.Tensor, positions: torch.Tensor, rope: RopeTable,
              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotate x [T, heads, head_dim] to ``positions`` [T] into ``out`` (None:

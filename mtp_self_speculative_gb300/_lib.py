@@ -125,6 +125,7 @@ SIGNATURES = {
     "mtp_tree_loop": (c_int, [c_void_p, c_void_p, ctypes.POINTER(MTPKV), ctypes.POINTER(MTPLoop),
                               ctypes.POINTER(MTPTree), c_int]),
     "mtp_rope_table_make": (c_int, [ctypes.POINTER(MTPRopeParams), ctypes.POINTER(MTPRopeTable)]),
+    "mtp_set_rope": (c_int, [c_void_p, ctypes.POINTER(MTPRopeTable)]),
     "mtp_rope": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int64, P_i32, ctypes.POINTER(MTPRopeTable),
                          c_void_p, c_int64]),
     "mtp_kv8_append": (c_int, [c_void_p, c_void_p, c_int, c_int, P_i32, c_void_p, c_int64, c_void_p, c_int64, P_i32,

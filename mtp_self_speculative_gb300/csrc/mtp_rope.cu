@@ -9,6 +9,7 @@
 // and pairs allow.  A thread owns one unit of a token's head, computes that
 // unit's cosines and sines once, and walks over the heads.
 #include <math.h>
+#include <stdlib.h>
 
 #include "mtp_kv8.cuh"
 
@@ -217,6 +218,29 @@ mtp_status mtp_rope_table_make(const mtp_rope_params* p, mtp_rope_table* out) {
   }
   *out = t;
   return MTP_OK;
+}
+
+mtp_status mtp_set_rope(mtp_ctx* ctx, const mtp_rope_table* rope) {
+  if (!ctx || !ctx->has_weights || !rope_table_ok(rope, ctx->cfg.head_dim)) return MTP_ERR_INVALID;
+  const int half = ctx->cfg.head_dim / 2;
+  if (rope->layout != MTP_ROPE_HALF || rope->rotary_dim != ctx->cfg.head_dim) return MTP_ERR_INVALID;
+  DeviceGuard dev(ctx->device);
+  if (!dev.ok) return MTP_ERR_CUDA;
+  const size_t n = (size_t)ctx->cfg.max_pos * half;
+  float2* tab = (float2*)malloc(n * sizeof(float2));
+  if (!tab) return MTP_ERR_OOM;
+  for (int p = 0; p < ctx->cfg.max_pos; ++p)
+    for (int i = 0; i < half; ++i) {
+      // the exact phase, as a signed fraction of a turn, to an angle
+      const double turn = (double)(int64_t)((uint64_t)p * rope->turns[i]) / 18446744073709551616.0;
+      const double ang = turn * 6.283185307179586476925;
+      tab[(size_t)p * half + i] = make_float2((float)(cos(ang) * rope->magnitude), (float)(sin(ang) * rope->magnitude));
+    }
+  // work that reads the old table finishes first
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(ctx->rope, tab, n * sizeof(float2), cudaMemcpyHostToDevice);
+  free(tab);
+  return launch_status(e);
 }
 
 mtp_status mtp_rope(mtp_ctx* ctx, void* stream, int T, int heads, const void* x, int64_t x_stride,

@@ -225,3 +225,36 @@ def test_drafts_captured_and_replayed():
             np.testing.assert_array_equal(host(ids), want[0])
             np.testing.assert_array_equal(host(logits), want[1])
         assert M.mtp_get_device_error(case.ctx) == 0
+
+
+@pytest.mark.parametrize("cfg,tol,persistent", [(synth.TINY_F32, F32_LOGIT_TOL, 0), (small("rope_b1", 1), LOGIT_TOL, 0),
+                                                (small("rope_p", 2), LOGIT_TOL, 4), (small("rope_b7", 7), LOGIT_TOL, 0)],
+                         ids=["f32", "b1", "persistent", "b7"])
+@pytest.mark.parametrize("kw", [dict(scaling="linear", factor=4.0), dict(scaling="yarn", factor=8.0, original_max_pos=64),
+                                dict(theta=5000.0, magnitude=0.5)], ids=["linear", "yarn", "theta"])
+def test_drafts_with_a_rotary_table_of_their_own(cfg, tol, persistent, kw, monkeypatch):
+    """mtp_set_rope: the head's drafts follow the table's frequencies and magnitude; the default table gives the default."""
+    M = M_()
+    case = Case(cfg, norm="random", persistent_max_batch=persistent)
+    plain = case.gpu_draft()[1]
+    kw = {"theta": cfg.rope_theta, **kw}
+    M.mtp_set_rope(case.ctx, M.RopeTable(cfg.head_dim, **kw))
+    ids, logits, hout, _ = case.gpu_draft()
+    with monkeypatch.context() as m:
+        m.setattr(core, "rope", lambda x, pos, theta: V.rope(x[None], [pos], **kw)[0])
+        res, _ = case.oracle(np.arange(case.B))
+    check_logits(logits, res.logits, tol)
+    assert not np.array_equal(logits, plain)
+    M.mtp_set_rope(case.ctx, M.RopeTable(cfg.head_dim, theta=cfg.rope_theta))
+    check_logits(case.gpu_draft()[1], plain.astype(np.float64), 1e-3 if cfg.dtype == "f32" else 1e-2)
+
+
+def test_rotary_tables_that_do_not_fit_the_head_are_refused():
+    M = M_()
+    case = Case(synth.TINY_F32)
+    for kw in (dict(rotary_dim=32), dict(rotary_dim=64, layout="interleaved"), dict(rotary_dim=128)):
+        with pytest.raises(M.MTPError):
+            M.mtp_set_rope(case.ctx, M.RopeTable(**kw))
+    bare = M.mtp_init(M.make_config(hidden=256, n_q_heads=4, n_kv_heads=2, head_dim=64, ffn=256, vocab=100))
+    with pytest.raises(M.MTPError):
+        M.mtp_set_rope(bare, M.RopeTable(64))

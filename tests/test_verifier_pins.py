@@ -97,6 +97,9 @@ def test_calls_without_context_are_rejected():
     assert lib.mtp_token_counts_add(None, None, 1, 16, 1, 16, 0, 16) == L.MTP_ERR_INVALID
     assert lib.mtp_logits_process(None, None, ctypes.byref(la)) == L.MTP_ERR_INVALID
     assert lib.mtp_rope_table_make(None, t) == L.MTP_ERR_INVALID
+    assert lib.mtp_set_rope(None, t) == L.MTP_ERR_INVALID
+    assert lib.mtp_draft_kv8_workspace_bytes(None) == 0
+    assert lib.mtp_draft_kv8(None, None, 1, 16, 16, 16, k, 1, None, 16, None, None, 256, 1 << 30) == L.MTP_ERR_INVALID
 
 
 def cpu_context(**kw):
