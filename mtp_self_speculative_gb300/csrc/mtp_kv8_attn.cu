@@ -230,9 +230,10 @@ __device__ __forceinline__ void attn8_take(float& M, float& Ls, float4& x, float
   M = mn;
 }
 
-template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, sizeof(T) == 4 ? 2 : 1>::kBlocks)) kv8_attn_kernel(const Attn8Args a) {
-  constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
+// SPLIT: halves of Q and P (2 keeps 22 bits; 1 is for results that bf16
+// arithmetic goes on with).
+template <typename T, int HD, int NT, int SPLIT>
+__global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlocks)) kv8_attn_kernel(const Attn8Args a) {
   using S = Attn8Shape<HD, NT, SPLIT>;
   constexpr int KS = HD / 16;                 // k-steps of Q K^T
   constexpr int MT = HD / 16;                 // m-tiles of V^T P^T
@@ -809,11 +810,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8
 constexpr int kA8MaxBlocks = 3;
 static size_t a8_meta_bytes(const mtp_ctx* ctx) { return (size_t)kA8MaxBlocks * ctx->num_sms * 2 * sizeof(int4); }
 
-template <typename T, int HD, int NT>
+template <typename T, int HD, int NT, int SPLIT = sizeof(T) == 4 ? 2 : 1>
 static cudaError_t attn8_launch(mtp_ctx* ctx, cudaStream_t s, Attn8Args a) {
-  using S = Attn8Shape<HD, NT, sizeof(T) == 4 ? 2 : 1>;
+  using S = Attn8Shape<HD, NT, SPLIT>;
   static_assert(S::kBlocks <= kA8MaxBlocks, "workspace");
-  cudaError_t e = ensure_smem((const void*)kv8_attn_kernel<T, HD, NT>, S::kBytes);
+  cudaError_t e = ensure_smem((const void*)kv8_attn_kernel<T, HD, NT, SPLIT>, S::kBytes);
   if (e != cudaSuccess) return e;
   const int grid = S::kBlocks * ctx->num_sms;
   const int cols = a.max_rows << a.g_shift;   // of the longest request
@@ -821,7 +822,7 @@ static cudaError_t attn8_launch(mtp_ctx* ctx, cudaStream_t s, Attn8Args a) {
   a.max_tiles = (cols + S::kCols - 1) / S::kCols;
   const long long segments = (long long)a.B * a.n_kv * a.max_tiles;
   a.by_segment = segments <= grid;
-  e = launch_pdl(kv8_attn_kernel<T, HD, NT>, dim3(grid), dim3(kA8Threads), S::kBytes, s, a);
+  e = launch_pdl(kv8_attn_kernel<T, HD, NT, SPLIT>, dim3(grid), dim3(kA8Threads), S::kBytes, s, a);
   if (e != cudaSuccess) return e;
   // columns that a block joins at a time, for twice the average of pieces
   const int even = kJoinThreads / join_ways((int)(2 * grid / segments + 1)) / (HD / 4), per = even > 1 ? even : 1;
@@ -840,21 +841,15 @@ static cudaError_t attn8_pick(mtp_ctx* ctx, cudaStream_t s, const Attn8Args& a, 
   }
 }
 
-// Fills in what follows from the context and the queries' type, and launches.
-static cudaError_t attn8_run(mtp_ctx* ctx, cudaStream_t s, Attn8Args& a, bool bf16, float scale) {
+// Fills in what follows from the context and the queries.
+static void attn8_fill(const mtp_ctx* ctx, Attn8Args& a, size_t q_bytes, float scale) {
   const mtp_config& c = ctx->cfg;
   a.n_kv = c.n_kv_heads;
   const int G = c.n_q_heads / c.n_kv_heads;
   for (a.g_shift = 0; (1 << a.g_shift) < G; ++a.g_shift) {
   }
   a.qscale = scale * 1.4426950408889634f;
-  const size_t q4 = 4 * (bf16 ? 2 : 4);
-  a.q_vec = (uintptr_t)a.q % q4 == 0 && a.q_stride % 4 == 0;
-  // columns per tile: the fewest tiles of at most 32 columns, evenly filled
-  const int cols = a.max_rows * G, tiles = (cols + kA8MaxCols - 1) / kA8MaxCols;
-  const int nt = (cols + 8 * tiles - 1) / (8 * tiles);
-  return c.head_dim == 128 ? (bf16 ? attn8_pick<uint16_t, 128>(ctx, s, a, nt) : attn8_pick<float, 128>(ctx, s, a, nt))
-                           : (bf16 ? attn8_pick<uint16_t, 64>(ctx, s, a, nt) : attn8_pick<float, 64>(ctx, s, a, nt));
+  a.q_vec = (uintptr_t)a.q % (4 * q_bytes) == 0 && a.q_stride % 4 == 0;
 }
 
 // --------------------------------------------- draft steps on an 8-bit cache
@@ -961,7 +956,11 @@ cudaError_t launch_attention_kv8(mtp_ctx* ctx, cudaStream_t s, int B, int k) {
   a.T = B;
   a.max_rows = 1;
   ctx->launches += 3;
-  return attn8_run(ctx, s, a, false, 1.0f / sqrtf((float)c.head_dim));
+  attn8_fill(ctx, a, 4, 1.0f / sqrtf((float)c.head_dim));
+  // one row: at most 8 columns.  A bf16 head's next projection takes bf16, so
+  // its queries and weights need no second half.
+  if (bf) return c.head_dim == 128 ? attn8_launch<float, 128, 1, 1>(ctx, s, a) : attn8_launch<float, 64, 1, 1>(ctx, s, a);
+  return c.head_dim == 128 ? attn8_launch<float, 128, 1>(ctx, s, a) : attn8_launch<float, 64, 1>(ctx, s, a);
 }
 
 // Workspace of a draft call: the attention's, then the staging cache.
@@ -1066,7 +1065,15 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
   a.T = T;
   a.max_rows = max_rows;
   a.mask_words = mask_words;
-  const cudaError_t e = attn8_run(ctx, (cudaStream_t)stream, a, c.dtype == MTP_DTYPE_BF16, scale);
+  const bool bf = c.dtype == MTP_DTYPE_BF16;
+  attn8_fill(ctx, a, bf ? 2 : 4, scale);
+  // columns per tile: the fewest tiles of at most 32 columns, evenly filled
+  const int cols = max_rows << a.g_shift, tiles = (cols + kA8MaxCols - 1) / kA8MaxCols;
+  const int nt = (cols + 8 * tiles - 1) / (8 * tiles);
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e =
+      c.head_dim == 128 ? (bf ? attn8_pick<uint16_t, 128>(ctx, s, a, nt) : attn8_pick<float, 128>(ctx, s, a, nt))
+                        : (bf ? attn8_pick<uint16_t, 64>(ctx, s, a, nt) : attn8_pick<float, 64>(ctx, s, a, nt));
   ctx->launches += 2;
   return launch_status(e);
 }
