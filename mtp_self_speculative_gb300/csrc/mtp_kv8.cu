@@ -175,6 +175,8 @@ __device__ __forceinline__ void append_queries(const Append8Args& a, const mtp_r
 // computes their cosine once, and nothing goes through shared memory but the
 // two maxima.  What bounds a decoding step is the chain of dependent loads:
 // lengths, then rows, positions and block id together, then the old scale.
+// 32 requests x 6 rows with 32 query heads, and reading 461 entries back: 9.8 us
+// for both; four prompts of 2425 rows together, 25.3 us.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append8Args a,
                                                                     const __grid_constant__ mtp_rope_table tab) {
@@ -357,6 +359,8 @@ struct Read8Args {
 };
 
 // Thread block: one row, all kv heads; a thread turns 8 codes into 16 bytes.
+// Bound by its three dependent loads (offsets, block id, codes): 2425 rows of 8
+// heads 7.8 us.
 template <int HD>
 __global__ void __launch_bounds__(128) kv8_read_kernel(const Read8Args a) {
   const int r = blockIdx.x;
@@ -426,7 +430,8 @@ constexpr int kEditThreads = 128;
 
 // Thread block (kv head, request).  Zeroes the dropped slots of its head; a
 // path commit first takes the kept entries into shared memory as codes with
-// their blocks' scales.
+// their blocks' scales.  A few KB per request: launch and two dependent loads
+// bound it.
 __global__ void __launch_bounds__(kEditThreads) kv8_edit_kernel(const Edit8Args a) {
   extern __shared__ __align__(16) uint8_t kept[];   // path: [n][hd] codes
   __shared__ float kept_scale[kPathMax];
