@@ -408,8 +408,9 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
       }
       cp_commit();
     };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+    // two stages now, the others once the queries are in place
+    issue(0);
+    if constexpr (S::kStages > 2) issue(1);
 
     // ---- queries: per column a power of two that brings them into fp16's
     // range, then fragments in the order the lanes read them
@@ -460,6 +461,9 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
       qfac[nt][0] = qfac_s[nt * 8 + 2 * ti];
       qfac[nt][1] = qfac_s[nt * 8 + 2 * ti + 1];
     }
+
+#pragma unroll
+    for (int i = 2; i < S::kStages - 1; ++i) issue(i);
 
     float o[NT][MT][4], m_run[NT][2], l_run[NT][2];
 #pragma unroll
@@ -764,7 +768,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const Attn8
     // lengths do not change during the call
     const int b = blockIdx.x / (a.n_kv * a.max_tiles), tile = blockIdx.x % a.max_tiles;
     int o0, n, L;
-    if (!attn8_request(a, b, o0, n, L) || tile * a.tile_cols >= n << a.g_shift) return;
+    if (!attn8_request(a, b, o0, n, L) || tile * a.tile_cols >= n << a.g_shift) {
+      pdl_wait();   // this kernel must not end before the first one
+      return;
+    }
   }
   pdl_wait();
   pdl_trigger();
