@@ -35,7 +35,7 @@
 // Memory bounds decoding batches: 64 requests of up to 8192 entries (494 MB)
 // 88 us, 5.6 TB/s; 128 of up to 4096 (542 MB) 95 us.  One request of 32768
 // entries takes 21 us, of which 4 are the join and as much the way to the first
-// data.  Draft rows add products: 16 x 6 rows over up to 4096 entries 33 us, at
+// data.  Draft rows add products: 16 x 6 rows over up to 4096 entries 30 us, at
 // two warps per scheduler bound by the products' latencies; 8 x 61 rows 110 us,
 // 166 TFLOP/s.
 #include <math.h>
@@ -183,8 +183,11 @@ struct Attn8Shape {
   // 48: 115), so it grows with the width.
   static constexpr int kLead = (16 + 8 * NT) / JB, kMinShare = kA8MinShare / JB;
   static constexpr int kBlocks = SPLIT == 1 && NT == 1 ? 3 : 2;   // thread blocks per SM (registers)
-  // stages of a warp's ring: what the shared memory of an SM holds for them
-  static constexpr int kStages = (kBlocks == 3 || (SPLIT == 2 && NT >= 3) ? 2 : 3) * 2 / JB;
+  // Stages of a warp's ring.  Two of 32 tokens for three blocks per SM; four
+  // of 16 tokens for two: six (what the shared memory would hold) make the
+  // start longer and gain nothing (16 x 6 rows 31.3 against 30.0 us, one
+  // request of 6 rows on 32768 entries 28.1 against 26.0 us; three: 30.6, 26.5).
+  static constexpr int kStages = NT == 1 ? 2 : 4;
   static constexpr int kRing = kA8Warps * kStages * kStage;
   static constexpr int kCols = 8 * NT;
   static constexpr int kPitch = HD + 4;                    // floats of a merged row
@@ -710,6 +713,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
     const uint32_t c_first = seg_u0 / share, c_last = (seg_u0 + (uint32_t)steps - 1) / share;
     const bool whole = c_first == c_last;
     const int slot = blockIdx.x == c_first ? 1 : 0;
+#pragma unroll 2
     for (int i = tid; i < ncols * (HD / 4); i += kA8Threads) {
       const int c = i / (HD / 4), d4 = i - c * (HD / 4);
       float M = kA8Least;
