@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   const int b = sh[0];
   if (b < 0) return;
   const int o0 = sh[1], n_new = sh[2] - o0, P = sh[4];
+  const int all = (append_unit(sh[2], b + 1) - append_unit(o0, b)) * a.n_kv;   // the request's thread blocks
   if (sh[3] < 0 || P < 0 || sh[3] > INT32_MAX - P) {
     if (tid == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
     return;
@@ -223,7 +224,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     return;
   }
   const int first = start >> 4, last = (start + n_new - 1) >> 4, bi = first + (u - append_unit(o0, b));
-  if (bi > last) return;
+  if (bi > last) {   // no rows left for it; it has read the old length, so it counts
+    if (tid == 0 && arrive_last(a.kv.arrive + b, all)) a.kv.pending[b] = P + n_new;
+    return;
+  }
   const int s0 = max(start - bi * kBlk, 0);                  // first new slot within the block
   const int s1 = min(start + n_new - bi * kBlk, kBlk);       // one past the last
   const int r0 = o0 + bi * kBlk + s0 - start;                // input row of slot s0
@@ -343,8 +347,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     }
   }
   // the last of the request's thread blocks publishes the new length: all
-  // have read the old one by then
-  if (tid == 0 && arrive_last(a.kv.arrive + b, (last - first + 1) * a.n_kv)) a.kv.pending[b] = P + n_new;
+  // have read the old one by then, those that had no rows to write too (one
+  // that starts late would take the new length for the old)
+  if (tid == 0 && arrive_last(a.kv.arrive + b, all)) a.kv.pending[b] = P + n_new;
 }
 
 // -------------------------------------------------------------------- read

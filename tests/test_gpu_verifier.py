@@ -207,6 +207,19 @@ def test_append_and_edits_are_bit_exact(dtype, n_q, n_kv, hd):
     clean(ctx)
 
 
+def test_append_in_more_waves_than_fit_the_gpu():
+    """Thousands of thread blocks, half of them for a second cache block that a request's rows do not reach: one that
+    starts after the others of its request have ended still counts from the old length.  Starts 0, 6, 12, 18, 24: from
+    6 on, rows counted from the new length would reach the second block."""
+    ctx = context(8, 8, 64, "bf16", max_batch=500)
+    rng = np.random.default_rng(11)
+    kv, twin = make_cache(ctx, 500, 2, rng)
+    for _ in range(5):
+        append_both(ctx, kv, twin, [6] * 500, rng)
+        check_cache(ctx, kv, twin)
+    clean(ctx)
+
+
 @pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("f32", 64)])
 def test_append_of_extreme_values(dtype, hd):
     """Zeros of both signs, the type's largest and smallest numbers, infinities and NaN; appended in two steps."""
