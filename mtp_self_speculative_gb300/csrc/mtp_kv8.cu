@@ -175,8 +175,8 @@ __device__ __forceinline__ void append_queries(const Append8Args& a, const mtp_r
 // computes their cosine once, and nothing goes through shared memory but the
 // two maxima.  What bounds a decoding step is the chain of dependent loads:
 // lengths, then rows, positions and block id together, then the old scale.
-// 32 requests x 6 rows with 32 query heads, and reading 461 entries back: 9.8 us
-// for both; four prompts of 2425 rows together, 25.3 us.
+// 32 requests x 6 rows with 32 query heads, and reading 461 entries back: 10.3 us
+// for both; four prompts of 2425 rows together, 26.5 us.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append8Args a,
                                                                     const __grid_constant__ mtp_rope_table tab) {
