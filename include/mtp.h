@@ -612,9 +612,13 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
                              float scale, void* out, float* lse, void* ws, size_t ws_bytes);
 
 /* mtp_draft on an 8-bit cache of the head: the same steps, arguments and
- * checks (pending[b] == 0 on entry, K afterwards; rotary, dtype and kernels of
- * the projections as there), the cache's entries quantized as in
- * mtp_kv8_append from keys and values of the context's dtype.  Commit or roll
+ * checks (pending[b] == 0 on entry; rotary, dtype and kernels of the
+ * projections as there), the cache's entries quantized as in mtp_kv8_append
+ * from keys and values of the context's dtype.  Afterwards pending[b] = K, or
+ * the number of steps whose slots lie within max_blocks (MTP_ERR_CAPACITY).
+ * A step with a position outside 0..max_pos-1 or a block id outside the pool
+ * writes no entry (its slot stays zero bits, the block's scale as it is) but
+ * counts as pending (MTP_ERR_CAPACITY).  Commit or roll
  * back with mtp_kv8_commit_accepted and the others.  B: at most 1024; the
  * persistent kernel is not used.  ws: mtp_draft_kv8_workspace_bytes(ctx) bytes
  * (0 for a NULL context or one without weights), 256-byte aligned, not

@@ -889,6 +889,7 @@ static void attn8_fill(const mtp_ctx* ctx, Attn8Args& a, size_t q_bytes, float s
 struct Kv8Draft {
   mtp_kv8 kv;
   mtp_kv stage;
+  const int32_t* positions;
   const int32_t* row_offsets;   // 0, 1, .. B
   void* attn_ws;
 };
@@ -909,10 +910,13 @@ __global__ void __launch_bounds__(128) kv8_stage_kernel(int B, int blocks, int32
 }
 
 // Thread block (kv head, request): warp 0 the key, warp 1 the value row of
-// step k.
+// step k.  At a position outside the rotary table the projections write no
+// staged row (its bytes are the workspace's), so the entry stays zero bits and
+// the block's scale as it is; the request counts it as pending all the same,
+// as on a 16-bit cache.
 template <typename T, int HD>
 __global__ void __launch_bounds__(64) kv8_stage_append_kernel(mtp_kv8 kv, mtp_kv stage, const int* req_bad, int* err,
-                                                              int n_kv, int k) {
+                                                              const int32_t* positions, int max_pos, int n_kv, int k) {
   constexpr int DPL = HD / 32;
   pdl_wait();
   pdl_trigger();
@@ -924,6 +928,11 @@ __global__ void __launch_bounds__(64) kv8_stage_append_kernel(mtp_kv8 kv, mtp_kv
     return;
   }
   if (g == 0 && threadIdx.x == 0) kv.pending[b] = k;
+  const long long pos = (long long)positions[b] + k - 1;
+  if (pos < 0 || pos >= max_pos) {
+    if (threadIdx.x == 0) set_error(err, MTP_ERR_CAPACITY);
+    return;
+  }
   const int blk = kv.block_table[(long long)b * kv.max_blocks + (slot >> 4)], off = (int)(slot & 15);
   if (blk < 0 || blk >= kv.num_blocks) {
     if (threadIdx.x == 0) set_error(err, MTP_ERR_CAPACITY);
@@ -962,12 +971,12 @@ cudaError_t launch_attention_kv8(mtp_ctx* ctx, cudaStream_t s, int B, int k) {
   const mtp_config& c = ctx->cfg;
   const dim3 grid(c.n_kv_heads, B), block(64);
   const bool bf = c.dtype == MTP_DTYPE_BF16;
-  cudaError_t e =
-      c.head_dim == 128
-          ? (bf ? launch_pdl(kv8_stage_append_kernel<uint16_t, 128>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k)
-                : launch_pdl(kv8_stage_append_kernel<float, 128>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k))
-          : (bf ? launch_pdl(kv8_stage_append_kernel<uint16_t, 64>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k)
-                : launch_pdl(kv8_stage_append_kernel<float, 64>, grid, block, 0, s, d.kv, d.stage, (const int*)ctx->req_bad, ctx->err, c.n_kv_heads, k));
+  const int* req_bad = ctx->req_bad;
+  auto append = [&](auto kernel) {
+    return launch_pdl(kernel, grid, block, 0, s, d.kv, d.stage, req_bad, ctx->err, d.positions, c.max_pos, c.n_kv_heads, k);
+  };
+  cudaError_t e = c.head_dim == 128 ? (bf ? append(kv8_stage_append_kernel<uint16_t, 128>) : append(kv8_stage_append_kernel<float, 128>))
+                                    : (bf ? append(kv8_stage_append_kernel<uint16_t, 64>) : append(kv8_stage_append_kernel<float, 64>));
   if (e != cudaSuccess) return e;
   Attn8Args a{};
   a.q = ctx->q;
@@ -1046,6 +1055,7 @@ mtp_status mtp_draft_kv8(mtp_ctx* ctx, void* stream, int B, const void* hidden, 
   d.stage.pending = (int32_t*)(base + L.pending);
   d.stage.num_blocks = ctx->cfg.max_batch * L.blocks;
   d.stage.max_blocks = L.blocks;
+  d.positions = positions;
   d.row_offsets = (const int32_t*)(base + L.offsets);
   d.attn_ws = base + L.attn;
   cudaError_t e = launch_pdl(kv8_stage_kernel, dim3((B + 128) / 128), dim3(128), 0, s, B, L.blocks, d.stage.block_table,

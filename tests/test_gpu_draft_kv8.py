@@ -258,3 +258,91 @@ def test_rotary_tables_that_do_not_fit_the_head_are_refused():
     bare = M.mtp_init(M.make_config(hidden=256, n_q_heads=4, n_kv_heads=2, head_dim=64, ffn=256, vocab=100))
     with pytest.raises(M.MTPError):
         M.mtp_set_rope(bare, M.RopeTable(64))
+
+
+RANGE_CASES = [(small("kv8_range_b2", 2), {}), (small("kv8_range_b7", 7), {}),          # the streamed and the tcgen05 projections
+               (small("kv8_range_f32", 3, n_q=4, n_kv=4, head_dim=64, dtype="f32"), {}),
+               (small("kv8_range_q4", 2, H=1024, ffn=2048, vocab=4099), dict(weight_format="int4_g64"))]
+
+
+@pytest.mark.parametrize("cfg,kw", RANGE_CASES, ids=[c[0].name for c in RANGE_CASES])
+def test_positions_out_of_range_leave_the_entries_and_scales(cfg, kw):
+    """A step whose position lies outside 0 .. max_pos - 1 writes no entry, whatever the workspace held: its slot stays
+    zero, the scales and the committed entries of the tail block stay as they were; `pending` grows as on a 16-bit
+    cache.  Request 0 leaves the range at step 2, request 1 before step 1, and is below it in a second run."""
+    M = M_()
+    lens = [21, 37, 5, 16, 1, 60, 33][:cfg.batch]
+    limit = max(lens) + cfg.K + 8
+    fields = ("k_pool", "v_pool", "k_scale", "v_scale")
+
+    def bytes_of(case, b):
+        return [getattr(case.kv, f)[case.kv.block_table[b][case.kv.block_table[b] >= 0].long()].clone() for f in fields]
+
+    for pos1 in (limit, -cfg.K):
+        got = []
+        for K in (cfg.K, 1):
+            case = Case8(cfg, lens=lens, **kw)
+            assert case.ctx.cfg.max_pos == limit
+            case.inputs[2][:2] = torch.tensor([limit - 1, pos1])
+            case.ws.ws.fill_(0x7E)                # 8e37 in both types
+            before = bytes_of(case, 1)
+            case.K = K
+            _, logits, _ = case.draft()
+            assert M.mtp_get_device_error(case.ctx) == M.MTP_ERR_CAPACITY
+            assert case.kv.pending.tolist() == [K] * case.B
+            for a, b in zip(bytes_of(case, 1), before):
+                assert torch.equal(a, b)
+            # the slots that were skipped: no bits
+            for b, first in ((0, lens[0] + 1), (1, lens[1])):
+                for s in range(first, lens[b] + K):
+                    for pool in (case.kv.k_pool, case.kv.v_pool):
+                        assert not pool[case.kv.block_table[b, s // 16].long(), :, s % 16].any()
+            got.append((bytes_of(case, 0), logits))
+            M.mtp_kv8_rollback(case.ctx, case.kv)
+            for a, b in zip(bytes_of(case, 1), before):
+                assert torch.equal(a, b)
+        # after three steps request 0 holds what it holds after its only one within the range
+        for a, b in zip(got[0][0], got[1][0]):
+            assert torch.equal(a, b)
+        if cfg.batch > 2:                         # the others draft as they would
+            good = Case8(cfg, lens=lens, **kw).draft()[1]
+            np.testing.assert_array_equal(got[0][1][2:], good[2:])
+
+
+@pytest.mark.parametrize("cfg", [small("kv8_tail", 3), small("kv8_tail_b7", 7), small("kv8_tail_f32", 2, dtype="f32", head_dim=64)],
+                         ids=lambda c: c.name)
+def test_a_drafted_entry_that_raises_its_blocks_scale(cfg):
+    """Committed entries of a tail block, far smaller than the drafted one: their codes are the old ones, rounded once
+    to the scale that the block has afterwards."""
+    M = M_()
+    lens = [21, 37, 5, 15, 1, 60, 33][:cfg.batch]
+    case = Case8(cfg, lens=lens)
+    rng = np.random.default_rng(7)
+    zero = np.zeros(case.B, np.int32)
+    M.mtp_kv8_truncate(case.ctx, case.kv, dev(zero))
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    rows = torch.from_numpy(rng.normal(size=(off[-1], cfg.n_kv, cfg.head_dim)) * 2.0 ** -5)
+    rows = rows.to(torch.bfloat16 if cfg.dtype == "bf16" else torch.float32)
+    for b in range(case.B):
+        case.twin.truncate(b, 0)
+        case.twin.append(b, rows[off[b]:off[b + 1]].double().numpy(), rows[off[b]:off[b + 1]].double().numpy())
+        case.twin.commit(b, lens[b])
+    M.mtp_kv8_append(case.ctx, case.kv, rows.cuda(), rows.cuda(), dev(off))
+    M.mtp_kv8_commit(case.ctx, case.kv, case.kv.pending)
+    case.K = 1
+    case.draft()
+    assert M.mtp_get_device_error(case.ctx) == 0
+    grown = 0
+    for b in range(case.B):
+        blk, held = case.twin.table[b, lens[b] // 16], lens[b] % 16
+        for w, (pool, scale) in enumerate(((case.kv.k_pool, case.kv.k_scale), (case.kv.v_pool, case.kv.v_scale))):
+            codes, now = pool[blk].cpu().numpy(), scale[blk].double().cpu().numpy()
+            was = case.twin.scale[w][blk]
+            assert np.all(now >= was)
+            grown += int(np.sum((now > was) & (was > 0)))
+            for g in range(cfg.n_kv):
+                if held:
+                    want = V.e4m3_encode(V.VALUES[case.twin.codes[w][blk, g, :held]] * (was[g] / now[g]))
+                    np.testing.assert_array_equal(codes[g, :held], want)
+            assert not codes[:, held + 1:].any()
+    assert grown > 0
