@@ -483,9 +483,10 @@ mtp_status mtp_rope_table_make(const mtp_rope_params* params, mtp_rope_table* ou
 
 /* Use the table for the head's own rotary embedding in every later draft of
  * the context (mtp_init takes rope_theta, unscaled): layout HALF, rotary_dim =
- * head_dim, any scaling.  Waits for the device's work and replaces the
- * context's table of cosines and sines; not for a stream capture, and graphs
- * captured before read the new table too.  MTP_ERR_INVALID for a context
+ * head_dim, any scaling.  Waits for the device's work, replaces the context's
+ * table of cosines and sines and returns when the new one is in place, for
+ * drafts on any stream; not for a stream capture, and graphs captured before
+ * read the new table too.  MTP_ERR_INVALID for a context
  * without weights or another layout or width. */
 mtp_status mtp_set_rope(mtp_ctx* ctx, const mtp_rope_table* rope);
 

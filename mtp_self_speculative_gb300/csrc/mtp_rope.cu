@@ -237,9 +237,12 @@ mtp_status mtp_set_rope(mtp_ctx* ctx, const mtp_rope_table* rope) {
       const double ang = turn * 6.283185307179586476925;
       tab[(size_t)p * half + i] = make_float2((float)(cos(ang) * rope->magnitude), (float)(sin(ang) * rope->magnitude));
     }
-  // work that reads the old table finishes first
+  // work that reads the old table finishes first; a copy from pageable memory
+  // may return before its last bytes have arrived, and a draft on a stream that
+  // does not wait for the default one may come next
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(ctx->rope, tab, n * sizeof(float2), cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   free(tab);
   return launch_status(e);
 }

@@ -346,3 +346,31 @@ def test_a_drafted_entry_that_raises_its_blocks_scale(cfg):
                     np.testing.assert_array_equal(codes[g, :held], want)
             assert not codes[:, held + 1:].any()
     assert grown > 0
+
+
+def test_a_rotary_table_is_in_place_when_mtp_set_rope_returns():
+    """A draft on another stream, right behind the call, reads the new table to its end."""
+    M = M_()
+    case = Case(synth.TINY_F32, norm="random")
+    cfg, limit = case.cfg, 1 << 18
+    ctx = M.mtp_init(M.make_config(cfg.H, cfg.n_q, cfg.n_kv, cfg.head_dim, cfg.ffn, cfg.vocab, cfg.eps, cfg.rope_theta,
+                                   cfg.dtype, case.B, case.K, 16, limit), case.wdev)
+    case.ctx = ctx
+    case.inputs[2].fill_(limit - case.K)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for theta in (5000.0, 1e6, 20000.0):
+        got = []
+        for fresh in (True, False):
+            kvd = M.KVCache(*(dev(x) for x in (case.kv0.k_pool, case.kv0.v_pool, case.kv0.block_table, case.kv0.seq_len,
+                                               case.kv0.pending)))
+            ids = torch.empty(case.B, case.K, dtype=torch.int32, device="cuda")
+            logits = torch.empty(case.B, case.K, cfg.vocab, device="cuda")
+            torch.cuda.synchronize()
+            if fresh:
+                M.mtp_set_rope(ctx, M.RopeTable(cfg.head_dim, theta=theta))
+            M.mtp_draft(ctx, *case.inputs, kvd, case.K, ids, logits, stream=side)
+            torch.cuda.synchronize()
+            got.append(host(logits))
+        np.testing.assert_array_equal(*got)
+    assert M.mtp_get_device_error(ctx) == 0
