@@ -329,6 +329,13 @@ mtp_status mtp_init(const mtp_config* cfg, const mtp_weights* weights, int devic
       return st;
     }
   }
+  // the copies and fills above may still run, and the first call may come on a
+  // stream that does not wait for the default one
+  if (cudaStreamSynchronize(0) != cudaSuccess) {
+    cudaGetLastError();
+    mtp_destroy(ctx);
+    return MTP_ERR_CUDA;
+  }
   *out = ctx;
   return MTP_OK;
 }
@@ -450,6 +457,8 @@ mtp_status mtp_get_device_error(mtp_ctx* ctx) {
       (cudaMemset(ctx->lm_cnt, 0, 4) != cudaSuccess || cudaMemset(ctx->lm_tick, 0, 64 * 8) != cudaSuccess ||
        cudaMemset(ctx->lm_keys, 0, (size_t)ctx->cfg.max_batch * 8) != cudaSuccess))
     return MTP_ERR_CUDA;
+  // (fills return early: a later call on another stream must not be overtaken)
+  if (word && cudaStreamSynchronize(0) != cudaSuccess) return MTP_ERR_CUDA;
   return (mtp_status)word;
 }
 

@@ -374,3 +374,30 @@ def test_a_rotary_table_is_in_place_when_mtp_set_rope_returns():
             got.append(host(logits))
         np.testing.assert_array_equal(*got)
     assert M.mtp_get_device_error(ctx) == 0
+
+
+def test_a_new_context_is_ready_for_any_stream():
+    """A draft on another stream right behind mtp_init reads the whole rotary table; an error word that was read and
+    cleared takes nothing with it that a later call on that stream reports."""
+    M = M_()
+    case = Case(synth.TINY_F32, norm="random")
+    cfg, limit = case.cfg, 1 << 18
+    case.inputs[2].fill_(limit - case.K)
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(2):
+        kvd = M.KVCache(*(dev(x) for x in (case.kv0.k_pool, case.kv0.v_pool, case.kv0.block_table, case.kv0.seq_len,
+                                           case.kv0.pending)))
+        ids = torch.empty(case.B, case.K, dtype=torch.int32, device="cuda")
+        logits = torch.empty(case.B, case.K, cfg.vocab, device="cuda")
+        torch.cuda.synchronize()
+        if not got:
+            ctx = M.mtp_init(M.make_config(cfg.H, cfg.n_q, cfg.n_kv, cfg.head_dim, cfg.ffn, cfg.vocab, cfg.eps,
+                                           cfg.rope_theta, cfg.dtype, case.B, case.K, 16, limit), case.wdev)
+        M.mtp_draft(ctx, *case.inputs, kvd, case.K, ids, logits, stream=side)
+        torch.cuda.synchronize()
+        got.append(host(logits))
+    np.testing.assert_array_equal(*got)
+    for _ in range(50):       # pending entries left by the drafts above: refused each time
+        M.mtp_draft(ctx, *case.inputs, kvd, case.K, ids, logits, stream=side)
+        assert M.mtp_get_device_error(ctx) == M.MTP_ERR_DEVICE_ARGS
