@@ -577,7 +577,9 @@ mtp_status mtp_kv8_truncate(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv
  * packed tree): they move to slots seq_len[b] + j, are requantized to the
  * scales of the blocks they enter (as in mtp_kv8_append), and the other
  * pending entries are dropped.  At most 256 pending entries
- * (MTP_ERR_DEVICE_ARGS, as for a bad list; the request is then unchanged). */
+ * (MTP_ERR_DEVICE_ARGS, as for a bad list); a kept entry whose block id, or
+ * that of the block it would move to, lies outside the pool is
+ * MTP_ERR_CAPACITY.  The request is then unchanged. */
 mtp_status mtp_kv8_commit_path(mtp_ctx* ctx, void* stream, int B, const mtp_kv8* kv, const int32_t* keep,
                                int keep_stride, const int32_t* n_keep);
 

@@ -478,11 +478,6 @@ __global__ void __launch_bounds__(kEditThreads) kv8_edit_kernel(const Edit8Args 
     } else if (!good) {
       set_error(a.err, MTP_ERR_DEVICE_ARGS);
     }
-    // the last head's block publishes the lengths; all have read them
-    if (good && arrive_last(a.kv.arrive + b, a.n_kv)) {
-      a.kv.seq_len[b] = nl;
-      a.kv.pending[b] = 0;
-    }
     sh[0] = good;
     sh[1] = nl;
     sh[2] = L;
@@ -492,6 +487,24 @@ __global__ void __launch_bounds__(kEditThreads) kv8_edit_kernel(const Edit8Args 
   if (!sh[0]) return;
   const int nl = sh[1], L = sh[2], end = sh[3];
   const int32_t* row = a.kv.block_table + (long long)b * a.kv.max_blocks;
+  if (keep) {
+    // a kept entry that lies in a block outside the pool, or would move to one,
+    // would be lost: the request stays as it is
+    int lost = 0;
+    for (int j = tid; j < nl - L; j += kEditThreads) {
+      const int from = row[(L + keep[j]) >> 4], to = row[(L + j) >> 4];
+      lost |= from < 0 || from >= a.kv.num_blocks || to < 0 || to >= a.kv.num_blocks;
+    }
+    if (__syncthreads_or(lost)) {
+      if (tid == 0) set_error(a.err, MTP_ERR_CAPACITY);
+      return;
+    }
+  }
+  // the last head's block publishes the lengths; all have read them
+  if (tid == 0 && arrive_last(a.kv.arrive + b, a.n_kv)) {
+    a.kv.seq_len[b] = nl;
+    a.kv.pending[b] = 0;
+  }
   const int vec = a.hd / 16;
   for (int w = 0; w < 2; ++w) {
     uint4* pool = (uint4*)(w ? a.kv.v_pool : a.kv.k_pool);
@@ -505,8 +518,8 @@ __global__ void __launch_bounds__(kEditThreads) kv8_edit_kernel(const Edit8Args 
       for (int i = tid; i < n * vec; i += kEditThreads) {
         const int j = i / vec, e = i - j * vec, slot = L + keep[j];
         const long long t = tile_of(slot);
-        ((uint4*)kept)[i] = t >= 0 ? pool[(t * kBlk + (slot & 15)) * vec + e] : make_uint4(0, 0, 0, 0);
-        if (e == 0) kept_scale[j] = t >= 0 ? scale[t] : 0.0f;
+        ((uint4*)kept)[i] = pool[(t * kBlk + (slot & 15)) * vec + e];
+        if (e == 0) kept_scale[j] = scale[t];
       }
       __syncthreads();
       for (int bi = L >> 4; bi * kBlk < nl; ++bi) {
@@ -524,26 +537,24 @@ __global__ void __launch_bounds__(kEditThreads) kv8_edit_kernel(const Edit8Args 
         __syncthreads();
         for (int i = 0; i < kEditThreads / 32; ++i) m = fmaxf(m, red[i]);
         const long long t = tile_of(bi * kBlk);
-        if (t >= 0) {
-          uint16_t* tile = (uint16_t*)(pool + t * kBlk * vec);
-          const float was = s0 > 0 ? scale[t] : 0.0f;
-          const float now = fmaxf(was, e4m3_scale(m));
-          const float inv = now > 0.0f ? 1.0f / now : 0.0f;
-          if (was > 0.0f && now > was) {
-            for (int i = tid; i < s0 * (a.hd / 2); i += kEditThreads) {
-              const float2 x = e4m3_to_float2(tile[i]);
-              tile[i] = (uint16_t)e4m3_pack2(x.x * (was * inv), x.y * (was * inv));
-            }
+        uint16_t* tile = (uint16_t*)(pool + t * kBlk * vec);
+        const float was = s0 > 0 ? scale[t] : 0.0f;
+        const float now = fmaxf(was, e4m3_scale(m));
+        const float inv = now > 0.0f ? 1.0f / now : 0.0f;
+        if (was > 0.0f && now > was) {
+          for (int i = tid; i < s0 * (a.hd / 2); i += kEditThreads) {
+            const float2 x = e4m3_to_float2(tile[i]);
+            tile[i] = (uint16_t)e4m3_pack2(x.x * (was * inv), x.y * (was * inv));
           }
-          for (int i = tid; i < (s1 - s0) * (a.hd / 2); i += kEditThreads) {
-            const int j = j0 + i / (a.hd / 2);
-            const float2 x = e4m3_to_float2(((const uint16_t*)kept)[(long long)j0 * (a.hd / 2) + i]);
-            tile[s0 * (a.hd / 2) + i] =
-                (uint16_t)e4m3_pack2(x.x * kept_scale[j] * inv, x.y * kept_scale[j] * inv);
-          }
-          __syncthreads();
-          if (tid == 0) scale[t] = now;
         }
+        for (int i = tid; i < (s1 - s0) * (a.hd / 2); i += kEditThreads) {
+          const int j = j0 + i / (a.hd / 2);
+          const float2 x = e4m3_to_float2(((const uint16_t*)kept)[(long long)j0 * (a.hd / 2) + i]);
+          tile[s0 * (a.hd / 2) + i] =
+              (uint16_t)e4m3_pack2(x.x * kept_scale[j] * inv, x.y * kept_scale[j] * inv);
+        }
+        __syncthreads();
+        if (tid == 0) scale[t] = now;
         __syncthreads();
       }
     }

@@ -1124,3 +1124,58 @@ def test_two_streams_at_once():
     for (kv, q, out, ws, off), w in zip(sets, want):
         assert torch.equal(out, w)
     clean(ctx)
+
+
+# ----------------------------------------------------- limits and bad inputs
+
+def test_path_commit_of_entries_in_blocks_outside_the_pool():
+    """A kept entry's own block, or the one it would move to, has no place in the pool: reported, the request left as it
+    was.  Where only dropped entries lie in such a block, the path is committed and the block reported."""
+    M = M_()
+    rng = np.random.default_rng(71)
+    ctx = context(4, 2, 64, "bf16", max_batch=5)
+    kv, twin = make_cache(ctx, 5, 4, rng)
+    append_both(ctx, kv, twin, [12] * 5, rng)
+    M.mtp_kv8_commit(ctx, kv, i32([12] * 5))
+    for b in range(5):
+        twin.commit(b, 12)
+    append_both(ctx, kv, twin, [24] * 5, rng)             # slots 12 .. 35: blocks 0, 1, 2
+    table = kv.block_table.clone()
+    nb = kv.k_pool.shape[0]
+    kv.block_table[0, 1] = nb                             # every entry kept
+    kv.block_table[1, 2] = -1                             # kept entries come from block 2 only
+    kv.block_table[2, 0] = 2 ** 31 - 1                    # entries of block 2 would move into block 0
+    kv.block_table[3, 2] = nb + 7                         # block 2 holds dropped entries only
+    paths = [list(range(24)), [0, 1, 20, 23], [21, 22], [0, 2, 9], [1, 5, 23]]
+    keep = np.zeros((5, 24), np.int64)
+    for b, p in enumerate(paths):
+        keep[b, :len(p)] = p
+    M.mtp_kv8_commit_path(ctx, kv, i32(keep), i32([len(p) for p in paths]))
+    assert M.mtp_get_device_error(ctx) == M.MTP_ERR_CAPACITY
+    assert kv.seq_len.tolist() == [12, 12, 12, 15, 15] and kv.pending.tolist() == [24, 24, 24, 0, 0]
+    assert not kv.arrive.any()
+    lost = twin.table[3, 2]
+    left = [(w[lost].copy(), s[lost].copy()) for w, s in zip(twin.codes, twin.scale)]
+    for b in (3, 4):
+        twin.commit(b, len(paths[b]), paths[b])
+    for w in range(2):                                    # the block that could not be reached keeps its bytes
+        twin.codes[w][lost], twin.scale[w][lost] = left[w]
+    check_cache(ctx, kv, twin)
+    kv.block_table.copy_(table)
+    M.mtp_kv8_commit_path(ctx, kv, i32(keep), i32([24, 4, 2, 0, 0]))
+    for b in range(3):
+        twin.commit(b, len(paths[b]), paths[b])
+    check_cache(ctx, kv, twin)
+    clean(ctx)
+
+
+def test_a_path_commit_that_keeps_everything_reports_a_bad_block():
+    M = M_()
+    rng = np.random.default_rng(72)
+    ctx = context(2, 2, 128, "f32", max_batch=1)
+    kv, twin = make_cache(ctx, 1, 2, rng)
+    append_both(ctx, kv, twin, [20], rng)
+    kv.block_table[0, 1] = -1
+    M.mtp_kv8_commit_path(ctx, kv, i32(np.arange(20)[None]), i32([20]))
+    assert M.mtp_get_device_error(ctx) == M.MTP_ERR_CAPACITY
+    check_cache(ctx, kv, twin)
