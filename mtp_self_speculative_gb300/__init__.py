@@ -421,6 +421,8 @@ def _row_ptr(ctx: Context, t: torch.Tensor, name: str, rows: int, heads: int):
     context's dtype whose rows are contiguous (a slice of a packed [rows,
     width] projection, say)."""
     hd, dt = ctx.head_dim, ctx.dtype
+    if t.get_device() == ctx.device and t.dtype is dt and t.is_contiguous() and t.shape == (rows, heads, hd):
+        return t.data_ptr(), heads * hd
     if t.shape != (rows, heads, hd):
         raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, hd, tuple(t.shape)))
     if t.dtype is not dt:
@@ -515,17 +517,15 @@ class KVCache8:
 
     def _checked_struct(self, ctx: Context):
         """(struct, B, n_q, n_kv, head_dim).  The checks run again when a field
-        is another tensor, a tensor has other storage, or the context has
-        another configuration."""
-        kp, vp, ks, vs, bt, sl, pe, ar = fields = (self.k_pool, self.v_pool, self.k_scale, self.v_scale,
-                                                   self.block_table, self.seq_len, self.pending, self.arrive)
-        ptrs = (kp.data_ptr(), vp.data_ptr(), ks.data_ptr(), vs.data_ptr(), bt.data_ptr(), sl.data_ptr(),
-                pe.data_ptr(), ar.data_ptr())
+        was assigned, has other storage or another size than when they last
+        ran (the block table: another shape or layout), and for another
+        context."""
         done = self.__dict__.get("_checked")
-        if done is not None and done[0] == ptrs and done[3] is ctx.cfg:
-            f = done[1]
-            if (f[0] is kp and f[1] is vp and f[2] is ks and f[3] is vs and f[4] is bt and f[5] is sl and f[6] is pe
-                    and f[7] is ar):
+        if done is not None and done[3] is ctx.cfg and done[4] == ctx.device:
+            kp, vp, ks, vs, bt, sl, pe, ar = done[1]
+            if done[0] == (kp.data_ptr(), vp.data_ptr(), ks.data_ptr(), vs.data_ptr(), bt.data_ptr(), sl.data_ptr(),
+                           pe.data_ptr(), ar.data_ptr(), kp.nbytes, vp.nbytes, ks.nbytes, vs.nbytes, sl.nbytes,
+                           pe.nbytes, ar.nbytes, bt.shape) and bt.is_contiguous():
                 return done[2]
         c = ctx.cfg
         nb, B = int(self.k_pool.shape[0]), int(self.seq_len.shape[0])
@@ -543,8 +543,19 @@ class KVCache8:
                     _dev_ptr(ctx, self.pending, i32, "pending", (B,)),
                     _dev_ptr(ctx, self.arrive, i32, "arrive", (B,)), nb, int(self.block_table.shape[1]))
         got = (st, B, int(c.n_q_heads), int(c.n_kv_heads), int(c.head_dim))
-        self.__dict__["_checked"] = (ptrs, fields, got, c)
+        fields = kp, vp, ks, vs, bt, sl, pe, ar = (self.k_pool, self.v_pool, self.k_scale, self.v_scale,
+                                                   self.block_table, self.seq_len, self.pending, self.arrive)
+        seen = tuple(t.data_ptr() for t in fields) + tuple(t.nbytes for t in (kp, vp, ks, vs, sl, pe, ar)) + (bt.shape,)
+        self.__dict__["_checked"] = (seen, fields, got, c, ctx.device)
         return got
+
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_checked", None)
+        object.__setattr__(self, name, value)
+
+    def __getstate__(self):
+        """A copy (copy.deepcopy, pickle) is checked for itself."""
+        return {k: v for k, v in self.__dict__.items() if k != "_checked"}
 
 
 def mtp_kv8_append(ctx: Context, kv: KVCache8, k: torch.Tensor, v: torch.Tensor, row_offsets: torch.Tensor,

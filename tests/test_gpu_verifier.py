@@ -1179,3 +1179,37 @@ def test_a_path_commit_that_keeps_everything_reports_a_bad_block():
     M.mtp_kv8_commit_path(ctx, kv, i32(np.arange(20)[None]), i32([20]))
     assert M.mtp_get_device_error(ctx) == M.MTP_ERR_CAPACITY
     check_cache(ctx, kv, twin)
+
+
+def test_a_cache_is_checked_again_for_another_context_and_after_a_change():
+    """Its device, shapes and layout belong to what was checked; a copy is a cache of its own."""
+    import copy
+    M = M_()
+    rng = np.random.default_rng(73)
+    ctx = context(4, 2, 64, "bf16", max_batch=2)
+    kv, twin = make_cache(ctx, 2, 6, rng)
+    append_both(ctx, kv, twin, [20, 3], rng)
+    other = M.Context(0, ctx.cfg, None, device=1)
+    other.cfg = ctx.cfg
+    with pytest.raises(ValueError):
+        kv.struct(other)
+    two = copy.deepcopy(kv)
+    assert two.k_pool.data_ptr() != kv.k_pool.data_ptr() and two.struct(ctx).k_pool == two.k_pool.data_ptr()
+    M.mtp_kv8_rollback(ctx, two)
+    assert two.pending.tolist() == [0, 0] and kv.pending.tolist() == [20, 3]
+    kept = kv.block_table.clone()
+    kv.block_table.resize_(2, 3)
+    kv.block_table.copy_(kept[:, :3])
+    assert kv.struct(ctx).max_blocks == 3
+    append_both(ctx, kv, twin, [5, 5], rng)
+    check_cache(ctx, kv, twin)
+    kv.block_table.t_()
+    with pytest.raises(ValueError):
+        kv.struct(ctx)
+    kv.block_table.t_()
+    kv.arrive.resize_(1)
+    with pytest.raises(ValueError):
+        kv.struct(ctx)
+    kv.arrive.resize_(2)
+    kv.struct(ctx)
+    clean(ctx)

@@ -139,6 +139,53 @@ def test_wrappers_check_shapes_before_any_call():
         M.mtp_logits_process(ctx, x, torch.zeros(2, **i32), mask=torch.zeros(1, 4, **i32))
 
 
+def test_a_cache_is_checked_for_each_context_and_after_a_change(monkeypatch):
+    """What was checked belongs to a context's device and configuration and to the fields' shapes and layout (pointers
+    are not looked at here: the tensors are the CPU's)."""
+    import copy
+    import mtp_self_speculative_gb300 as M
+    checked = []
+
+    def pointer(ctx, t, dtype, name, shape=None):
+        checked.append((ctx.device, name))
+        if (dtype is not None and t.dtype is not dtype) or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+            raise ValueError(name)
+        return t.data_ptr()
+
+    monkeypatch.setattr(M, "_dev_ptr", pointer)
+    ctx, other = cpu_context(), cpu_context()
+    other.cfg, ctx.device, other.device = ctx.cfg, 0, 1
+    kv = M.KVCache8.empty(ctx, 3, torch.zeros(2, 6, dtype=torch.int32))
+    assert kv.struct(ctx).max_blocks == 6
+    checked.clear()
+    kv.struct(other)
+    assert {d for d, _ in checked} == {1} and len(checked) == 8
+    two = copy.deepcopy(kv)
+    assert two.struct(ctx).k_pool == two.k_pool.data_ptr() != kv.k_pool.data_ptr()
+    kv.block_table.resize_(2, 3)
+    assert kv.struct(ctx).max_blocks == 3
+    for change, back in ((lambda: kv.block_table.t_(), lambda: kv.block_table.t_()),
+                         (lambda: kv.pending.resize_(1), lambda: kv.pending.resize_(2)),
+                         (lambda: kv.v_scale.resize_(3, 1), lambda: kv.v_scale.resize_(3, 2)),
+                         (lambda: setattr(kv, "v_scale", kv.v_scale.view(torch.int32)),
+                          lambda: setattr(kv, "v_scale", kv.v_scale.view(torch.float32)))):
+        change()
+        with pytest.raises(ValueError):
+            kv.struct(ctx)
+        back()
+        kv.struct(ctx)
+    kv.block_table = torch.zeros(2, 2, dtype=torch.int32)
+    assert kv.struct(ctx).max_blocks == 2
+    kv.block_table.t_()                       # the same shape
+    with pytest.raises(ValueError):
+        kv.struct(ctx)
+    kv.block_table.t_()
+    small = cpu_context(n_kv_heads=1)
+    small.device = 0
+    with pytest.raises(ValueError):
+        kv.struct(small)
+
+
 def test_processed_logits_of_a_hand_made_row():
     z = np.array([2.0, -2.0, 1.0, 0.5, 3.0])
     counts = np.array([1, 2, 0, -2 ** 31, 0], dtype=np.int64).astype(np.int32)
