@@ -84,7 +84,7 @@ class Context:
     def __init__(self, handle: int, cfg: MTPConfig, weights: Optional[Dict[str, torch.Tensor]],
                  device: Optional[int] = None):
         self.handle = handle
-        self.cfg = cfg
+        self.cfg = MTPConfig.from_buffer_copy(cfg)   # the library's copy does not change either
         self.weights = weights
         self.device = device
         self.dtype, self.head_dim, self.vocab = torch_dtype(cfg.dtype), int(cfg.head_dim), int(cfg.vocab)

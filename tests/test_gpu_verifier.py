@@ -1213,3 +1213,21 @@ def test_a_cache_is_checked_again_for_another_context_and_after_a_change():
     kv.arrive.resize_(2)
     kv.struct(ctx)
     clean(ctx)
+
+
+def test_a_context_keeps_the_configuration_it_was_made_with():
+    """Changing the struct for the next context changes nothing about the first."""
+    M = M_()
+    rng = np.random.default_rng(74)
+    cfg = M.make_config(hidden=256, n_q_heads=4, n_kv_heads=2, head_dim=64, ffn=256, vocab=100, dtype="bf16", max_batch=2, max_k=5)
+    ctx = M.mtp_init(cfg)
+    cfg.head_dim, cfg.n_kv_heads, cfg.vocab = 128, 4, 50
+    M.mtp_init(cfg)
+    kv, twin = make_cache(ctx, 2, 3, rng)
+    assert tuple(kv.k_pool.shape[1:]) == (2, 16, 64)
+    append_both(ctx, kv, twin, [20, 3], rng)
+    check_cache(ctx, kv, twin)
+    counts = torch.zeros(2, 100, dtype=torch.int32, device="cuda")
+    M.mtp_token_counts_add(ctx, counts, i32([[99], [0]]), i32([1, 1]))
+    assert counts[0, 99] == 1 and int(counts.sum()) == 2
+    clean(ctx)

@@ -186,6 +186,14 @@ def test_a_cache_is_checked_for_each_context_and_after_a_change(monkeypatch):
         kv.struct(small)
 
 
+def test_a_context_keeps_the_configuration_it_was_made_with():
+    import mtp_self_speculative_gb300 as M
+    cfg = M.make_config(hidden=256, n_q_heads=8, n_kv_heads=2, head_dim=64, ffn=256, vocab=100, dtype="bf16", max_batch=4)
+    ctx = M.Context(0, cfg, None)
+    cfg.head_dim, cfg.vocab = 128, 7
+    assert (ctx.cfg.head_dim, ctx.cfg.vocab, ctx.head_dim, ctx.vocab) == (64, 100, 64, 100)
+
+
 def test_processed_logits_of_a_hand_made_row():
     z = np.array([2.0, -2.0, 1.0, 0.5, 3.0])
     counts = np.array([1, 2, 0, -2 ** 31, 0], dtype=np.int64).astype(np.int32)
