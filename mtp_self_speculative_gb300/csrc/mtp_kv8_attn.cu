@@ -50,6 +50,7 @@ constexpr int kA8MaxB = 1024;      // requests of a call (prefix sums in shared 
 constexpr int kA8MinShare = 16;    // cache blocks of a thread block's share at least
 constexpr int kA8MaxCols = 32;     // columns of a tile
 constexpr float kA8Least = -3.4028235e38f;   // the reference of a column that has seen nothing
+constexpr float kA8Coarse = 16777216.0f;     // from 2^24 on float32 holds scores in steps of two and more
 
 struct Attn8Args {
   const void* q;
@@ -491,6 +492,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
       return (uint32_t)a.mask[(long long)(o0 + i) * a.mask_words + (j >> 5)] >> (j & 31) & 1u;
     };
 
+    bool coarse = false;   // some column's reference is kA8Coarse or more (the same for the whole warp)
     for (int it = 0; it < n_my; ++it) {
       cp_wait<S::kStages - 2>();
       __syncwarp();
@@ -541,7 +543,10 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
       // maximum across the lanes and no rescaling.  When one is above, r
       // becomes 9 below the maximum, a whole number: fp16 then keeps 11 bits
       // of weights down to 2^-23 of the largest.  (Beyond 2^20 that sum would
-      // round, and r is the maximum itself.)
+      // round, and r is the maximum itself.)  That maximum is a product rounded
+      // to float32, up to half a step off: from kA8Coarse on the scores are
+      // rounded like it before r is taken off, and r follows every maximum;
+      // else the largest weights would be 2^8, 2^16, .. and pass fp16's range.
       float fac[JB][NT][2];
       bool above = false;
 #pragma unroll
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
             }
             above |= fmaf(fmaxf(sc[j][nt][e], sc[j][nt][2 + e]), f, -m_run[nt][e]) > 15.0f;
           }
-      if (__any_sync(0xffffffffu, above)) {
+      if (__any_sync(0xffffffffu, above) || coarse) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float alpha[2];
@@ -579,6 +584,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
             alpha[e] = ex2(m_run[nt][e] - rn);
             m_run[nt][e] = rn;
             l_run[nt][e] *= alpha[e];
+            coarse |= fabsf(rn) >= kA8Coarse && rn != kA8Least;
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -587,6 +593,21 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
             o[nt][mt][2] *= alpha[0];
             o[nt][mt][3] *= alpha[1];
           }
+        }
+        coarse = __any_sync(0xffffffffu, coarse);
+        if (coarse) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (fabsf(m_run[nt][e]) >= kA8Coarse) {
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                  sc[j][nt][e] = __fmul_rn(sc[j][nt][e], fac[j][nt][e]);
+                  sc[j][nt][2 + e] = __fmul_rn(sc[j][nt][2 + e], fac[j][nt][e]);
+                  fac[j][nt][e] = 1.0f;
+                }
+              }
         }
       }
 #pragma unroll

@@ -1231,3 +1231,81 @@ def test_a_context_keeps_the_configuration_it_was_made_with():
     M.mtp_token_counts_add(ctx, counts, i32([[99], [0]]), i32([1, 1]))
     assert counts[0, 99] == 1 and int(counts.sum()) == 2
     clean(ctx)
+
+
+@pytest.mark.parametrize("dtype,n_q,n_kv,hd", [("bf16", 4, 2, 128), ("f32", 4, 2, 128), ("bf16", 8, 1, 64), ("f32", 2, 2, 64)])
+@pytest.mark.parametrize("rows", [1, 5])
+def test_scores_beyond_the_24_bits_of_a_float(dtype, n_q, n_kv, hd, rows):
+    """Scores so large that float32 holds them in steps of many whole units: the result is still a weighted mean of the
+    values seen, the entry itself where one leads by more than the scores' own rounding, and lse follows the scores.
+
+    A score is off by 2^-18 S at most (S as above), so an entry that leads the next by 2^-16 S and by 64 units leads
+    it by more than 30 units when computed: the others weigh less than e^-30 each, 200 of them below 2^-34.  Its own
+    weight is off by 2^-11 where weights are held in 11 bits."""
+    rng = np.random.default_rng(rows + hd)
+    ctx = context(n_q, n_kv, hd, dtype, max_batch=3)
+    new = [rows, 1, rows]
+    for qsize in (1e6, 3e6, 1e7, 3e7, 1e8, 3e8, 1e9, 1e12, 1e20, 1e30):
+        kv, twin = filled(ctx, [200, 77, 0], new, rng)
+        off = np.concatenate([[0], np.cumsum(new)])
+        q, q64 = normal(rng, (int(off[-1]), n_q, hd), dtype, qsize)
+        got, lse = attend(ctx, kv, q, off, rows)
+        clean(ctx)
+        sure = 0
+        for b in range(3):
+            n, L = new[b], int(twin.seq_len[b] + twin.pending[b])
+            k, v = twin.values(b, 0, L)
+            _, ls, _, size = V.attention(q64[off[b]:off[b + 1]], k, v, V.causal(n, L), hd ** -0.5)
+            close(lse[off[b]:off[b + 1]], ls, 2.0 ** -18 * size + 2.0 ** -20 * np.abs(ls), "lse")
+            for i in range(n):
+                seen = L - n + i + 1
+                for h in range(n_q):
+                    g, o = h // (n_q // n_kv), got[off[b] + i, h]
+                    lo, hi = v[:seen, g].min(0), v[:seen, g].max(0)
+                    # a mean in float32, and the type's half step
+                    room = (2.0 ** -9 + HALF_STEP[dtype]) * np.abs(v[:seen, g]).max()
+                    assert np.all(o >= lo - room) and np.all(o <= hi + room), (qsize, b, i, h)
+                    z = np.sort(hd ** -0.5 * (k[:seen, g] @ q64[off[b] + i, h]))[::-1]
+                    if seen == 1 or z[0] - z[1] > 2.0 ** -16 * size[i, h] + 64:
+                        top = int(np.argmax(k[:seen, g] @ q64[off[b] + i, h]))
+                        w = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -20
+                        room = (HALF_STEP[dtype] + w) * np.abs(v[top, g]) + 2.0 ** -20 * np.abs(v[:seen, g]).max()
+                        assert np.all(np.abs(o - v[top, g]) <= room), (qsize, b, i, h)
+                        sure += 1
+        assert sure >= sum(new) * n_q * 3 // 4
+
+
+@pytest.mark.parametrize("dtype,hd,rows", [("bf16", 128, 1), ("f32", 128, 1), ("bf16", 64, 6), ("f32", 64, 3)])
+def test_close_scores_far_from_zero(dtype, hd, rows):
+    """Every key has the same large product with the query and one of its own within 28 units: what float32 keeps of the
+    difference decides, the result is a weighted mean of the values seen and lse follows the scores."""
+    rng = np.random.default_rng(rows)
+    ctx = context(8, 2, hd, dtype, max_batch=2)
+    new, off = [rows, rows], np.array([0, rows, 2 * rows])
+    for e in range(18, 36):
+        kv, twin = filled(ctx, [150, 40], new, rng)
+        held = twin.scale[0] > 0
+        twin.codes[0][:] = 0
+        twin.codes[0][held, :, 0] = V.e4m3_encode(1.0)
+        twin.codes[0][held, :, 1] = V.e4m3_encode(rng.uniform(-28, 28, (int(held.sum()), 16)))
+        twin.scale[0][held] = 1.0
+        for b, L in ((0, 150 + rows), (1, 40 + rows)):      # nothing behind the last entry
+            if L % 16:
+                twin.codes[0][twin.table[b, L // 16], :, L % 16:] = 0
+        kv.k_pool.copy_(torch.from_numpy(twin.codes[0]))
+        kv.k_scale.copy_(torch.from_numpy(twin.scale[0]))
+        q64 = np.zeros((2 * rows, 8, hd))
+        q64[..., 0] = 2.0 ** e * rng.integers(128, 256, (2 * rows, 8)) / 128 * rng.choice([-1, 1], (2 * rows, 8))
+        q64[..., 1] = 1.0
+        got, lse = attend(ctx, kv, torch.from_numpy(q64).to(TORCH[dtype]).cuda(), off, rows, scale=1.0)
+        clean(ctx)
+        for b in range(2):
+            L = int(twin.seq_len[b] + twin.pending[b])
+            k, v = twin.values(b, 0, L)
+            _, ls, _, size = V.attention(q64[off[b]:off[b + 1]], k, v, V.causal(rows, L), 1.0)
+            close(lse[off[b]:off[b + 1]], ls, 2.0 ** -18 * size + 2.0 ** -20 * np.abs(ls), "lse")
+            for i in range(rows):
+                seen = v[:L - rows + i + 1].repeat(4, 1)
+                room = (2.0 ** -9 + HALF_STEP[dtype]) * np.abs(seen).max((0, 2))[:, None]
+                o = got[off[b] + i]
+                assert np.all(o >= seen.min(0) - room) and np.all(o <= seen.max(0) + room), (e, b, i)
