@@ -662,7 +662,7 @@ typedef struct {
                                   not overlap them otherwise                   */
   const int32_t* counts;       /* [B, vocab] (mtp_token_counts_add), or NULL   */
   const int32_t* drafts;       /* [B, drafts_stride] or NULL; needs counts     */
-  int drafts_stride;           /* n_b - 1 <= drafts_stride with drafts         */
+  int drafts_stride;           /* >= 0; n_b - 1 <= drafts_stride with drafts   */
   const float* repetition;     /* [B] finite, > 0, or NULL (1); needs counts   */
   const float* frequency;      /* [B] finite, or NULL (0); needs counts        */
   const float* presence;       /* [B] finite, or NULL (0); needs counts        */

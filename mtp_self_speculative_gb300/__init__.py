@@ -743,7 +743,9 @@ def mtp_logits_process(ctx: Context, logits: torch.Tensor, row_offsets: torch.Te
         a.counts = _dev_ptr(ctx, counts, i32, "counts", (B, V))
     if drafts is not None:
         a.drafts_stride = drafts.shape[-1]
-        a.drafts = _dev_ptr(ctx, drafts, i32, "drafts", (B, a.drafts_stride))
+        # (drafts of no width have no memory: with counts, any address says that
+        # they are given, so that a request's second row is refused)
+        a.drafts = _dev_ptr(ctx, drafts, i32, "drafts", (B, a.drafts_stride)) or (a.counts and a.row_offsets)
     one = (B,)
     if repetition is not None:
         a.repetition = _dev_ptr(ctx, repetition, f32, "repetition", one)

@@ -259,7 +259,7 @@ mtp_status mtp_logits_process(mtp_ctx* ctx, void* stream, const mtp_logits_args*
   if (a.B < 1 || a.B > ctx->cfg.max_batch || a.B > 65535 || a.num_rows < 0 || !a.row_offsets || !a.logits || !a.out)
     return MTP_ERR_INVALID;
   if ((a.drafts || a.repetition || a.frequency || a.presence) && !a.counts) return MTP_ERR_INVALID;
-  if (a.drafts && a.drafts_stride < 1) return MTP_ERR_INVALID;
+  if (a.drafts && a.drafts_stride < 0) return MTP_ERR_INVALID;
   if (a.bias_offsets && (a.num_bias < 0 || (a.num_bias > 0 && (!a.bias_tokens || !a.bias_values))))
     return MTP_ERR_INVALID;
   if (a.mask && (!a.mask_index || a.num_masks < 1)) return MTP_ERR_INVALID;

@@ -1309,3 +1309,22 @@ def test_close_scores_far_from_zero(dtype, hd, rows):
                 room = (2.0 ** -9 + HALF_STEP[dtype]) * np.abs(seen).max((0, 2))[:, None]
                 o = got[off[b] + i]
                 assert np.all(o >= seen.min(0) - room) and np.all(o <= seen.max(0) + room), (e, b, i)
+
+
+def test_logits_with_drafts_of_no_width():
+    """No drafts (K = 0): one row a request; a second row has no draft to follow and is refused."""
+    M = M_()
+    rng = np.random.default_rng(75)
+    ctx, z, z64, kw, ref = logits_case(rng, 2, 300, "f32", [1, 1], drafts=False)
+    none = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    want = M.mtp_logits_process(ctx, z, i32(ref["off"]), torch.full_like(z, 3.0), **kw)
+    got = M.mtp_logits_process(ctx, z, i32(ref["off"]), torch.full_like(z, 3.0), drafts=none, **kw)
+    clean(ctx)
+    assert torch.equal(got, want)
+    out = torch.full_like(z, 3.0)
+    M.mtp_logits_process(ctx, z, i32([0, 2, 3]), out, drafts=none, **kw)
+    assert M.mtp_get_device_error(ctx) == M.MTP_ERR_DEVICE_ARGS
+    assert bool((out[:2] == 3).all()) and bool((out[2] != 3).any())
+    M.mtp_logits_process(ctx, z, i32([0, 2, 3]), out, drafts=none)         # nothing is counted: no penalties
+    clean(ctx)
+    assert torch.equal(out[:3], z[:3])
