@@ -1328,3 +1328,48 @@ def test_logits_with_drafts_of_no_width():
     M.mtp_logits_process(ctx, z, i32([0, 2, 3]), out, drafts=none)         # nothing is counted: no penalties
     clean(ctx)
     assert torch.equal(out[:3], z[:3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_appended_keys_and_the_attention_over_them(dtype):
+    """Append and attend step by step: every code is the oracle's or the next one, and the attention over the codes that
+    the cache holds is within its own tolerance, with no exceptions; then the draft rows are committed as accepted."""
+    M = M_()
+    rng = np.random.default_rng(76)
+    ctx = context(8, 2, 64, dtype, max_batch=3)
+    kv, twin = make_cache(ctx, 3, 8, rng)
+    tab, ws = M.RopeTable(64), M.Attention8Workspace(ctx)
+    for step in range(5):
+        new = [5, 5, int(rng.integers(1, 6))]
+        off = np.concatenate([[0], np.cumsum(new)])
+        T = int(off[-1])
+        (q, q64), (k, k64), (v, v64) = (normal(rng, (T, n, 64), dtype) for n in (8, 2, 2))
+        pos = np.concatenate([twin.seq_len[b] + np.arange(new[b]) for b in range(3)])
+        q_out = torch.empty_like(q)
+        M.mtp_kv8_append(ctx, kv, k, v, i32(off), q=q, q_out=q_out, positions=i32(pos), rope=tab)
+        got, lse = attend(ctx, kv, q_out, off, 5, ws=ws)
+        clean(ctx)
+        want_k = V.rope(k64, pos)
+        for b in range(3):
+            start = int(twin.seq_len[b])
+            twin.append(b, want_k[off[b]:off[b + 1]], v64[off[b]:off[b + 1]])
+            for slot in range(start, start + new[b]):
+                blk, s = twin.table[b, slot // 16], slot % 16
+                for w, (pool, scale) in enumerate(((kv.k_pool, kv.k_scale), (kv.v_pool, kv.v_scale))):
+                    ds, os_ = scale[blk].double().cpu().numpy()[:, None], twin.scale[w][blk][:, None]
+                    dv, ov = V.VALUES[pool[blk, :, s].cpu().numpy()] * ds, V.VALUES[twin.codes[w][blk, :, s]] * os_
+                    if w:
+                        np.testing.assert_array_equal(dv, ov)
+                    else:
+                        assert np.all(np.abs(dv - ov) <= np.maximum(2.0 ** -3 * np.maximum(np.abs(dv), np.abs(ov)),
+                                                                    2.0 ** -9 * np.maximum(ds, os_)))
+            for blk in twin.table[b, start // 16:(start + new[b] + 15) // 16]:
+                for w, (pool, scale) in enumerate(((kv.k_pool, kv.k_scale), (kv.v_pool, kv.v_scale))):
+                    twin.codes[w][blk], twin.scale[w][blk] = pool[blk].cpu().numpy(), scale[blk].double().cpu().numpy()
+        compare_attention(ctx, twin, host(q_out), off, got, lse, dtype)
+        acc = rng.integers(0, 5, 3)
+        M.mtp_kv8_commit_accepted(ctx, kv, i32(acc), extra=1)
+        for b in range(3):
+            twin.commit(b, min(int(acc[b]) + 1, new[b]))
+        check_cache(ctx, kv, twin)
+    clean(ctx)
