@@ -448,7 +448,7 @@ typedef enum { MTP_ROPE_HALF = 0, MTP_ROPE_INTERLEAVED = 1 } mtp_rope_layout;
  *           rotary_dim - 1), c(b) = rotary_dim ln(L0 / (2pi b)) / (2 ln theta)
  *           (hi - lo at least 0.001), and the rotated elements are multiplied
  *           by 0.1 ln s + 1 (1 for s <= 1)
- * magnitude, if not 0, replaces the factor on the rotated elements. */
+ * magnitude (>= 0), if not 0, replaces the factor on the rotated elements. */
 typedef enum { MTP_ROPE_SCALE_NONE = 0, MTP_ROPE_SCALE_LINEAR = 1, MTP_ROPE_SCALE_PARTS = 2,
                MTP_ROPE_SCALE_YARN = 3 } mtp_rope_scaling;
 
@@ -508,7 +508,8 @@ mtp_status mtp_rope(mtp_ctx* ctx, void* stream, int T, int heads, const void* x,
  *   k_scale, v_scale: [num_blocks, n_kv] float32, one scale for a block of 16
  *                     tokens and a head: 0 or a power of two of at least
  *                     2^-126; an entry's value is code * scale, which bf16
- *                     holds exactly.
+ *                     holds exactly (but for the smallest codes of scales
+ *                     2^-126 and 2^-125).
  *   block_table, seq_len, pending: as in mtp_kv.
  *   arrive:           [B] int32, zeroed once by the caller and left zero by
  *                     every call (the calls count their thread blocks in it).
@@ -533,8 +534,9 @@ typedef struct {
  * entries: slots seq_len[b] + pending[b] on, then pending[b] grows by the row
  * count.  With rope (and positions [T]) k is rotated first, in float32,
  * without rounding in between; q [T, n_q, head_dim], if not NULL, is rotated
- * by the same table into q_out (dtype; may be q itself).  rope NULL: k is
- * stored as given, and q must be NULL.
+ * by the same table into q_out (dtype; may be q itself with the same stride,
+ * but not overlap the inputs otherwise).  rope NULL: k is stored as given, and
+ * q must be NULL.
  *   Quantization, per (block, kv head), K and V apart: the scale becomes the
  * smallest power of two s with max|x| <= 448 s over the new finite values, or
  * stays if it was larger and the block held entries; entries it held are
@@ -554,8 +556,9 @@ mtp_status mtp_kv8_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_
                           int64_t q_out_stride, const mtp_kv8* kv);
 
 /* Read entries back: row row_offsets[b] + i of k_out and v_out ([T, n_kv,
- * head_dim] bf16, whatever the dtype: bf16 holds every entry) receives slot
- * start[b] + i.  The slots must be held (below seq_len[b] + pending[b]; else
+ * head_dim] bf16, whatever the dtype) receives slot start[b] + i, exactly, or
+ * rounded to bf16 where that lies below its smallest number (scales of 2^-126
+ * and 2^-125).  The slots must be held (below seq_len[b] + pending[b]; else
  * MTP_ERR_DEVICE_ARGS and that request's rows are left as they were).  Rows
  * outside row_offsets are left as they were.  k_out and v_out: 16-byte
  * aligned. */
@@ -601,8 +604,15 @@ size_t mtp_kv8_attention_workspace_bytes(const mtp_ctx* ctx);
  * words (mask [T, mask_words] int32, bit j of word j / 32; bits from n_b on
  * are ignored).  A row that sees nothing gives zeros and lse = -inf.  NaN
  * entries reach only the rows that see them.  out [T, n_q, head_dim]
- * contiguous, dtype; lse [T, n_q] float32 or NULL: the natural logarithm of
- * the softmax sum.  Sums, maxima and products are held in float32.
+ * contiguous, dtype, must not overlap q; lse [T, n_q] float32 or NULL: the
+ * natural logarithm of the softmax sum.
+ *   Scores, maxima and sums are held in float32.  The products' operands are
+ * fp16: bf16 heads' queries (exact, but for elements below 2^-31 of the row's
+ * largest) and softmax weights in one number (11 bits), float32 heads' in two
+ * (22 bits); the normalising sum takes the weights before that rounding.
+ * Weights are relative to a reference up to 15 (powers of two) below the
+ * largest score: values of 2^96 and more may pass float32's range before they
+ * are normalised.  Scores must lie within that range.
  *   max_rows: at least every n_b (1..256); mask_words >= ceil(max_rows / 32)
  * with a mask.  scale: finite, > 0.  B: at most 1024.  Rows outside
  * row_offsets are left as they were.  Device errors: MTP_ERR_DEVICE_ARGS (bad offsets, n_b >
@@ -625,7 +635,12 @@ mtp_status mtp_kv8_attention(mtp_ctx* ctx, void* stream, int B, int T, const int
  * back with mtp_kv8_commit_accepted and the others.  B: at most 1024; the
  * persistent kernel is not used.  ws: mtp_draft_kv8_workspace_bytes(ctx) bytes
  * (0 for a NULL context or one without weights), 256-byte aligned, not
- * initialised, one per call that may run at the same time. */
+ * initialised.  As with mtp_draft, the drafts of one context share its
+ * activations and must be ordered by the caller (one stream, or events),
+ * graphs that contain them included.  The attention runs on the float32 queries
+ * of the head: float32 heads as in mtp_kv8_attention, bf16 heads with queries
+ * and weights in one fp16 number (11 bits; mtp_draft's tensor-core attention
+ * holds them in bf16, 8 bits). */
 size_t mtp_draft_kv8_workspace_bytes(const mtp_ctx* ctx);
 mtp_status mtp_draft_kv8(mtp_ctx* ctx, void* stream, int B, const void* hidden, const void* embeds,
                          const int32_t* positions, const mtp_kv8* kv, int K, const int32_t* chain_ids,

@@ -670,8 +670,8 @@ def mtp_kv8_attention(ctx: Context, kv: KVCache8, q: torch.Tensor, row_offsets: 
 
 
 class Draft8Workspace:
-    """Scratch of mtp_draft_kv8; calls that may run at the same time need one
-    each."""
+    """Scratch of mtp_draft_kv8.  Drafts of one context share its activations
+    too, so they are ordered by the caller, on one workspace or several."""
 
     def __init__(self, ctx: Context):
         n = int(_clib.mtp_draft_kv8_workspace_bytes(ctx.handle))

@@ -13,9 +13,12 @@
 //   O^T[16 dims, 8 cols]  += V^T[16, 16 tokens] P^T
 // e4m3 codes convert to fp16 exactly; the block scales multiply the float32
 // accumulators.  Queries are scaled per column by a power of two into fp16's
-// range (bf16 queries are then exact), P is held as 2^14 p (11 bits).  Float32
+// range (bf16 queries are then exact).  P is held relative to the reference, 2^8
+// to 2^15 at its largest (1 for scores beyond 2^20), in 11 bits down to 2^-22
+// (2^-14) of the largest and in steps of 2^-32 (2^-24) of it below: fp16 has more
+// bits than bf16 at the same rate, and codes become fp16 exactly.  Float32
 // heads split both Q and P into a high and a low half (22 bits) and issue each
-// product twice.  P^T comes out of the S^T accumulators with one movmatrix per
+// product twice.  The normalising sum takes the weights unrounded.  P^T comes out of the S^T accumulators with one movmatrix per
 // 8 x 8; V is read 4 tokens x 16 dims per lane and its bytes are interleaved
 // in registers, so no transposed copy of V exists anywhere.
 //
@@ -33,11 +36,13 @@
 // 72 us of a call.
 //
 // Memory bounds decoding batches: 64 requests of up to 8192 entries (494 MB)
-// 88 us, 5.6 TB/s; 128 of up to 4096 (542 MB) 95 us.  One request of 32768
-// entries takes 21 us, of which 4 are the join and as much the way to the first
-// data.  Draft rows add products: 16 x 6 rows over up to 4096 entries 30 us, at
-// two warps per scheduler bound by the products' latencies; 8 x 61 rows 110 us,
-// 166 TFLOP/s.
+// 88-94 us, 5.3-5.6 TB/s; 128 of up to 4096 (542 MB) 95 us.  One request of
+// 32768 entries takes 21 us, of which 4 are the join and as much the way to the
+// first data.  Draft rows add products: 16 x 6 rows over up to 4096 entries 30.6
+// us, at two warps per scheduler bound by the products' latencies.  Many rows
+// are far from what the machine can do (8 x 61 rows 108 us, 169 TFLOP/s, floor
+// about 10 us): each tile of at most 32 columns reads and converts the cache
+// again.
 #include <math.h>
 
 #include "mtp_kv8.cuh"
@@ -172,8 +177,9 @@ template <> struct Quad<uint16_t> {
 template <int HD, int NT, int SPLIT>
 struct Attn8Shape {
   // Cache blocks of a step.  Wide tiles have the registers for one (two spill
-  // at NT = 3 and 4: 16 x 6 rows 52.6 -> 50.1 us); one column tile gains
-  // from the longer softmax step.
+  // more at NT = 3 and 4: 16 x 6 rows 52.6 -> 50.1 us; with one, NT = 3 and 4
+  // of 128-wide heads still spill 8 and 24 bytes in bf16, 20 and 68 in
+  // float32); one column tile gains from the longer softmax step.
   static constexpr int JB = NT == 1 ? 2 : 1;
   static constexpr int kStep = kBlk * JB;                  // tokens of a step
   static constexpr int kTile = kStep * HD;                 // bytes of a staged K (or V) tile
@@ -542,7 +548,7 @@ __global__ void __launch_bounds__(kA8Threads, (Attn8Shape<HD, NT, SPLIT>::kBlock
       // score is at most r + 15 (fp16 holds 2^15.9), so most steps need no
       // maximum across the lanes and no rescaling.  When one is above, r
       // becomes 9 below the maximum, a whole number: fp16 then keeps 11 bits
-      // of weights down to 2^-23 of the largest.  (Beyond 2^20 that sum would
+      // of weights down to 2^-22 of the largest.  (Beyond 2^20 that sum would
       // round, and r is the maximum itself.)  That maximum is a product rounded
       // to float32, up to half a step off: from kA8Coarse on the scores are
       // rounded like it before r is taken off, and r follows every maximum;

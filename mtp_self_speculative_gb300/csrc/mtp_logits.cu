@@ -10,9 +10,11 @@
 // the factor and offset that its counts and biases make stay in registers while
 // it walks over the request's rows, two of them in flight, and a draft changes
 // its token's on the way.  Memory would bound it (64 requests x 6 rows of 151936
-// with counts, biases and masks: 274 MB, 40 us); it takes 70 us, 3.9 TB/s, since
-// selects and bit tests run at half rate and fill half of their pipe.  1 x 6
-// rows: 4.5 us.
+// with counts, biases and masks: 274 MB, 40 us); it takes 70 us, 3.9 TB/s, with
+// nothing saturated: selects and bit tests keep the half-rate pipe half busy,
+// 46 % of the warps are active at 64 registers a thread (bf16 vectors; 28 bytes
+// are spilled, eight thread blocks per SM instead of six), and the loads of
+// two rows ahead do not hide their latency.  1 x 6 rows: 4.5 us.
 #include "mtp_kv8.cuh"
 
 namespace mtp {

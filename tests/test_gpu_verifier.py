@@ -1373,3 +1373,29 @@ def test_appended_keys_and_the_attention_over_them(dtype):
             twin.commit(b, min(int(acc[b]) + 1, new[b]))
         check_cache(ctx, kv, twin)
     clean(ctx)
+
+
+def test_entries_below_bf16_are_read_back_rounded():
+    """Scales of 2^-124 and more: every entry exactly.  2^-126 and 2^-125: the smallest codes lie below bf16's smallest
+    number and are rounded to it."""
+    M = M_()
+    rng = np.random.default_rng(77)
+    ctx = context(2, 2, 64, "f32", max_batch=4)
+    kv, twin = make_cache(ctx, 4, 1, rng)
+    top = np.array([448.0 * 2.0 ** -126, 448.0 * 2.0 ** -125, 448.0 * 2.0 ** -124, 1.0])
+    rows = np.repeat(top, 16)[:, None, None] * 2.0 ** rng.uniform(-22, 0, (64, 2, 64)) * rng.choice([-1, 1], (64, 2, 64))
+    rows[::16, :, 0] = top[:, None]
+    t = torch.from_numpy(rows).float()
+    M.mtp_kv8_append(ctx, kv, t.cuda(), t.cuda(), i32(np.arange(5) * 16))
+    for b in range(4):
+        twin.append(b, t[16 * b:16 * b + 16].double().numpy(), t[16 * b:16 * b + 16].double().numpy())
+    check_cache(ctx, kv, twin)
+    out = [torch.empty(64, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    M.mtp_kv8_read(ctx, kv, i32([0] * 4), i32(np.arange(5) * 16), *out)
+    clean(ctx)
+    for b in range(4):
+        assert (twin.scale[0][twin.table[b, 0]] == (top[b] / 448 if b < 3 else 2.0 ** -8)).all()
+        for got, want in zip(out, twin.values(b, 0, 16)):
+            assert torch.equal(got[16 * b:16 * b + 16].cpu(), torch.from_numpy(want).float().bfloat16())
+            if b >= 2:
+                np.testing.assert_array_equal(host(got[16 * b:16 * b + 16]), want)
