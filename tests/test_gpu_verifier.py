@@ -1399,3 +1399,34 @@ def test_entries_below_bf16_are_read_back_rounded():
             assert torch.equal(got[16 * b:16 * b + 16].cpu(), torch.from_numpy(want).float().bfloat16())
             if b >= 2:
                 np.testing.assert_array_equal(host(got[16 * b:16 * b + 16]), want)
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("f32", 64)])
+def test_path_commit_of_the_most_entries(dtype, hd):
+    """256 pending entries, all kept or every second one; 257 are refused."""
+    M = M_()
+    rng = np.random.default_rng(78)
+    ctx = context(2, 2, hd, dtype, max_batch=3)
+    kv, twin = make_cache(ctx, 3, 18, rng)
+    append_both(ctx, kv, twin, [7, 16, 0], rng, 8.0)
+    M.mtp_kv8_commit(ctx, kv, kv.pending)
+    for b, n in enumerate([7, 16, 0]):
+        twin.commit(b, n)
+    for n in (100, 156):
+        append_both(ctx, kv, twin, [n, n, n + n // 156], rng, 1.0 + n)
+    keep = np.zeros((3, 256), np.int64)
+    keep[0], keep[1, :128] = np.arange(256), np.arange(1, 256, 2)
+    M.mtp_kv8_commit_path(ctx, kv, i32(keep), i32([256, 128, 1]))
+    twin.commit(0, 256, keep[0])
+    twin.commit(1, 128, keep[1, :128])
+    assert M.mtp_get_device_error(ctx) == M.MTP_ERR_DEVICE_ARGS
+    check_cache(ctx, kv, twin)
+
+
+def test_attention_of_the_most_requests():
+    """1024 requests of 0 to 2 rows, each with a length of its own."""
+    rng = np.random.default_rng(79)
+    ctx = context(4, 2, 64, "bf16", max_batch=1024)
+    new = rng.integers(0, 3, 1024)
+    kv, twin = filled(ctx, rng.integers(0, 70, 1024), new, rng)
+    check_attention(ctx, kv, twin, new, rng, "bf16")
