@@ -646,6 +646,124 @@ mtp_status mtp_draft_kv8(mtp_ctx* ctx, void* stream, int B, const void* hidden, 
                          const int32_t* positions, const mtp_kv8* kv, int K, const int32_t* chain_ids,
                          int32_t* draft_ids, float* logits, float* hidden_out, void* ws, size_t ws_bytes);
 
+/* ------------------------------------------------------------------------
+ * The paged cache in the context's own type (mtp_kv, the one the head drafts
+ * on) as a cache of new rows: append with norms and rotation, attention of any
+ * number of new rows over it (a prompt, a chunk of one, draft rows, packed trees,
+ * one decoding token, or all of these in one batch), the attention weight that
+ * entries gather, and eviction by that weight.  Commits and edits are
+ * mtp_kv_commit and the others.  ("How OpenVINO MTP Speculative Decoding Works
+ * Internally", "The MTP inputs": the MTP KV cache; "Speculative Decoding",
+ * "Overview": the target scores the drafted rows over its cache.)
+ * As the calls above, these take their head counts, head_dim and dtype from
+ * the context, which needs no weights, allocate nothing and can be captured.
+ * ---------------------------------------------------------------------- */
+
+/* Norms of query and key heads with their rotation: for each head x of q [T,
+ * n_q, head_dim] and k [T, n_kv, head_dim] (dtype, rows of contiguous heads,
+ * strides in elements between rows)
+ *   y = x / sqrt(mean x^2 + eps) * weight      (weight [head_dim] dtype; NULL:
+ *   y = x), and y's pairs turned to positions [T] by the table as in mtp_rope
+ * (rope NULL: not turned, positions ignored).  Computed in float32, rounded
+ * once.  q or k may be NULL (left out); q_out may be q itself and k_out k, with
+ * the same stride, but not overlap the inputs otherwise.  T = 0 is a no-op.
+ * Host errors: neither q nor k, neither a weight nor a table for what is given,
+ * eps not finite and > 0 with a weight, strides below the row. */
+mtp_status mtp_qk_norm_rope(mtp_ctx* ctx, void* stream, int T, const void* q, int64_t q_stride, const void* q_weight,
+                            void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, const void* k_weight,
+                            void* k_out, int64_t k_out_stride, float eps, const int32_t* positions,
+                            const mtp_rope_table* rope);
+
+/* Append rows row_offsets[b] .. row_offsets[b+1]-1 of k and v ([T, n_kv,
+ * head_dim], dtype) to request b as pending entries: slots seq_len[b] +
+ * pending[b] on, then pending[b] grows by the row count.  k is normed by
+ * k_weight and turned by rope first where they are given, as in
+ * mtp_qk_norm_rope; v is stored as it is.  q [T, n_q, head_dim], if not NULL,
+ * goes through q_weight and rope into q_out in the same launch (one of the two
+ * must be given then).
+ *   arrive [B] int32: zeroed once by the caller and left zero by every call
+ * (the call counts its thread blocks in it); calls that may run at the same time
+ * need one each.
+ *   row_offsets [B+1] int32, ascending from >= 0 to <= T; rows outside are not
+ * read.  Device errors as in mtp_kv8_append: MTP_ERR_DEVICE_ARGS for bad offsets
+ * or lengths, MTP_ERR_CAPACITY for slots beyond max_blocks (the request's cache
+ * is then left as it was) or a block id outside the pool (its rows are not
+ * stored); with bad offsets the call does nothing, else q is processed whatever
+ * becomes of the cache.  T = 0 is a no-op. */
+mtp_status mtp_kv_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, const void* k,
+                         int64_t k_stride, const void* k_weight, const void* v, int64_t v_stride, const void* q,
+                         int64_t q_stride, const void* q_weight, void* q_out, int64_t q_out_stride, float eps,
+                         const int32_t* positions, const mtp_rope_table* rope, const mtp_kv* kv, int32_t* arrive);
+
+/* Bytes of a workspace of mtp_kv_attention for this context's device; 0 for a
+ * NULL context.  It needs no initialisation and carries nothing from one call to
+ * the next.  Calls that may run at the same time need workspaces of their own,
+ * graphs that contain such calls included. */
+size_t mtp_kv_attention_workspace_bytes(const mtp_ctx* ctx);
+
+/* Attention of new rows over the paged cache.  Rows, masks, results and device
+ * errors are those of mtp_kv8_attention, over entries in the context's dtype:
+ * request b's rows belong to its last n_b entries, row i sees the slots below
+ * base_b and of the n_b last ones those up to itself (mask NULL) or those named
+ * by its mask words.  max_rows: at least every n_b, with a mask at most 256,
+ * without one any number.  Blocks' slots that hold no entry, and entries that a
+ * row does not see, do not reach its result, whatever they hold (an entry that
+ * is not finite makes the results of the rows that see it not finite).
+ *   Scores, maxima and sums are held in float32.  bf16 heads: the products'
+ * operands are bf16, the softmax weights rounded to it (8 bits; the normalising
+ * sum takes them unrounded).  float32 heads: float32 throughout.  out: 16-byte
+ * aligned.  B: at most 1024; entries of a request: at most 2^30. */
+mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
+                            const void* q, int64_t q_stride, const mtp_kv* kv, const int32_t* mask, int mask_words,
+                            float scale, void* out, float* lse, void* ws, size_t ws_bytes);
+
+/* The attention weight that each entry gathers: for slot t of request b and
+ * kv head g
+ *   w[t, g] = (t < first[b] ? w[t, g] : 0)
+ *             + sum over rows r that see t, heads h of g's group, of
+ *               exp(scale * q[r, h] . K[t, g] - lse[r, h]),
+ * the softmax weights of the rows where lse [T, n_q] is what mtp_kv_attention
+ * gave for the same rows, mask and scale (rows of lse -inf weigh nothing).  q
+ * may hold the last rows of a longer chunk only: they belong to the last n_b
+ * entries, as there.
+ *   weights: [num_blocks, n_kv, 16] float32, laid out as the pools' blocks.
+ *   first:   [B] int32 >= 0: from that slot on entries have no weight yet (what
+ *            is stored there is not read); NULL: base_b, the first new entry.
+ * Requests without rows, and slots that hold no entry, are left as they were.
+ * The sums are in float32, their order depends on nothing but the lengths.
+ * Other arguments and device errors as in mtp_kv_attention. */
+mtp_status mtp_kv_attention_weights(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
+                                    const void* q, int64_t q_stride, const mtp_kv* kv, const int32_t* mask,
+                                    int mask_words, float scale, const float* lse, const int32_t* first,
+                                    float* weights);
+
+/* Thin a cache out: of request b's L = seq_len[b] entries each kv head keeps
+ * n = min(L, budget[b]), and they move in their order to slots 0 .. n-1 of the
+ * request's blocks in `to`.  If L > budget[b] these are the first `sink`, the
+ * last `recent` and, of those between, the ones with the largest weights (equal
+ * ones from the lowest slot on; -0 counts as 0, NaN as less than everything).
+ *   weights, to_weights: as in mtp_kv_attention_weights, of `from` and `to`;
+ *            the kept entries' weights move along (to_weights NULL: not).
+ *   kept:    [B, n_kv, kept_width] int32 out: the slot in `from` of each kept
+ *            entry, -1 from n on.  kept_width >= every n.
+ *   to:      seq_len[b] = n and pending[b] = 0 are written.  Its blocks (of the
+ *            same pools or others) must hold nothing and must not be among
+ *            from's.  `from` is left as it was: release it with
+ *            mtp_kv_truncate to 0.
+ * Every head of a request keeps the same number, so lengths stay common, and
+ * the cache serves mtp_kv_attention and mtp_draft as any other; slots are no
+ * longer positions, which the rows carry by themselves.
+ *   Device errors, which leave the request's blocks and kept list as they were:
+ * MTP_ERR_DEVICE_ARGS for pending[b] != 0 in `from`, a negative length or
+ * budget, sink + recent > budget[b]; MTP_ERR_CAPACITY for n above kept_width or
+ * to's max_blocks.  A block id outside its pool is MTP_ERR_CAPACITY too: entries
+ * of such a block of `from` count as zeros, those for one of `to` are dropped.
+ * Host errors: NULL pointers, sink or recent < 0, lengths or tables shared by
+ * `from` and `to`. */
+mtp_status mtp_kv_evict(mtp_ctx* ctx, void* stream, int B, const mtp_kv* from, const float* weights,
+                        const int32_t* budget, int sink, int recent, const mtp_kv* to, float* to_weights,
+                        int32_t* kept, int kept_width);
+
 /* Add tokens to the per-request counts [B, vocab] int32: tokens[b * stride +
  * i], i < n_tokens[b].  in_prompt = 0: the token's count grows by one for
  * each time it is named; 1: its top bit (bit 31: the token occurs in the

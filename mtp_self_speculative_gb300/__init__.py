@@ -70,6 +70,45 @@ class KVCache:
     block_table: torch.Tensor   # [B, max_blocks] int32
     seq_len: torch.Tensor       # [B] int32
     pending: torch.Tensor       # [B] int32
+    arrive: Optional[torch.Tensor] = None   # [B] int32, zeroed once (mtp_kv_append)
+
+    @classmethod
+    def empty(cls, ctx: "Context", num_blocks: int, block_table: torch.Tensor) -> "KVCache":
+        """An empty cache of num_blocks blocks for the requests of block_table."""
+        c, dev, B = ctx.cfg, block_table.device, int(block_table.shape[0])
+        pools = [torch.zeros((num_blocks, c.n_kv_heads, 16, c.head_dim), dtype=ctx.dtype, device=dev) for _ in range(2)]
+        ints = [torch.zeros(B, dtype=torch.int32, device=dev) for _ in range(3)]
+        return cls(pools[0], pools[1], block_table, ints[0], ints[1], ints[2])
+
+    def _checked_struct(self, ctx: "Context"):
+        """(struct, B, n_q, n_kv, head_dim), with the checks of devices, types
+        and shapes; they run again when a field is another tensor, has other
+        storage or another size than when they last ran, and for another
+        context."""
+        kp, vp, bt, sl, pe, ar = fields = (self.k_pool, self.v_pool, self.block_table, self.seq_len, self.pending,
+                                           self.arrive)
+        seen = (kp.data_ptr(), vp.data_ptr(), bt.data_ptr(), sl.data_ptr(), pe.data_ptr(), kp.shape, vp.shape, bt.shape,
+                sl.shape, pe.shape, None if ar is None else (ar.data_ptr(), ar.shape))
+        done = self.__dict__.get("_checked")
+        if (done is not None and done[0] == seen and done[1] is ctx.cfg and done[2] == ctx.device
+                and all(x is y for x, y in zip(done[3], fields)) and all(x is None or x.is_contiguous() for x in fields)):
+            return done[4]
+        c = ctx.cfg
+        if kp.dim() != 4 or sl.dim() != 1 or bt.dim() != 2:
+            raise ValueError("k_pool must be [num_blocks, n_kv, 16, head_dim], seq_len [B], block_table [B, max_blocks]")
+        nb, B, width = int(kp.shape[0]), int(sl.shape[0]), int(bt.shape[1])
+        pool, i32 = (nb, int(c.n_kv_heads), 16, int(c.head_dim)), torch.int32
+        _dev_ptr(ctx, ar, i32, "arrive", (B,))
+        st = MTPKV(_dev_ptr(ctx, kp, ctx.dtype, "k_pool", pool), _dev_ptr(ctx, vp, ctx.dtype, "v_pool", pool),
+                   _dev_ptr(ctx, bt, i32, "block_table", (B, width)), _dev_ptr(ctx, sl, i32, "seq_len", (B,)),
+                   _dev_ptr(ctx, pe, i32, "pending", (B,)), nb, width)
+        got = (st, B, int(c.n_q_heads), int(c.n_kv_heads), int(c.head_dim))
+        self.__dict__["_checked"] = (seen, c, ctx.device, fields, got)
+        return got
+
+    def __getstate__(self):
+        """A copy (copy.deepcopy, pickle) is checked for itself."""
+        return {k: v for k, v in self.__dict__.items() if k != "_checked"}
 
     def struct(self) -> MTPKV:
         return MTPKV(_ptr(self.k_pool, name="k_pool"), _ptr(self.v_pool, name="v_pool"),
@@ -699,6 +738,150 @@ def mtp_draft_kv8(ctx: Context, hidden: torch.Tensor, embeds: torch.Tensor, posi
                                _dev_ptr(ctx, logits, f32, "logits", (B, K, V)),
                                _dev_ptr(ctx, hidden_out, f32, "hidden_out", (B, H)), ws.ptr, ws.bytes),
            "mtp_draft_kv8")
+
+
+# ------------- the paged cache in the context's type: new rows, weights, eviction
+
+def mtp_qk_norm_rope(ctx: Context, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                     q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, positions: Optional[torch.Tensor] = None, rope: Optional[RopeTable] = None,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Norm the heads of q [T, n_q, head_dim] and k [T, n_kv, head_dim] by
+    their weights [head_dim] (None: not) and turn them to ``positions`` [T] by
+    ``rope`` (None: not) into q_out and k_out (None: in place); rows may be
+    strided, q or k may be None.  Returns (q_out, k_out)."""
+    c = ctx.cfg
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("neither q nor k")
+    T = int(one.shape[0])
+    side = []
+    for x, w, out, heads, name in ((q, q_weight, q_out, c.n_q_heads, "q"), (k, k_weight, k_out, c.n_kv_heads, "k")):
+        if x is None:
+            if w is not None or out is not None:
+                raise ValueError("%s_weight and %s_out need %s" % (name, name, name))
+            side += [None, 0, None, None, 0]
+            continue
+        xp, xs = _row_ptr(ctx, x, name, T, heads)
+        op, os_ = (xp, xs) if out is None or out is x else _row_ptr(ctx, out, name + "_out", T, heads)
+        side += [xp, xs, _dev_ptr(ctx, w, ctx.dtype, name + "_weight", (ctx.head_dim,)), op, os_]
+    pp = _dev_ptr(ctx, positions, torch.int32, "positions", (T,))
+    if T:
+        _check(_clib.mtp_qk_norm_rope(ctx.handle, _ctx_stream(ctx, stream), T, *side, eps, pp, rope),
+               "mtp_qk_norm_rope")
+    return (q if q_out is None else q_out), (k if k_out is None else k_out)
+
+
+def mtp_kv_append(ctx: Context, kv: KVCache, k: torch.Tensor, v: torch.Tensor, row_offsets: torch.Tensor,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  positions: Optional[torch.Tensor] = None, rope: Optional[RopeTable] = None,
+                  q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  stream=None) -> None:
+    """Append the rows of k and v [T, n_kv, head_dim] to the requests' caches
+    as pending entries, k normed by ``k_weight`` and turned by ``rope`` at
+    ``positions`` where given; q [T, n_q, head_dim] goes through q_weight and
+    rope into q_out (None: in place).  Rows may be strided.  The cache needs its
+    ``arrive`` field."""
+    st, B, n_q, n_kv, hd = kv._checked_struct(ctx)
+    if kv.arrive is None:
+        raise ValueError("mtp_kv_append needs the cache's arrive field ([B] int32, zeroed once)")
+    T = k.shape[0]
+    kp, ks = _row_ptr(ctx, k, "k", T, n_kv)
+    vp, vs = _row_ptr(ctx, v, "v", T, n_kv)
+    qp, qs, qop, qos = None, 0, None, 0
+    if q is not None:
+        qp, qs = _row_ptr(ctx, q, "q", T, n_q)
+        qop, qos = (qp, qs) if q_out is None or q_out is q else _row_ptr(ctx, q_out, "q_out", T, n_q)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    kw, qw = _dev_ptr(ctx, k_weight, ctx.dtype, "k_weight", (hd,)), _dev_ptr(ctx, q_weight, ctx.dtype, "q_weight", (hd,))
+    if T == 0:
+        return
+    _check(_clib.mtp_kv_append(ctx.handle, _ctx_stream(ctx, stream), B, T,
+                               _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), kp, ks, kw, vp, vs, qp,
+                               qs, qw, qop, qos, eps, _dev_ptr(ctx, positions, torch.int32, "positions", (T,)), rope,
+                               st, kv.arrive.data_ptr()), "mtp_kv_append")
+
+
+class AttentionWorkspace:
+    """Scratch of mtp_kv_attention; calls that may run at the same time need
+    one each (graphs that contain such calls included)."""
+
+    def __init__(self, ctx: Context):
+        n = int(_clib.mtp_kv_attention_workspace_bytes(ctx.handle))
+        if n == 0:
+            raise MTPError(MTP_ERR_INVALID, "mtp_kv_attention_workspace_bytes")
+        self.device, self.bytes = ctx.device, n
+        self.ws = torch.empty(n, dtype=torch.uint8, device="cuda:%d" % ctx.device)
+        self.ptr = self.ws.data_ptr()
+
+
+def mtp_kv_attention(ctx: Context, kv: KVCache, q: torch.Tensor, row_offsets: torch.Tensor, out: torch.Tensor,
+                     ws: AttentionWorkspace, max_rows: int, mask: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None) -> None:
+    """out [T, n_q, head_dim] = attention of the rows q (may be strided) over
+    the requests' caches: the rows of request b are its last entries; causal
+    among them, or as the bits of mask [T, words] say.  ``max_rows``: at least
+    the rows of any request; lse [T, n_q] float32; scale: 1 / sqrt(head_dim)."""
+    st, B, n_q, _, hd = kv._checked_struct(ctx)
+    T = q.shape[0]
+    qp, qs = _row_ptr(ctx, q, "q", T, n_q)
+    op = _dev_ptr(ctx, out, ctx.dtype, "out", (T, n_q, hd))
+    lp = _dev_ptr(ctx, lse, torch.float32, "lse", (T, n_q))
+    words = mask.shape[-1] if mask is not None else 0
+    mp = _dev_ptr(ctx, mask, torch.int32, "mask", (T, words))
+    if ws.device != ctx.device:
+        raise ValueError("the workspace belongs to cuda:%s" % ws.device)
+    if T == 0:
+        return
+    _check(_clib.mtp_kv_attention(ctx.handle, _ctx_stream(ctx, stream), B, T,
+                                  _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), max_rows, qp, qs, st,
+                                  mp, words, hd ** -0.5 if scale is None else scale, op, lp, ws.ptr, ws.bytes),
+           "mtp_kv_attention")
+
+
+def mtp_kv_attention_weights(ctx: Context, kv: KVCache, q: torch.Tensor, row_offsets: torch.Tensor, lse: torch.Tensor,
+                             weights: torch.Tensor, max_rows: int, mask: Optional[torch.Tensor] = None,
+                             first: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None) -> None:
+    """Add the softmax weights of the rows q [T, n_q, head_dim] (lse [T, n_q]
+    as mtp_kv_attention gave it) to weights [num_blocks, n_kv, 16] float32;
+    entries from slot first[b] on (None: the rows' own) start from zero."""
+    st, B, n_q, n_kv, hd = kv._checked_struct(ctx)
+    T = q.shape[0]
+    qp, qs = _row_ptr(ctx, q, "q", T, n_q)
+    words = mask.shape[-1] if mask is not None else 0
+    mp = _dev_ptr(ctx, mask, torch.int32, "mask", (T, words))
+    lp = _dev_ptr(ctx, lse, torch.float32, "lse", (T, n_q))
+    wp = _dev_ptr(ctx, weights, torch.float32, "weights", (st.num_blocks, n_kv, 16))
+    if T == 0:
+        return
+    _check(_clib.mtp_kv_attention_weights(ctx.handle, _ctx_stream(ctx, stream), B, T,
+                                          _dev_ptr(ctx, row_offsets, torch.int32, "row_offsets", (B + 1,)), max_rows, qp,
+                                          qs, st, mp, words, hd ** -0.5 if scale is None else scale, lp,
+                                          _dev_ptr(ctx, first, torch.int32, "first", (B,)), wp),
+           "mtp_kv_attention_weights")
+
+
+def mtp_kv_evict(ctx: Context, kv: KVCache, weights: torch.Tensor, budget: torch.Tensor, to: KVCache,
+                 to_weights: Optional[torch.Tensor], kept: torch.Tensor, sink: int = 0, recent: int = 0,
+                 stream=None) -> None:
+    """Each kv head keeps min(seq_len, budget[b]) entries of request b -- the
+    first ``sink``, the last ``recent`` and those of the largest weights -- which
+    move to the blocks of ``to``; kept [B, n_kv, width] int32 receives their
+    slots in ``kv``.  Release the old blocks with mtp_kv_truncate to 0."""
+    st, B, _, n_kv, _ = kv._checked_struct(ctx)
+    ts, tb = to._checked_struct(ctx)[:2]
+    if tb != B:
+        raise ValueError("to must hold B=%d requests, got %d" % (B, tb))
+    f32, i32 = torch.float32, torch.int32
+    if kept.dim() != 3:
+        raise ValueError("kept must be [B, n_kv, width], got %s" % (tuple(kept.shape),))
+    _check(_clib.mtp_kv_evict(ctx.handle, _ctx_stream(ctx, stream), B, st,
+                              _dev_ptr(ctx, weights, f32, "weights", (st.num_blocks, n_kv, 16)),
+                              _dev_ptr(ctx, budget, i32, "budget", (B,)), int(sink), int(recent), ts,
+                              _dev_ptr(ctx, to_weights, f32, "to_weights", (ts.num_blocks, n_kv, 16)),
+                              _dev_ptr(ctx, kept, i32, "kept", (B, n_kv, int(kept.shape[2]))), int(kept.shape[2])),
+           "mtp_kv_evict")
 
 
 def mtp_token_counts_add(ctx: Context, counts: torch.Tensor, tokens: torch.Tensor, n_tokens: torch.Tensor,

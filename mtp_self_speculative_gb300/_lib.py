@@ -142,6 +142,18 @@ SIGNATURES = {
     "mtp_draft_kv8_workspace_bytes": (c_size_t, [c_void_p]),
     "mtp_draft_kv8": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, P_i32, P_kv8, c_int, P_i32, P_i32,
                               c_void_p, c_void_p, c_void_p, c_size_t]),
+    "mtp_qk_norm_rope": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p,
+                                 c_int64, c_void_p, c_void_p, c_int64, c_float, P_i32, ctypes.POINTER(MTPRopeTable)]),
+    "mtp_kv_append": (c_int, [c_void_p, c_void_p, c_int, c_int, P_i32, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
+                              c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_float, P_i32,
+                              ctypes.POINTER(MTPRopeTable), ctypes.POINTER(MTPKV), P_i32]),
+    "mtp_kv_attention_workspace_bytes": (c_size_t, [c_void_p]),
+    "mtp_kv_attention": (c_int, [c_void_p, c_void_p, c_int, c_int, P_i32, c_int, c_void_p, c_int64,
+                                 ctypes.POINTER(MTPKV), P_i32, c_int, c_float, c_void_p, c_void_p, c_void_p, c_size_t]),
+    "mtp_kv_attention_weights": (c_int, [c_void_p, c_void_p, c_int, c_int, P_i32, c_int, c_void_p, c_int64,
+                                         ctypes.POINTER(MTPKV), P_i32, c_int, c_float, c_void_p, P_i32, c_void_p]),
+    "mtp_kv_evict": (c_int, [c_void_p, c_void_p, c_int, ctypes.POINTER(MTPKV), c_void_p, P_i32, c_int, c_int,
+                             ctypes.POINTER(MTPKV), c_void_p, P_i32, c_int]),
     "mtp_token_counts_add": (c_int, [c_void_p, c_void_p, c_int, P_i32, c_int, P_i32, c_int, P_i32]),
     "mtp_logits_process": (c_int, [c_void_p, c_void_p, ctypes.POINTER(MTPLogitsArgs)]),
     "mtp_selftest_wait_timeout": (c_int, [c_void_p, c_void_p, c_int]),

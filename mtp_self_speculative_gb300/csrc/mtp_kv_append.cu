@@ -1,0 +1,371 @@
+// Norms of query and key heads with their rotation, and appending to the paged
+// cache in the context's type.
+//
+//   y = x / sqrt(mean x^2 + eps) * w   over each head,
+//   out = magnitude * (a cos - b sin, b cos + a sin) for its pairs (a, b).
+//
+// The work is a copy with some thirty operations per element, so memory bounds
+// it.  HD / 16 lanes share a head, eight pairs each: both members of a pair and
+// their cosine stay in one thread, the mean is three (two) shuffles, and a
+// thread computes its eight cosines once for all heads that it walks over.
+#include <math.h>
+
+#include "mtp_kv16.cuh"
+
+namespace mtp {
+
+constexpr int kNormThreads = 128;
+
+struct NormSide {
+  const void* x;         // [T, heads, HD], rows `stride` apart, or null
+  const void* w;         // [HD] or null: no norm
+  void* out;
+  long long stride, out_stride, extent;   // elements; the extent for bounds-checked builds
+  int heads, per;        // heads of a thread block
+};
+
+struct NormArgs {
+  NormSide q, k;
+  const void* v;         // append: [T, n_kv, HD]
+  long long v_stride;
+  const int32_t* positions;
+  const int32_t* row_offsets;
+  mtp_kv kv;
+  int32_t* arrive;
+  int* err;
+  float eps;
+  int B, T, rd;          // rd: rotated elements of a head (0: none)
+  int k_groups;          // grid.y below it: keys (and values); from it on: queries
+};
+
+// The eight pairs of a unit: pair-slot j = 8 u + e is the rotating pair j of
+// the head, or behind those the two elements rd + 2 (j - rd / 2).
+__device__ __forceinline__ void pair_at(int j, int rd, int layout, int& ia, int& ib) {
+  if (j >= rd / 2) {
+    ia = 2 * j;
+    ib = ia + 1;
+  } else if (layout == MTP_ROPE_HALF) {
+    ia = j;
+    ib = j + rd / 2;
+  } else {
+    ia = 2 * j;
+    ib = ia + 1;
+  }
+}
+
+// Sixteen elements of a head, x[e] and x[8 + e] the members of pair e.  VEC:
+// rows on 16 bytes and rd a multiple of 16; then a unit is two runs of eight
+// (half layout, rotating) or one of sixteen.
+template <typename T, bool VEC>
+__device__ __forceinline__ void unit_load(const T* head, int u, int rd, int layout, float (&x)[16]) {
+  if constexpr (VEC) {
+    constexpr int N = 16 / sizeof(T);
+    const bool split = layout == MTP_ROPE_HALF && 8 * u < rd / 2;
+    const T* pa = head + (split ? 8 * u : 16 * u);
+    const T* pb = split ? pa + rd / 2 : pa + 8;
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 8; i += N) {
+      widen16<T>(*reinterpret_cast<const uint4*>(pa + i), y + i);
+      widen16<T>(*reinterpret_cast<const uint4*>(pb + i), y + 8 + i);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = split ? y[e] : y[2 * e];
+      x[8 + e] = split ? y[8 + e] : y[2 * e + 1];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int ia, ib;
+      pair_at(8 * u + e, rd, layout, ia, ib);
+      x[e] = elem<T>(head + ia);
+      x[8 + e] = elem<T>(head + ib);
+    }
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void unit_store(T* head, int u, int rd, int layout, const float (&x)[16]) {
+  if constexpr (VEC) {
+    constexpr int N = 16 / sizeof(T);
+    const bool split = layout == MTP_ROPE_HALF && 8 * u < rd / 2;
+    T* pa = head + (split ? 8 * u : 16 * u);
+    T* pb = split ? pa + rd / 2 : pa + 8;
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = split ? x[i] : x[(i & 1) * 8 + i / 2];
+      y[8 + i] = split ? x[8 + i] : x[(i & 1) * 8 + 4 + i / 2];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += N) {
+      *reinterpret_cast<uint4*>(pa + i) = narrow16<T>(y + i);
+      *reinterpret_cast<uint4*>(pb + i) = narrow16<T>(y + 8 + i);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int ia, ib;
+      pair_at(8 * u + e, rd, layout, ia, ib);
+      Elem<T>::store1(head + ia, x[e]);
+      Elem<T>::store1(head + ib, x[8 + e]);
+    }
+  }
+}
+
+// Thread block (tokens, group of heads): LPH lanes a token and head.  With
+// CACHE a group of key heads takes the value heads along and writes both into
+// the cache.
+template <typename T, int HD, bool VEC, bool CACHE>
+__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormArgs a,
+                                                                    const __grid_constant__ mtp_rope_table tab) {
+  constexpr int LPH = HD / 16;
+  constexpr int TOK = kNormThreads / LPH;     // tokens of a thread block
+  __shared__ long long at_s[TOK];             // append: element offset of a token's slot at kv head 0, or -1
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, u = tid % LPH, t0 = blockIdx.x * TOK, t = t0 + tid / LPH;
+  const bool keys = (int)blockIdx.y < a.k_groups;
+  const NormSide& s = keys ? a.k : a.q;
+  const int group = keys ? blockIdx.y : blockIdx.y - a.k_groups;
+  const int h0 = group * s.per, h1 = min(s.heads, h0 + s.per);
+  if constexpr (CACHE) {
+    // every thread block looks at all offsets; lengths come along, so that the
+    // common batch waits for one round of loads
+    int bad = 0, sl0 = 0, pe0 = 0;
+    if (tid < TOK) at_s[tid] = -2;            // a row of no request
+    if (keys && tid < a.B) {
+      sl0 = a.kv.seq_len[tid];
+      pe0 = a.kv.pending[tid];
+    }
+    for (int b = tid; b < a.B; b += kNormThreads) {
+      const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1];
+      bad |= o0 < 0 || o1 < o0 || o1 > a.T;
+    }
+    if (__syncthreads_or(bad)) {
+      if (tid == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
+      return;
+    }
+    for (int b = tid; b < a.B; b += kNormThreads) {
+      const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1];
+      const int lo = max(o0, t0), hi = min(o1, t0 + TOK);
+      if (lo >= hi) continue;
+      if (!keys) {
+        for (int x = lo; x < hi; ++x) at_s[x - t0] = 0;
+        continue;
+      }
+      const int sl = b == tid ? sl0 : a.kv.seq_len[b], pe = b == tid ? pe0 : a.kv.pending[b];
+      int e = MTP_OK;
+      if (sl < 0 || pe < 0 || sl > INT32_MAX - pe) e = MTP_ERR_DEVICE_ARGS;
+      else if ((long long)sl + pe + (o1 - o0) > (long long)a.kv.max_blocks * kBlk) e = MTP_ERR_CAPACITY;
+      if (e != MTP_OK) {
+        set_error(a.err, e);
+        continue;
+      }
+      int held = -1, blk = 0;
+      for (int x = lo; x < hi; ++x) {
+        const int slot = sl + pe + (x - o0);
+        if (slot >> 4 != held) {
+          held = slot >> 4;
+          blk = a.kv.block_table[(long long)b * a.kv.max_blocks + held];
+          if (blk < 0 || blk >= a.kv.num_blocks) {
+            set_error(a.err, MTP_ERR_CAPACITY);
+            blk = -1;
+          }
+        }
+        at_s[x - t0] = blk < 0 ? -1 : ((long long)blk * a.k.heads * kBlk + (slot & 15)) * HD;
+      }
+      // all of the request's thread blocks have read its old length before the
+      // last one of them publishes the new one
+      const int blocks = (o1 - 1) / TOK - o0 / TOK + 1;
+      if (arrive_last(a.arrive + b, blocks * a.k_groups)) a.kv.pending[b] = pe + (o1 - o0);
+    }
+    __syncthreads();
+  }
+  const bool live = t < a.T && (!CACHE || at_s[tid / LPH] >= 0);
+  if (!__any_sync(0xffffffffu, live)) return;
+  const int rd = a.rd;
+  float2 cs[8];
+  const int pos = live && rd ? a.positions[t] : 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    cs[e] = 8 * u + e < rd / 2 ? rope_cos_sin(pos, tab.turns[8 * u + e], tab.magnitude) : make_float2(1.0f, 0.0f);
+  float w[16];
+  if (s.w) {
+    unit_load<T, false>((const T*)s.w, u, rd, tab.layout, w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = 1.0f;
+  }
+  const long long kv_extent = (long long)a.kv.num_blocks * a.k.heads * kBlk * HD;
+  (void)kv_extent;   // bounds-checked builds only
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+    float x[16];
+    if (live) {
+      unit_load<T, VEC>((const T*)s.x + (long long)t * s.stride + (long long)h * HD, u, rd, tab.layout, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+    }
+    if (s.w) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+      for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(ss * (1.0f / HD) + a.eps);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] *= r * w[e];
+    }
+    if (!live) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (8 * u + e >= rd / 2) continue;
+      const float p = x[e], y = x[8 + e];
+      x[e] = rope_first(p, y, cs[e]);
+      x[8 + e] = rope_second(p, y, cs[e]);
+    }
+    if (CACHE && keys) {
+      const long long at = at_s[tid / LPH] + (long long)h * kBlk * HD;
+      if (MTP_IN_BOUNDS(a.err, at + HD - 1, kv_extent))
+        unit_store<T, VEC>((T*)a.kv.k_pool + at, u, rd, tab.layout, x);
+    } else {
+      const long long at = (long long)t * s.out_stride + (long long)h * HD;
+      if (MTP_IN_BOUNDS(a.err, at + HD - 1, s.extent)) unit_store<T, VEC>((T*)s.out + at, u, rd, tab.layout, x);
+    }
+  }
+  if constexpr (CACHE) {
+    if (!keys || !live) return;
+    for (int h = h0; h < h1; ++h) {   // values: a copy
+      const T* src = (const T*)a.v + (long long)t * a.v_stride + (long long)h * HD;
+      const long long at = at_s[tid / LPH] + (long long)h * kBlk * HD;
+      if (!MTP_IN_BOUNDS(a.err, at + HD - 1, kv_extent)) continue;
+      T* dst = (T*)a.kv.v_pool + at;
+      if constexpr (VEC) {
+        constexpr int N = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 16 / N; ++i)
+          *reinterpret_cast<uint4*>(dst + (i * LPH + u) * N) = *reinterpret_cast<const uint4*>(src + (i * LPH + u) * N);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[i * LPH + u] = src[i * LPH + u];
+      }
+    }
+  }
+}
+
+template <typename T, bool CACHE>
+static cudaError_t norm_launch(mtp_ctx* ctx, cudaStream_t s, NormArgs a, const mtp_rope_table& tab) {
+  const int hd = ctx->cfg.head_dim, tok = kNormThreads / (hd / 16);
+  constexpr int N = 16 / sizeof(T);
+  uintptr_t bits = (uintptr_t)a.q.x | (uintptr_t)a.q.out | (uintptr_t)a.k.x | (uintptr_t)a.k.out | (uintptr_t)a.v;
+  long long strides = a.q.stride | a.q.out_stride | a.k.stride | a.k.out_stride | a.v_stride;
+  const bool vec = !(bits & 15) && strides % N == 0 && a.rd % 16 == 0;
+  const int gx = (a.T + tok - 1) / tok;
+  // a thread computes its cosines once for its heads; few tokens split the
+  // heads over more thread blocks until there are about 8 per SM
+  const int heads = (a.q.x ? a.q.heads : 0) + (a.k.x ? a.k.heads * (CACHE ? 2 : 1) : 0);
+  int groups = (8 * ctx->num_sms + gx - 1) / gx;
+  int per = (heads + groups - 1) / groups;
+  per = per < 1 ? 1 : per;
+  a.q.per = per;
+  a.k.per = CACHE ? (per + 1) / 2 : per;
+  a.k_groups = a.k.x ? (a.k.heads + a.k.per - 1) / a.k.per : 0;
+  const int q_groups = a.q.x ? (a.q.heads + a.q.per - 1) / a.q.per : 0;
+  const dim3 grid(gx, a.k_groups + q_groups), block(kNormThreads);
+  ctx->launches++;
+  if (hd == 128)
+    return vec ? launch_pdl(qk_norm_rope_kernel<T, 128, true, CACHE>, grid, block, 0, s, a, tab)
+               : launch_pdl(qk_norm_rope_kernel<T, 128, false, CACHE>, grid, block, 0, s, a, tab);
+  return vec ? launch_pdl(qk_norm_rope_kernel<T, 64, true, CACHE>, grid, block, 0, s, a, tab)
+             : launch_pdl(qk_norm_rope_kernel<T, 64, false, CACHE>, grid, block, 0, s, a, tab);
+}
+
+// A side's checks: rows of `heads` heads, in place only with one stride.
+static bool side_ok(const NormSide& s, int hd) {
+  const int64_t row = (int64_t)s.heads * hd;
+  return s.out && s.stride >= row && s.out_stride >= row && (s.x != s.out || s.stride == s.out_stride);
+}
+
+}  // namespace mtp
+
+using namespace mtp;
+
+extern "C" {
+
+mtp_status mtp_qk_norm_rope(mtp_ctx* ctx, void* stream, int T, const void* q, int64_t q_stride, const void* q_weight,
+                            void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, const void* k_weight,
+                            void* k_out, int64_t k_out_stride, float eps, const int32_t* positions,
+                            const mtp_rope_table* rope) {
+  if (!ctx || T < 0 || T > (1 << 30) || (!q && !k)) return MTP_ERR_INVALID;
+  const mtp_config& c = ctx->cfg;
+  if (rope && (!rope_table_ok(rope, c.head_dim) || !positions)) return MTP_ERR_INVALID;
+  if (!rope && (!q || !q_weight) && (!k || !k_weight)) return MTP_ERR_INVALID;   // nothing to do
+  if ((q_weight || k_weight) && (!(eps > 0.0f) || !isfinite(eps))) return MTP_ERR_INVALID;
+  NormArgs a{};
+  a.q.heads = c.n_q_heads;
+  a.k.heads = c.n_kv_heads;
+  if (q) {
+    a.q = {q, q_weight, q_out, q_stride, q_out_stride, (int64_t)(T - 1) * q_out_stride + c.n_q_heads * c.head_dim, c.n_q_heads, 0};
+    if (!side_ok(a.q, c.head_dim)) return MTP_ERR_INVALID;
+  }
+  if (k) {
+    a.k = {k, k_weight, k_out, k_stride, k_out_stride, (int64_t)(T - 1) * k_out_stride + c.n_kv_heads * c.head_dim, c.n_kv_heads, 0};
+    if (!side_ok(a.k, c.head_dim)) return MTP_ERR_INVALID;
+  }
+  if (T == 0) return MTP_OK;
+  DeviceGuard dev(ctx->device);
+  if (!dev.ok) return MTP_ERR_CUDA;
+  a.positions = positions;
+  a.err = ctx->err;
+  a.eps = eps;
+  a.T = T;
+  mtp_rope_table tab = {};
+  if (rope) tab = *rope;
+  a.rd = tab.rotary_dim;
+  return launch_status(c.dtype == MTP_DTYPE_BF16 ? norm_launch<uint16_t, false>(ctx, (cudaStream_t)stream, a, tab)
+                                                 : norm_launch<float, false>(ctx, (cudaStream_t)stream, a, tab));
+}
+
+mtp_status mtp_kv_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, const void* k,
+                         int64_t k_stride, const void* k_weight, const void* v, int64_t v_stride, const void* q,
+                         int64_t q_stride, const void* q_weight, void* q_out, int64_t q_out_stride, float eps,
+                         const int32_t* positions, const mtp_rope_table* rope, const mtp_kv* kv, int32_t* arrive) {
+  if (!ctx || B < 1 || B > ctx->cfg.max_batch || T < 0 || T > (1 << 30) || !row_offsets || !k || !v || !arrive ||
+      !kv16_ok(kv))
+    return MTP_ERR_INVALID;
+  const mtp_config& c = ctx->cfg;
+  const int64_t kw = (int64_t)c.n_kv_heads * c.head_dim;
+  if (k_stride < kw || v_stride < kw) return MTP_ERR_INVALID;
+  if (rope && (!rope_table_ok(rope, c.head_dim) || !positions)) return MTP_ERR_INVALID;
+  if ((q_weight || k_weight) && (!(eps > 0.0f) || !isfinite(eps))) return MTP_ERR_INVALID;
+  NormArgs a{};
+  a.q.heads = c.n_q_heads;
+  if (q) {
+    if (!rope && !q_weight) return MTP_ERR_INVALID;
+    a.q = {q, q_weight, q_out, q_stride, q_out_stride, (int64_t)(T - 1) * q_out_stride + c.n_q_heads * c.head_dim, c.n_q_heads, 0};
+    if (!side_ok(a.q, c.head_dim)) return MTP_ERR_INVALID;
+  }
+  if (T == 0) return MTP_OK;
+  DeviceGuard dev(ctx->device);
+  if (!dev.ok) return MTP_ERR_CUDA;
+  a.k = {k, k_weight, nullptr, k_stride, 0, 0, c.n_kv_heads, 0};
+  a.v = v;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.row_offsets = row_offsets;
+  a.kv = *kv;
+  a.arrive = arrive;
+  a.err = ctx->err;
+  a.eps = eps;
+  a.B = B;
+  a.T = T;
+  mtp_rope_table tab = {};
+  if (rope) tab = *rope;
+  a.rd = tab.rotary_dim;
+  return launch_status(c.dtype == MTP_DTYPE_BF16 ? norm_launch<uint16_t, true>(ctx, (cudaStream_t)stream, a, tab)
+                                                 : norm_launch<float, true>(ctx, (cudaStream_t)stream, a, tab));
+}
+
+}  // extern "C"

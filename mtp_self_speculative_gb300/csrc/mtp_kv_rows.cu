@@ -1,0 +1,508 @@
+// Attention of new rows over the paged cache, and the attention weight that
+// its entries gather, on the float32 pipe: the form for float32 heads.
+//
+//   out[r, h] = sum_t p_t V[t, g] / sum_t p_t,  p_t = 2^(c s_t - m),
+//   s_t = q[r, h] . K[t, g], c = scale * log2 e, m the running maximum;
+//   w[t, g] += sum_{r, h} 2^(c s_t - log2 e * lse[r, h]).
+//
+// The (row, query head) pairs that share a kv head are the rows of a tile; a
+// step takes 64 slots.  16 x 16 threads hold RT x 4 scores each and read both
+// operands from shared memory as float4 (queries and keys transposed), so that
+// for RT = 4 two shared loads feed sixteen multiply-adds and the float32 pipe is
+// the bound; RT = 1 serves decoding rows, which are bound by the cache's bytes.
+#include <math.h>
+
+#include "mtp_kv16.cuh"
+
+namespace mtp {
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsStep = 64;       // slots of a step
+constexpr int kRowsPitch = kRowsStep + 4;
+
+template <bool V> struct Flag { static constexpr bool value = V; };
+
+template <int HD, int RT>
+struct RowsShape {
+  static constexpr int kRows = 16 * RT;                    // pairs of a tile
+  static constexpr int kQ = HD * kRows, kK = HD * kRowsPitch, kV = kRowsStep * HD, kP = kRowsStep * kRows;   // floats
+  static constexpr int kBytes = (kQ + kK + kV + kP) * 4;
+  static constexpr int kWeightBytes = (kQ + kK) * 4;
+};
+
+// Queries of a tile, transposed: qs[d][pair]; pairs past the request's rows are zero.
+template <typename T, int HD, int ROWS>
+__device__ __forceinline__ void load_queries(const RowsArgs& a, float* qs, int o0, int i0, int n, int g) {
+  const int G = 1 << a.g_shift;
+  for (int x = threadIdx.x; x < ROWS * (HD / 4); x += kRowsThreads) {
+    const int r = x % ROWS, d = x / ROWS * 4, i = i0 + (r >> a.g_shift);
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i < n) {
+      const T* p = (const T*)a.q + (long long)(o0 + i) * a.q_stride + (long long)(g * G + (r & (G - 1))) * HD + d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = elem<T>(p + e);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) qs[(d + e) * ROWS + r] = y[e];
+  }
+}
+
+// Entries of a step: keys transposed (ks[d][slot]) or values as they lie
+// (vs[slot][d]).  Slots from `end` on, and blocks outside the pool, are zero.
+template <typename T, int HD, bool TRANSPOSE>
+__device__ __forceinline__ void load_entries(const RowsArgs& a, const void* pool, float* dst, const int* blocks, int t0,
+                                             int end, int g) {
+  for (int x = threadIdx.x; x < kRowsStep * (HD / 4); x += kRowsThreads) {
+    int t, d;
+    if (TRANSPOSE) {   // a warp takes 8 slots x 4 quads: whole sectors, two lanes a bank
+      const int w = x >> 5, l = x & 31;
+      t = (w % (kRowsStep / 8)) * 8 + (l & 7);
+      d = ((w / (kRowsStep / 8)) * 4 + (l >> 3)) * 4;
+    } else {
+      t = x / (HD / 4);
+      d = x % (HD / 4) * 4;
+    }
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int blk = blocks[t >> 4];
+    if (t0 + t < end && blk >= 0) {
+      const T* p = (const T*)pool + (((long long)blk * a.n_kv + g) * kBlk + (t & 15)) * HD + d;
+      if constexpr (sizeof(T) == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p);
+        y[0] = u.x; y[1] = u.y; y[2] = u.z; y[3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        y[0] = bf16_lo(u.x); y[1] = bf16_hi(u.x); y[2] = bf16_lo(u.y); y[3] = bf16_hi(u.y);
+      }
+    }
+    if (TRANSPOSE) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dst[(d + e) * kRowsPitch + t] = y[e];
+    } else {
+      *reinterpret_cast<float4*>(dst + t * HD + d) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+  }
+}
+
+// The step's block ids (-1: outside the pool).
+__device__ __forceinline__ void load_blocks(const RowsArgs& a, int* blocks, int b, int t0, int end) {
+  if (threadIdx.x < kRowsStep / kBlk) {
+    const int t = t0 + threadIdx.x * kBlk;
+    int blk = -1;
+    if (t < end) {
+      blk = a.kv.block_table[(long long)b * a.kv.max_blocks + (t >> 4)];
+      if (blk < 0 || blk >= a.kv.num_blocks) {
+        set_error(a.err, MTP_ERR_CAPACITY);
+        blk = -1;
+      }
+    }
+    blocks[threadIdx.x] = blk;
+  }
+}
+
+// Scores of pairs RT ty .. and slots 4 tx ..
+template <int HD, int RT>
+__device__ __forceinline__ void tile_scores(const float* qs, const float* ks, int ty, int tx, float (&s)[RT][4]) {
+  constexpr int ROWS = 16 * RT;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 8
+  for (int d = 0; d < HD; ++d) {
+    float q[RT];
+    if constexpr (RT == 4) {
+      const float4 u = *reinterpret_cast<const float4*>(qs + d * ROWS + 4 * ty);
+      q[0] = u.x; q[1] = u.y; q[2] = u.z; q[3] = u.w;
+    } else {
+      q[0] = qs[d * ROWS + ty];
+    }
+    const float4 k = *reinterpret_cast<const float4*>(ks + d * kRowsPitch + 4 * tx);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      s[i][0] = fmaf(q[i], k.x, s[i][0]);
+      s[i][1] = fmaf(q[i], k.y, s[i][1]);
+      s[i][2] = fmaf(q[i], k.z, s[i][2]);
+      s[i][3] = fmaf(q[i], k.w, s[i][3]);
+    }
+  }
+}
+
+template <typename T, int HD, int RT>
+__global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs a, const SegShape sh) {
+  using S = RowsShape<HD, RT>;
+  constexpr int ROWS = S::kRows;
+  constexpr int OC = HD / 64;     // float4 columns of the result per thread and pair
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int pre[kKvMaxB + 1];
+  __shared__ long long wsum[kRowsThreads / 32];
+  __shared__ int blocks[kRowsStep / kBlk];
+  float* qs = smem;
+  float* ks = qs + S::kQ;
+  float* vs = ks + S::kK;
+  float* ps = vs + S::kV;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  Split sp;
+  if (!rows_split<kRowsThreads>(a, sh, sh.lead + 4, pre, wsum, sp)) return;
+  for (uint32_t u = sp.u0; u < sp.u1;) {
+    Piece p;
+    find_piece(a, sh, pre, sp, u, p);
+    u = p.next;
+    if (p.s_lo >= p.s_hi) continue;
+    const int i0 = p.tile * sh.rows;
+    __syncthreads();
+    load_queries<T, HD, ROWS>(a, qs, p.o0, i0, p.n, p.g);
+    float o[RT][OC][4], m[RT], l[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      m[i] = kKvLeast;
+      l[i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < OC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][c][e] = 0.0f;
+    }
+    for (int step = p.s_lo; step < p.s_hi; ++step) {
+      const int t0 = step * kRowsStep;
+      // slots that some row of the tile does not see: from the first new one that its first row may not see
+      const bool edge = t0 + kRowsStep > p.base + (a.mask ? 0 : i0 + 1);
+      __syncthreads();
+      load_blocks(a, blocks, p.b, t0, p.end);
+      __syncthreads();
+      load_entries<T, HD, true>(a, a.kv.k_pool, ks, blocks, t0, p.end, p.g);
+      load_entries<T, HD, false>(a, a.kv.v_pool, vs, blocks, t0, p.end, p.g);
+      __syncthreads();
+      float s[RT][4];
+      tile_scores<HD, RT>(qs, ks, ty, tx, s);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int row = i0 + ((ty * RT + i) >> a.g_shift);
+        const int32_t* words = a.mask && row < p.n ? a.mask + (long long)(p.o0 + row) * a.mask_words : nullptr;
+        bool seen[4];
+        float mx = kKvLeast;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = t0 + 4 * tx + j;
+          seen[j] = !edge || (row < p.n && t < p.end && row_sees(words, row, t, p.base, p.n));
+          s[i][j] *= a.c;
+          if (seen[j]) mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float mn = fmaxf(m[i], mx), alpha = exp2f(m[i] - mn);
+        m[i] = mn;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = seen[j] ? exp2f(s[i][j] - mn) : 0.0f;
+          sum += e;
+          // (-1: unseen, so that 0 times an entry that is not finite is left out)
+          ps[(4 * tx + j) * ROWS + ty * RT + i] = seen[j] ? e : -1.0f;
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l[i] = l[i] * alpha + sum;
+#pragma unroll
+        for (int c = 0; c < OC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][c][e] *= alpha;
+      }
+      __syncwarp();   // a warp reads back only its own pairs
+      const int slots = min(kRowsStep, p.end - t0);
+      auto values = [&](auto checked) {
+#pragma unroll 4
+        for (int t = 0; t < slots; ++t) {
+          float w[RT];
+          if constexpr (RT == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(ps + t * ROWS + 4 * ty);
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+          } else {
+            w[0] = ps[t * ROWS + ty];
+          }
+#pragma unroll
+          for (int c = 0; c < OC; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(vs + t * HD + 64 * c + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              if (decltype(checked)::value && w[i] == -1.0f) continue;
+              o[i][c][0] = fmaf(w[i], v.x, o[i][c][0]);
+              o[i][c][1] = fmaf(w[i], v.y, o[i][c][1]);
+              o[i][c][2] = fmaf(w[i], v.z, o[i][c][2]);
+              o[i][c][3] = fmaf(w[i], v.w, o[i][c][3]);
+            }
+          }
+        }
+      };
+      if (edge) values(Flag<true>{});
+      else values(Flag<false>{});
+    }
+    // ---- results, or a piece of them
+    const bool whole = p.c_first == p.c_last;
+    const int slot = (int)blockIdx.x == p.c_first ? 1 : 0;
+    const int valid = min(ROWS, (p.n - i0) << a.g_shift), G = 1 << a.g_shift;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = ty * RT + i;
+      if (r >= valid) continue;
+      const long long row = (long long)(p.o0 + i0 + (r >> a.g_shift)) * (a.n_kv << a.g_shift) + p.g * G + (r & (G - 1));
+#pragma unroll
+      for (int c = 0; c < OC; ++c) {
+        const float4 x = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+        if (whole) {
+          rows_finish<T, HD>(a, row, 16 * c + tx, x, m[i], l[i]);
+        } else {
+          float* pr = a.part + ((2ll * blockIdx.x + slot) * ROWS + r) * (HD + 4);
+          *reinterpret_cast<float4*>(pr + 64 * c + 4 * tx) = x;
+          if (c == 0 && tx == 0) *reinterpret_cast<float2*>(pr + HD) = make_float2(m[i], l[i]);
+        }
+      }
+    }
+    if (tid == 0 && slot == 1 && !whole) {
+      a.meta[2 * blockIdx.x] = make_int4(p.c_last - p.c_first + 1, p.c_first, valid, p.g);
+      a.meta[2 * blockIdx.x + 1] = make_int4(p.o0 + i0, 0, 0, 0);
+    }
+  }
+}
+
+// Joins the pieces of the segments that span thread blocks: thread block (x,
+// y) takes the segment that begins in the first kernel's block x, and of its
+// pairs the y-th group; a thread owns four elements of a pair.
+constexpr int kRowsJoinThreads = 256;
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRowsJoinThreads) rows_join_kernel(const RowsArgs a, int rows) {
+  constexpr int LANES = HD / 4, PER = kRowsJoinThreads / LANES, AHEAD = 4;
+  pdl_wait();
+  pdl_trigger();
+  const int4 seg = a.meta[2 * blockIdx.x];
+  if (seg.x == 0) return;
+  const int first_row = a.meta[2 * blockIdx.x + 1].x, d4 = threadIdx.x % LANES, G = 1 << a.g_shift;
+  for (int r = blockIdx.y * PER + threadIdx.x / LANES; r < seg.z; r += PER * gridDim.y) {
+    float M = kKvLeast, Ls = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k0 = 0; k0 < seg.x; k0 += AHEAD) {
+      float2 ml[AHEAD];
+      float4 y[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {   // no branches: all loads go out together
+        const int kk = min(k0 + k, seg.x - 1);
+        const float* pr = a.part + ((2ll * (seg.y + kk) + (kk == 0 ? 1 : 0)) * rows + r) * (HD + 4);
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(pr + HD));
+        y[k] = __ldcg(reinterpret_cast<const float4*>(pr) + d4);
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (k0 + k >= seg.x) break;
+        const float mn = fmaxf(M, ml[k].x), f0 = exp2f(M - mn), f1 = exp2f(ml[k].x - mn);
+        Ls = Ls * f0 + ml[k].y * f1;
+        x.x = x.x * f0 + y[k].x * f1;
+        x.y = x.y * f0 + y[k].y * f1;
+        x.z = x.z * f0 + y[k].z * f1;
+        x.w = x.w * f0 + y[k].w * f1;
+        M = mn;
+      }
+    }
+    const long long row = (long long)(first_row + (r >> a.g_shift)) * (a.n_kv << a.g_shift) + seg.w * G + (r & (G - 1));
+    rows_finish<T, HD>(a, row, d4, x, M, Ls);
+  }
+}
+
+// Thread block (step of slots, kv head, request): the weights of 64 entries, its
+// keys kept in shared memory, all rows that may see them in tiles of 64 pairs.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRowsThreads) rows_weights_kernel(const RowsArgs a) {
+  constexpr int RT = 4, ROWS = 64;
+  using S = RowsShape<HD, RT>;
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int blocks[kRowsStep / kBlk];
+  __shared__ float lse_s[ROWS];
+  __shared__ float sums[16][kRowsStep + 1];
+  float* qs = smem;
+  float* ks = qs + S::kQ;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int t0 = blockIdx.x * kRowsStep, g = blockIdx.y, b = blockIdx.z, G = 1 << a.g_shift;
+  int bad = 0;
+  for (int x = tid; x < a.B; x += kRowsThreads) {
+    const int r0 = a.row_offsets[x], r1 = a.row_offsets[x + 1];
+    bad |= r0 < 0 || r1 < r0 || r1 > a.T;
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) set_error(a.err, MTP_ERR_DEVICE_ARGS);
+    return;
+  }
+  int o0, n, L;
+  const int err = rows_request(a, b, o0, n, L);
+  if (n == 0) return;
+  const int base = L - n, first = a.first ? a.first[b] : base;
+  if (err != MTP_OK || first < 0) {
+    if (tid == 0 && t0 == 0 && g == 0) set_error(a.err, err != MTP_OK ? err : MTP_ERR_DEVICE_ARGS);
+    return;
+  }
+  if (t0 >= L) return;
+  load_blocks(a, blocks, b, t0, L);
+  __syncthreads();
+  load_entries<T, HD, true>(a, a.kv.k_pool, ks, blocks, t0, L, g);
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int row0 = a.mask ? 0 : max(0, t0 - base);   // rows before it see none of these slots
+  const int tile_rows = ROWS >> a.g_shift;
+  for (int i0 = row0; i0 < n; i0 += tile_rows) {
+    __syncthreads();
+    load_queries<T, HD, ROWS>(a, qs, o0, i0, n, g);
+    if (tid < ROWS) {
+      const int i = i0 + (tid >> a.g_shift);
+      const float l = i < n ? a.lse[(long long)(o0 + i) * (a.n_kv << a.g_shift) + g * G + (tid & (G - 1))] : -INFINITY;
+      lse_s[tid] = l == -INFINITY ? INFINITY : l * kLog2e;   // a row that sees nothing weighs nothing
+    }
+    __syncthreads();
+    float s[RT][4];
+    tile_scores<HD, RT>(qs, ks, ty, tx, s);
+    const bool edge = t0 + kRowsStep > base + (a.mask ? 0 : i0 + 1) || i0 + tile_rows > n;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = ty * RT + i, row = i0 + (r >> a.g_shift);
+      const int32_t* words = a.mask && row < n ? a.mask + (long long)(o0 + row) * a.mask_words : nullptr;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t0 + 4 * tx + j;
+        if (!edge || (row < n && t < L && row_sees(words, row, t, base, n)))
+          acc[j] += exp2f(fmaf(s[i][j], a.c, -lse_s[r]));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sums[ty][4 * tx + j] = acc[j];
+  __syncthreads();
+  const int t = t0 + tid;
+  if (tid < kRowsStep && t < L && blocks[tid >> 4] >= 0) {
+    float x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x += sums[i][tid];
+    const long long at = ((long long)blocks[tid >> 4] * a.n_kv + g) * kBlk + (t & 15);
+    if (MTP_IN_BOUNDS(a.err, at, (long long)a.kv.num_blocks * a.n_kv * kBlk))
+      a.weights[at] = (t < first ? a.weights[at] : 0.0f) + x;
+  }
+}
+
+template <typename T, int HD, int RT>
+static cudaError_t rows_attn_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+  using S = RowsShape<HD, RT>;
+  cudaError_t e = ensure_smem((const void*)rows_attn_kernel<T, HD, RT>, S::kBytes);
+  if (e != cudaSuccess) return e;
+  const SegShape sh{S::kRows >> a.g_shift, kRowsStep, 2};
+  const int grid = (RT == 1 ? 2 : 1) * ctx->num_sms;
+  e = launch_pdl(rows_attn_kernel<T, HD, RT>, dim3(grid), dim3(kRowsThreads), S::kBytes, s, a, sh);
+  if (e != cudaSuccess) return e;
+  const int per = kRowsJoinThreads / (HD / 4);
+  return launch_pdl(rows_join_kernel<T, HD>, dim3(grid, (S::kRows + per - 1) / per), dim3(kRowsJoinThreads), 0, s, a,
+                    (int)S::kRows);
+}
+template <typename T>
+cudaError_t launch_rows_attn(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+  const bool few = (a.max_rows << a.g_shift) <= 16;
+  ctx->launches += 2;
+  if (ctx->cfg.head_dim == 128)
+    return few ? rows_attn_launch<T, 128, 1>(ctx, s, a) : rows_attn_launch<T, 128, 4>(ctx, s, a);
+  return few ? rows_attn_launch<T, 64, 1>(ctx, s, a) : rows_attn_launch<T, 64, 4>(ctx, s, a);
+}
+
+template <typename T, int HD>
+static cudaError_t rows_weights_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+  const int smem = RowsShape<HD, 4>::kWeightBytes;
+  const cudaError_t e = ensure_smem((const void*)rows_weights_kernel<T, HD>, smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = (int)(((long long)a.kv.max_blocks * kBlk + kRowsStep - 1) / kRowsStep);
+  return launch_pdl(rows_weights_kernel<T, HD>, dim3(tiles, a.n_kv, a.B), dim3(kRowsThreads), smem, s, a);
+}
+template <typename T>
+cudaError_t launch_rows_weights(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+  ctx->launches++;
+  return ctx->cfg.head_dim == 128 ? rows_weights_launch<T, 128>(ctx, s, a) : rows_weights_launch<T, 64>(ctx, s, a);
+}
+
+// Workspace: what the join kernel joins, then two pieces a thread block.
+constexpr int kRowsMaxBlocks = 2;    // thread blocks per SM at most
+constexpr int kRowsMaxPairs = 64;    // pairs of a tile at most
+static size_t rows_meta_bytes(const mtp_ctx* ctx) { return (size_t)kRowsMaxBlocks * ctx->num_sms * 2 * sizeof(int4); }
+
+// The checks that both calls share; fills in the common arguments.
+static mtp_status rows_args(mtp_ctx* ctx, int B, int T, const int32_t* row_offsets, int max_rows, const void* q,
+                            int64_t q_stride, const mtp_kv* kv, const int32_t* mask, int mask_words, float scale,
+                            RowsArgs& a) {
+  if (!ctx || B < 1 || B > ctx->cfg.max_batch || B > kKvMaxB || T < 0 || T > (1 << 30) || !row_offsets || !q ||
+      !kv16_ok(kv))
+    return MTP_ERR_INVALID;
+  const mtp_config& c = ctx->cfg;
+  if (max_rows < 1 || q_stride < (int64_t)c.n_q_heads * c.head_dim) return MTP_ERR_INVALID;
+  if (mask && (max_rows > 256 || mask_words < (max_rows + 31) / 32)) return MTP_ERR_INVALID;
+  if (!(scale > 0.0f) || !isfinite(scale)) return MTP_ERR_INVALID;
+  a.q = q;
+  a.row_offsets = row_offsets;
+  a.mask = mask;
+  a.kv = *kv;
+  a.err = ctx->err;
+  a.q_stride = q_stride;
+  a.B = B;
+  a.T = T;
+  a.max_rows = max_rows;
+  a.mask_words = mask_words;
+  a.n_kv = c.n_kv_heads;
+  a.g_shift = group_shift(c);
+  const int per16 = c.dtype == MTP_DTYPE_BF16 ? 8 : 4;
+  a.q_vec = !((uintptr_t)q & 15) && q_stride % per16 == 0;
+  a.c = scale * kLog2e;
+  return MTP_OK;
+}
+
+}  // namespace mtp
+
+using namespace mtp;
+
+extern "C" {
+
+size_t mtp_kv_attention_workspace_bytes(const mtp_ctx* ctx) {
+  if (!ctx) return 0;
+  return rows_meta_bytes(ctx) +
+         (size_t)2 * kRowsMaxBlocks * ctx->num_sms * kRowsMaxPairs * (ctx->cfg.head_dim + 4) * sizeof(float);
+}
+
+mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
+                            const void* q, int64_t q_stride, const mtp_kv* kv, const int32_t* mask, int mask_words,
+                            float scale, void* out, float* lse, void* ws, size_t ws_bytes) {
+  RowsArgs a{};
+  const mtp_status st = rows_args(ctx, B, T, row_offsets, max_rows, q, q_stride, kv, mask, mask_words, scale, a);
+  if (st != MTP_OK) return st;
+  if (!out || ((uintptr_t)out & 15) || !ws || ((uintptr_t)ws & 15) || ws_bytes < mtp_kv_attention_workspace_bytes(ctx))
+    return MTP_ERR_INVALID;
+  if (T == 0) return MTP_OK;
+  DeviceGuard dev(ctx->device);
+  if (!dev.ok) return MTP_ERR_CUDA;
+  a.out = out;
+  a.lse = lse;
+  a.meta = (int4*)ws;
+  a.part = (float*)((char*)ws + rows_meta_bytes(ctx));
+  return launch_status(ctx->cfg.dtype == MTP_DTYPE_BF16 ? launch_rows_attn<uint16_t>(ctx, (cudaStream_t)stream, a)
+                                                        : launch_rows_attn<float>(ctx, (cudaStream_t)stream, a));
+}
+
+mtp_status mtp_kv_attention_weights(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
+                                    const void* q, int64_t q_stride, const mtp_kv* kv, const int32_t* mask,
+                                    int mask_words, float scale, const float* lse, const int32_t* first,
+                                    float* weights) {
+  RowsArgs a{};
+  const mtp_status st = rows_args(ctx, B, T, row_offsets, max_rows, q, q_stride, kv, mask, mask_words, scale, a);
+  if (st != MTP_OK) return st;
+  if (!lse || !weights || a.n_kv > 65535) return MTP_ERR_INVALID;
+  if (T == 0) return MTP_OK;
+  DeviceGuard dev(ctx->device);
+  if (!dev.ok) return MTP_ERR_CUDA;
+  a.lse = const_cast<float*>(lse);
+  a.first = first;
+  a.weights = weights;
+  return launch_status(ctx->cfg.dtype == MTP_DTYPE_BF16 ? launch_rows_weights<uint16_t>(ctx, (cudaStream_t)stream, a)
+                                                        : launch_rows_weights<float>(ctx, (cudaStream_t)stream, a));
+}
+
+}  // extern "C"
