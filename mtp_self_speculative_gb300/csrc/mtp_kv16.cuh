@@ -80,6 +80,12 @@ struct RowsArgs {
   const int32_t* first;          // [B] or null
 };
 
+constexpr int kAtPairs = 256;      // pairs of a tile of the tensor-core kernel
+
+// The tensor-core form of the attention (bf16 heads); its pieces are joined as
+// the other form's.
+cudaError_t launch_attn_tc(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a);
+
 // Request b's first row, rows and entries; 0, or the error that leaves it out.
 __device__ __forceinline__ int rows_request(const RowsArgs& a, int b, int& o0, int& n, int& L) {
   o0 = a.row_offsets[b];

@@ -1,0 +1,734 @@
+// Attention of new rows over the paged cache on the tensor cores (tcgen05),
+// bf16 heads: prompts, chunks of them, draft rows and decoding rows alike.
+//
+//   out[r, h] = sum_t p_t V[t, g] / sum_t p_t,  p_t = 2^(c s_t - m),
+//   s_t = q[r, h] . K[t, g], c = scale * log2 e, m a reference near the running
+// maximum.
+//
+// A segment is 256 (row, query head) pairs of one kv head; a step takes 128
+// slots (eight cache blocks).  One thread block per SM, twelve warps:
+//   warps 0-3, 4-7  two softmax groups; group w owns the 128 x 128 scores S_w
+//            and the result O_w in tensor memory, a thread a row: it reads its
+//            128 scores, takes the reference off, writes the weights as bf16
+//            over the scores (the A operand of the second product) and keeps the
+//            sum.  O_w is scaled only when a row's maximum passes its reference
+//            by 8 (powers of two), so most steps touch it with products alone.
+//   warp 8   finds the segments of the block's share, and loads cache blocks
+//            (2 KB boxes, 128-byte swizzle) into a ring of K and V tiles, into
+//            the next segment's as soon as the ring has room
+//   warp 9   issues the products: S_w = Q_w K^T, O_w += P_w V, the two groups'
+//            in turn, so that one group's softmax runs under the other's products
+//   warps 10, 11  look through the V tiles that some row sees only part of for
+//            entries that are not finite (0 * inf) and put zeros there; the rows
+//            that see such an entry get it at the end.
+// With more than 128 pairs the groups take 128 pairs each of every step; with up
+// to 128 (decoding rows, the end of a chunk) both take all of them, of
+// every other step, and the two results are joined from tensor memory.
+//
+// Work is split over the flattened (request, kv head, tile, step) sequence in
+// equal shares, found on the device from the lengths; a segment that spans
+// thread blocks leaves its pieces in the workspace for rows_join_kernel.
+#include <cuda.h>
+#include <math.h>
+
+#include "mtp_kv16.cuh"
+
+namespace mtp {
+
+constexpr int kAtThreads = 384;
+constexpr int kAtStep = 128;        // slots of a step
+constexpr uint32_t kAtWait = 1u << 23;
+constexpr float kAtSlack = 8.0f;    // how far (powers of two) a maximum may pass its reference
+constexpr float kAtCoarse = 67108864.0f;   // from 2^26 on the reference's rounding is some units
+
+template <int HD>
+struct AtShape {
+  static constexpr int kHalves = HD / 64;
+  static constexpr int kTile = kAtStep * HD * 2;              // bytes of a K or V tile, and of 128 pairs' queries
+  static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr int kBytes = 2 * kTile + kStages * kTile + 1024;
+};
+
+struct AtPiece {
+  int b;            // request, or -1: no more work
+  int g, o0, n, base, end, i0;
+  int s_lo, tiles;  // first step, number of steps
+  int edge;         // the first step that some row sees only part of
+  int valid;        // pairs
+  int slot;         // where a piece of a spanning segment goes; -1: the whole segment
+  int dirty;        // an entry that is not finite was taken out of V
+};
+
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t i = 0; i < kAtWait; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255) == 255 && *abort_flag) return false;
+  }
+  return false;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void at_tma(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(dst)),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+// Shared-memory operands with 128-byte swizzle.  K-major: rows of 64 elements,
+// 1024 bytes between groups of eight rows.  MN-major (V: the products' columns
+// lie next to one another): 64 columns of eight slots are 1024 bytes, `lead`
+// bytes to the next 64 columns.
+__device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t lead) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+#define AT_R32(v) \
+  "=r"((v)[0]), "=r"((v)[1]), "=r"((v)[2]), "=r"((v)[3]), "=r"((v)[4]), "=r"((v)[5]), "=r"((v)[6]), "=r"((v)[7]),   \
+      "=r"((v)[8]), "=r"((v)[9]), "=r"((v)[10]), "=r"((v)[11]), "=r"((v)[12]), "=r"((v)[13]), "=r"((v)[14]),         \
+      "=r"((v)[15]), "=r"((v)[16]), "=r"((v)[17]), "=r"((v)[18]), "=r"((v)[19]), "=r"((v)[20]), "=r"((v)[21]),       \
+      "=r"((v)[22]), "=r"((v)[23]), "=r"((v)[24]), "=r"((v)[25]), "=r"((v)[26]), "=r"((v)[27]), "=r"((v)[28]),       \
+      "=r"((v)[29]), "=r"((v)[30]), "=r"((v)[31])
+#define AT_W32(v) \
+  "r"((v)[0]), "r"((v)[1]), "r"((v)[2]), "r"((v)[3]), "r"((v)[4]), "r"((v)[5]), "r"((v)[6]), "r"((v)[7]), "r"((v)[8]), \
+      "r"((v)[9]), "r"((v)[10]), "r"((v)[11]), "r"((v)[12]), "r"((v)[13]), "r"((v)[14]), "r"((v)[15]), "r"((v)[16]),  \
+      "r"((v)[17]), "r"((v)[18]), "r"((v)[19]), "r"((v)[20]), "r"((v)[21]), "r"((v)[22]), "r"((v)[23]), "r"((v)[24]), \
+      "r"((v)[25]), "r"((v)[26]), "r"((v)[27]), "r"((v)[28]), "r"((v)[29]), "r"((v)[30]), "r"((v)[31])
+
+// 32 columns of this thread's row.  The registers hold them after tmem_ready.
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : AT_R32(v)
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Keeps uses of the registers behind the wait above.
+__device__ __forceinline__ void tmem_ready(uint32_t* v) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]),
+                 "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::AT_W32(v),
+      "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two floats at a time.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void untwo(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Halves of a word that hold bf16 numbers that are not finite: bit 15, bit 31.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
+// Ring positions of a piece of n steps: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
+__device__ __forceinline__ uint32_t ring_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ uint32_t ring_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+
+template <int HD>
+struct AtShared {
+  uint64_t full[AtShape<HD>::kStages], empty[AtShape<HD>::kStages];
+  uint64_t s_full[2], p_ready[2], q_ready[2], scan, clean, merged, piece_full[2], piece_empty[2];
+  AtPiece piece[2];
+  float ml[2][128][2];
+  uint32_t tmem;
+  volatile int abort_flag;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                                   const __grid_constant__ CUtensorMap vmap,
+                                                                   const RowsArgs a, const SegShape sh) {
+  using S = AtShape<HD>;
+  constexpr int NS = S::kStages;
+  extern __shared__ __align__(1024) unsigned char at_smem_raw[];
+  __shared__ AtShared<HD> sm;
+  __shared__ int pre[kKvMaxB + 1];
+  __shared__ long long wsum[kAtThreads / 32];
+  unsigned char* smem = (unsigned char*)(((uintptr_t)at_smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* ring = smem + 2 * S::kTile;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = 1 << a.g_shift;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sm.s_full[w], 1);
+      mbar_init(&sm.p_ready[w], 4);
+      mbar_init(&sm.q_ready[w], 4);
+      mbar_init(&sm.piece_full[w], 1);
+      mbar_init(&sm.piece_empty[w], 11);
+    }
+    mbar_init(&sm.scan, 1);
+    mbar_init(&sm.clean, 2);
+    mbar_init(&sm.merged, 8);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tmem_before();
+  __syncthreads();
+  tmem_after();
+  const uint32_t tmem = sm.tmem;
+  pdl_wait();
+  pdl_trigger();
+  if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  Split sp;
+  const bool work = rows_split<kAtThreads>(a, sh, sh.lead + 1, pre, wsum, sp);
+
+  if (work && warp == 8) {
+    // ------------------------------------------------------------- producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    uint32_t rb = 0, issued = 0;
+    int np = 0;
+    bool ok = true;
+    const int page = lane & 7, half = lane >> 3;
+    const int oob = a.kv.num_blocks * a.n_kv * kBlk;   // rows of the pool: a box from there on is zeros
+    uint32_t u = sp.u0;
+    while (ok) {
+      Piece p{};
+      bool any = false;
+      while (u < sp.u1) {
+        find_piece(a, sh, pre, sp, u, p);
+        u = p.next;
+        if (p.s_lo < p.s_hi) {
+          any = true;
+          break;
+        }
+      }
+      ok = __all_sync(0xffffffffu, at_wait(&sm.piece_empty[np & 1], ((np >> 1) & 1) ^ 1, &sm.abort_flag));
+      if (!ok) break;
+      const bool whole = p.c_first == p.c_last;
+      const int i0 = p.tile * sh.rows, valid = min(kAtPairs, (p.n - i0) << a.g_shift);
+      if (lane == 0) {
+        AtPiece& q = sm.piece[np & 1];
+        q.b = any ? p.b : -1;
+        q.g = p.g;
+        q.o0 = p.o0;
+        q.n = p.n;
+        q.base = p.base;
+        q.end = p.end;
+        q.i0 = i0;
+        q.s_lo = p.s_lo;
+        q.tiles = p.s_hi - p.s_lo;
+        // the first step with a slot that the segment's first row (or, under a mask, some row) may not see
+        q.edge = (p.base + (a.mask ? 0 : i0 + 1)) / kAtStep;
+        q.valid = valid;
+        q.slot = whole ? -1 : ((int)blockIdx.x == p.c_first ? 1 : 0);
+        q.dirty = 0;
+        mbar_arrive(&sm.piece_full[np & 1]);
+        if (any && !whole && (int)blockIdx.x == p.c_first) {
+          a.meta[2 * blockIdx.x] = make_int4(p.c_last - p.c_first + 1, p.c_first, valid, p.g);
+          a.meta[2 * blockIdx.x + 1] = make_int4(p.o0 + i0, 0, 0, 0);
+        }
+      }
+      ++np;
+      if (!any) break;
+      const int n = p.s_hi - p.s_lo;
+      const int32_t* table = a.kv.block_table + (long long)p.b * a.kv.max_blocks;
+      auto row_of = [&](int j) -> int {   // pool row of this lane's box in step j
+        const int t = (p.s_lo + j) * kAtStep + page * kBlk;
+        if (j >= n || t >= p.end || half >= S::kHalves) return oob;
+        const int blk = table[t >> 4];
+        if (blk < 0 || blk >= a.kv.num_blocks) {
+          set_error(a.err, MTP_ERR_CAPACITY);
+          return oob;
+        }
+        return (blk * a.n_kv + p.g) * kBlk;
+      };
+      auto issue = [&](const CUtensorMap* map, uint32_t it, int row) -> bool {
+        const int st = it % NS;
+        if (!__all_sync(0xffffffffu, at_wait(&sm.empty[st], ((it / NS) & 1) ^ 1, &sm.abort_flag))) return false;
+        if (lane == 0) mbar_expect_tx(&sm.full[st], S::kTile);
+        __syncwarp();
+        if (half < S::kHalves)
+          at_tma(ring + (size_t)st * S::kTile + half * (kAtStep * 128) + page * (kBlk * 128), map, half * 64, row, &sm.full[st]);
+        issued = it + 1;
+        return true;
+      };
+      int r0 = row_of(0), r1 = row_of(1);
+      ok = issue(&kmap, rb, r0);
+      for (int j = 0; j < n && ok; ++j) {
+        const int r2 = row_of(j + 2);   // looked up two steps ahead
+        if (j + 1 < n) ok = issue(&kmap, rb + ring_k(j + 1), r1);
+        if (ok) ok = issue(&vmap, rb + ring_v(j, n), r0);
+        r0 = r1;
+        r1 = r2;
+      }
+      rb += 2 * n;
+    }
+    if (!ok) {
+      if (lane == 0) set_error(a.err, MTP_ERR_TIMEOUT);
+      sm.abort_flag = 1;
+      // copies in flight land before the block ends
+      for (uint32_t it = issued > NS ? issued - NS : 0; it < issued; ++it)
+        mbar_wait_bounded(&sm.full[it % NS], (it / NS) & 1, 1u << 20);
+    }
+  } else if (work && warp == 9) {
+    // ------------------------------------------------------------- products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (lane == 0) {
+      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
+      constexpr uint32_t kIdS = kBase | ((uint32_t)(kAtStep >> 3) << 17);
+      constexpr uint32_t kIdO = kBase | (1u << 16) | ((uint32_t)(HD >> 3) << 17);   // B (V) is MN-major
+      uint32_t rb = 0, cleans = 0, p_count[2] = {0, 0};
+      bool ok = true;
+      const uint32_t q_at = smem_addr(smem), ring_at = smem_addr(ring);
+      for (int np = 0; ok; ++np) {
+        ok = at_wait(&sm.piece_full[np & 1], (np >> 1) & 1, &sm.abort_flag);
+        if (!ok) break;
+        const AtPiece& p = sm.piece[np & 1];
+        if (p.b < 0) break;
+        const int n = p.tiles, s_lo = p.s_lo, edge = p.edge;
+        const bool split = p.valid <= 128;
+        mbar_arrive(&sm.piece_empty[np & 1]);
+        auto scores = [&](int w, int j) {   // S_w = Q K_j^T
+          const uint32_t qa = q_at + (split ? 0 : w * S::kTile), ka = ring_at + ((rb + ring_k(j)) % NS) * S::kTile;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kAtStep * 128) + (kk & 3) * 32;
+            mma_ss(tmem + w * 128, at_desc(qa + off, 16), at_desc(ka + off, 16), kIdS, kk > 0);
+          }
+        };
+        auto values = [&](int w, int j, bool first) {   // O_w += P_w V_j
+          const uint32_t va = ring_at + ((rb + ring_v(j, n)) % NS) * S::kTile;
+#pragma unroll
+          for (int kk = 0; kk < kAtStep / 16; ++kk)
+            mma_ts(tmem + 256 + w * HD, tmem + w * 128 + kk * 8, at_desc(va + kk * (kBlk * 128), kAtStep * 128), kIdO,
+                   !(first && kk == 0));
+        };
+        auto wait_ring = [&](uint32_t pos) {
+          const uint32_t it = rb + pos;
+          if (!at_wait(&sm.full[it % NS], (it / NS) & 1, &sm.abort_flag)) return false;
+          tmem_after();
+          return true;
+        };
+        auto free_ring = [&](uint32_t pos) { mma_commit(&sm.empty[(rb + pos) % NS]); };
+        // V_j is there; where some row sees only part of it, it is looked through
+        // meanwhile (the scanning warps come when they are called: ahead of the
+        // ring they could not tell its phases apart)
+        auto wait_v = [&](int j) {
+          if (!wait_ring(ring_v(j, n))) return false;
+          if (s_lo + j >= edge) mbar_arrive(&sm.scan);
+          return true;
+        };
+        auto wait_clean = [&](int j) {   // V_j holds finite numbers alone
+          if (s_lo + j < edge) return true;
+          return at_wait(&sm.clean, cleans++ & 1, &sm.abort_flag);
+        };
+        auto wait_p = [&](int w) {
+          if (!at_wait(&sm.p_ready[w], p_count[w]++ & 1, &sm.abort_flag)) return false;
+          tmem_after();
+          return true;
+        };
+        ok = at_wait(&sm.q_ready[0], np & 1, &sm.abort_flag) && wait_ring(ring_k(0));
+        if (!ok) break;
+        scores(0, 0);
+        mma_commit(&sm.s_full[0]);
+        if (split) free_ring(ring_k(0));
+        ok = at_wait(&sm.q_ready[1], np & 1, &sm.abort_flag);
+        if (!ok) break;
+        if (!split) {
+          scores(1, 0);
+          mma_commit(&sm.s_full[1]);
+          free_ring(ring_k(0));
+          for (int j = 0; j < n && ok; ++j) {
+            const bool more = j + 1 < n;
+            ok = (!more || wait_ring(ring_k(j + 1))) && wait_v(j);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              ok = ok && wait_p(w) && (w == 1 || wait_clean(j));
+              if (!ok) break;
+              values(w, j, j == 0);
+              if (more) scores(w, j + 1);
+              mma_commit(&sm.s_full[w]);
+            }
+            if (!ok) break;
+            if (more) free_ring(ring_k(j + 1));
+            free_ring(ring_v(j, n));
+          }
+        } else {
+          if (n > 1) {
+            ok = wait_ring(ring_k(1));
+            if (!ok) break;
+            scores(1, 1);
+            mma_commit(&sm.s_full[1]);
+            free_ring(ring_k(1));
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            const int w = j & 1;
+            const bool more = j + 2 < n;
+            ok = wait_v(j) && wait_p(w) && wait_clean(j);
+            if (!ok) break;
+            values(w, j, j < 2);
+            free_ring(ring_v(j, n));
+            if (more) {
+              ok = wait_ring(ring_k(j + 2));
+              if (!ok) break;
+              scores(w, j + 2);
+              free_ring(ring_k(j + 2));
+            }
+            mma_commit(&sm.s_full[w]);
+          }
+        }
+        rb += 2 * n;
+      }
+      if (!ok) {
+        sm.abort_flag = 1;
+        set_error(a.err, MTP_ERR_TIMEOUT);
+      }
+    }
+    __syncwarp();
+  } else if (work && warp >= 10) {
+    // ------------------------------------- entries of V that are not finite
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    uint32_t rb = 0, scans = 0;
+    bool ok = true;
+    for (int np = 0; ok; ++np) {
+      ok = __all_sync(0xffffffffu, at_wait(&sm.piece_full[np & 1], (np >> 1) & 1, &sm.abort_flag));
+      if (!ok) break;
+      AtPiece& p = sm.piece[np & 1];
+      if (p.b < 0) break;
+      const int n = p.tiles;
+      for (int j = max(0, p.edge - p.s_lo); j < n && ok; ++j) {
+        const uint32_t it = rb + ring_v(j, n);
+        ok = __all_sync(0xffffffffu, at_wait(&sm.scan, scans++ & 1, &sm.abort_flag) &&
+                                         at_wait(&sm.full[it % NS], (it / NS) & 1, &sm.abort_flag));
+        if (!ok) break;
+        uint4* tile = reinterpret_cast<uint4*>(ring + (size_t)(it % NS) * S::kTile);
+        bool found = false;
+#pragma unroll 8
+        for (int i = (warp - 10) * 32 + lane; i < S::kTile / 16; i += 64) {
+          const uint4 x = tile[i];
+          if (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) found = true;
+        }
+        if (found) {
+          for (int i = (warp - 10) * 32 + lane; i < S::kTile / 16; i += 64) {
+            uint4 x = tile[i];
+            x.x &= ~((not_finite2(x.x) >> 15) * 0xFFFFu);
+            x.y &= ~((not_finite2(x.y) >> 15) * 0xFFFFu);
+            x.z &= ~((not_finite2(x.z) >> 15) * 0xFFFFu);
+            x.w &= ~((not_finite2(x.w) >> 15) * 0xFFFFu);
+            tile[i] = x;
+          }
+          *(volatile int*)&p.dirty = 1;
+          fence_async();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.clean);
+      }
+      rb += 2 * n;
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&sm.piece_empty[np & 1]);
+    }
+    if (!ok) sm.abort_flag = 1;
+  } else if (work) {
+    // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int w = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256;
+    uint32_t s_count = 0, merges = 0;   // phases of s_full[w] and of merged
+    bool ok = true;
+    for (int np = 0; ok; ++np) {
+      ok = __all_sync(0xffffffffu, at_wait(&sm.piece_full[np & 1], (np >> 1) & 1, &sm.abort_flag));
+      if (!ok) break;
+      const AtPiece& p = sm.piece[np & 1];
+      if (p.b < 0) break;
+      const int n = p.tiles, s_lo = p.s_lo, i0 = p.i0, rows = p.n, base = p.base, g = p.g, o0 = p.o0;
+      const bool split = p.valid <= 128;
+      const int mine = split ? (n + 1 - w) / 2 : n;       // steps of this group
+      // ---- queries: this group's 128 pairs, swizzled as the products read them
+      if (!split || w == 0) {
+        unsigned char* qt = smem + w * S::kTile;
+        constexpr int CH = HD / 8;                         // 16-byte chunks of a pair
+        const uint16_t* q = (const uint16_t*)a.q;
+#pragma unroll 8
+        for (int x = r; x < 128 * CH; x += 128) {
+          const int pr = x / CH, c = x % CH, i = i0 + ((w * 128 + pr) >> a.g_shift);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (i < rows) {
+            const uint16_t* src = q + (long long)(o0 + i) * a.q_stride + (long long)(g * G + (pr & (G - 1))) * HD + c * 8;
+            if (a.q_vec) {
+              v = *reinterpret_cast<const uint4*>(src);
+            } else {
+              v = make_uint4((uint32_t)src[0] | (uint32_t)src[1] << 16, (uint32_t)src[2] | (uint32_t)src[3] << 16,
+                             (uint32_t)src[4] | (uint32_t)src[5] << 16, (uint32_t)src[6] | (uint32_t)src[7] << 16);
+            }
+          }
+          *reinterpret_cast<uint4*>(qt + (c >> 3) * (128 * 128) + pr * 128 + (((c & 7) ^ (pr & 7)) << 4)) = v;
+        }
+        fence_async();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_ready[w]);
+      // ---- this thread's row
+      const int pr = split ? r : w * 128 + r;
+      const int i = i0 + (pr >> a.g_shift);
+      const bool live = i < rows;
+      const int last = min(base + i, p.end - 1);           // the last slot that the row sees (without a mask)
+      const int32_t* words = a.mask && live ? a.mask + (long long)(o0 + i) * a.mask_words : nullptr;
+      // the first step that some row of this group sees only part of
+      const int edge = a.mask || split ? p.edge : (base + i0 + ((w * 128) >> a.g_shift) + 1) / kAtStep;
+      float m = kKvLeast, l = 0.0f;
+      for (int x = 0; x < mine; ++x) {
+        const int j = split ? 2 * x + w : x;
+        ok = __all_sync(0xffffffffu, at_wait(&sm.s_full[w], s_count & 1, &sm.abort_flag));
+        if (!ok) break;
+        ++s_count;
+        tmem_after();
+        uint32_t s[128];
+        tmem_ld(s_at, s);
+        tmem_ld(s_at + 32, s + 32);
+        tmem_ld(s_at + 64, s + 64);
+        tmem_ld(s_at + 96, s + 96);
+        tmem_wait_ld();
+        tmem_ready(s);
+        tmem_ready(s + 32);
+        tmem_ready(s + 64);
+        tmem_ready(s + 96);
+        if (s_lo + j >= edge) {
+          const int t0 = (s_lo + j) * kAtStep;
+          if (a.mask) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e) {
+              const int t = t0 + e;
+              if (!(live && t < p.end && row_sees(words, i, t, base, rows))) s[e] = 0xFF800000u;
+            }
+          } else {
+            const int most = last - t0;
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e > most) s[e] = 0xFF800000u;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[e]);
+#pragma unroll
+        for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+        const float top = fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast);
+        const bool above = top > m + kAtSlack;
+        if (__any_sync(0xffffffffu, above)) {
+          const float mn = above ? top : m, alpha = exp2_fast(m - mn);
+          m = mn;
+          l *= alpha;
+          if (x > 0) {   // (S_w full: the products into O_w before it have ended)
+            const uint32_t o = o_at + w * HD;
+#pragma unroll
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+              uint32_t v[32];
+              tmem_ld(o + c0, v);
+              tmem_wait_ld();
+              tmem_ready(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st(o + c0, v);
+            }
+          }
+        }
+        uint64_t sum[2] = {0ull, 0ull};
+        if (__any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast)) {
+          // scores so large that the reference is rounded to whole units: round them like it
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) {
+            const float p0 = exp2_fast(__fmul_rn(__uint_as_float(s[e]), a.c) - m);
+            const float p1 = exp2_fast(__fmul_rn(__uint_as_float(s[e + 1]), a.c) - m);
+            sum[0] = add2(sum[0], two(p0, p1));
+            s[e / 2] = pack2_bf16(p0, p1);
+          }
+        } else {
+          const uint64_t cc = two(a.c, a.c), mm = two(-m, -m);
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) {
+            float p0, p1;
+            untwo(fma2(two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mm), p0, p1);
+            p0 = exp2_fast(p0);
+            p1 = exp2_fast(p1);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(p0, p1));
+            s[e / 2] = pack2_bf16(p0, p1);
+          }
+        }
+        tmem_st(s_at, s);
+        tmem_st(s_at + 32, s + 32);
+        float l0, l1;
+        untwo(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
+        tmem_wait_st();
+        tmem_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[w]);
+      }
+      if (!ok) break;
+      // ---- results: O_w of 128 pairs, or both groups' parts of the same pairs, half of the columns each
+      if (mine > 0) {
+        ok = __all_sync(0xffffffffu, at_wait(&sm.s_full[w], s_count & 1, &sm.abort_flag));
+        if (!ok) break;
+        ++s_count;
+      }
+      float f0 = 1.0f, f1 = 0.0f;
+      const bool both = split && n > 1;
+      if (split) {
+        if (w == 0 || mine > 0) {
+          sm.ml[w][r][0] = m;
+          sm.ml[w][r][1] = l;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merged);
+        ok = __all_sync(0xffffffffu, at_wait(&sm.merged, merges++ & 1, &sm.abort_flag));
+        if (!ok) break;
+        if (!both) {
+          m = sm.ml[0][r][0];
+          l = sm.ml[0][r][1];
+        } else {
+          const float m0 = sm.ml[0][r][0], m1 = sm.ml[1][r][0];
+          m = fmaxf(m0, m1);
+          f0 = exp2_fast(m0 - m);
+          f1 = exp2_fast(m1 - m);
+          l = sm.ml[0][r][1] * f0 + sm.ml[1][r][1] * f1;
+        }
+      }
+      tmem_after();
+      const int c_lo = split ? w * (HD / 2) : 0, c_hi = split ? c_lo + HD / 2 : HD;
+      const uint32_t o_mine = split ? o_at : o_at + w * HD;
+      const bool dirty = *(volatile const int*)&p.dirty;
+      const long long row = (long long)(o0 + i) * (a.n_kv << a.g_shift) + g * G + (pr & (G - 1));
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+      for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+        uint32_t v[32];
+        float y[32];
+        tmem_ld(o_mine + c0, v);
+        tmem_wait_ld();
+        tmem_ready(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]);
+        if (both) {
+          tmem_ld(o_at + HD + c0, v);
+          tmem_wait_ld();
+          tmem_ready(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = y[e] * f0 + __uint_as_float(v[e]) * f1;
+        }
+        if (dirty && live) {
+          // what the row sees of the entries that were taken out
+          for (int t = max(s_lo, p.edge) * kAtStep; t < min(p.end, (s_lo + n) * kAtStep); ++t) {
+            if (!row_sees(words, i, t, base, rows)) continue;
+            const int blk = a.kv.block_table[(long long)p.b * a.kv.max_blocks + (t >> 4)];
+            if (blk < 0 || blk >= a.kv.num_blocks) continue;
+            const uint16_t* vr = (const uint16_t*)a.kv.v_pool + (((long long)blk * a.n_kv + g) * kBlk + (t & 15)) * HD + c0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((vr[e] & 0x7F80u) == 0x7F80u) y[e] += elem<uint16_t>(vr + e);
+          }
+        }
+        if (!live) continue;
+        if (p.slot < 0) {
+          if (!MTP_IN_BOUNDS(a.err, row * HD + c0 + 31, (long long)a.T * (a.n_kv << a.g_shift) * HD)) continue;
+          uint4* op = reinterpret_cast<uint4*>((uint16_t*)a.out + row * HD + c0);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] *= inv;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) op[e] = narrow16<uint16_t>(y + 8 * e);
+        } else {
+          float* pt = a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pr) * (HD + 4);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(pt + c0 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          if (c0 == 0) *reinterpret_cast<float2*>(pt + HD) = make_float2(m, l);
+        }
+      }
+      if (live && c_lo == 0 && p.slot < 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (split) {
+        // the other group's part is read: it may go on to its next products
+        tmem_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merged);
+        ok = __all_sync(0xffffffffu, at_wait(&sm.merged, merges++ & 1, &sm.abort_flag));
+        if (!ok) break;
+        tmem_after();
+      }
+      tmem_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.piece_empty[np & 1]);
+    }
+    if (!ok) {
+      sm.abort_flag = 1;
+      if (lane == 0) set_error(a.err, MTP_ERR_TIMEOUT);
+    }
+  }
+  tmem_before();
+  __syncthreads();
+  if (warp == 9) {
+    tmem_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+template <int HD>
+static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+  using S = AtShape<HD>;
+  CUtensorMap km, vm;
+  const uint64_t rows = (uint64_t)a.kv.num_blocks * a.n_kv * kBlk;
+  if (rows > INT32_MAX || !make_map(&km, a.kv.k_pool, rows, HD, kBlk) || !make_map(&vm, a.kv.v_pool, rows, HD, kBlk))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = ensure_smem((const void*)kv_attn_tc_kernel<HD>, S::kBytes);
+  if (e != cudaSuccess) return e;
+  const SegShape sh{kAtPairs >> a.g_shift, kAtStep, 2};
+  return launch_pdl(kv_attn_tc_kernel<HD>, dim3(ctx->num_sms), dim3(kAtThreads), S::kBytes, s, km, vm, a, sh);
+}
+cudaError_t launch_attn_tc(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+  return ctx->cfg.head_dim == 128 ? attn_tc_launch<128>(ctx, s, a) : attn_tc_launch<64>(ctx, s, a);
+}
+
+}  // namespace mtp

@@ -386,26 +386,33 @@ __global__ void __launch_bounds__(kRowsThreads) rows_weights_kernel(const RowsAr
   }
 }
 
-template <typename T, int HD, int RT>
+template <typename T, int HD>
+static cudaError_t rows_join_launch(cudaStream_t s, const RowsArgs& a, int grid, int pairs) {
+  const int per = kRowsJoinThreads / (HD / 4);
+  return launch_pdl(rows_join_kernel<T, HD>, dim3(grid, (pairs + per - 1) / per), dim3(kRowsJoinThreads), 0, s, a, pairs);
+}
+
+template <int HD, int RT>
 static cudaError_t rows_attn_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
   using S = RowsShape<HD, RT>;
-  cudaError_t e = ensure_smem((const void*)rows_attn_kernel<T, HD, RT>, S::kBytes);
+  cudaError_t e = ensure_smem((const void*)rows_attn_kernel<float, HD, RT>, S::kBytes);
   if (e != cudaSuccess) return e;
   const SegShape sh{S::kRows >> a.g_shift, kRowsStep, 2};
   const int grid = (RT == 1 ? 2 : 1) * ctx->num_sms;
-  e = launch_pdl(rows_attn_kernel<T, HD, RT>, dim3(grid), dim3(kRowsThreads), S::kBytes, s, a, sh);
-  if (e != cudaSuccess) return e;
-  const int per = kRowsJoinThreads / (HD / 4);
-  return launch_pdl(rows_join_kernel<T, HD>, dim3(grid, (S::kRows + per - 1) / per), dim3(kRowsJoinThreads), 0, s, a,
-                    (int)S::kRows);
+  e = launch_pdl(rows_attn_kernel<float, HD, RT>, dim3(grid), dim3(kRowsThreads), S::kBytes, s, a, sh);
+  return e != cudaSuccess ? e : rows_join_launch<float, HD>(s, a, grid, S::kRows);
 }
-template <typename T>
-cudaError_t launch_rows_attn(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
-  const bool few = (a.max_rows << a.g_shift) <= 16;
+static cudaError_t launch_rows_attn(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
   ctx->launches += 2;
-  if (ctx->cfg.head_dim == 128)
-    return few ? rows_attn_launch<T, 128, 1>(ctx, s, a) : rows_attn_launch<T, 128, 4>(ctx, s, a);
-  return few ? rows_attn_launch<T, 64, 1>(ctx, s, a) : rows_attn_launch<T, 64, 4>(ctx, s, a);
+  if (ctx->cfg.dtype == MTP_DTYPE_BF16) {
+    const cudaError_t e = launch_attn_tc(ctx, s, a);
+    if (e != cudaSuccess) return e;
+    return ctx->cfg.head_dim == 128 ? rows_join_launch<uint16_t, 128>(s, a, ctx->num_sms, kAtPairs)
+                                    : rows_join_launch<uint16_t, 64>(s, a, ctx->num_sms, kAtPairs);
+  }
+  const bool few = (a.max_rows << a.g_shift) <= 16;
+  if (ctx->cfg.head_dim == 128) return few ? rows_attn_launch<128, 1>(ctx, s, a) : rows_attn_launch<128, 4>(ctx, s, a);
+  return few ? rows_attn_launch<64, 1>(ctx, s, a) : rows_attn_launch<64, 4>(ctx, s, a);
 }
 
 template <typename T, int HD>
@@ -424,7 +431,6 @@ cudaError_t launch_rows_weights(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a)
 
 // Workspace: what the join kernel joins, then two pieces a thread block.
 constexpr int kRowsMaxBlocks = 2;    // thread blocks per SM at most
-constexpr int kRowsMaxPairs = 64;    // pairs of a tile at most
 static size_t rows_meta_bytes(const mtp_ctx* ctx) { return (size_t)kRowsMaxBlocks * ctx->num_sms * 2 * sizeof(int4); }
 
 // The checks that both calls share; fills in the common arguments.
@@ -464,8 +470,8 @@ extern "C" {
 
 size_t mtp_kv_attention_workspace_bytes(const mtp_ctx* ctx) {
   if (!ctx) return 0;
-  return rows_meta_bytes(ctx) +
-         (size_t)2 * kRowsMaxBlocks * ctx->num_sms * kRowsMaxPairs * (ctx->cfg.head_dim + 4) * sizeof(float);
+  const int pairs = ctx->cfg.dtype == MTP_DTYPE_BF16 ? kAtPairs : kRowsMaxBlocks * 64;   // of an SM's thread blocks
+  return rows_meta_bytes(ctx) + (size_t)2 * ctx->num_sms * pairs * (ctx->cfg.head_dim + 4) * sizeof(float);
 }
 
 mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
@@ -483,8 +489,7 @@ mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int3
   a.lse = lse;
   a.meta = (int4*)ws;
   a.part = (float*)((char*)ws + rows_meta_bytes(ctx));
-  return launch_status(ctx->cfg.dtype == MTP_DTYPE_BF16 ? launch_rows_attn<uint16_t>(ctx, (cudaStream_t)stream, a)
-                                                        : launch_rows_attn<float>(ctx, (cudaStream_t)stream, a));
+  return launch_status(launch_rows_attn(ctx, (cudaStream_t)stream, a));
 }
 
 mtp_status mtp_kv_attention_weights(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
