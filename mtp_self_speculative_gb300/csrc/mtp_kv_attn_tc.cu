@@ -88,19 +88,42 @@ __device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t lead) {
   d |= (uint64_t)2 << 61;
   return d;
 }
+// Products are issued by a whole warp with one thread elected in the
+// instruction sequence itself: under a branch on the lane the compiler cannot
+// know that the operands are uniform, and each product costs about 95 cycles of
+// issue instead of its own 64 (a 256 x 128 step 2.2 us instead of 1.5).
+// One k-step of 16: D += A B, A and B in shared memory; `off`: of both descriptors.
+template <uint32_t OFF>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n .reg .pred p, e;\n .reg .b64 x, y;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s64 x, %1, %5;\n add.s64 y, %2, %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(OFF));
 }
+// The same with A in tensor memory, `a_off` columns on.
+template <uint32_t A_OFF, uint32_t B_OFF>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n .reg .pred p, e;\n .reg .b32 x;\n .reg .b64 y;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s32 x, %1, %5;\n add.s64 y, %2, %6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A_OFF), "n"(B_OFF));
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
+      : "memory");
+}
+// Calls f(0), f(1), .. f(N - 1) with compile-time arguments.
+template <int I> struct Index { static constexpr int value = I; };
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(Index<I>{});
+    unrolled<N, I + 1>(f);
+  }
 }
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -143,6 +166,15 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The largest of three; a NaN is passed over.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+template <bool V> struct Flag { static constexpr bool value = V; };
+
 // Two floats at a time.
 __device__ __forceinline__ uint64_t two(float lo, float hi) {
   uint64_t r;
@@ -159,6 +191,20 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// Bit e: whether a row sees slot t + e.  Without mask words it sees the slots
+// up to `last`; with them those below base, and of the n new ones those named.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t at_seen(const int32_t* words, int last, int t, int base, int n) {
+  if (!words) return low_bits(last - t + 1);
+  const int j = t - base;
+  if (j <= -32) return ~0u;
+  const int have = (n + 31) >> 5;       // words that hold the row's bits
+  if (j < 0) return low_bits(-j) | ((uint32_t)words[0] & low_bits(n)) << -j;
+  const int x = j >> 5;
+  const uint32_t lo = x < have ? (uint32_t)words[x] : 0u, hi = x + 1 < have ? (uint32_t)words[x + 1] : 0u;
+  return __funnelshift_r(lo, hi, j & 31) & low_bits(n - j);
 }
 
 // Halves of a word that hold bf16 numbers that are not finite: bit 15, bit 31.
@@ -318,118 +364,114 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
   } else if (work && warp == 9) {
     // ------------------------------------------------------------- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (lane == 0) {
-      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
-      constexpr uint32_t kIdS = kBase | ((uint32_t)(kAtStep >> 3) << 17);
-      constexpr uint32_t kIdO = kBase | (1u << 16) | ((uint32_t)(HD >> 3) << 17);   // B (V) is MN-major
-      uint32_t rb = 0, cleans = 0, p_count[2] = {0, 0};
-      bool ok = true;
-      const uint32_t q_at = smem_addr(smem), ring_at = smem_addr(ring);
-      for (int np = 0; ok; ++np) {
-        ok = at_wait(&sm.piece_full[np & 1], (np >> 1) & 1, &sm.abort_flag);
-        if (!ok) break;
-        const AtPiece& p = sm.piece[np & 1];
-        if (p.b < 0) break;
-        const int n = p.tiles, s_lo = p.s_lo, edge = p.edge;
-        const bool split = p.valid <= 128;
-        mbar_arrive(&sm.piece_empty[np & 1]);
-        auto scores = [&](int w, int j) {   // S_w = Q K_j^T
-          const uint32_t qa = q_at + (split ? 0 : w * S::kTile), ka = ring_at + ((rb + ring_k(j)) % NS) * S::kTile;
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kAtStep * 128) + (kk & 3) * 32;
-            mma_ss(tmem + w * 128, at_desc(qa + off, 16), at_desc(ka + off, 16), kIdS, kk > 0);
+    constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
+    constexpr uint32_t kIdS = kBase | ((uint32_t)(kAtStep >> 3) << 17);
+    constexpr uint32_t kIdO = kBase | (1u << 16) | ((uint32_t)(HD >> 3) << 17);   // B (V) is MN-major
+    // (descriptors differ in the address field alone, which counts 16 bytes)
+    const uint64_t q_desc = at_desc(smem_addr(smem), 16), k_desc = at_desc(smem_addr(ring), 16),
+                   v_desc = at_desc(smem_addr(ring), kAtStep * 128);
+    uint32_t rb = 0, cleans = 0, p_count[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, at_wait(bar, parity, &sm.abort_flag));
+      return ok;
+    };
+    for (int np = 0; wait(&sm.piece_full[np & 1], (np >> 1) & 1); ++np) {
+      const AtPiece& p = sm.piece[np & 1];
+      if (p.b < 0) break;
+      const int n = p.tiles, first_edge = max(0, p.edge - p.s_lo);
+      const bool split = p.valid <= 128;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.piece_empty[np & 1]);
+      auto at_ring = [&](uint32_t pos) { return (rb + pos) % NS; };
+      auto wait_ring = [&](uint32_t pos) { return wait(&sm.full[at_ring(pos)], ((rb + pos) / NS) & 1); };
+      auto free_ring = [&](uint32_t pos) { mma_commit(&sm.empty[at_ring(pos)]); };
+      auto scores = [&](int w, int j) {                // S_w = Q K_j^T
+        const uint64_t qd = q_desc + (split ? 0 : w * (S::kTile >> 4)), kd = k_desc + at_ring(ring_k(j)) * (S::kTile >> 4);
+        tmem_after();
+        unrolled<HD / 16>([&](auto x) {
+          constexpr int kk = decltype(x)::value;
+          mma_ss<(kk >> 2) * (kAtStep * 128 >> 4) + (kk & 3) * 2>(tmem + w * 128, qd, kd, kIdS, kk > 0);
+        });
+      };
+      auto values = [&](int w, int j, bool start) {    // O_w += P_w V_j
+        const uint64_t vd = v_desc + at_ring(ring_v(j, n)) * (S::kTile >> 4);
+        tmem_after();
+        unrolled<kAtStep / 16>([&](auto x) {
+          constexpr int kk = decltype(x)::value;
+          mma_ts<kk * 8, kk * (kBlk * 128 >> 4)>(tmem + 256 + w * HD, tmem + w * 128, vd, kIdO, !(start && kk == 0));
+        });
+      };
+      // V_j is there; where some row sees only part of it, it is looked through
+      // meanwhile (the scanning warps come when they are called: ahead of the
+      // ring they could not tell its phases apart)
+      auto wait_v = [&](int j) {
+        if (!wait_ring(ring_v(j, n))) return false;
+        if (j >= first_edge && lane == 0) mbar_arrive(&sm.scan);
+        __syncwarp();
+        return true;
+      };
+      auto wait_clean = [&](int j) { return j < first_edge || wait(&sm.clean, cleans++ & 1); };
+      auto wait_p = [&](int w) { return wait(&sm.p_ready[w], p_count[w]++ & 1); };
+      if (!wait(&sm.q_ready[0], np & 1) || !wait_ring(ring_k(0))) break;
+      scores(0, 0);
+      mma_commit(&sm.s_full[0]);
+      if (split) free_ring(ring_k(0));
+      if (!wait(&sm.q_ready[1], np & 1)) break;
+      // A wait takes some 150 cycles even when there is nothing to wait for, and
+      // the products in the pipe cover about 200: one wait at most stands
+      // between two runs of eight products.
+      if (!split) {
+        scores(1, 0);
+        mma_commit(&sm.s_full[1]);
+        free_ring(ring_k(0));
+        if (!wait_v(0)) break;
+        for (int j = 0; j < n; ++j) {
+          const bool more = j + 1 < n;
+          if (!wait_p(0) || !wait_clean(j)) break;
+          values(0, j, j == 0);
+          if (more) {
+            if (!wait_ring(ring_k(j + 1))) break;
+            scores(0, j + 1);
           }
-        };
-        auto values = [&](int w, int j, bool first) {   // O_w += P_w V_j
-          const uint32_t va = ring_at + ((rb + ring_v(j, n)) % NS) * S::kTile;
-#pragma unroll
-          for (int kk = 0; kk < kAtStep / 16; ++kk)
-            mma_ts(tmem + 256 + w * HD, tmem + w * 128 + kk * 8, at_desc(va + kk * (kBlk * 128), kAtStep * 128), kIdO,
-                   !(first && kk == 0));
-        };
-        auto wait_ring = [&](uint32_t pos) {
-          const uint32_t it = rb + pos;
-          if (!at_wait(&sm.full[it % NS], (it / NS) & 1, &sm.abort_flag)) return false;
-          tmem_after();
-          return true;
-        };
-        auto free_ring = [&](uint32_t pos) { mma_commit(&sm.empty[(rb + pos) % NS]); };
-        // V_j is there; where some row sees only part of it, it is looked through
-        // meanwhile (the scanning warps come when they are called: ahead of the
-        // ring they could not tell its phases apart)
-        auto wait_v = [&](int j) {
-          if (!wait_ring(ring_v(j, n))) return false;
-          if (s_lo + j >= edge) mbar_arrive(&sm.scan);
-          return true;
-        };
-        auto wait_clean = [&](int j) {   // V_j holds finite numbers alone
-          if (s_lo + j < edge) return true;
-          return at_wait(&sm.clean, cleans++ & 1, &sm.abort_flag);
-        };
-        auto wait_p = [&](int w) {
-          if (!at_wait(&sm.p_ready[w], p_count[w]++ & 1, &sm.abort_flag)) return false;
-          tmem_after();
-          return true;
-        };
-        ok = at_wait(&sm.q_ready[0], np & 1, &sm.abort_flag) && wait_ring(ring_k(0));
-        if (!ok) break;
-        scores(0, 0);
-        mma_commit(&sm.s_full[0]);
-        if (split) free_ring(ring_k(0));
-        ok = at_wait(&sm.q_ready[1], np & 1, &sm.abort_flag);
-        if (!ok) break;
-        if (!split) {
-          scores(1, 0);
+          mma_commit(&sm.s_full[0]);
+          if (!wait_p(1)) break;
+          values(1, j, j == 0);
+          free_ring(ring_v(j, n));
+          if (more) scores(1, j + 1);
           mma_commit(&sm.s_full[1]);
-          free_ring(ring_k(0));
-          for (int j = 0; j < n && ok; ++j) {
-            const bool more = j + 1 < n;
-            ok = (!more || wait_ring(ring_k(j + 1))) && wait_v(j);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              ok = ok && wait_p(w) && (w == 1 || wait_clean(j));
-              if (!ok) break;
-              values(w, j, j == 0);
-              if (more) scores(w, j + 1);
-              mma_commit(&sm.s_full[w]);
-            }
-            if (!ok) break;
-            if (more) free_ring(ring_k(j + 1));
-            free_ring(ring_v(j, n));
-          }
-        } else {
-          if (n > 1) {
-            ok = wait_ring(ring_k(1));
-            if (!ok) break;
-            scores(1, 1);
-            mma_commit(&sm.s_full[1]);
-            free_ring(ring_k(1));
-          }
-          for (int j = 0; j < n && ok; ++j) {
-            const int w = j & 1;
-            const bool more = j + 2 < n;
-            ok = wait_v(j) && wait_p(w) && wait_clean(j);
-            if (!ok) break;
-            values(w, j, j < 2);
-            free_ring(ring_v(j, n));
-            if (more) {
-              ok = wait_ring(ring_k(j + 2));
-              if (!ok) break;
-              scores(w, j + 2);
-              free_ring(ring_k(j + 2));
-            }
-            mma_commit(&sm.s_full[w]);
+          if (more) {
+            free_ring(ring_k(j + 1));
+            if (!wait_v(j + 1)) break;
           }
         }
-        rb += 2 * n;
+      } else {
+        if (n > 1) {
+          if (!wait_ring(ring_k(1))) break;
+          scores(1, 1);
+          mma_commit(&sm.s_full[1]);
+          free_ring(ring_k(1));
+        }
+        for (int j = 0; j < n; ++j) {
+          const int w = j & 1;
+          if (!wait_v(j) || !wait_p(w) || !wait_clean(j)) break;
+          values(w, j, j < 2);
+          free_ring(ring_v(j, n));
+          if (j + 2 < n) {
+            if (!wait_ring(ring_k(j + 2))) break;
+            scores(w, j + 2);
+            free_ring(ring_k(j + 2));
+          }
+          mma_commit(&sm.s_full[w]);
+        }
       }
-      if (!ok) {
-        sm.abort_flag = 1;
-        set_error(a.err, MTP_ERR_TIMEOUT);
-      }
+      if (!ok) break;
+      rb += 2 * n;
     }
-    __syncwarp();
+    if (!ok) {
+      sm.abort_flag = 1;
+      if (lane == 0) set_error(a.err, MTP_ERR_TIMEOUT);
+    }
   } else if (work && warp >= 10) {
     // ------------------------------------- entries of V that are not finite
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -441,7 +483,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       AtPiece& p = sm.piece[np & 1];
       if (p.b < 0) break;
       const int n = p.tiles;
-      for (int j = max(0, p.edge - p.s_lo); j < n && ok; ++j) {
+      for (int j = max(0, p.edge - p.s_lo); j < n; ++j) {
         const uint32_t it = rb + ring_v(j, n);
         ok = __all_sync(0xffffffffu, at_wait(&sm.scan, scans++ & 1, &sm.abort_flag) &&
                                          at_wait(&sm.full[it % NS], (it / NS) & 1, &sm.abort_flag));
@@ -451,7 +493,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
 #pragma unroll 8
         for (int i = (warp - 10) * 32 + lane; i < S::kTile / 16; i += 64) {
           const uint4 x = tile[i];
-          if (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) found = true;
+          found |= (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) != 0;
         }
         if (found) {
           for (int i = (warp - 10) * 32 + lane; i < S::kTile / 16; i += 64) {
@@ -462,7 +504,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
             x.w &= ~((not_finite2(x.w) >> 15) * 0xFFFFu);
             tile[i] = x;
           }
-          *(volatile int*)&p.dirty = 1;
+          *(volatile int*)&p.dirty = 1;   // (before the products that the results wait for)
           fence_async();
         }
         __syncwarp();
@@ -475,44 +517,63 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     if (!ok) sm.abort_flag = 1;
   } else if (work) {
     // -------------------------------------------------------------- softmax
+    // registers of the block's launch, 384 x 168: 256 x 208 and 128 x 80
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256;
     uint32_t s_count = 0, merges = 0;   // phases of s_full[w] and of merged
     bool ok = true;
-    for (int np = 0; ok; ++np) {
-      ok = __all_sync(0xffffffffu, at_wait(&sm.piece_full[np & 1], (np >> 1) & 1, &sm.abort_flag));
-      if (!ok) break;
-      const AtPiece& p = sm.piece[np & 1];
-      if (p.b < 0) break;
-      const int n = p.tiles, s_lo = p.s_lo, i0 = p.i0, rows = p.n, base = p.base, g = p.g, o0 = p.o0;
-      const bool split = p.valid <= 128;
-      const int mine = split ? (n + 1 - w) / 2 : n;       // steps of this group
-      // ---- queries: this group's 128 pairs, swizzled as the products read them
-      if (!split || w == 0) {
-        unsigned char* qt = smem + w * S::kTile;
-        constexpr int CH = HD / 8;                         // 16-byte chunks of a pair
-        const uint16_t* q = (const uint16_t*)a.q;
-#pragma unroll 8
-        for (int x = r; x < 128 * CH; x += 128) {
-          const int pr = x / CH, c = x % CH, i = i0 + ((w * 128 + pr) >> a.g_shift);
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (i < rows) {
-            const uint16_t* src = q + (long long)(o0 + i) * a.q_stride + (long long)(g * G + (pr & (G - 1))) * HD + c * 8;
-            if (a.q_vec) {
-              v = *reinterpret_cast<const uint4*>(src);
-            } else {
-              v = make_uint4((uint32_t)src[0] | (uint32_t)src[1] << 16, (uint32_t)src[2] | (uint32_t)src[3] << 16,
+    // A segment's queries: this group's 128 pairs (both groups' in the first
+    // tile, for up to 128), in registers first, so that all loads go out
+    // together, then swizzled as the products read them.
+    constexpr int CH = HD / 8;                             // 16-byte chunks of a pair; loads of a thread
+    uint4 qr[CH];
+    auto load_q = [&](const AtPiece& p) {
+      if (p.b < 0 || (p.valid <= 128 && w == 1)) return;
+      const int c = r % CH;
+#pragma unroll
+      for (int x = 0; x < CH; ++x) {
+        const int pr = r / CH + x * (128 / CH), i = p.i0 + ((w * 128 + pr) >> a.g_shift);
+        qr[x] = make_uint4(0, 0, 0, 0);
+        if (i >= p.n) continue;
+        const uint16_t* src = (const uint16_t*)a.q + (long long)(p.o0 + i) * a.q_stride +
+                              (long long)(p.g * G + (pr & (G - 1))) * HD + c * 8;
+        if (a.q_vec)
+          qr[x] = *reinterpret_cast<const uint4*>(src);
+        else
+          qr[x] = make_uint4((uint32_t)src[0] | (uint32_t)src[1] << 16, (uint32_t)src[2] | (uint32_t)src[3] << 16,
                              (uint32_t)src[4] | (uint32_t)src[5] << 16, (uint32_t)src[6] | (uint32_t)src[7] << 16);
-            }
-          }
-          *reinterpret_cast<uint4*>(qt + (c >> 3) * (128 * 128) + pr * 128 + (((c & 7) ^ (pr & 7)) << 4)) = v;
+      }
+    };
+    auto store_q = [&](const AtPiece& p) {
+      if (p.b < 0) return;
+      if (p.valid > 128 || w == 0) {
+        const int c = r % CH;
+#pragma unroll
+        for (int x = 0; x < CH; ++x) {
+          const int pr = r / CH + x * (128 / CH);
+          *reinterpret_cast<uint4*>(smem + w * S::kTile + (c >> 3) * (128 * 128) + pr * 128 + (((c & 7) ^ (pr & 7)) << 4)) = qr[x];
         }
         fence_async();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_ready[w]);
+    };
+    auto wait_piece = [&](int np) {
+      return (bool)__all_sync(0xffffffffu, at_wait(&sm.piece_full[np & 1], (np >> 1) & 1, &sm.abort_flag));
+    };
+    ok = wait_piece(0);
+    if (ok) {
+      load_q(sm.piece[0]);
+      store_q(sm.piece[0]);
+    }
+    for (int np = 0; ok; ++np) {
+      const AtPiece& p = sm.piece[np & 1];
+      if (p.b < 0) break;
+      const int n = p.tiles, s_lo = p.s_lo, i0 = p.i0, rows = p.n, base = p.base, g = p.g, o0 = p.o0;
+      const bool split = p.valid <= 128;
+      const int mine = split ? (n + 1 - w) / 2 : n;       // steps of this group
       // ---- this thread's row
       const int pr = split ? r : w * 128 + r;
       const int i = i0 + (pr >> a.g_shift);
@@ -528,45 +589,83 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         if (!ok) break;
         ++s_count;
         tmem_after();
-        uint32_t s[128];
-        tmem_ld(s_at, s);
-        tmem_ld(s_at + 32, s + 32);
-        tmem_ld(s_at + 64, s + 64);
-        tmem_ld(s_at + 96, s + 96);
-        tmem_wait_ld();
-        tmem_ready(s);
-        tmem_ready(s + 32);
-        tmem_ready(s + 64);
-        tmem_ready(s + 96);
-        if (s_lo + j >= edge) {
-          const int t0 = (s_lo + j) * kAtStep;
-          if (a.mask) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e) {
-              const int t = t0 + e;
-              if (!(live && t < p.end && row_sees(words, i, t, base, rows))) s[e] = 0xFF800000u;
-            }
-          } else {
-            const int most = last - t0;
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e > most) s[e] = 0xFF800000u;
-          }
-        }
+        // One pass, 32 columns at a time: weights by the reference as it is, and
+        // the maximum next to them.  Where that passes the reference by more than
+        // the slack (a piece's first step, rarely later) the reference moves
+        // and the pass is made again; the scores are still there, the weights
+        // go over them at the end.
+        const bool part = s_lo + j >= edge;                // some row sees only part of the step
+        const int t0 = (s_lo + j) * kAtStep;
+        uint32_t pw[64];
+        uint64_t sum[2];
         float mx[4];
+        // plain: every row sees all columns, and no reference is coarse.  (With
+        // the two questions asked per 32 columns the loads' latency shows:
+        // 1910 instead of 1240 cycles a step.)
+        auto pass = [&](auto plain, bool coarse) {
+          const uint64_t cc = two(a.c, a.c), mm = two(-m, -m);
+          auto columns = [&](uint32_t (&v)[32], int c) {
+            if (!decltype(plain)::value && part) {
+              const uint32_t bits = at_seen(words, last, t0 + 32 * c, base, rows);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[e]);
+              for (int e = 0; e < 32; ++e)
+                if (!(bits >> e & 1u)) v[e] = 0xFF800000u;
+            }
 #pragma unroll
-        for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
-        const float top = fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast);
-        const bool above = top > m + kAtSlack;
-        if (__any_sync(0xffffffffu, above)) {
+            for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            if (!decltype(plain)::value && coarse) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c) - m);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x0, x1;
+                untwo(fma2(two(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, mm), x0, x1);
+                v[e] = __float_as_uint(x0);
+                v[e + 1] = __float_as_uint(x1);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = exp2_fast(__uint_as_float(v[e])), p1 = exp2_fast(__uint_as_float(v[e + 1]));
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(p0, p1));
+              pw[16 * c + e / 2] = pack2_bf16(p0, p1);
+            }
+          };
+          sum[0] = sum[1] = 0ull;
+          mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
+          uint32_t va[32], vb[32];
+          tmem_ld(s_at, va);
+          tmem_wait_ld();
+          tmem_ready(va);
+          tmem_ld(s_at + 32, vb);
+          columns(va, 0);
+          tmem_wait_ld();
+          tmem_ready(vb);
+          tmem_ld(s_at + 64, va);
+          columns(vb, 1);
+          tmem_wait_ld();
+          tmem_ready(va);
+          tmem_ld(s_at + 96, vb);
+          columns(va, 2);
+          tmem_wait_ld();
+          tmem_ready(vb);
+          columns(vb, 3);
+        };
+        for (int again = 0; again < 2; ++again) {
+          // from kAtCoarse on the reference is rounded to whole units: scores are then rounded like it
+          const bool coarse = __any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast);
+          if (part || coarse) pass(Flag<false>{}, coarse);
+          else pass(Flag<true>{}, false);
+          const float top = fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast);
+          const bool above = top > m + kAtSlack;
+          if (again || !__any_sync(0xffffffffu, above)) break;
           const float mn = above ? top : m, alpha = exp2_fast(m - mn);
           m = mn;
           l *= alpha;
           if (x > 0) {   // (S_w full: the products into O_w before it have ended)
             const uint32_t o = o_at + w * HD;
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
               uint32_t v[32];
               tmem_ld(o + c0, v);
@@ -578,30 +677,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
             }
           }
         }
-        uint64_t sum[2] = {0ull, 0ull};
-        if (__any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast)) {
-          // scores so large that the reference is rounded to whole units: round them like it
-#pragma unroll
-          for (int e = 0; e < 128; e += 2) {
-            const float p0 = exp2_fast(__fmul_rn(__uint_as_float(s[e]), a.c) - m);
-            const float p1 = exp2_fast(__fmul_rn(__uint_as_float(s[e + 1]), a.c) - m);
-            sum[0] = add2(sum[0], two(p0, p1));
-            s[e / 2] = pack2_bf16(p0, p1);
-          }
-        } else {
-          const uint64_t cc = two(a.c, a.c), mm = two(-m, -m);
-#pragma unroll
-          for (int e = 0; e < 128; e += 2) {
-            float p0, p1;
-            untwo(fma2(two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mm), p0, p1);
-            p0 = exp2_fast(p0);
-            p1 = exp2_fast(p1);
-            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(p0, p1));
-            s[e / 2] = pack2_bf16(p0, p1);
-          }
-        }
-        tmem_st(s_at, s);
-        tmem_st(s_at + 32, s + 32);
+        tmem_st(s_at, pw);
+        tmem_st(s_at + 32, pw + 32);
         float l0, l1;
         untwo(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
@@ -612,11 +689,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       }
       if (!ok) break;
       // ---- results: O_w of 128 pairs, or both groups' parts of the same pairs, half of the columns each
+      // The next segment's queries are fetched under the last products; when
+      // those have ended no product reads the old ones any more (all scores
+      // are issued before a group's last values), so the new ones take their
+      // place and the next scores run while the results are written.
+      ok = wait_piece(np + 1);
+      if (!ok) break;
+      const AtPiece& next = sm.piece[(np + 1) & 1];
+      load_q(next);
       if (mine > 0) {
         ok = __all_sync(0xffffffffu, at_wait(&sm.s_full[w], s_count & 1, &sm.abort_flag));
         if (!ok) break;
         ++s_count;
       }
+      if (!split) store_q(next);
       float f0 = 1.0f, f1 = 0.0f;
       const bool both = split && n > 1;
       if (split) {
@@ -628,6 +714,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         if (lane == 0) mbar_arrive(&sm.merged);
         ok = __all_sync(0xffffffffu, at_wait(&sm.merged, merges++ & 1, &sm.abort_flag));
         if (!ok) break;
+        // only now: a group that had no step of this segment would otherwise be
+        // two segments ahead of the products
+        store_q(next);
         if (!both) {
           m = sm.ml[0][r][0];
           l = sm.ml[0][r][1];
