@@ -372,6 +372,11 @@ bool attn_tensor_maps(mtp_ctx* ctx, const mtp_kv* kv, const CUtensorMap** km, co
 // 2-D bf16 tensor map over [rows, cols] (row-major) with a [box_rows, 64]
 // box and 128-byte swizzle; false if the driver rejects it.
 bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// Map of a [rows, cols] bf16 cache pool (cols 64 or 128) whose box is a block
+// of 16 rows, stored as groups of 8 rows x 64 columns (1024 bytes, 128-byte
+// swizzle), the columns' halves of a group next to one another: coordinates
+// (0, 0, 0, row / 8).
+bool make_block_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols);
 cudaError_t launch_draft_step_tc(mtp_ctx* ctx, cudaStream_t s, int B, int k, int K, const void* hidden,
                                  const void* embeds, const int32_t* positions, const mtp_kv* kv,
                                  const int32_t* chain_ids, int32_t* draft_ids, float* logits, float* hidden_out);

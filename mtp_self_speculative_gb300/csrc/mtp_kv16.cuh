@@ -75,6 +75,7 @@ struct RowsArgs {
   // attention: pieces of segments that span thread blocks
   float* part;                   // [2 * grid][rows of a segment][HD + 4]: o, then reference and sum
   int4* meta;                    // [2 * grid]: per thread block, the spanning segment that begins in it
+  int* pre;                      // tensor-core form: [grid][kKvMaxB + 1] units before each request
   // weights
   float* weights;                // [num_blocks, n_kv, 16]
   const int32_t* first;          // [B] or null

@@ -14,7 +14,7 @@
 //            sum.  O_w is scaled only when a row's maximum passes its reference
 //            by 8 (powers of two), so most steps touch it with products alone.
 //   warp 8   finds the segments of the block's share, and loads cache blocks
-//            (2 KB boxes, 128-byte swizzle) into a ring of K and V tiles, into
+//            (a box each, 128-byte swizzle) into a ring of K and V tiles, into
 //            the next segment's as soon as the ring has room
 //   warp 9   issues the products: S_w = Q_w K^T, O_w += P_w V, the two groups'
 //            in turn, so that one group's softmax runs under the other's products
@@ -45,8 +45,10 @@ template <int HD>
 struct AtShape {
   static constexpr int kHalves = HD / 64;
   static constexpr int kTile = kAtStep * HD * 2;              // bytes of a K or V tile, and of 128 pairs' queries
-  static constexpr int kStages = HD == 128 ? 4 : 8;
-  static constexpr int kBytes = 2 * kTile + kStages * kTile + 1024;
+  // Five tiles of 32 KB are what fits; four leave V waiting (a step 3250 instead
+  // of 2900 cycles).
+  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr int kBytes = 2 * kTile + kStages * kTile;
 };
 
 struct AtPiece {
@@ -69,21 +71,24 @@ __device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void at_tma(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+// A cache block, issued by a whole warp with one thread elected (as the products
+// below).  One box of 4 KB: two of 2 KB take twice the time, some 75 cycles a box.
+__device__ __forceinline__ void at_tma(uint32_t dst, const CUtensorMap* map, int group, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_addr(dst)),
-      "l"((uint64_t)map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%4, %4, %4, %2}], [%3];\n}\n" ::"r"(dst),
+      "l"((uint64_t)map), "r"(group), "r"(bar), "r"(0)
       : "memory");
 }
-// Shared-memory operands with 128-byte swizzle.  K-major: rows of 64 elements,
-// 1024 bytes between groups of eight rows.  MN-major (V: the products' columns
-// lie next to one another): 64 columns of eight slots are 1024 bytes, `lead`
-// bytes to the next 64 columns.
-__device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t lead) {
+// Shared-memory operands with 128-byte swizzle: groups of eight rows x 64
+// columns (1024 bytes), `step` bytes from one group of rows to the next and
+// `lead` bytes from 64 columns to the next 64.  (K-major operands need the
+// first alone: their 64 columns are four k-steps and are addressed one by one.
+// V is MN-major: the product's columns lie next to one another.)
+__device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t step, uint32_t lead) {
   uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
   d |= (uint64_t)(lead >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)(step >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
@@ -92,14 +97,14 @@ __device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t lead) {
 // instruction sequence itself: under a branch on the lane the compiler cannot
 // know that the operands are uniform, and each product costs about 95 cycles of
 // issue instead of its own 64 (a 256 x 128 step 2.2 us instead of 1.5).
-// One k-step of 16: D += A B, A and B in shared memory; `off`: of both descriptors.
-template <uint32_t OFF>
+// One k-step of 16: D += A B, A and B in shared memory.
+template <uint32_t A_OFF, uint32_t B_OFF>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p, e;\n .reg .b64 x, y;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " add.s64 x, %1, %5;\n add.s64 y, %2, %5;\n"
+      " add.s64 x, %1, %5;\n add.s64 y, %2, %6;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(OFF));
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A_OFF), "n"(B_OFF));
 }
 // The same with A in tensor memory, `a_off` columns on.
 template <uint32_t A_OFF, uint32_t B_OFF>
@@ -173,8 +178,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-template <bool V> struct Flag { static constexpr bool value = V; };
-
 // Two floats at a time.
 __device__ __forceinline__ uint64_t two(float lo, float hi) {
   uint64_t r;
@@ -219,7 +222,7 @@ __device__ __forceinline__ uint32_t ring_v(int j, int n) { return j == n - 1 ? 2
 template <int HD>
 struct AtShared {
   uint64_t full[AtShape<HD>::kStages], empty[AtShape<HD>::kStages];
-  uint64_t s_full[2], p_ready[2], q_ready[2], scan, clean, merged, piece_full[2], piece_empty[2];
+  uint64_t s_full[2], p_ready[2], q_ready[2], written[2], scan, clean, merged, piece_full[2], piece_empty[2];
   AtPiece piece[2];
   float ml[2][128][2];
   uint32_t tmem;
@@ -232,15 +235,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
                                                                    const RowsArgs a, const SegShape sh) {
   using S = AtShape<HD>;
   constexpr int NS = S::kStages;
-  extern __shared__ __align__(1024) unsigned char at_smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem[];   // tiles: the swizzle wants 1024-byte boundaries
   __shared__ AtShared<HD> sm;
-  __shared__ int pre[kKvMaxB + 1];
   __shared__ long long wsum[kAtThreads / 32];
-  unsigned char* smem = (unsigned char*)(((uintptr_t)at_smem_raw + 1023) & ~(uintptr_t)1023);
+  int* pre = a.pre + (long long)blockIdx.x * (kKvMaxB + 1);
   unsigned char* ring = smem + 2 * S::kTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = 1 << a.g_shift;
 
+  if (smem_addr(smem) & 1023) {   // (the declaration above asks for it)
+    if (tid == 0) set_error(a.err, MTP_ERR_BOUNDS);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sm.full[i], 1);
@@ -250,6 +256,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       mbar_init(&sm.s_full[w], 1);
       mbar_init(&sm.p_ready[w], 4);
       mbar_init(&sm.q_ready[w], 4);
+      mbar_init(&sm.written[w], 4);
       mbar_init(&sm.piece_full[w], 1);
       mbar_init(&sm.piece_empty[w], 11);
     }
@@ -275,12 +282,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
 
   if (work && warp == 8) {
     // ------------------------------------------------------------- producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     uint32_t rb = 0, issued = 0;
     int np = 0;
     bool ok = true;
-    const int page = lane & 7, half = lane >> 3;
-    const int oob = a.kv.num_blocks * a.n_kv * kBlk;   // rows of the pool: a box from there on is zeros
+    const int page = lane & 7;
+    const int oob = a.kv.num_blocks * a.n_kv * 2;   // groups of the pool: a box from there on is zeros
     uint32_t u = sp.u0;
     while (ok) {
       Piece p{};
@@ -323,23 +330,25 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       if (!any) break;
       const int n = p.s_hi - p.s_lo;
       const int32_t* table = a.kv.block_table + (long long)p.b * a.kv.max_blocks;
-      auto row_of = [&](int j) -> int {   // pool row of this lane's box in step j
+      auto row_of = [&](int j) -> int {   // the pool's group of eight rows where this lane's block of step j begins
         const int t = (p.s_lo + j) * kAtStep + page * kBlk;
-        if (j >= n || t >= p.end || half >= S::kHalves) return oob;
+        if (j >= n || t >= p.end) return oob;
         const int blk = table[t >> 4];
         if (blk < 0 || blk >= a.kv.num_blocks) {
           set_error(a.err, MTP_ERR_CAPACITY);
           return oob;
         }
-        return (blk * a.n_kv + p.g) * kBlk;
+        return (blk * a.n_kv + p.g) * 2;
       };
       auto issue = [&](const CUtensorMap* map, uint32_t it, int row) -> bool {
         const int st = it % NS;
         if (!__all_sync(0xffffffffu, at_wait(&sm.empty[st], ((it / NS) & 1) ^ 1, &sm.abort_flag))) return false;
         if (lane == 0) mbar_expect_tx(&sm.full[st], S::kTile);
         __syncwarp();
-        if (half < S::kHalves)
-          at_tma(ring + (size_t)st * S::kTile + half * (kAtStep * 128) + page * (kBlk * 128), map, half * 64, row, &sm.full[st]);
+        const uint32_t dst = smem_addr(ring) + st * S::kTile, bar = smem_addr(&sm.full[st]);
+#pragma unroll
+        for (int pg = 0; pg < kAtStep / kBlk; ++pg)
+          at_tma(dst + pg * (kBlk * HD * 2), map, __shfl_sync(0xffffffffu, row, pg), bar);
         issued = it + 1;
         return true;
       };
@@ -363,13 +372,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     }
   } else if (work && warp == 9) {
     // ------------------------------------------------------------- products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
     constexpr uint32_t kIdS = kBase | ((uint32_t)(kAtStep >> 3) << 17);
     constexpr uint32_t kIdO = kBase | (1u << 16) | ((uint32_t)(HD >> 3) << 17);   // B (V) is MN-major
     // (descriptors differ in the address field alone, which counts 16 bytes)
-    const uint64_t q_desc = at_desc(smem_addr(smem), 16), k_desc = at_desc(smem_addr(ring), 16),
-                   v_desc = at_desc(smem_addr(ring), kAtStep * 128);
+    constexpr uint32_t kGroup = S::kHalves * 1024;       // bytes of eight rows
+    const uint64_t q_desc = at_desc(smem_addr(smem), kGroup, 16), k_desc = at_desc(smem_addr(ring), kGroup, 16),
+                   v_desc = at_desc(smem_addr(ring), kGroup, 1024);
     uint32_t rb = 0, cleans = 0, p_count[2] = {0, 0};
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -391,7 +401,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         tmem_after();
         unrolled<HD / 16>([&](auto x) {
           constexpr int kk = decltype(x)::value;
-          mma_ss<(kk >> 2) * (kAtStep * 128 >> 4) + (kk & 3) * 2>(tmem + w * 128, qd, kd, kIdS, kk > 0);
+          constexpr uint32_t at = (kk >> 2) * (1024 >> 4) + (kk & 3) * 2;
+          mma_ss<at, at>(tmem + w * 128, qd, kd, kIdS, kk > 0);
         });
       };
       auto values = [&](int w, int j, bool start) {    // O_w += P_w V_j
@@ -399,7 +410,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         tmem_after();
         unrolled<kAtStep / 16>([&](auto x) {
           constexpr int kk = decltype(x)::value;
-          mma_ts<kk * 8, kk * (kBlk * 128 >> 4)>(tmem + 256 + w * HD, tmem + w * 128, vd, kIdO, !(start && kk == 0));
+          mma_ts<kk * 8, kk * (kBlk * HD * 2 >> 4)>(tmem + 256 + w * HD, tmem + w * 128, vd, kIdO, !(start && kk == 0));
         });
       };
       // V_j is there; where some row sees only part of it, it is looked through
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     }
   } else if (work && warp >= 10) {
     // ------------------------------------- entries of V that are not finite
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     uint32_t rb = 0, scans = 0;
     bool ok = true;
     for (int np = 0; ok; ++np) {
@@ -517,8 +528,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     if (!ok) sm.abort_flag = 1;
   } else if (work) {
     // -------------------------------------------------------------- softmax
-    // registers of the block's launch, 384 x 168: 256 x 208 and 128 x 80
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // registers of the block's launch, 384 x 168: 256 x 216 and 128 x 72
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256;
@@ -529,31 +540,34 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     // together, then swizzled as the products read them.
     constexpr int CH = HD / 8;                             // 16-byte chunks of a pair; loads of a thread
     uint4 qr[CH];
+    auto q_at = [&](const AtPiece& p, int x) {   // (pairs past the last row read that one, and become zeros)
+      const int pr = r / CH + x * (128 / CH), i = min(p.i0 + ((w * 128 + pr) >> a.g_shift), p.n - 1);
+      return (const uint16_t*)a.q + (long long)(p.o0 + i) * a.q_stride + (long long)(p.g * G + (pr & (G - 1))) * HD + r % CH * 8;
+    };
+    auto has_q = [&](const AtPiece& p) { return p.b >= 0 && (p.valid > 128 || w == 0); };
     auto load_q = [&](const AtPiece& p) {
-      if (p.b < 0 || (p.valid <= 128 && w == 1)) return;
-      const int c = r % CH;
+      if (!a.q_vec || !has_q(p)) return;
 #pragma unroll
-      for (int x = 0; x < CH; ++x) {
-        const int pr = r / CH + x * (128 / CH), i = p.i0 + ((w * 128 + pr) >> a.g_shift);
-        qr[x] = make_uint4(0, 0, 0, 0);
-        if (i >= p.n) continue;
-        const uint16_t* src = (const uint16_t*)a.q + (long long)(p.o0 + i) * a.q_stride +
-                              (long long)(p.g * G + (pr & (G - 1))) * HD + c * 8;
-        if (a.q_vec)
-          qr[x] = *reinterpret_cast<const uint4*>(src);
-        else
-          qr[x] = make_uint4((uint32_t)src[0] | (uint32_t)src[1] << 16, (uint32_t)src[2] | (uint32_t)src[3] << 16,
-                             (uint32_t)src[4] | (uint32_t)src[5] << 16, (uint32_t)src[6] | (uint32_t)src[7] << 16);
-      }
+      for (int x = 0; x < CH; ++x) qr[x] = __ldg(reinterpret_cast<const uint4*>(q_at(p, x)));
     };
     auto store_q = [&](const AtPiece& p) {
       if (p.b < 0) return;
-      if (p.valid > 128 || w == 0) {
-        const int c = r % CH;
+      if (has_q(p)) {
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
-          const int pr = r / CH + x * (128 / CH);
-          *reinterpret_cast<uint4*>(smem + w * S::kTile + (c >> 3) * (128 * 128) + pr * 128 + (((c & 7) ^ (pr & 7)) << 4)) = qr[x];
+          const int pr = r / CH + x * (128 / CH), c = r % CH;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (p.i0 + ((w * 128 + pr) >> a.g_shift) < p.n) {
+            if (a.q_vec) {
+              v = qr[x];
+            } else {   // rows off 16 bytes: fetched here
+              const uint16_t* s = q_at(p, x);
+              v = make_uint4((uint32_t)s[0] | (uint32_t)s[1] << 16, (uint32_t)s[2] | (uint32_t)s[3] << 16,
+                             (uint32_t)s[4] | (uint32_t)s[5] << 16, (uint32_t)s[6] | (uint32_t)s[7] << 16);
+            }
+          }
+          *reinterpret_cast<uint4*>(smem + w * S::kTile + ((pr >> 3) * S::kHalves + (c >> 3)) * 1024 + (pr & 7) * 128 +
+                                    (((c & 7) ^ (pr & 7)) << 4)) = v;
         }
         fence_async();
       }
@@ -591,29 +605,33 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         tmem_after();
         // One pass, 32 columns at a time: weights by the reference as it is, and
         // the maximum next to them.  Where that passes the reference by more than
-        // the slack (a piece's first step, rarely later) the reference moves
-        // and the pass is made again; the scores are still there, the weights
+        // the slack (rarely, behind the first step) the reference moves and
+        // the pass is made again; the scores are still there, the weights
         // go over them at the end.
         const bool part = s_lo + j >= edge;                // some row sees only part of the step
         const int t0 = (s_lo + j) * kAtStep;
         uint32_t pw[64];
         uint64_t sum[2];
         float mx[4];
-        // plain: every row sees all columns, and no reference is coarse.  (With
-        // the two questions asked per 32 columns the loads' latency shows:
-        // 1910 instead of 1240 cycles a step.)
-        auto pass = [&](auto plain, bool coarse) {
+        // KIND 0: every row sees all columns; 1: those up to `last`; 2: any mask,
+        // or a coarse reference.  (Asked per 32 columns instead, the loads' latency
+        // shows: 1910 instead of 1240 cycles a step.)
+        auto hide = [&](auto kind, uint32_t (&v)[32], int c) {
+          constexpr int KIND = decltype(kind)::value;
+          if constexpr (KIND > 0) {
+            const uint32_t bits = KIND == 1 ? low_bits(last - t0 - 32 * c + 1) : at_seen(words, last, t0 + 32 * c, base, rows);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : 0xFF800000u;
+          }
+        };
+        auto pass = [&](auto kind, bool coarse) {
+          constexpr int KIND = decltype(kind)::value;
           const uint64_t cc = two(a.c, a.c), mm = two(-m, -m);
           auto columns = [&](uint32_t (&v)[32], int c) {
-            if (!decltype(plain)::value && part) {
-              const uint32_t bits = at_seen(words, last, t0 + 32 * c, base, rows);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(bits >> e & 1u)) v[e] = 0xFF800000u;
-            }
+            if (KIND < 2 || part) hide(kind, v, c);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-            if (!decltype(plain)::value && coarse) {
+            if (KIND == 2 && coarse) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c) - m);
             } else {
@@ -652,11 +670,32 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
           tmem_ready(vb);
           columns(vb, 3);
         };
+        if (x == 0) {   // no reference yet: the maximum first
+          auto most = [&](uint32_t (&v)[32], int c) {
+            if (part) hide(Index<2>{}, v, c);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          };
+          mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
+          uint32_t va[32], vb[32];
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_ld(s_at + 32 * c, va);
+            tmem_ld(s_at + 32 * c + 32, vb);
+            tmem_wait_ld();
+            tmem_ready(va);
+            tmem_ready(vb);
+            most(va, c);
+            most(vb, c + 1);
+          }
+          m = fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast);
+        }
         for (int again = 0; again < 2; ++again) {
           // from kAtCoarse on the reference is rounded to whole units: scores are then rounded like it
           const bool coarse = __any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast);
-          if (part || coarse) pass(Flag<false>{}, coarse);
-          else pass(Flag<true>{}, false);
+          if (coarse || (part && a.mask)) pass(Index<2>{}, coarse);
+          else if (part) pass(Index<1>{}, false);
+          else pass(Index<0>{}, false);
           const float top = fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast);
           const bool above = top > m + kAtSlack;
           if (again || !__any_sync(0xffffffffu, above)) break;
@@ -689,10 +728,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       }
       if (!ok) break;
       // ---- results: O_w of 128 pairs, or both groups' parts of the same pairs, half of the columns each
-      // The next segment's queries are fetched under the last products; when
-      // those have ended no product reads the old ones any more (all scores
-      // are issued before a group's last values), so the new ones take their
-      // place and the next scores run while the results are written.
+      // the next segment's queries are fetched under the last products
       ok = wait_piece(np + 1);
       if (!ok) break;
       const AtPiece& next = sm.piece[(np + 1) & 1];
@@ -702,7 +738,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         if (!ok) break;
         ++s_count;
       }
-      if (!split) store_q(next);
       float f0 = 1.0f, f1 = 0.0f;
       const bool both = split && n > 1;
       if (split) {
@@ -714,9 +749,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         if (lane == 0) mbar_arrive(&sm.merged);
         ok = __all_sync(0xffffffffu, at_wait(&sm.merged, merges++ & 1, &sm.abort_flag));
         if (!ok) break;
-        // only now: a group that had no step of this segment would otherwise be
-        // two segments ahead of the products
-        store_q(next);
         if (!both) {
           m = sm.ml[0][r][0];
           l = sm.ml[0][r][1];
@@ -733,7 +765,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       const uint32_t o_mine = split ? o_at : o_at + w * HD;
       const bool dirty = *(volatile const int*)&p.dirty;
       const long long row = (long long)(o0 + i) * (a.n_kv << a.g_shift) + g * G + (pr & (G - 1));
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = p.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      // Rows go out through the group's part of the queries' memory, which no
+      // product reads any more, 32 columns of a warp's 32 rows at a time, so that
+      // a store instruction writes whole sectors (a thread writing its own row:
+      // 6500 cycles a segment).
+      float* stage = reinterpret_cast<float*>(smem + w * S::kTile + (warp & 3) * (32 * 32 * 4));
+      const int row_first = (warp & 3) * 32 + (split ? 0 : w * 128);       // pair of the warp's first row
 #pragma unroll 1
       for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
         uint32_t v[32];
@@ -762,21 +800,28 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
               if ((vr[e] & 0x7F80u) == 0x7F80u) y[e] += elem<uint16_t>(vr + e);
           }
         }
-        if (!live) continue;
-        if (p.slot < 0) {
-          if (!MTP_IN_BOUNDS(a.err, row * HD + c0 + 31, (long long)a.T * (a.n_kv << a.g_shift) * HD)) continue;
-          uint4* op = reinterpret_cast<uint4*>((uint16_t*)a.out + row * HD + c0);
+        // eight lanes a row from here on: four columns each, rows lane / 8 + 4 k
+        __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] *= inv;
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(stage + lane * 32 + (e ^ (lane & 7) * 4)) = make_float4(y[e] * inv, y[e + 1] * inv, y[e + 2] * inv, y[e + 3] * inv);
+        __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) op[e] = narrow16<uint16_t>(y + 8 * e);
-        } else {
-          float* pt = a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pr) * (HD + 4);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(pt + c0 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-          if (c0 == 0) *reinterpret_cast<float2*>(pt + HD) = make_float2(m, l);
+        for (int k = 0; k < 8; ++k) {
+          const int rr = lane / 8 + 4 * k, pair = row_first + rr, ii = i0 + (pair >> a.g_shift), col = c0 + (lane & 7) * 4;
+          if (ii >= rows) continue;
+          const float4 z = *reinterpret_cast<const float4*>(stage + rr * 32 + ((lane ^ rr) & 7) * 4);
+          if (p.slot < 0) {
+            const long long at = ((long long)(o0 + ii) * (a.n_kv << a.g_shift) + g * G + (pair & (G - 1))) * HD + col;
+            if (!MTP_IN_BOUNDS(a.err, at + 3, (long long)a.T * (a.n_kv << a.g_shift) * HD)) continue;
+            *reinterpret_cast<uint2*>((uint16_t*)a.out + at) = make_uint2(pack2_bf16(z.x, z.y), pack2_bf16(z.z, z.w));
+          } else {
+            *reinterpret_cast<float4*>(a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pair) * (HD + 4) + col) = z;
+          }
         }
       }
+      if (live && c_lo == 0 && p.slot >= 0)
+        *reinterpret_cast<float2*>(a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pr) * (HD + 4) + HD) = make_float2(m, l);
       if (live && c_lo == 0 && p.slot < 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (split) {
         // the other group's part is read: it may go on to its next products
@@ -789,6 +834,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       }
       tmem_before();
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.written[w]);
+      ok = __all_sync(0xffffffffu, at_wait(&sm.written[w], np & 1, &sm.abort_flag));
+      if (!ok) break;
+      store_q(next);     // the group's rows have left the memory that the next queries go to
       if (lane == 0) mbar_arrive(&sm.piece_empty[np & 1]);
     }
     if (!ok) {
@@ -809,7 +858,7 @@ static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& 
   using S = AtShape<HD>;
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.kv.num_blocks * a.n_kv * kBlk;
-  if (rows > INT32_MAX || !make_map(&km, a.kv.k_pool, rows, HD, kBlk) || !make_map(&vm, a.kv.v_pool, rows, HD, kBlk))
+  if (rows > INT32_MAX || !make_block_map(&km, a.kv.k_pool, rows, HD) || !make_block_map(&vm, a.kv.v_pool, rows, HD))
     return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem((const void*)kv_attn_tc_kernel<HD>, S::kBytes);
   if (e != cudaSuccess) return e;

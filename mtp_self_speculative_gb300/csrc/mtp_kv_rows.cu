@@ -432,6 +432,9 @@ cudaError_t launch_rows_weights(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a)
 // Workspace: what the join kernel joins, then two pieces a thread block.
 constexpr int kRowsMaxBlocks = 2;    // thread blocks per SM at most
 static size_t rows_meta_bytes(const mtp_ctx* ctx) { return (size_t)kRowsMaxBlocks * ctx->num_sms * 2 * sizeof(int4); }
+static size_t rows_pre_bytes(const mtp_ctx* ctx) {
+  return ((size_t)ctx->num_sms * (kKvMaxB + 1) * sizeof(int) + 255) & ~(size_t)255;
+}
 
 // The checks that both calls share; fills in the common arguments.
 static mtp_status rows_args(mtp_ctx* ctx, int B, int T, const int32_t* row_offsets, int max_rows, const void* q,
@@ -471,7 +474,7 @@ extern "C" {
 size_t mtp_kv_attention_workspace_bytes(const mtp_ctx* ctx) {
   if (!ctx) return 0;
   const int pairs = ctx->cfg.dtype == MTP_DTYPE_BF16 ? kAtPairs : kRowsMaxBlocks * 64;   // of an SM's thread blocks
-  return rows_meta_bytes(ctx) + (size_t)2 * ctx->num_sms * pairs * (ctx->cfg.head_dim + 4) * sizeof(float);
+  return rows_meta_bytes(ctx) + rows_pre_bytes(ctx) + (size_t)2 * ctx->num_sms * pairs * (ctx->cfg.head_dim + 4) * sizeof(float);
 }
 
 mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
@@ -488,7 +491,8 @@ mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int3
   a.out = out;
   a.lse = lse;
   a.meta = (int4*)ws;
-  a.part = (float*)((char*)ws + rows_meta_bytes(ctx));
+  a.pre = (int*)((char*)ws + rows_meta_bytes(ctx));
+  a.part = (float*)((char*)ws + rows_meta_bytes(ctx) + rows_pre_bytes(ctx));
   return launch_status(launch_rows_attn(ctx, (cudaStream_t)stream, a));
 }
 
