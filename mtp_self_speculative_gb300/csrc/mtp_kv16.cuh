@@ -76,6 +76,7 @@ struct RowsArgs {
   float* part;                   // [2 * grid][rows of a segment][HD + 4]: o, then reference and sum
   int4* meta;                    // [2 * grid]: per thread block, the spanning segment that begins in it
   int* pre;                      // tensor-core form: [grid][kKvMaxB + 1] units before each request
+  int* plan;                     // tensor-core form, or null: RowsPlan
   // weights
   float* weights;                // [num_blocks, n_kv, 16]
   const int32_t* first;          // [B] or null
@@ -86,6 +87,14 @@ constexpr int kAtPairs = 256;      // pairs of a tile of the tensor-core kernel
 // The tensor-core form of the attention (bf16 heads); its pieces are joined as
 // the other form's.
 cudaError_t launch_attn_tc(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a);
+// The same of the entries' weights.
+cudaError_t launch_weights_tc(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a);
+
+// A call's segments in the order of their size, for calls of many segments:
+// whole ones are then handed out, the largest first, and none leaves pieces.
+// plan[0]: 1, or 0 for the split in equal shares; plan[1]: items (a tile and a
+// kv head each); plan[2]: the next item; from plan[4] on (request, tile).
+constexpr int kPlanTiles = 32768;
 
 // Request b's first row, rows and entries; 0, or the error that leaves it out.
 __device__ __forceinline__ int rows_request(const RowsArgs& a, int b, int& o0, int& n, int& L) {
@@ -147,13 +156,15 @@ __host__ __device__ __forceinline__ long long seg_units_before(const SegShape& s
 
 // The split of a call: units before each request, and the share of a thread
 // block.  Every thread of the block calls rows_split; false: nothing to do.
+// units(L, n, b): those of a request with n rows among L entries; less than 0:
+// the request is left out as its arguments are wrong.
 struct Split {
   int share;        // units of a thread block
   uint32_t u0, u1;  // this block's
 };
-template <int THREADS>
-__device__ __forceinline__ bool rows_split(const RowsArgs& a, const SegShape& s, int min_share, int* pre,
-                                           long long* wsum, Split& sp) {
+template <int THREADS, typename F>
+__device__ __forceinline__ bool rows_split(const RowsArgs& a, F&& request_units, int min_share, int* pre, long long* wsum,
+                                           Split& sp) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long long carry = 0;
   int bad = 0;
@@ -166,11 +177,15 @@ __device__ __forceinline__ bool rows_split(const RowsArgs& a, const SegShape& s,
         bad = 1;
       } else if (r1 > r0) {
         int o0, n, L;
-        const int e = rows_request(a, b, o0, n, L);
-        if (e == MTP_OK)
-          units = a.n_kv * seg_units_before(s, seg_tiles(s, n), L - n, n, a.mask != nullptr);
-        else if (blockIdx.x == 0)
-          set_error(a.err, e);
+        int e = rows_request(a, b, o0, n, L);
+        if (e == MTP_OK) {
+          units = request_units(L, n, b);
+          if (units < 0) {
+            units = 0;
+            e = MTP_ERR_DEVICE_ARGS;
+          }
+        }
+        if (e != MTP_OK && blockIdx.x == 0) set_error(a.err, e);
       }
     }
     long long x = units;  // inclusive scan over the block
@@ -205,6 +220,15 @@ __device__ __forceinline__ bool rows_split(const RowsArgs& a, const SegShape& s,
   sp.u1 = (uint32_t)min(u + sp.share, (unsigned long long)total);
   return true;
 }
+
+// Units of a request of the attention.
+struct SegUnits {
+  const RowsArgs& a;
+  const SegShape& s;
+  __device__ __forceinline__ long long operator()(int L, int n, int) const {
+    return a.n_kv * seg_units_before(s, seg_tiles(s, n), L - n, n, a.mask != nullptr);
+  }
+};
 
 // The part of a segment that falls into a thread block's share.
 struct Piece {

@@ -31,13 +31,11 @@
 #include <cuda.h>
 #include <math.h>
 
-#include "mtp_kv16.cuh"
+#include "mtp_kv_tc.cuh"
 
 namespace mtp {
 
 constexpr int kAtThreads = 384;
-constexpr int kAtStep = 128;        // slots of a step
-constexpr uint32_t kAtWait = 1u << 23;
 constexpr float kAtSlack = 8.0f;    // how far (powers of two) a maximum may pass its reference
 constexpr float kAtCoarse = 67108864.0f;   // from 2^26 on the reference's rounding is some units
 
@@ -61,144 +59,8 @@ struct AtPiece {
   int dirty;        // an entry that is not finite was taken out of V
 };
 
-__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  for (uint32_t i = 0; i < kAtWait; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255) == 255 && *abort_flag) return false;
-  }
-  return false;
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-// A cache block, issued by a whole warp with one thread elected (as the products
-// below).  One box of 4 KB: two of 2 KB take twice the time, some 75 cycles a box.
-__device__ __forceinline__ void at_tma(uint32_t dst, const CUtensorMap* map, int group, uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%4, %4, %4, %2}], [%3];\n}\n" ::"r"(dst),
-      "l"((uint64_t)map), "r"(group), "r"(bar), "r"(0)
-      : "memory");
-}
-// Shared-memory operands with 128-byte swizzle: groups of eight rows x 64
-// columns (1024 bytes), `step` bytes from one group of rows to the next and
-// `lead` bytes from 64 columns to the next 64.  (K-major operands need the
-// first alone: their 64 columns are four k-steps and are addressed one by one.
-// V is MN-major: the product's columns lie next to one another.)
-__device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t step, uint32_t lead) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(lead >> 4) << 16;
-  d |= (uint64_t)(step >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-// Products are issued by a whole warp with one thread elected in the
-// instruction sequence itself: under a branch on the lane the compiler cannot
-// know that the operands are uniform, and each product costs about 95 cycles of
-// issue instead of its own 64 (a 256 x 128 step 2.2 us instead of 1.5).
-// One k-step of 16: D += A B, A and B in shared memory.
-template <uint32_t A_OFF, uint32_t B_OFF>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 x, y;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " add.s64 x, %1, %5;\n add.s64 y, %2, %6;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A_OFF), "n"(B_OFF));
-}
-// The same with A in tensor memory, `a_off` columns on.
-template <uint32_t A_OFF, uint32_t B_OFF>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b32 x;\n .reg .b64 y;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " add.s32 x, %1, %5;\n add.s64 y, %2, %6;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A_OFF), "n"(B_OFF));
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
-      : "memory");
-}
-// Calls f(0), f(1), .. f(N - 1) with compile-time arguments.
-template <int I> struct Index { static constexpr int value = I; };
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void unrolled(F&& f) {
-  if constexpr (I < N) {
-    f(Index<I>{});
-    unrolled<N, I + 1>(f);
-  }
-}
-__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-#define AT_R32(v) \
-  "=r"((v)[0]), "=r"((v)[1]), "=r"((v)[2]), "=r"((v)[3]), "=r"((v)[4]), "=r"((v)[5]), "=r"((v)[6]), "=r"((v)[7]),   \
-      "=r"((v)[8]), "=r"((v)[9]), "=r"((v)[10]), "=r"((v)[11]), "=r"((v)[12]), "=r"((v)[13]), "=r"((v)[14]),         \
-      "=r"((v)[15]), "=r"((v)[16]), "=r"((v)[17]), "=r"((v)[18]), "=r"((v)[19]), "=r"((v)[20]), "=r"((v)[21]),       \
-      "=r"((v)[22]), "=r"((v)[23]), "=r"((v)[24]), "=r"((v)[25]), "=r"((v)[26]), "=r"((v)[27]), "=r"((v)[28]),       \
-      "=r"((v)[29]), "=r"((v)[30]), "=r"((v)[31])
-#define AT_W32(v) \
-  "r"((v)[0]), "r"((v)[1]), "r"((v)[2]), "r"((v)[3]), "r"((v)[4]), "r"((v)[5]), "r"((v)[6]), "r"((v)[7]), "r"((v)[8]), \
-      "r"((v)[9]), "r"((v)[10]), "r"((v)[11]), "r"((v)[12]), "r"((v)[13]), "r"((v)[14]), "r"((v)[15]), "r"((v)[16]),  \
-      "r"((v)[17]), "r"((v)[18]), "r"((v)[19]), "r"((v)[20]), "r"((v)[21]), "r"((v)[22]), "r"((v)[23]), "r"((v)[24]), \
-      "r"((v)[25]), "r"((v)[26]), "r"((v)[27]), "r"((v)[28]), "r"((v)[29]), "r"((v)[30]), "r"((v)[31])
-
-// 32 columns of this thread's row.  The registers hold them after tmem_ready.
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : AT_R32(v)
-      : "r"(at));
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// Keeps uses of the registers behind the wait above.
-__device__ __forceinline__ void tmem_ready(uint32_t* v) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]),
-                 "+r"(v[i + 6]), "+r"(v[i + 7]));
-}
-__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::AT_W32(v),
-      "r"(at)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// The largest of three; a NaN is passed over.
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
-// Two floats at a time.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void untwo(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // Bit e: whether a row sees slot t + e.  Without mask words it sees the slots
 // up to `last`; with them those below base, and of the n new ones those named.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 __device__ __forceinline__ uint32_t at_seen(const int32_t* words, int last, int t, int base, int n) {
   if (!words) return low_bits(last - t + 1);
   const int j = t - base;
@@ -278,7 +140,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
   pdl_trigger();
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   Split sp;
-  const bool work = rows_split<kAtThreads>(a, sh, sh.lead + 1, pre, wsum, sp);
+  const bool sorted = a.plan && __ldcg(a.plan) == 1;
+  const bool work = sorted || rows_split<kAtThreads>(a, SegUnits{a, sh}, sh.lead + 1, pre, wsum, sp);
 
   if (work && warp == 8) {
     // ------------------------------------------------------------- producer
@@ -289,10 +152,26 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     const int page = lane & 7;
     const int oob = a.kv.num_blocks * a.n_kv * 2;   // groups of the pool: a box from there on is zeros
     uint32_t u = sp.u0;
+    const int items = sorted ? __ldcg(a.plan + 1) : 0;
     while (ok) {
       Piece p{};
       bool any = false;
-      while (u < sp.u1) {
+      if (sorted) {
+        int item = lane == 0 ? atomicAdd(a.plan + 2, 1) : 0;
+        item = __shfl_sync(0xffffffffu, item, 0);
+        if (item < items) {
+          any = true;
+          const int2 t = __ldcg(reinterpret_cast<const int2*>(a.plan + 4) + item / a.n_kv);
+          p.b = t.x;
+          p.tile = t.y;
+          p.g = item % a.n_kv;
+          rows_request(a, p.b, p.o0, p.n, p.L);
+          p.base = p.L - p.n;
+          p.end = seg_end(sh, p.tile, p.base, p.n, a.mask != nullptr);
+          p.s_hi = (p.end + kAtStep - 1) / kAtStep;
+        }
+      }
+      while (!sorted && u < sp.u1) {
         find_piece(a, sh, pre, sp, u, p);
         u = p.next;
         if (p.s_lo < p.s_hi) {
@@ -853,8 +732,112 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
   }
 }
 
+// Sorts a call's tiles by their steps (counting sort, the largest first), or
+// leaves the call to the split in equal shares where that is the better one:
+// where a segment is larger than a share, or too few of them would leave SMs
+// idle at the end.  Causal prompts: the split's pieces cost a segment's write
+// and read in float32, all thread blocks at the same time, and a start and
+// an end each (8192 rows 512 -> 406 us, 4096 rows 185 -> 138).
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBins = 1024;
+__global__ void __launch_bounds__(kPlanThreads) rows_plan_kernel(const RowsArgs a, const SegShape sh, int blocks) {
+  __shared__ int before[kKvMaxB + 1];    // tiles before each request
+  __shared__ int bins[kPlanBins];
+  __shared__ long long warps[32];
+  __shared__ int most_s;
+  pdl_wait();
+  pdl_trigger();
+  const int b = threadIdx.x, lane = b & 31, warp = b >> 5;
+  const bool masked = a.mask != nullptr;
+  static_assert(kKvMaxB <= kPlanThreads, "a thread a request");
+  int bad = 0, tiles = 0, most = 0;
+  long long units = 0;
+  if (b == 0) most_s = 0;
+  if (b < kPlanBins) bins[b] = 0;
+  if (b < a.B) {
+    const int r0 = a.row_offsets[b], r1 = a.row_offsets[b + 1];
+    if (r0 < 0 || r1 < r0 || r1 > a.T) {
+      bad = 1;
+    } else if (r1 > r0) {
+      int o0, n, L;
+      const int e = rows_request(a, b, o0, n, L);
+      if (e != MTP_OK) {
+        set_error(a.err, e);   // (that request is left out)
+      } else {
+        tiles = seg_tiles(sh, n);
+        units = a.n_kv * seg_units_before(sh, tiles, L - n, n, masked);
+        most = (L + sh.step - 1) / sh.step;
+      }
+    }
+  }
+  // sums over the requests: tiles in the low 31 bits, units above (tiles of a call fit: T < 2^30)
+  bad = __syncthreads_or(bad);
+  auto scan = [&](long long v, long long& all) {
+    long long x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = x;
+    __syncthreads();
+    long long add = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) add += warps[w];
+      all += warps[w];
+    }
+    return add + x - v;
+  };
+  long long all_tiles, all_units;
+  const long long tile0 = scan(tiles, all_tiles);
+  scan(units, all_units);
+  if (b < a.B) before[b] = (int)min(tile0, (long long)INT32_MAX);
+  if (b == 0) before[a.B] = (int)min(all_tiles, (long long)INT32_MAX);
+  if (tiles) atomicMax(&most_s, most);
+  __syncthreads();
+  const long long share = (all_units + blocks - 1) / blocks;
+  const bool sort = !bad && all_tiles <= kPlanTiles && all_tiles * a.n_kv >= 2 * blocks && most_s + sh.lead <= share;
+  if (b == 0) {
+    a.plan[0] = sort;
+    a.plan[1] = sort ? (int)(all_tiles * a.n_kv) : 0;
+    a.plan[2] = 0;
+  }
+  if (!sort) return;
+  const int nt = (int)all_tiles;
+  auto find = [&](int e, int& req, int& tile) {   // entry e, and its bin (0: the most steps)
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (before[m] <= e) lo = m;
+      else hi = m;
+    }
+    req = lo;
+    tile = e - before[lo];
+    int o0, n, L;
+    rows_request(a, lo, o0, n, L);
+    const int steps = (seg_end(sh, tile, L - n, n, masked) + sh.step - 1) / sh.step;
+    return kPlanBins - 1 - (int)((long long)steps * (kPlanBins - 1) / most_s);
+  };
+  int req, tile;
+  for (int e = b; e < nt; e += kPlanThreads) atomicAdd(&bins[find(e, req, tile)], 1);
+  __syncthreads();
+  long long none;
+  const int at = (int)scan(bins[b], none);
+  __syncthreads();
+  bins[b] = at;
+  __syncthreads();
+  int2* list = reinterpret_cast<int2*>(a.plan + 4);
+  for (int e = b; e < nt; e += kPlanThreads) {
+    const int bin = find(e, req, tile);
+    list[atomicAdd(&bins[bin], 1)] = make_int2(req, tile);
+  }
+}
+
 template <int HD>
-static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, RowsArgs a) {
   using S = AtShape<HD>;
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.kv.num_blocks * a.n_kv * kBlk;
@@ -863,6 +846,14 @@ static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& 
   const cudaError_t e = ensure_smem((const void*)kv_attn_tc_kernel<HD>, S::kBytes);
   if (e != cudaSuccess) return e;
   const SegShape sh{kAtPairs >> a.g_shift, kAtStep, 2};
+  // enough rows for two segments a thread block: the plan may sort them
+  if (((long long)a.T << a.g_shift) * a.n_kv < 2ll * kAtPairs * ctx->num_sms) {
+    a.plan = nullptr;
+  } else {
+    const cudaError_t pe = launch_pdl(rows_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, sh, ctx->num_sms);
+    if (pe != cudaSuccess) return pe;
+    ctx->launches++;
+  }
   return launch_pdl(kv_attn_tc_kernel<HD>, dim3(ctx->num_sms), dim3(kAtThreads), S::kBytes, s, km, vm, a, sh);
 }
 cudaError_t launch_attn_tc(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {

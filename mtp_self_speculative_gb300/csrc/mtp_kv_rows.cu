@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   Split sp;
-  if (!rows_split<kRowsThreads>(a, sh, sh.lead + 4, pre, wsum, sp)) return;
+  if (!rows_split<kRowsThreads>(a, SegUnits{a, sh}, sh.lead + 4, pre, wsum, sp)) return;
   for (uint32_t u = sp.u0; u < sp.u1;) {
     Piece p;
     find_piece(a, sh, pre, sp, u, p);
@@ -415,23 +415,24 @@ static cudaError_t launch_rows_attn(mtp_ctx* ctx, cudaStream_t s, const RowsArgs
   return few ? rows_attn_launch<64, 1>(ctx, s, a) : rows_attn_launch<64, 4>(ctx, s, a);
 }
 
-template <typename T, int HD>
+template <int HD>
 static cudaError_t rows_weights_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
   const int smem = RowsShape<HD, 4>::kWeightBytes;
-  const cudaError_t e = ensure_smem((const void*)rows_weights_kernel<T, HD>, smem);
+  const cudaError_t e = ensure_smem((const void*)rows_weights_kernel<float, HD>, smem);
   if (e != cudaSuccess) return e;
   const int tiles = (int)(((long long)a.kv.max_blocks * kBlk + kRowsStep - 1) / kRowsStep);
-  return launch_pdl(rows_weights_kernel<T, HD>, dim3(tiles, a.n_kv, a.B), dim3(kRowsThreads), smem, s, a);
+  return launch_pdl(rows_weights_kernel<float, HD>, dim3(tiles, a.n_kv, a.B), dim3(kRowsThreads), smem, s, a);
 }
-template <typename T>
-cudaError_t launch_rows_weights(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
+static cudaError_t launch_rows_weights(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
   ctx->launches++;
-  return ctx->cfg.head_dim == 128 ? rows_weights_launch<T, 128>(ctx, s, a) : rows_weights_launch<T, 64>(ctx, s, a);
+  if (ctx->cfg.dtype == MTP_DTYPE_BF16) return launch_weights_tc(ctx, s, a);
+  return ctx->cfg.head_dim == 128 ? rows_weights_launch<128>(ctx, s, a) : rows_weights_launch<64>(ctx, s, a);
 }
 
 // Workspace: what the join kernel joins, then two pieces a thread block.
 constexpr int kRowsMaxBlocks = 2;    // thread blocks per SM at most
 static size_t rows_meta_bytes(const mtp_ctx* ctx) { return (size_t)kRowsMaxBlocks * ctx->num_sms * 2 * sizeof(int4); }
+constexpr size_t kPlanBytes = (4 + 2 * (size_t)kPlanTiles) * sizeof(int);
 static size_t rows_pre_bytes(const mtp_ctx* ctx) {
   return ((size_t)ctx->num_sms * (kKvMaxB + 1) * sizeof(int) + 255) & ~(size_t)255;
 }
@@ -474,7 +475,7 @@ extern "C" {
 size_t mtp_kv_attention_workspace_bytes(const mtp_ctx* ctx) {
   if (!ctx) return 0;
   const int pairs = ctx->cfg.dtype == MTP_DTYPE_BF16 ? kAtPairs : kRowsMaxBlocks * 64;   // of an SM's thread blocks
-  return rows_meta_bytes(ctx) + rows_pre_bytes(ctx) + (size_t)2 * ctx->num_sms * pairs * (ctx->cfg.head_dim + 4) * sizeof(float);
+  return rows_meta_bytes(ctx) + rows_pre_bytes(ctx) + kPlanBytes + (size_t)2 * ctx->num_sms * pairs * (ctx->cfg.head_dim + 4) * sizeof(float);
 }
 
 mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
@@ -492,7 +493,8 @@ mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int3
   a.lse = lse;
   a.meta = (int4*)ws;
   a.pre = (int*)((char*)ws + rows_meta_bytes(ctx));
-  a.part = (float*)((char*)ws + rows_meta_bytes(ctx) + rows_pre_bytes(ctx));
+  a.plan = (int*)((char*)ws + rows_meta_bytes(ctx) + rows_pre_bytes(ctx));
+  a.part = (float*)((char*)a.plan + kPlanBytes);
   return launch_status(launch_rows_attn(ctx, (cudaStream_t)stream, a));
 }
 
@@ -510,8 +512,7 @@ mtp_status mtp_kv_attention_weights(mtp_ctx* ctx, void* stream, int B, int T, co
   a.lse = const_cast<float*>(lse);
   a.first = first;
   a.weights = weights;
-  return launch_status(ctx->cfg.dtype == MTP_DTYPE_BF16 ? launch_rows_weights<uint16_t>(ctx, (cudaStream_t)stream, a)
-                                                        : launch_rows_weights<float>(ctx, (cudaStream_t)stream, a));
+  return launch_status(launch_rows_weights(ctx, (cudaStream_t)stream, a));
 }
 
 }  // extern "C"
