@@ -124,30 +124,31 @@ __device__ __forceinline__ bool row_sees(const int32_t* row_words, int i, int t,
 // before a tile has a closed form:
 //   sum_{y=1..t} ceil((base + y rows) / STEP).
 struct SegShape {
-  int rows, step;   // new rows of a tile; slots of a step
+  int rows, step;   // shifts: new rows of a tile; slots of a step
   int lead;         // steps that a segment's start and end count for
 };
-__host__ __device__ __forceinline__ long long ceil_sum(long long x, int q) {   // sum_{y=1..x} ceil(y / q)
-  const long long a = x / q, r = x - a * q;
-  return q * (a * (a + 1) / 2) + r * (a + 1);
+__host__ __device__ __forceinline__ int ceil_shift(int x, int s) { return (x + (1 << s) - 1) >> s; }
+__host__ __device__ __forceinline__ long long ceil_sum(long long x, int s) {   // sum_{y=1..x} ceil(y / 2^s)
+  const long long a = x >> s, r = x - (a << s);
+  return (a * (a + 1) << s >> 1) + r * (a + 1);
 }
-__host__ __device__ __forceinline__ int seg_tiles(const SegShape& s, int n) { return (n + s.rows - 1) / s.rows; }
+__host__ __device__ __forceinline__ int seg_tiles(const SegShape& s, int n) { return ceil_shift(n, s.rows); }
 // One past the last slot that a row of tile t sees.
 __host__ __device__ __forceinline__ int seg_end(const SegShape& s, int t, int base, int n, bool masked) {
-  const long long e = (long long)(t + 1) * s.rows;
+  const long long e = (long long)(t + 1) << s.rows;
   return masked || e > n ? base + n : base + (int)e;
 }
 // Units (steps, and `lead` more for each tile) before tile t of a head.
 __host__ __device__ __forceinline__ long long seg_units_before(const SegShape& s, int t, int base, int n, bool masked) {
   const int all = seg_tiles(s, n);
-  const long long last = (base + n + s.step - 1) / s.step;
+  const long long last = ceil_shift(base + n, s.step);
   if (masked) return t * (last + s.lead);
   const int full = t < all ? t : all - 1;       // tiles that end at a multiple of their rows
   long long u;
   if (s.rows >= s.step) {
-    u = full * (long long)((base + s.step - 1) / s.step) + (s.rows / s.step) * ((long long)full * (full + 1) / 2);
+    u = full * (long long)ceil_shift(base, s.step) + ((long long)full * (full + 1) / 2 << (s.rows - s.step));
   } else {
-    const int c = (base + s.rows - 1) / s.rows, q = s.step / s.rows;
+    const int c = ceil_shift(base, s.rows), q = s.step - s.rows;
     u = ceil_sum((long long)c + full, q) - ceil_sum(c, q);
   }
   if (t == all) u += last;
@@ -263,7 +264,7 @@ __device__ __forceinline__ void find_piece(const RowsArgs& a, const SegShape& s,
   }
   p.tile = t0;
   p.end = seg_end(s, t0, p.base, p.n, masked);
-  const int steps = (p.end + s.step - 1) / s.step;
+  const int steps = ceil_shift(p.end, s.step);
   const uint32_t seg0 = (uint32_t)pre[lo] + (uint32_t)p.g * per_head + (uint32_t)seg_units_before(s, t0, p.base, p.n, masked);
   const uint32_t work0 = seg0 + s.lead, seg1 = work0 + steps;
   p.s_lo = u > work0 ? (int)(u - work0) : 0;

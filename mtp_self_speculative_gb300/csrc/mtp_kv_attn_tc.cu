@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       ok = __all_sync(0xffffffffu, at_wait(&sm.piece_empty[np & 1], ((np >> 1) & 1) ^ 1, &sm.abort_flag));
       if (!ok) break;
       const bool whole = p.c_first == p.c_last;
-      const int i0 = p.tile * sh.rows, valid = min(kAtPairs, (p.n - i0) << a.g_shift);
+      const int i0 = p.tile << sh.rows, valid = min(kAtPairs, (p.n - i0) << a.g_shift);
       if (lane == 0) {
         AtPiece& q = sm.piece[np & 1];
         q.b = any ? p.b : -1;
@@ -419,34 +419,48 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     // together, then swizzled as the products read them.
     constexpr int CH = HD / 8;                             // 16-byte chunks of a pair; loads of a thread
     uint4 qr[CH];
-    auto q_at = [&](const AtPiece& p, int x) {   // (pairs past the last row read that one, and become zeros)
-      const int pr = r / CH + x * (128 / CH), i = min(p.i0 + ((w * 128 + pr) >> a.g_shift), p.n - 1);
-      return (const uint16_t*)a.q + (long long)(p.o0 + i) * a.q_stride + (long long)(p.g * G + (pr & (G - 1))) * HD + r % CH * 8;
-    };
+    // Thread r has chunk r % CH of every (128 / CH)-th pair, which are whole rows
+    // apart (a group has at most eight heads): one address and a stride.  (Code
+    // that runs once a segment is kept small: it is fetched anew each time.)
+    const int q_rows = (128 / CH) >> a.g_shift, q_pair = r / CH;
     auto has_q = [&](const AtPiece& p) { return p.b >= 0 && (p.valid > 128 || w == 0); };
+    auto q_first = [&](const AtPiece& p, int& i) {       // the first pair's row, and where it lies
+      i = p.i0 + ((w * 128 + q_pair) >> a.g_shift);
+      return (const uint16_t*)a.q + (long long)(p.o0 + i) * a.q_stride + (long long)(p.g * G + (q_pair & (G - 1))) * HD + r % CH * 8;
+    };
     auto load_q = [&](const AtPiece& p) {
       if (!a.q_vec || !has_q(p)) return;
+      int i;
+      const uint16_t* src = q_first(p, i);
+      const long long step = q_rows * a.q_stride;
+      const int n = p.n;
 #pragma unroll
-      for (int x = 0; x < CH; ++x) qr[x] = __ldg(reinterpret_cast<const uint4*>(q_at(p, x)));
+      for (int x = 0; x < CH; ++x) {
+        qr[x] = make_uint4(0, 0, 0, 0);
+        if (i + x * q_rows < n) qr[x] = __ldg(reinterpret_cast<const uint4*>(src + x * step));
+      }
     };
     auto store_q = [&](const AtPiece& p) {
       if (p.b < 0) return;
       if (has_q(p)) {
+        const int c = r % CH;
+        unsigned char* dst = smem + w * S::kTile + ((q_pair >> 3) * S::kHalves + (c >> 3)) * 1024 + (q_pair & 7) * 128 +
+                             (((c & 7) ^ (q_pair & 7)) << 4);
+        constexpr int kNext = 128 / CH / 8 * S::kHalves * 1024;    // (the pair's place among eight stays)
+        if (a.q_vec) {
 #pragma unroll
-        for (int x = 0; x < CH; ++x) {
-          const int pr = r / CH + x * (128 / CH), c = r % CH;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (p.i0 + ((w * 128 + pr) >> a.g_shift) < p.n) {
-            if (a.q_vec) {
-              v = qr[x];
-            } else {   // rows off 16 bytes: fetched here
-              const uint16_t* s = q_at(p, x);
-              v = make_uint4((uint32_t)s[0] | (uint32_t)s[1] << 16, (uint32_t)s[2] | (uint32_t)s[3] << 16,
-                             (uint32_t)s[4] | (uint32_t)s[5] << 16, (uint32_t)s[6] | (uint32_t)s[7] << 16);
-            }
+          for (int x = 0; x < CH; ++x) *reinterpret_cast<uint4*>(dst + x * kNext) = qr[x];
+        } else {   // rows off 16 bytes: fetched here
+          int i;
+          const uint16_t* src = q_first(p, i);
+#pragma unroll 1
+          for (int x = 0; x < CH; ++x, i += q_rows, src += q_rows * a.q_stride) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i < p.n)
+              v = make_uint4((uint32_t)src[0] | (uint32_t)src[1] << 16, (uint32_t)src[2] | (uint32_t)src[3] << 16,
+                             (uint32_t)src[4] | (uint32_t)src[5] << 16, (uint32_t)src[6] | (uint32_t)src[7] << 16);
+            *reinterpret_cast<uint4*>(dst + x * kNext) = v;
           }
-          *reinterpret_cast<uint4*>(smem + w * S::kTile + ((pr >> 3) * S::kHalves + (c >> 3)) * 1024 + (pr & 7) * 128 +
-                                    (((c & 7) ^ (pr & 7)) << 4)) = v;
         }
         fence_async();
       }
@@ -476,127 +490,127 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       // the first step that some row of this group sees only part of
       const int edge = a.mask || split ? p.edge : (base + i0 + ((w * 128) >> a.g_shift) + 1) / kAtStep;
       float m = kKvLeast, l = 0.0f;
+      bool coarse = false;
       for (int x = 0; x < mine; ++x) {
         const int j = split ? 2 * x + w : x;
         ok = __all_sync(0xffffffffu, at_wait(&sm.s_full[w], s_count & 1, &sm.abort_flag));
         if (!ok) break;
         ++s_count;
         tmem_after();
-        // One pass, 32 columns at a time: weights by the reference as it is, and
-        // the maximum next to them.  Where that passes the reference by more than
-        // the slack (rarely, behind the first step) the reference moves and
-        // the pass is made again; the scores are still there, the weights
-        // go over them at the end.
         const bool part = s_lo + j >= edge;                // some row sees only part of the step
         const int t0 = (s_lo + j) * kAtStep;
-        uint32_t pw[64];
-        uint64_t sum[2];
-        float mx[4];
-        // KIND 0: every row sees all columns; 1: those up to `last`; 2: any mask,
-        // or a coarse reference.  (Asked per 32 columns instead, the loads' latency
-        // shows: 1910 instead of 1240 cycles a step.)
-        auto hide = [&](auto kind, uint32_t (&v)[32], int c) {
-          constexpr int KIND = decltype(kind)::value;
-          if constexpr (KIND > 0) {
-            const uint32_t bits = KIND == 1 ? low_bits(last - t0 - 32 * c + 1) : at_seen(words, last, t0 + 32 * c, base, rows);
+        uint64_t sum[2] = {0ull, 0ull};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto most = [&](const uint32_t (&v)[32]) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : 0xFF800000u;
+          for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        };
+        auto top = [&]() { return fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast); };
+        auto weights = [&](uint32_t (&v)[32], uint32_t* pw, uint64_t cc, uint64_t mm) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            untwo(fma2(two(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, mm), x0, x1);
+            x0 = exp2_fast(x0);
+            x1 = exp2_fast(x1);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(x0, x1));
+            pw[e / 2] = pack2_bf16(x0, x1);
           }
         };
-        auto pass = [&](auto kind, bool coarse) {
-          constexpr int KIND = decltype(kind)::value;
+        bool done = false;
+        if (x > 0 && !part && !coarse) {
+          // One pass, 32 columns at a time: weights by the reference as it is, and
+          // the maximum next to them.  Where that passes the reference by more
+          // than the slack (rarely) the pass counts for nothing; the scores
+          // are still there, as the weights go over them at the end.  (No
+          // question is asked within it: with two per 32 columns the loads'
+          // latency showed, 1910 instead of 1240 cycles a step.)
+          uint32_t pw[64], va[32], vb[32];
           const uint64_t cc = two(a.c, a.c), mm = two(-m, -m);
-          auto columns = [&](uint32_t (&v)[32], int c) {
-            if (KIND < 2 || part) hide(kind, v, c);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-            if (KIND == 2 && coarse) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c) - m);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float x0, x1;
-                untwo(fma2(two(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, mm), x0, x1);
-                v[e] = __float_as_uint(x0);
-                v[e + 1] = __float_as_uint(x1);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float p0 = exp2_fast(__uint_as_float(v[e])), p1 = exp2_fast(__uint_as_float(v[e + 1]));
-              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(p0, p1));
-              pw[16 * c + e / 2] = pack2_bf16(p0, p1);
-            }
-          };
-          sum[0] = sum[1] = 0ull;
-          mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
-          uint32_t va[32], vb[32];
           tmem_ld(s_at, va);
           tmem_wait_ld();
           tmem_ready(va);
           tmem_ld(s_at + 32, vb);
-          columns(va, 0);
+          most(va);
+          weights(va, pw, cc, mm);
           tmem_wait_ld();
           tmem_ready(vb);
           tmem_ld(s_at + 64, va);
-          columns(vb, 1);
+          most(vb);
+          weights(vb, pw + 16, cc, mm);
           tmem_wait_ld();
           tmem_ready(va);
           tmem_ld(s_at + 96, vb);
-          columns(va, 2);
+          most(va);
+          weights(va, pw + 32, cc, mm);
           tmem_wait_ld();
           tmem_ready(vb);
-          columns(vb, 3);
-        };
-        if (x == 0) {   // no reference yet: the maximum first
-          auto most = [&](uint32_t (&v)[32], int c) {
-            if (part) hide(Index<2>{}, v, c);
+          most(vb);
+          weights(vb, pw + 48, cc, mm);
+          done = !__any_sync(0xffffffffu, top() > m + kAtSlack);
+          if (done) {
+            tmem_st(s_at, pw);
+            tmem_st(s_at + 32, pw + 32);
+          }
+        }
+        if (!done) {
+          // The first step, steps that some row sees only part of, and those that
+          // move the reference: the maximum first, then the weights, in little
+          // code.  The weights of columns 32 c .. go, two a word, over columns
+          // 16 c .., which are done with.
+          uint32_t v[32];
+          auto load = [&](int c) {
+            tmem_ld(s_at + 32 * c, v);
+            tmem_wait_ld();
+            tmem_ready(v);
+            if (part) {
+              const uint32_t bits = at_seen(words, last, t0 + 32 * c, base, rows);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : 0xFF800000u;
+            }
           };
           mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
-          uint32_t va[32], vb[32];
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            tmem_ld(s_at + 32 * c, va);
-            tmem_ld(s_at + 32 * c + 32, vb);
-            tmem_wait_ld();
-            tmem_ready(va);
-            tmem_ready(vb);
-            most(va, c);
-            most(vb, c + 1);
+          for (int c = 0; c < 4; ++c) {
+            load(c);
+            most(v);
           }
-          m = fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast);
-        }
-        for (int again = 0; again < 2; ++again) {
-          // from kAtCoarse on the reference is rounded to whole units: scores are then rounded like it
-          const bool coarse = __any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast);
-          if (coarse || (part && a.mask)) pass(Index<2>{}, coarse);
-          else if (part) pass(Index<1>{}, false);
-          else pass(Index<0>{}, false);
-          const float top = fmaxf(__fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c), kKvLeast);
-          const bool above = top > m + kAtSlack;
-          if (again || !__any_sync(0xffffffffu, above)) break;
-          const float mn = above ? top : m, alpha = exp2_fast(m - mn);
-          m = mn;
-          l *= alpha;
-          if (x > 0) {   // (S_w full: the products into O_w before it have ended)
-            const uint32_t o = o_at + w * HD;
+          const float t = top();
+          if (x == 0) {
+            m = t;
+          } else if (__any_sync(0xffffffffu, t > m + kAtSlack)) {
+            const float mn = t > m + kAtSlack ? t : m, alpha = exp2_fast(m - mn);
+            m = mn;
+            l *= alpha;
+            // (S_w full: the products into O_w before it have ended)
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
-              uint32_t v[32];
-              tmem_ld(o + c0, v);
+              tmem_ld(o_at + w * HD + c0, v);
               tmem_wait_ld();
               tmem_ready(v);
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tmem_st(o + c0, v);
+              tmem_st(o_at + w * HD + c0, v);
             }
           }
+          // from kAtCoarse on the reference is rounded to whole units: scores are
+          // then rounded like it before it is taken off
+          coarse = __any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast);
+          sum[0] = sum[1] = 0ull;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            load(c);
+            float f = a.c;
+            if (coarse) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c));
+              f = 1.0f;
+            }
+            uint32_t pw[16];
+            weights(v, pw, two(f, f), two(-m, -m));
+            tmem_st16(s_at + 16 * c, pw);
+          }
         }
-        tmem_st(s_at, pw);
-        tmem_st(s_at + 32, pw + 32);
         float l0, l1;
         untwo(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
@@ -766,7 +780,7 @@ __global__ void __launch_bounds__(kPlanThreads) rows_plan_kernel(const RowsArgs 
       } else {
         tiles = seg_tiles(sh, n);
         units = a.n_kv * seg_units_before(sh, tiles, L - n, n, masked);
-        most = (L + sh.step - 1) / sh.step;
+        most = ceil_shift(L, sh.step);
       }
     }
   }
@@ -818,7 +832,7 @@ __global__ void __launch_bounds__(kPlanThreads) rows_plan_kernel(const RowsArgs 
     tile = e - before[lo];
     int o0, n, L;
     rows_request(a, lo, o0, n, L);
-    const int steps = (seg_end(sh, tile, L - n, n, masked) + sh.step - 1) / sh.step;
+    const int steps = ceil_shift(seg_end(sh, tile, L - n, n, masked), sh.step);
     return kPlanBins - 1 - (int)((long long)steps * (kPlanBins - 1) / most_s);
   };
   int req, tile;
@@ -845,7 +859,8 @@ static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, RowsArgs a) {
     return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem((const void*)kv_attn_tc_kernel<HD>, S::kBytes);
   if (e != cudaSuccess) return e;
-  const SegShape sh{kAtPairs >> a.g_shift, kAtStep, 2};
+  const SegShape sh{8 - a.g_shift, 7, 2};   // 256 pairs, 128 slots
+  static_assert(kAtPairs == 1 << 8 && kAtStep == 1 << 7, "shifts");
   // enough rows for two segments a thread block: the plan may sort them
   if (((long long)a.T << a.g_shift) * a.n_kv < 2ll * kAtPairs * ctx->num_sms) {
     a.plan = nullptr;

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
     find_piece(a, sh, pre, sp, u, p);
     u = p.next;
     if (p.s_lo >= p.s_hi) continue;
-    const int i0 = p.tile * sh.rows;
+    const int i0 = p.tile << sh.rows;
     __syncthreads();
     load_queries<T, HD, ROWS>(a, qs, p.o0, i0, p.n, p.g);
     float o[RT][OC][4], m[RT], l[RT];
@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(kRowsThreads) rows_weights_kernel(const RowsAr
 template <typename T, int HD>
 static cudaError_t rows_join_launch(cudaStream_t s, const RowsArgs& a, int grid, int pairs) {
   const int per = kRowsJoinThreads / (HD / 4);
-  return launch_pdl(rows_join_kernel<T, HD>, dim3(grid, (pairs + per - 1) / per), dim3(kRowsJoinThreads), 0, s, a, pairs);
+  const long long most = (long long)a.max_rows << a.g_shift;   // pairs of a segment
+  const int groups = ((int)(most < pairs ? most : pairs) + per - 1) / per;
+  return launch_pdl(rows_join_kernel<T, HD>, dim3(grid, groups), dim3(kRowsJoinThreads), 0, s, a, pairs);
 }
 
 template <int HD, int RT>
@@ -397,7 +399,8 @@ static cudaError_t rows_attn_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs
   using S = RowsShape<HD, RT>;
   cudaError_t e = ensure_smem((const void*)rows_attn_kernel<float, HD, RT>, S::kBytes);
   if (e != cudaSuccess) return e;
-  const SegShape sh{S::kRows >> a.g_shift, kRowsStep, 2};
+  const SegShape sh{(RT == 1 ? 4 : 6) - a.g_shift, 6, 2};   // 16 or 64 pairs, 64 slots
+  static_assert(S::kRows == (RT == 1 ? 16 : 64) && kRowsStep == 64, "shifts");
   const int grid = (RT == 1 ? 2 : 1) * ctx->num_sms;
   e = launch_pdl(rows_attn_kernel<float, HD, RT>, dim3(grid), dim3(kRowsThreads), S::kBytes, s, a, sh);
   return e != cudaSuccess ? e : rows_join_launch<float, HD>(s, a, grid, S::kRows);
