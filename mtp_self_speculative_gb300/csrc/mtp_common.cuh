@@ -377,6 +377,11 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
 // swizzle), the columns' halves of a group next to one another: coordinates
 // (0, 0, 0, row / 8).
 bool make_block_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols);
+// Map of queries [T, heads, cols] bf16 (rows row_stride elements apart, base and
+// stride on 16 bytes) whose box is 128 (row, head) pairs of a group of heads x 64
+// columns, pairs of a row next to one another, 128-byte swizzle: coordinates (0,
+// 0, row, columns / 64, kv head).  Rows from T on are zeros.
+bool make_query_map(CUtensorMap* m, const void* base, int64_t row_stride, int T, int heads, int group, int cols);
 cudaError_t launch_draft_step_tc(mtp_ctx* ctx, cudaStream_t s, int B, int k, int K, const void* hidden,
                                  const void* embeds, const int32_t* positions, const mtp_kv* kv,
                                  const int32_t* chain_ids, int32_t* draft_ids, float* logits, float* hidden_out);

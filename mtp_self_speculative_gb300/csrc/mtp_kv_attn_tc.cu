@@ -84,7 +84,7 @@ __device__ __forceinline__ uint32_t ring_v(int j, int n) { return j == n - 1 ? 2
 template <int HD>
 struct AtShared {
   uint64_t full[AtShape<HD>::kStages], empty[AtShape<HD>::kStages];
-  uint64_t s_full[2], p_ready[2], q_ready[2], written[2], scan, clean, merged, piece_full[2], piece_empty[2];
+  uint64_t s_full[2], p_ready[2], q_full[2], q_empty[2], q_ready[2], scan, clean, merged, piece_full[2], piece_empty[2];
   AtPiece piece[2];
   float ml[2][128][2];
   uint32_t tmem;
@@ -92,7 +92,8 @@ struct AtShared {
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                                   const __grid_constant__ CUtensorMap kmap,
                                                                    const __grid_constant__ CUtensorMap vmap,
                                                                    const RowsArgs a, const SegShape sh) {
   using S = AtShape<HD>;
@@ -118,7 +119,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       mbar_init(&sm.s_full[w], 1);
       mbar_init(&sm.p_ready[w], 4);
       mbar_init(&sm.q_ready[w], 4);
-      mbar_init(&sm.written[w], 4);
+      mbar_init(&sm.q_full[w], 1);
+      mbar_init(&sm.q_empty[w], 1);
       mbar_init(&sm.piece_full[w], 1);
       mbar_init(&sm.piece_empty[w], 11);
     }
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
   if (work && warp == 8) {
     // ------------------------------------------------------------- producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    uint32_t rb = 0, issued = 0;
+    uint32_t rb = 0, issued = 0, asked[2] = {0, 0};
     int np = 0;
     bool ok = true;
     const int page = lane & 7;
@@ -231,8 +233,23 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         issued = it + 1;
         return true;
       };
+      // queries: 128 pairs a group, or all of up to 128 in the first tile (those
+      // past the request's rows are another's, or zeros: nobody writes their results)
+      auto queries = [&](int w) -> bool {
+        if (!__all_sync(0xffffffffu, at_wait(&sm.q_empty[w], (asked[w] & 1) ^ 1, &sm.abort_flag))) return false;
+        if (lane == 0) mbar_expect_tx(&sm.q_full[w], S::kTile);
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < S::kHalves; ++half)
+          at_tma_q(smem_addr(smem) + w * S::kTile + half * (128 * 128), &qmap, p.o0 + i0 + ((w * 128) >> a.g_shift), half, p.g,
+                   smem_addr(&sm.q_full[w]));
+        ++asked[w];
+        return true;
+      };
       int r0 = row_of(0), r1 = row_of(1);
-      ok = issue(&kmap, rb, r0);
+      if (a.q_vec) ok = queries(0);
+      if (ok) ok = issue(&kmap, rb, r0);
+      if (ok && a.q_vec && valid > 128) ok = queries(1);
       for (int j = 0; j < n && ok; ++j) {
         const int r2 = row_of(j + 2);   // looked up two steps ahead
         if (j + 1 < n) ok = issue(&kmap, rb + ring_k(j + 1), r1);
@@ -248,6 +265,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       // copies in flight land before the block ends
       for (uint32_t it = issued > NS ? issued - NS : 0; it < issued; ++it)
         mbar_wait_bounded(&sm.full[it % NS], (it / NS) & 1, 1u << 20);
+      for (int w = 0; w < 2; ++w)
+        if (asked[w]) mbar_wait_bounded(&sm.q_full[w], (asked[w] - 1) & 1, 1u << 20);
     }
   } else if (work && warp == 9) {
     // ------------------------------------------------------------- products
@@ -257,9 +276,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     constexpr uint32_t kIdO = kBase | (1u << 16) | ((uint32_t)(HD >> 3) << 17);   // B (V) is MN-major
     // (descriptors differ in the address field alone, which counts 16 bytes)
     constexpr uint32_t kGroup = S::kHalves * 1024;       // bytes of eight rows
-    const uint64_t q_desc = at_desc(smem_addr(smem), kGroup, 16), k_desc = at_desc(smem_addr(ring), kGroup, 16),
+    const uint64_t q_desc = at_desc(smem_addr(smem), 1024, 16), k_desc = at_desc(smem_addr(ring), kGroup, 16),
                    v_desc = at_desc(smem_addr(ring), kGroup, 1024);
-    uint32_t rb = 0, cleans = 0, p_count[2] = {0, 0};
+    uint32_t rb = 0, cleans = 0, p_count[2] = {0, 0}, q_count[2] = {0, 0};
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && __all_sync(0xffffffffu, at_wait(bar, parity, &sm.abort_flag));
@@ -280,9 +299,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
         tmem_after();
         unrolled<HD / 16>([&](auto x) {
           constexpr int kk = decltype(x)::value;
-          constexpr uint32_t at = (kk >> 2) * (1024 >> 4) + (kk & 3) * 2;
-          mma_ss<at, at>(tmem + w * 128, qd, kd, kIdS, kk > 0);
+          mma_ss<(kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2, (kk >> 2) * (1024 >> 4) + (kk & 3) * 2>(tmem + w * 128, qd, kd,
+                                                                                                 kIdS, kk > 0);
         });
+        // the last product that reads these queries
+        if (j + 1 >= n && a.q_vec) mma_commit(&sm.q_empty[split ? 0 : w]);
       };
       auto values = [&](int w, int j, bool start) {    // O_w += P_w V_j
         const uint64_t vd = v_desc + at_ring(ring_v(j, n)) * (S::kTile >> 4);
@@ -303,11 +324,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       };
       auto wait_clean = [&](int j) { return j < first_edge || wait(&sm.clean, cleans++ & 1); };
       auto wait_p = [&](int w) { return wait(&sm.p_ready[w], p_count[w]++ & 1); };
-      if (!wait(&sm.q_ready[0], np & 1) || !wait_ring(ring_k(0))) break;
+      auto wait_q = [&](int w) {
+        return a.q_vec ? wait(&sm.q_full[w], q_count[w]++ & 1) : wait(&sm.q_ready[w], np & 1);
+      };
+      if (!wait_q(0) || !wait_ring(ring_k(0))) break;
       scores(0, 0);
       mma_commit(&sm.s_full[0]);
       if (split) free_ring(ring_k(0));
-      if (!wait(&sm.q_ready[1], np & 1)) break;
+      if ((!split || !a.q_vec) && !wait_q(1)) break;
       // A wait takes some 150 cycles even when there is nothing to wait for, and
       // the products in the pipe cover about 200: one wait at most stands
       // between two runs of eight products.
@@ -414,53 +438,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256;
     uint32_t s_count = 0, merges = 0;   // phases of s_full[w] and of merged
     bool ok = true;
-    // A segment's queries: this group's 128 pairs (both groups' in the first
-    // tile, for up to 128), in registers first, so that all loads go out
-    // together, then swizzled as the products read them.
-    constexpr int CH = HD / 8;                             // 16-byte chunks of a pair; loads of a thread
-    uint4 qr[CH];
-    // Thread r has chunk r % CH of every (128 / CH)-th pair, which are whole rows
-    // apart (a group has at most eight heads): one address and a stride.  (Code
-    // that runs once a segment is kept small: it is fetched anew each time.)
-    const int q_rows = (128 / CH) >> a.g_shift, q_pair = r / CH;
-    auto has_q = [&](const AtPiece& p) { return p.b >= 0 && (p.valid > 128 || w == 0); };
-    auto q_first = [&](const AtPiece& p, int& i) {       // the first pair's row, and where it lies
-      i = p.i0 + ((w * 128 + q_pair) >> a.g_shift);
-      return (const uint16_t*)a.q + (long long)(p.o0 + i) * a.q_stride + (long long)(p.g * G + (q_pair & (G - 1))) * HD + r % CH * 8;
-    };
-    auto load_q = [&](const AtPiece& p) {
-      if (!a.q_vec || !has_q(p)) return;
-      int i;
-      const uint16_t* src = q_first(p, i);
-      const long long step = q_rows * a.q_stride;
-      const int n = p.n;
-#pragma unroll
-      for (int x = 0; x < CH; ++x) {
-        qr[x] = make_uint4(0, 0, 0, 0);
-        if (i + x * q_rows < n) qr[x] = __ldg(reinterpret_cast<const uint4*>(src + x * step));
-      }
-    };
+    // Queries whose rows do not lie on 16 bytes: fetched by the groups themselves,
+    // between two segments.
     auto store_q = [&](const AtPiece& p) {
       if (p.b < 0) return;
-      if (has_q(p)) {
-        const int c = r % CH;
-        unsigned char* dst = smem + w * S::kTile + ((q_pair >> 3) * S::kHalves + (c >> 3)) * 1024 + (q_pair & 7) * 128 +
-                             (((c & 7) ^ (q_pair & 7)) << 4);
-        constexpr int kNext = 128 / CH / 8 * S::kHalves * 1024;    // (the pair's place among eight stays)
-        if (a.q_vec) {
-#pragma unroll
-          for (int x = 0; x < CH; ++x) *reinterpret_cast<uint4*>(dst + x * kNext) = qr[x];
-        } else {   // rows off 16 bytes: fetched here
-          int i;
-          const uint16_t* src = q_first(p, i);
+      if (p.valid > 128 || w == 0) {
 #pragma unroll 1
-          for (int x = 0; x < CH; ++x, i += q_rows, src += q_rows * a.q_stride) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (i < p.n)
-              v = make_uint4((uint32_t)src[0] | (uint32_t)src[1] << 16, (uint32_t)src[2] | (uint32_t)src[3] << 16,
-                             (uint32_t)src[4] | (uint32_t)src[5] << 16, (uint32_t)src[6] | (uint32_t)src[7] << 16);
-            *reinterpret_cast<uint4*>(dst + x * kNext) = v;
+        for (int x = r; x < 128 * HD / 8; x += 128) {
+          const int pair = x / (HD / 8), c = x % (HD / 8), i = p.i0 + ((w * 128 + pair) >> a.g_shift);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (i < p.n) {
+            const uint16_t* s = (const uint16_t*)a.q + (long long)(p.o0 + i) * a.q_stride + (long long)(p.g * G + (pair & (G - 1))) * HD + c * 8;
+            v = make_uint4((uint32_t)s[0] | (uint32_t)s[1] << 16, (uint32_t)s[2] | (uint32_t)s[3] << 16,
+                           (uint32_t)s[4] | (uint32_t)s[5] << 16, (uint32_t)s[6] | (uint32_t)s[7] << 16);
           }
+          *reinterpret_cast<uint4*>(smem + w * S::kTile + (c >> 3) * (128 * 128) + pair * 128 + (((c & 7) ^ (pair & 7)) << 4)) = v;
         }
         fence_async();
       }
@@ -470,14 +462,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     auto wait_piece = [&](int np) {
       return (bool)__all_sync(0xffffffffu, at_wait(&sm.piece_full[np & 1], (np >> 1) & 1, &sm.abort_flag));
     };
-    ok = wait_piece(0);
-    if (ok) {
-      load_q(sm.piece[0]);
-      store_q(sm.piece[0]);
-    }
     for (int np = 0; ok; ++np) {
+      ok = wait_piece(np);
+      if (!ok) break;
       const AtPiece& p = sm.piece[np & 1];
       if (p.b < 0) break;
+      if (!a.q_vec) store_q(p);
       const int n = p.tiles, s_lo = p.s_lo, i0 = p.i0, rows = p.n, base = p.base, g = p.g, o0 = p.o0;
       const bool split = p.valid <= 128;
       const int mine = split ? (n + 1 - w) / 2 : n;       // steps of this group
@@ -558,22 +548,29 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
           // move the reference: the maximum first, then the weights, in little
           // code.  The weights of columns 32 c .. go, two a word, over columns
           // 16 c .., which are done with.
-          uint32_t v[32];
-          auto load = [&](int c) {
+          uint32_t v[32], v2[32];
+          auto hide = [&](uint32_t (&v)[32], int c) {
+            const uint32_t bits = at_seen(words, last, t0 + 32 * c, base, rows);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : 0xFF800000u;
+          };
+          auto load = [&](int c) {   // columns 32 c .. 32 c + 63
             tmem_ld(s_at + 32 * c, v);
+            tmem_ld(s_at + 32 * c + 32, v2);
             tmem_wait_ld();
             tmem_ready(v);
+            tmem_ready(v2);
             if (part) {
-              const uint32_t bits = at_seen(words, last, t0 + 32 * c, base, rows);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : 0xFF800000u;
+              hide(v, c);
+              hide(v2, c + 1);
             }
           };
           mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 4; c += 2) {
             load(c);
             most(v);
+            most(v2);
           }
           const float t = top();
           if (x == 0) {
@@ -597,18 +594,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
           // then rounded like it before it is taken off
           coarse = __any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast);
           sum[0] = sum[1] = 0ull;
+          const float f = coarse ? 1.0f : a.c;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 4; c += 2) {
             load(c);
-            float f = a.c;
             if (coarse) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c));
-              f = 1.0f;
+              for (int e = 0; e < 32; ++e) {
+                v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c));
+                v2[e] = __float_as_uint(__fmul_rn(__uint_as_float(v2[e]), a.c));
+              }
             }
-            uint32_t pw[16];
+            uint32_t pw[32];
             weights(v, pw, two(f, f), two(-m, -m));
-            tmem_st16(s_at + 16 * c, pw);
+            weights(v2, pw + 16, two(f, f), two(-m, -m));
+            tmem_st(s_at + 16 * c, pw);
           }
         }
         float l0, l1;
@@ -621,11 +621,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       }
       if (!ok) break;
       // ---- results: O_w of 128 pairs, or both groups' parts of the same pairs, half of the columns each
-      // the next segment's queries are fetched under the last products
-      ok = wait_piece(np + 1);
-      if (!ok) break;
-      const AtPiece& next = sm.piece[(np + 1) & 1];
-      load_q(next);
       if (mine > 0) {
         ok = __all_sync(0xffffffffu, at_wait(&sm.s_full[w], s_count & 1, &sm.abort_flag));
         if (!ok) break;
@@ -658,13 +653,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       const uint32_t o_mine = split ? o_at : o_at + w * HD;
       const bool dirty = *(volatile const int*)&p.dirty;
       const long long row = (long long)(o0 + i) * (a.n_kv << a.g_shift) + g * G + (pr & (G - 1));
-      const float inv = p.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-      // Rows go out through the group's part of the queries' memory, which no
-      // product reads any more, 32 columns of a warp's 32 rows at a time, so that
-      // a store instruction writes whole sectors (a thread writing its own row:
-      // 6500 cycles a segment).
-      float* stage = reinterpret_cast<float*>(smem + w * S::kTile + (warp & 3) * (32 * 32 * 4));
-      const int row_first = (warp & 3) * 32 + (split ? 0 : w * 128);       // pair of the warp's first row
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      // A thread writes its row, 32 bytes at a time: whole sectors.
+      uint16_t* out = (uint16_t*)a.out + row * HD;
+      const bool out32 = !((uintptr_t)a.out & 31);
+      float* piece = p.slot < 0 ? nullptr : a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pr) * (HD + 4);
 #pragma unroll 1
       for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
         uint32_t v[32];
@@ -693,28 +686,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
               if ((vr[e] & 0x7F80u) == 0x7F80u) y[e] += elem<uint16_t>(vr + e);
           }
         }
-        // eight lanes a row from here on: four columns each, rows lane / 8 + 4 k
-        __syncwarp();
+        if (!live) continue;
+        if (piece) {   // (rows of HD + 4 floats: on 16 bytes)
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(stage + lane * 32 + (e ^ (lane & 7) * 4)) = make_float4(y[e] * inv, y[e + 1] * inv, y[e + 2] * inv, y[e + 3] * inv);
-        __syncwarp();
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(piece + c0 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          continue;
+        }
+        if (!MTP_IN_BOUNDS(a.err, row * HD + c0 + 31, (long long)a.T * (a.n_kv << a.g_shift) * HD)) continue;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = lane / 8 + 4 * k, pair = row_first + rr, ii = i0 + (pair >> a.g_shift), col = c0 + (lane & 7) * 4;
-          if (ii >= rows) continue;
-          const float4 z = *reinterpret_cast<const float4*>(stage + rr * 32 + ((lane ^ rr) & 7) * 4);
-          if (p.slot < 0) {
-            const long long at = ((long long)(o0 + ii) * (a.n_kv << a.g_shift) + g * G + (pair & (G - 1))) * HD + col;
-            if (!MTP_IN_BOUNDS(a.err, at + 3, (long long)a.T * (a.n_kv << a.g_shift) * HD)) continue;
-            *reinterpret_cast<uint2*>((uint16_t*)a.out + at) = make_uint2(pack2_bf16(z.x, z.y), pack2_bf16(z.z, z.w));
-          } else {
-            *reinterpret_cast<float4*>(a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pair) * (HD + 4) + col) = z;
-          }
+        for (int e = 0; e < 16; ++e) v[e] = pack2_bf16(y[2 * e] * inv, y[2 * e + 1] * inv);
+        if (out32) {
+          st_global32(out + c0, v);
+          st_global32(out + c0 + 16, v + 8);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(out + c0 + 2 * e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
       }
-      if (live && c_lo == 0 && p.slot >= 0)
-        *reinterpret_cast<float2*>(a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pr) * (HD + 4) + HD) = make_float2(m, l);
+      if (live && c_lo == 0 && piece) *reinterpret_cast<float2*>(piece + HD) = make_float2(m, l);
       if (live && c_lo == 0 && p.slot < 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (split) {
         // the other group's part is read: it may go on to its next products
@@ -727,10 +716,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       }
       tmem_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.written[w]);
-      ok = __all_sync(0xffffffffu, at_wait(&sm.written[w], np & 1, &sm.abort_flag));
-      if (!ok) break;
-      store_q(next);     // the group's rows have left the memory that the next queries go to
       if (lane == 0) mbar_arrive(&sm.piece_empty[np & 1]);
     }
     if (!ok) {
@@ -853,10 +838,12 @@ __global__ void __launch_bounds__(kPlanThreads) rows_plan_kernel(const RowsArgs 
 template <int HD>
 static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, RowsArgs a) {
   using S = AtShape<HD>;
-  CUtensorMap km, vm;
+  CUtensorMap qm, km, vm;
   const uint64_t rows = (uint64_t)a.kv.num_blocks * a.n_kv * kBlk;
   if (rows > INT32_MAX || !make_block_map(&km, a.kv.k_pool, rows, HD) || !make_block_map(&vm, a.kv.v_pool, rows, HD))
     return cudaErrorInvalidValue;
+  qm = km;   // (not read where the queries cannot be mapped)
+  if (a.q_vec && !make_query_map(&qm, a.q, a.q_stride, a.T, a.n_kv << a.g_shift, 1 << a.g_shift, HD)) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem((const void*)kv_attn_tc_kernel<HD>, S::kBytes);
   if (e != cudaSuccess) return e;
   const SegShape sh{8 - a.g_shift, 7, 2};   // 256 pairs, 128 slots
@@ -869,7 +856,7 @@ static cudaError_t attn_tc_launch(mtp_ctx* ctx, cudaStream_t s, RowsArgs a) {
     if (pe != cudaSuccess) return pe;
     ctx->launches++;
   }
-  return launch_pdl(kv_attn_tc_kernel<HD>, dim3(ctx->num_sms), dim3(kAtThreads), S::kBytes, s, km, vm, a, sh);
+  return launch_pdl(kv_attn_tc_kernel<HD>, dim3(ctx->num_sms), dim3(kAtThreads), S::kBytes, s, qm, km, vm, a, sh);
 }
 cudaError_t launch_attn_tc(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
   return ctx->cfg.head_dim == 128 ? attn_tc_launch<128>(ctx, s, a) : attn_tc_launch<64>(ctx, s, a);

@@ -31,6 +31,20 @@ __device__ __forceinline__ void at_tma(uint32_t dst, const CUtensorMap* map, int
       "l"((uint64_t)map), "r"(group), "r"(bar), "r"(0)
       : "memory");
 }
+// 64 columns of 128 pairs of a kv head's queries.
+__device__ __forceinline__ void at_tma_q(uint32_t dst, const CUtensorMap* map, int row, int half, int g, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%6, %6, %2, %3, %4}], [%5];\n}\n" ::"r"(dst),
+      "l"((uint64_t)map), "r"(row), "r"(half), "r"(g), "r"(bar), "r"(0)
+      : "memory");
+}
+// 32 bytes to global memory; a sector of its own for each thread.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // Shared-memory operands with 128-byte swizzle: groups of eight rows x 64
 // columns (1024 bytes), `step` bytes from one group of rows to the next and
 // `lead` bytes from 64 columns to the next 64.  (K-major operands need the

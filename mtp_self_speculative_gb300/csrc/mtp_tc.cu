@@ -891,6 +891,17 @@ bool make_block_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t co
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_query_map(CUtensorMap* m, const void* base, int64_t row_stride, int T, int heads, int group, int cols) {
+  if (!get_encode()) return false;
+  cuuint64_t dims[5] = {64, (cuuint64_t)group, (cuuint64_t)T, (cuuint64_t)cols / 64, (cuuint64_t)heads / group};
+  cuuint64_t strides[4] = {(cuuint64_t)cols * 2, (cuuint64_t)row_stride * 2, 128, (cuuint64_t)group * cols * 2};
+  cuuint32_t box[5] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group), 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_supported(const mtp_ctx* ctx, int B) {
   const mtp_config& c = ctx->cfg;
   return ctx->tc_ws != nullptr && c.dtype == MTP_DTYPE_BF16 && c.head_dim == 128 && B >= ctx->tc_min_batch &&
