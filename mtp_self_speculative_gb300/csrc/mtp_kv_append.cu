@@ -35,7 +35,8 @@ struct NormArgs {
   int* err;
   float eps;
   int B, T, rd;          // rd: rotated elements of a head (0: none)
-  int k_groups;          // grid.y below it: keys (and values); from it on: queries
+  int k_groups, v_groups; // grid.y: groups of key heads, of value heads (append), then of query heads
+  int v_per;
 };
 
 // The eight pairs of a unit: pair-slot j = 8 u + e is the rotating pair j of
@@ -114,8 +115,7 @@ __device__ __forceinline__ void unit_store(T* head, int u, int rd, int layout, c
 }
 
 // Thread block (tokens, group of heads): LPH lanes a token and head.  With
-// CACHE a group of key heads takes the value heads along and writes both into
-// the cache.
+// CACHE groups of value heads are copied into the cache, and keys go there too.
 template <typename T, int HD, bool VEC, bool CACHE>
 __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormArgs a,
                                                                     const __grid_constant__ mtp_rope_table tab) {
@@ -125,16 +125,16 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, u = tid % LPH, t0 = blockIdx.x * TOK, t = t0 + tid / LPH;
-  const bool keys = (int)blockIdx.y < a.k_groups;
+  const int y = blockIdx.y;
+  const bool keys = y < a.k_groups, vals = CACHE && !keys && y < a.k_groups + a.v_groups, cached = keys || vals;
   const NormSide& s = keys ? a.k : a.q;
-  const int group = keys ? blockIdx.y : blockIdx.y - a.k_groups;
-  const int h0 = group * s.per, h1 = min(s.heads, h0 + s.per);
+  const int group = keys ? y : y - a.k_groups - (vals ? 0 : a.v_groups);
   if constexpr (CACHE) {
     // every thread block looks at all offsets; lengths come along, so that the
     // common batch waits for one round of loads
     int bad = 0, sl0 = 0, pe0 = 0;
     if (tid < TOK) at_s[tid] = -2;            // a row of no request
-    if (keys && tid < a.B) {
+    if (cached && tid < a.B) {
       sl0 = a.kv.seq_len[tid];
       pe0 = a.kv.pending[tid];
     }
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
       const int o0 = a.row_offsets[b], o1 = a.row_offsets[b + 1];
       const int lo = max(o0, t0), hi = min(o1, t0 + TOK);
       if (lo >= hi) continue;
-      if (!keys) {
+      if (!cached) {
         for (int x = lo; x < hi; ++x) at_s[x - t0] = 0;
         continue;
       }
@@ -178,12 +178,37 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
       // all of the request's thread blocks have read its old length before the
       // last one of them publishes the new one
       const int blocks = (o1 - 1) / TOK - o0 / TOK + 1;
-      if (arrive_last(a.arrive + b, blocks * a.k_groups)) a.kv.pending[b] = pe + (o1 - o0);
+      if (arrive_last(a.arrive + b, blocks * (a.k_groups + a.v_groups))) a.kv.pending[b] = pe + (o1 - o0);
     }
     __syncthreads();
   }
   const bool live = t < a.T && (!CACHE || at_s[tid / LPH] >= 0);
   if (!__any_sync(0xffffffffu, live)) return;
+  const long long kv_extent = (long long)a.kv.num_blocks * a.k.heads * kBlk * HD;
+  (void)kv_extent;   // bounds-checked builds only
+  if constexpr (CACHE) {
+    if (vals) {        // a copy
+      if (!live) return;
+      const T* src = (const T*)a.v + (long long)t * a.v_stride;
+#pragma unroll 4
+      for (int h = group * a.v_per; h < min(a.k.heads, (group + 1) * a.v_per); ++h) {
+        const long long at = at_s[tid / LPH] + (long long)h * kBlk * HD;
+        if (!MTP_IN_BOUNDS(a.err, at + HD - 1, kv_extent)) continue;
+        T* dst = (T*)a.kv.v_pool + at;
+        if constexpr (VEC) {
+          constexpr int N = 16 / sizeof(T);
+#pragma unroll
+          for (int i = 0; i < 16 / N; ++i)
+            *reinterpret_cast<uint4*>(dst + (i * LPH + u) * N) = *reinterpret_cast<const uint4*>(src + h * HD + (i * LPH + u) * N);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dst[i * LPH + u] = src[h * HD + i * LPH + u];
+        }
+      }
+      return;
+    }
+  }
+  const int h0 = group * s.per, h1 = min(s.heads, h0 + s.per);
   const int rd = a.rd;
   float2 cs[8];
   const int pos = live && rd ? a.positions[t] : 0;
@@ -197,8 +222,6 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
 #pragma unroll
     for (int e = 0; e < 16; ++e) w[e] = 1.0f;
   }
-  const long long kv_extent = (long long)a.kv.num_blocks * a.k.heads * kBlk * HD;
-  (void)kv_extent;   // bounds-checked builds only
 #pragma unroll 2
   for (int h = h0; h < h1; ++h) {
     float x[16];
@@ -235,24 +258,6 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
       if (MTP_IN_BOUNDS(a.err, at + HD - 1, s.extent)) unit_store<T, VEC>((T*)s.out + at, u, rd, tab.layout, x);
     }
   }
-  if constexpr (CACHE) {
-    if (!keys || !live) return;
-    for (int h = h0; h < h1; ++h) {   // values: a copy
-      const T* src = (const T*)a.v + (long long)t * a.v_stride + (long long)h * HD;
-      const long long at = at_s[tid / LPH] + (long long)h * kBlk * HD;
-      if (!MTP_IN_BOUNDS(a.err, at + HD - 1, kv_extent)) continue;
-      T* dst = (T*)a.kv.v_pool + at;
-      if constexpr (VEC) {
-        constexpr int N = 16 / sizeof(T);
-#pragma unroll
-        for (int i = 0; i < 16 / N; ++i)
-          *reinterpret_cast<uint4*>(dst + (i * LPH + u) * N) = *reinterpret_cast<const uint4*>(src + (i * LPH + u) * N);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dst[i * LPH + u] = src[i * LPH + u];
-      }
-    }
-  }
 }
 
 template <typename T, bool CACHE>
@@ -270,10 +275,12 @@ static cudaError_t norm_launch(mtp_ctx* ctx, cudaStream_t s, NormArgs a, const m
   int per = (heads + groups - 1) / groups;
   per = per < 1 ? 1 : per;
   a.q.per = per;
-  a.k.per = CACHE ? (per + 1) / 2 : per;
-  a.k_groups = a.k.x ? (a.k.heads + a.k.per - 1) / a.k.per : 0;
+  a.k.per = per;
+  a.v_per = per;
+  a.k_groups = a.k.x ? (a.k.heads + per - 1) / per : 0;
+  a.v_groups = CACHE ? a.k_groups : 0;
   const int q_groups = a.q.x ? (a.q.heads + a.q.per - 1) / a.q.per : 0;
-  const dim3 grid(gx, a.k_groups + q_groups), block(kNormThreads);
+  const dim3 grid(gx, a.k_groups + a.v_groups + q_groups), block(kNormThreads);
   ctx->launches++;
   if (hd == 128)
     return vec ? launch_pdl(qk_norm_rope_kernel<T, 128, true, CACHE>, grid, block, 0, s, a, tab)

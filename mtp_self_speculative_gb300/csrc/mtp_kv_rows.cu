@@ -25,9 +25,14 @@ template <bool V> struct Flag { static constexpr bool value = V; };
 template <int HD, int RT>
 struct RowsShape {
   static constexpr int kRows = 16 * RT;                    // pairs of a tile
-  static constexpr int kQ = HD * kRows, kK = HD * kRowsPitch, kV = kRowsStep * HD, kP = kRowsStep * kRows;   // floats
-  static constexpr int kBytes = (kQ + kK + kV + kP) * 4;
+  static constexpr int kQ = HD * kRows, kK = HD * kRowsPitch;   // floats
   static constexpr int kWeightBytes = (kQ + kK) * 4;
+};
+template <int HD, int RT>
+struct AttnShape {
+  static constexpr int kRows = 16 * RT;
+  static constexpr int kQ = HD * kRows, kP = kRows * (kRowsStep + 4);   // floats
+  static constexpr int kBytes = (kQ + kP + 2 * 2 * kRowsStep * HD) * 4;
 };
 
 // Queries of a tile, transposed: qs[d][pair]; pairs past the request's rows are zero.
@@ -127,33 +132,83 @@ __device__ __forceinline__ void tile_scores(const float* qs, const float* ks, in
   }
 }
 
-template <typename T, int HD, int RT>
+// 16 bytes global -> shared; none of them (zeros) for bytes = 0.
+__device__ __forceinline__ void rows_cp(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// Staged rows of HD floats: 16-byte chunk c of row r lies at chunk c ^ (r & 7),
+// so that eight lanes that read one chunk of eight rows meet no bank twice.
+template <int HD>
+__device__ __forceinline__ int rows_at(int r, int c) {
+  return r * HD + ((c ^ (r & 7)) << 2);
+}
+
+template <int HD, int RT>
 __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs a, const SegShape sh) {
-  using S = RowsShape<HD, RT>;
-  constexpr int ROWS = S::kRows;
+  using S = AttnShape<HD, RT>;
+  constexpr int ROWS = S::kRows, CH = HD / 4, PASS = kRowsThreads / CH;   // rows that the block copies at a time
   constexpr int OC = HD / 64;     // float4 columns of the result per thread and pair
+  constexpr int PP = kRowsStep + 4;
   extern __shared__ __align__(16) float smem[];
   __shared__ int pre[kKvMaxB + 1];
   __shared__ long long wsum[kRowsThreads / 32];
-  __shared__ int blocks[kRowsStep / kBlk];
-  float* qs = smem;
-  float* ks = qs + S::kQ;
-  float* vs = ks + S::kK;
-  float* ps = vs + S::kV;
+  float* qs = smem;                       // [ROWS][HD]
+  float* ps = qs + S::kQ;                 // [ROWS][PP]
+  float* kv = ps + S::kP;                 // [2][keys, values][kRowsStep][HD]
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = 1 << a.g_shift;
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   Split sp;
-  if (!rows_split<kRowsThreads>(a, SegUnits{a, sh}, sh.lead + 4, pre, wsum, sp)) return;
+  if (!rows_split<kRowsThreads>(a, SegUnits{a, sh}, sh.lead + 1, pre, wsum, sp)) return;
   for (uint32_t u = sp.u0; u < sp.u1;) {
     Piece p;
     find_piece(a, sh, pre, sp, u, p);
     u = p.next;
     if (p.s_lo >= p.s_hi) continue;
     const int i0 = p.tile << sh.rows;
-    __syncthreads();
-    load_queries<T, HD, ROWS>(a, qs, p.o0, i0, p.n, p.g);
+    const int32_t* table = a.kv.block_table + (long long)p.b * a.kv.max_blocks;
+    // a step's block ids, the same for all threads; looked up a step ahead of the copy
+    int ids[kRowsStep / kBlk];
+    auto look = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < kRowsStep / kBlk; ++i) {
+        const int t = step * kRowsStep + i * kBlk;
+        ids[i] = step < p.s_hi && t < p.end ? table[t >> 4] : 0;
+      }
+    };
+    auto copy = [&](int step, int stage) {
+      if (step < p.s_hi) {
+        const int c = tid % CH, t0 = step * kRowsStep;
+        float* dst = kv + stage * (2 * kRowsStep * HD);
+#pragma unroll
+        for (int x = 0; x < kRowsStep / PASS; ++x) {
+          const int t = tid / CH + x * PASS, blk = ids[x * PASS / kBlk];
+          const bool good = blk >= 0 && blk < a.kv.num_blocks, there = good && t0 + t < p.end;
+          const long long at = (((long long)(there ? blk : 0) * a.n_kv + p.g) * kBlk + (t & 15)) * HD + c * 4;
+          rows_cp(dst + rows_at<HD>(t, c), (const float*)a.kv.k_pool + at, there);
+          rows_cp(dst + kRowsStep * HD + rows_at<HD>(t, c), (const float*)a.kv.v_pool + at, there);
+          if (!good && t0 + t < p.end && c == 0) set_error(a.err, MTP_ERR_CAPACITY);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look(p.s_lo);
+    __syncthreads();              // the last piece's tiles are done with
+    copy(p.s_lo, 0);
+    look(p.s_lo + 1);
+    // queries, a pair's row at a time; pairs past the request's rows are zero
+    for (int x = tid; x < ROWS * CH; x += kRowsThreads) {
+      const int r = x / CH, c = x % CH, i = i0 + (r >> a.g_shift);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i < p.n) {
+        const float* src = (const float*)a.q + (long long)(p.o0 + i) * a.q_stride + (long long)(p.g * G + (r & (G - 1))) * HD + c * 4;
+        if (a.q_vec) v = *reinterpret_cast<const float4*>(src);
+        else v = make_float4(src[0], src[1], src[2], src[3]);
+      }
+      *reinterpret_cast<float4*>(qs + r * HD + ((c ^ (r / RT & 7)) << 2)) = v;
+    }
     float o[RT][OC][4], m[RT], l[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -165,17 +220,38 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
         for (int e = 0; e < 4; ++e) o[i][c][e] = 0.0f;
     }
     for (int step = p.s_lo; step < p.s_hi; ++step) {
-      const int t0 = step * kRowsStep;
+      const int t0 = step * kRowsStep, stage = (step - p.s_lo) & 1;
       // slots that some row of the tile does not see: from the first new one that its first row may not see
       const bool edge = t0 + kRowsStep > p.base + (a.mask ? 0 : i0 + 1);
+      copy(step + 1, stage ^ 1);
+      look(step + 2);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
-      load_blocks(a, blocks, p.b, t0, p.end);
-      __syncthreads();
-      load_entries<T, HD, true>(a, a.kv.k_pool, ks, blocks, t0, p.end, p.g);
-      load_entries<T, HD, false>(a, a.kv.v_pool, vs, blocks, t0, p.end, p.g);
-      __syncthreads();
+      const float* ks = kv + stage * (2 * kRowsStep * HD);
+      const float* vs = ks + kRowsStep * HD;
+      // scores of pairs RT ty .. and slots tx + 16 j
       float s[RT][4];
-      tile_scores<HD, RT>(qs, ks, ty, tx, s);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 4
+      for (int c = 0; c < CH; ++c) {
+        float4 k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(ks + rows_at<HD>(tx + 16 * j, c));
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(qs + (ty * RT + i) * HD + ((c ^ (ty & 7)) << 2));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = fmaf(q.x, k[j].x, s[i][j]);
+            s[i][j] = fmaf(q.y, k[j].y, s[i][j]);
+            s[i][j] = fmaf(q.z, k[j].z, s[i][j]);
+            s[i][j] = fmaf(q.w, k[j].w, s[i][j]);
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const int row = i0 + ((ty * RT + i) >> a.g_shift);
@@ -184,7 +260,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
         float mx = kKvLeast;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int t = t0 + 4 * tx + j;
+          const int t = t0 + tx + 16 * j;
           seen[j] = !edge || (row < p.n && t < p.end && row_sees(words, row, t, p.base, p.n));
           s[i][j] *= a.c;
           if (seen[j]) mx = fmaxf(mx, s[i][j]);
@@ -199,7 +275,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
           const float e = seen[j] ? exp2f(s[i][j] - mn) : 0.0f;
           sum += e;
           // (-1: unseen, so that 0 times an entry that is not finite is left out)
-          ps[(4 * tx + j) * ROWS + ty * RT + i] = seen[j] ? e : -1.0f;
+          ps[(ty * RT + i) * PP + tx + 16 * j] = seen[j] ? e : -1.0f;
         }
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -210,38 +286,37 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
           for (int e = 0; e < 4; ++e) o[i][c][e] *= alpha;
       }
       __syncwarp();   // a warp reads back only its own pairs
-      const int slots = min(kRowsStep, p.end - t0);
       auto values = [&](auto checked) {
-#pragma unroll 4
-        for (int t = 0; t < slots; ++t) {
-          float w[RT];
-          if constexpr (RT == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(ps + t * ROWS + 4 * ty);
-            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-          } else {
-            w[0] = ps[t * ROWS + ty];
-          }
+#pragma unroll 2
+        for (int t = 0; t < kRowsStep; t += 4) {
+          float w[RT][4];
 #pragma unroll
-          for (int c = 0; c < OC; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(vs + t * HD + 64 * c + 4 * tx);
+          for (int i = 0; i < RT; ++i)
+            *reinterpret_cast<float4*>(w[i]) = *reinterpret_cast<const float4*>(ps + (ty * RT + i) * PP + t);
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              if (decltype(checked)::value && w[i] == -1.0f) continue;
-              o[i][c][0] = fmaf(w[i], v.x, o[i][c][0]);
-              o[i][c][1] = fmaf(w[i], v.y, o[i][c][1]);
-              o[i][c][2] = fmaf(w[i], v.z, o[i][c][2]);
-              o[i][c][3] = fmaf(w[i], v.w, o[i][c][3]);
+          for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int c = 0; c < OC; ++c) {
+              const float4 v = *reinterpret_cast<const float4*>(vs + rows_at<HD>(t + y, 16 * c + tx));
+#pragma unroll
+              for (int i = 0; i < RT; ++i) {
+                if (decltype(checked)::value && w[i][y] == -1.0f) continue;
+                o[i][c][0] = fmaf(w[i][y], v.x, o[i][c][0]);
+                o[i][c][1] = fmaf(w[i][y], v.y, o[i][c][1]);
+                o[i][c][2] = fmaf(w[i][y], v.z, o[i][c][2]);
+                o[i][c][3] = fmaf(w[i][y], v.w, o[i][c][3]);
+              }
             }
-          }
         }
       };
       if (edge) values(Flag<true>{});
       else values(Flag<false>{});
+      __syncthreads();   // the stage is free for the step after the next
     }
     // ---- results, or a piece of them
     const bool whole = p.c_first == p.c_last;
     const int slot = (int)blockIdx.x == p.c_first ? 1 : 0;
-    const int valid = min(ROWS, (p.n - i0) << a.g_shift), G = 1 << a.g_shift;
+    const int valid = min(ROWS, (p.n - i0) << a.g_shift);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int r = ty * RT + i;
@@ -251,7 +326,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
       for (int c = 0; c < OC; ++c) {
         const float4 x = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
         if (whole) {
-          rows_finish<T, HD>(a, row, 16 * c + tx, x, m[i], l[i]);
+          rows_finish<float, HD>(a, row, 16 * c + tx, x, m[i], l[i]);
         } else {
           float* pr = a.part + ((2ll * blockIdx.x + slot) * ROWS + r) * (HD + 4);
           *reinterpret_cast<float4*>(pr + 64 * c + 4 * tx) = x;
@@ -264,6 +339,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
       a.meta[2 * blockIdx.x + 1] = make_int4(p.o0 + i0, 0, 0, 0);
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Joins the pieces of the segments that span thread blocks: thread block (x,
@@ -396,13 +472,13 @@ static cudaError_t rows_join_launch(cudaStream_t s, const RowsArgs& a, int grid,
 
 template <int HD, int RT>
 static cudaError_t rows_attn_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
-  using S = RowsShape<HD, RT>;
-  cudaError_t e = ensure_smem((const void*)rows_attn_kernel<float, HD, RT>, S::kBytes);
+  using S = AttnShape<HD, RT>;
+  cudaError_t e = ensure_smem((const void*)rows_attn_kernel<HD, RT>, S::kBytes);
   if (e != cudaSuccess) return e;
   const SegShape sh{(RT == 1 ? 4 : 6) - a.g_shift, 6, 2};   // 16 or 64 pairs, 64 slots
   static_assert(S::kRows == (RT == 1 ? 16 : 64) && kRowsStep == 64, "shifts");
-  const int grid = (RT == 1 ? 2 : 1) * ctx->num_sms;
-  e = launch_pdl(rows_attn_kernel<float, HD, RT>, dim3(grid), dim3(kRowsThreads), S::kBytes, s, a, sh);
+  const int grid = (HD == 64 ? 2 : 1) * ctx->num_sms;   // what shared memory holds
+  e = launch_pdl(rows_attn_kernel<HD, RT>, dim3(grid), dim3(kRowsThreads), S::kBytes, s, a, sh);
   return e != cudaSuccess ? e : rows_join_launch<float, HD>(s, a, grid, S::kRows);
 }
 static cudaError_t launch_rows_attn(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
