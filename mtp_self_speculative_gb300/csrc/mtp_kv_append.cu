@@ -56,35 +56,49 @@ __device__ __forceinline__ void pair_at(int j, int rd, int layout, int& ia, int&
 
 // Sixteen elements of a head, x[e] and x[8 + e] the members of pair e.  VEC:
 // rows on 16 bytes and rd a multiple of 16; then a unit is two runs of eight
-// (half layout, rotating) or one of sixteen.
-template <typename T, bool VEC>
-__device__ __forceinline__ void unit_load(const T* head, int u, int rd, int layout, float (&x)[16]) {
-  if constexpr (VEC) {
-    constexpr int N = 16 / sizeof(T);
-    const bool split = layout == MTP_ROPE_HALF && 8 * u < rd / 2;
-    const T* pa = head + (split ? 8 * u : 16 * u);
-    const T* pb = split ? pa + rd / 2 : pa + 8;
-    float y[16];
+// (half layout, rotating) or one of sixteen, and is fetched first and widened
+// later, so that a thread has the next head's on its way.
+template <typename T, bool VEC> struct Unit {
+  static constexpr int N = 16 / sizeof(T);
+  uint4 v[VEC ? 16 / N : 1];
+  float f[VEC ? 1 : 16];
+  __device__ __forceinline__ void load(const T* head, int u, int rd, int layout) {
+    if constexpr (VEC) {
+      const bool split = layout == MTP_ROPE_HALF && 8 * u < rd / 2;
+      const T* pa = head + (split ? 8 * u : 16 * u);
+      const T* pb = split ? pa + rd / 2 : pa + 8;
 #pragma unroll
-    for (int i = 0; i < 8; i += N) {
-      widen16<T>(*reinterpret_cast<const uint4*>(pa + i), y + i);
-      widen16<T>(*reinterpret_cast<const uint4*>(pb + i), y + 8 + i);
-    }
+      for (int i = 0; i < 8; i += N) {
+        v[i / N] = *reinterpret_cast<const uint4*>(pa + i);
+        v[(8 + i) / N] = *reinterpret_cast<const uint4*>(pb + i);
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = split ? y[e] : y[2 * e];
-      x[8 + e] = split ? y[8 + e] : y[2 * e + 1];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      int ia, ib;
-      pair_at(8 * u + e, rd, layout, ia, ib);
-      x[e] = elem<T>(head + ia);
-      x[8 + e] = elem<T>(head + ib);
+      for (int e = 0; e < 8; ++e) {
+        int ia, ib;
+        pair_at(8 * u + e, rd, layout, ia, ib);
+        f[e] = elem<T>(head + ia);
+        f[8 + e] = elem<T>(head + ib);
+      }
     }
   }
-}
+  __device__ __forceinline__ void get(int u, int rd, int layout, float (&x)[16]) const {
+    if constexpr (VEC) {
+      const bool split = layout == MTP_ROPE_HALF && 8 * u < rd / 2;
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < 16; i += N) widen16<T>(v[i / N], y + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = split ? y[e] : y[2 * e];
+        x[8 + e] = split ? y[8 + e] : y[2 * e + 1];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = f[e];
+    }
+  }
+};
 template <typename T, bool VEC>
 __device__ __forceinline__ void unit_store(T* head, int u, int rd, int layout, const float (&x)[16]) {
   if constexpr (VEC) {
@@ -210,44 +224,84 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
   }
   const int h0 = group * s.per, h1 = min(s.heads, h0 + s.per);
   const int rd = a.rd;
-  float2 cs[8];
+  // two pairs at a time: (a, b) become (a c - b s, b c + a s), as rope_first and
+  // rope_second round them
+  uint64_t cc[4], ss[4], wa[4], wb[4];
   const int pos = live && rd ? a.positions[t] : 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    cs[e] = 8 * u + e < rd / 2 ? rope_cos_sin(pos, tab.turns[8 * u + e], tab.magnitude) : make_float2(1.0f, 0.0f);
-  float w[16];
-  if (s.w) {
-    unit_load<T, false>((const T*)s.w, u, rd, tab.layout, w);
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    float2 c[2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = 1.0f;
+    for (int e = 0; e < 2; ++e) {
+      const int j = 8 * u + 2 * i + e;
+      c[e] = j < rd / 2 ? rope_cos_sin(pos, tab.turns[j], tab.magnitude) : make_float2(1.0f, 0.0f);
+    }
+    cc[i] = two(c[0].x, c[1].x);
+    ss[i] = two(c[0].y, c[1].y);
   }
-#pragma unroll 2
+  {
+    float w[16];
+    if (s.w) {
+      Unit<T, false> v;
+      v.load((const T*)s.w, u, rd, tab.layout);
+      v.get(u, rd, tab.layout, w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      wa[i] = s.w ? two(w[2 * i], w[2 * i + 1]) : 0ull;
+      wb[i] = s.w ? two(w[8 + 2 * i], w[9 + 2 * i]) : 0ull;
+    }
+  }
+  const bool turns = 8 * u < rd / 2;      // (a unit that turns in part has pairs with cosine 1 and sine 0)
+  // Each thread has its next head on its way.  (out may be x, so the compiler may
+  // not fetch it ahead of the store by itself; two or three heads ahead cost
+  // more in registers than they gain.)
+  const T* row = (const T*)s.x + (long long)(live ? t : 0) * s.stride;
+  Unit<T, VEC> ahead;
+  ahead.load(row + (long long)h0 * HD, u, rd, tab.layout);
   for (int h = h0; h < h1; ++h) {
     float x[16];
-    if (live) {
-      unit_load<T, VEC>((const T*)s.x + (long long)t * s.stride + (long long)h * HD, u, rd, tab.layout, x);
-    } else {
+    ahead.get(u, rd, tab.layout, x);
+    if (h + 1 < h1) ahead.load(row + (long long)(h + 1) * HD, u, rd, tab.layout);
+    uint64_t A[4], B[4];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      A[i] = two(x[2 * i], x[2 * i + 1]);
+      B[i] = two(x[8 + 2 * i], x[9 + 2 * i]);
     }
     if (s.w) {
-      float ss = 0.0f;
+      uint64_t q0 = mul2(A[0], A[0]), q1 = mul2(B[0], B[0]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int i = 1; i < 4; ++i) {
+        q0 = fma2(A[i], A[i], q0);
+        q1 = fma2(B[i], B[i], q1);
+      }
+      float lo, hi;
+      untwo(add2(q0, q1), lo, hi);
+      float sq = lo + hi;
 #pragma unroll
-      for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(ss * (1.0f / HD) + a.eps);
+      for (int o = 1; o < LPH; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      const float r = rsqrtf(sq * (1.0f / HD) + a.eps);
+      const uint64_t rr = two(r, r);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] *= r * w[e];
+      for (int i = 0; i < 4; ++i) {
+        A[i] = mul2(mul2(A[i], rr), wa[i]);
+        B[i] = mul2(mul2(B[i], rr), wb[i]);
+      }
     }
     if (!live) continue;
+    if (turns) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (8 * u + e >= rd / 2) continue;
-      const float p = x[e], y = x[8 + e];
-      x[e] = rope_first(p, y, cs[e]);
-      x[8 + e] = rope_second(p, y, cs[e]);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t p = fma2(A[i], cc[i], mul2(B[i], ss[i]) ^ 0x8000000080000000ull);   // minus
+        B[i] = fma2(B[i], cc[i], mul2(A[i], ss[i]));
+        A[i] = p;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      untwo(A[i], x[2 * i], x[2 * i + 1]);
+      untwo(B[i], x[8 + 2 * i], x[9 + 2 * i]);
     }
     if (CACHE && keys) {
       const long long at = at_s[tid / LPH] + (long long)h * kBlk * HD;
