@@ -82,17 +82,21 @@ class KVCache:
 
     def _checked_struct(self, ctx: "Context"):
         """(struct, B, n_q, n_kv, head_dim), with the checks of devices, types
-        and shapes; they run again when a field is another tensor, has other
-        storage or another size than when they last ran, and for another
-        context."""
+        and shapes; they run again when a field was assigned, has other storage
+        or another size than when they last ran (the block table: another shape
+        or layout), and for another context."""
+        done = self.__dict__.get("_checked")
+        if done is not None and done[1] is ctx.cfg and done[2] == ctx.device:
+            kp, vp, bt, sl, pe, ar = done[3]
+            if done[0] == (kp.data_ptr(), vp.data_ptr(), bt.data_ptr(), sl.data_ptr(), pe.data_ptr(),
+                           ar if ar is None else ar.data_ptr(), kp.nbytes, vp.nbytes, sl.nbytes, pe.nbytes,
+                           ar if ar is None else ar.nbytes, bt.shape) and bt.is_contiguous():
+                return done[4]
         kp, vp, bt, sl, pe, ar = fields = (self.k_pool, self.v_pool, self.block_table, self.seq_len, self.pending,
                                            self.arrive)
-        seen = (kp.data_ptr(), vp.data_ptr(), bt.data_ptr(), sl.data_ptr(), pe.data_ptr(), kp.shape, vp.shape, bt.shape,
-                sl.shape, pe.shape, None if ar is None else (ar.data_ptr(), ar.shape))
-        done = self.__dict__.get("_checked")
-        if (done is not None and done[0] == seen and done[1] is ctx.cfg and done[2] == ctx.device
-                and all(x is y for x, y in zip(done[3], fields)) and all(x is None or x.is_contiguous() for x in fields)):
-            return done[4]
+        seen = (kp.data_ptr(), vp.data_ptr(), bt.data_ptr(), sl.data_ptr(), pe.data_ptr(),
+                ar if ar is None else ar.data_ptr(), kp.nbytes, vp.nbytes, sl.nbytes, pe.nbytes,
+                ar if ar is None else ar.nbytes, bt.shape)
         c = ctx.cfg
         if kp.dim() != 4 or sl.dim() != 1 or bt.dim() != 2:
             raise ValueError("k_pool must be [num_blocks, n_kv, 16, head_dim], seq_len [B], block_table [B, max_blocks]")
@@ -105,6 +109,10 @@ class KVCache:
         got = (st, B, int(c.n_q_heads), int(c.n_kv_heads), int(c.head_dim))
         self.__dict__["_checked"] = (seen, c, ctx.device, fields, got)
         return got
+
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_checked", None)
+        object.__setattr__(self, name, value)
 
     def __getstate__(self):
         """A copy (copy.deepcopy, pickle) is checked for itself."""
@@ -754,21 +762,24 @@ def mtp_qk_norm_rope(ctx: Context, q: Optional[torch.Tensor], k: Optional[torch.
     one = q if q is not None else k
     if one is None:
         raise ValueError("neither q nor k")
-    T = int(one.shape[0])
-    side = []
-    for x, w, out, heads, name in ((q, q_weight, q_out, c.n_q_heads, "q"), (k, k_weight, k_out, c.n_kv_heads, "k")):
-        if x is None:
-            if w is not None or out is not None:
-                raise ValueError("%s_weight and %s_out need %s" % (name, name, name))
-            side += [None, 0, None, None, 0]
-            continue
-        xp, xs = _row_ptr(ctx, x, name, T, heads)
-        op, os_ = (xp, xs) if out is None or out is x else _row_ptr(ctx, out, name + "_out", T, heads)
-        side += [xp, xs, _dev_ptr(ctx, w, ctx.dtype, name + "_weight", (ctx.head_dim,)), op, os_]
+    T, one_head, dt = one.shape[0], (ctx.head_dim,), ctx.dtype
+    qp, qs, qw, qop, qos, kp, ks, kw, kop, kos = None, 0, None, None, 0, None, 0, None, None, 0
+    if q is not None:
+        qp, qs = _row_ptr(ctx, q, "q", T, c.n_q_heads)
+        qop, qos = (qp, qs) if q_out is None or q_out is q else _row_ptr(ctx, q_out, "q_out", T, c.n_q_heads)
+        qw = _dev_ptr(ctx, q_weight, dt, "q_weight", one_head)
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    if k is not None:
+        kp, ks = _row_ptr(ctx, k, "k", T, c.n_kv_heads)
+        kop, kos = (kp, ks) if k_out is None or k_out is k else _row_ptr(ctx, k_out, "k_out", T, c.n_kv_heads)
+        kw = _dev_ptr(ctx, k_weight, dt, "k_weight", one_head)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
     pp = _dev_ptr(ctx, positions, torch.int32, "positions", (T,))
     if T:
-        _check(_clib.mtp_qk_norm_rope(ctx.handle, _ctx_stream(ctx, stream), T, *side, eps, pp, rope),
-               "mtp_qk_norm_rope")
+        _check(_clib.mtp_qk_norm_rope(ctx.handle, _ctx_stream(ctx, stream), T, qp, qs, qw, qop, qos, kp, ks, kw, kop, kos,
+                                      eps, pp, rope), "mtp_qk_norm_rope")
     return (q if q_out is None else q_out), (k if k_out is None else k_out)
 
 
