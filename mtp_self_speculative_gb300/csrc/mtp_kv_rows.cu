@@ -5,11 +5,28 @@
 //   s_t = q[r, h] . K[t, g], c = scale * log2 e, m the running maximum;
 //   w[t, g] += sum_{r, h} 2^(c s_t - log2 e * lse[r, h]).
 //
-// The (row, query head) pairs that share a kv head are the rows of a tile; a
-// step takes 64 slots.  16 x 16 threads hold RT x 4 scores each and read both
-// operands from shared memory as float4 (queries and keys transposed), so that
-// for RT = 4 two shared loads feed sixteen multiply-adds and the float32 pipe is
-// the bound; RT = 1 serves decoding rows, which are bound by the cache's bytes.
+// The (row, query head) pairs that share a kv head are the rows of a tile;
+// segments are cut over the thread blocks and joined as on the tensor cores.
+//
+// Few pairs (up to 32): a call is bound by the cache's bytes, and what has to be
+// short is the chain from an entry's arrival to the next.  Each warp keeps a
+// softmax of its own over eight slots of a step, copies those itself and waits
+// for nobody: a ring of halves (a step's keys, a step's values) holds 192 KB.
+// Four lanes share a key and hold its parts in registers; three exchanges sum
+// four pairs' products over them, so that each lane ends with one pair's score.
+// The warps' results are joined once a segment.  32 requests of 0 to 4096
+// entries, 32 query and 8 kv heads of 128: 102 us, 5.2 TB/s of entries (386 us
+// when a tile's threads shared one softmax and met twice a step).  Tiles of 8
+// pairs run 16 warps at 128 registers, tiles of 32 run 8 at 255: for 4 pairs
+// that is 102 us against 131; 24 pairs take 86 us against 136 in tiles of 64.
+//
+// Many pairs: the float32 pipe is the bound.  16 x 16 threads hold 4 x 4 scores
+// each, entries come in two stages; 256 rows on 16000 entries: 2.22 ms, 30
+// TFLOP/s (tiles of 32 as above: 3.42 ms).
+//
+// Weights: keys stay in registers, sixteen slots a warp, and the rows pass;
+// 32 decoding requests as above 77 us (385 us with the keys in shared memory),
+// 256 rows on 16000 entries 1.15 ms (1.86 ms).
 #include <math.h>
 
 #include "mtp_kv16.cuh"
@@ -18,136 +35,312 @@ namespace mtp {
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsStep = 64;       // slots of a step
-constexpr int kRowsPitch = kRowsStep + 4;
+constexpr int kRowsPairs = 64;      // pairs of a tile
+constexpr int kWeightSlots = 128;   // slots of a thread block of the weights' kernel, sixteen a warp
+constexpr int kWeightPairs = 64;
 
 template <bool V> struct Flag { static constexpr bool value = V; };
 
-template <int HD, int RT>
-struct RowsShape {
-  static constexpr int kRows = 16 * RT;                    // pairs of a tile
-  static constexpr int kQ = HD * kRows, kK = HD * kRowsPitch;   // floats
-  static constexpr int kWeightBytes = (kQ + kK) * 4;
+// Few pairs: a ring of halves, each the keys or the values of a step.
+template <int HD, int PAIRS>
+struct FewShape {
+  static constexpr int kWarps = PAIRS == 8 ? 16 : 8, kThreads = 32 * kWarps, kStep = 8 * kWarps;
+  static constexpr int kHalf = kStep * HD, kRing = 49152 / kHalf;   // floats; halves
+  static constexpr int kQ = PAIRS * HD, kP = kWarps * PAIRS * 8;
+  static constexpr int kBytes = (kQ + kP + kRing * kHalf) * 4;
+  static_assert(kRing * kHalf >= kWarps * PAIRS * (HD + 2), "the warps' results are joined in the ring's place");
 };
-template <int HD, int RT>
-struct AttnShape {
-  static constexpr int kRows = 16 * RT;
-  static constexpr int kQ = HD * kRows, kP = kRows * (kRowsStep + 4);   // floats
+// Many pairs: two stages of keys and values.
+template <int HD>
+struct ManyShape {
+  static constexpr int kQ = HD * kRowsPairs, kP = kRowsPairs * (kRowsStep + 4);   // floats
   static constexpr int kBytes = (kQ + kP + 2 * 2 * kRowsStep * HD) * 4;
 };
 
-// Queries of a tile, transposed: qs[d][pair]; pairs past the request's rows are zero.
-template <typename T, int HD, int ROWS>
-__device__ __forceinline__ void load_queries(const RowsArgs& a, float* qs, int o0, int i0, int n, int g) {
-  const int G = 1 << a.g_shift;
-  for (int x = threadIdx.x; x < ROWS * (HD / 4); x += kRowsThreads) {
-    const int r = x % ROWS, d = x / ROWS * 4, i = i0 + (r >> a.g_shift);
-    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (i < n) {
-      const T* p = (const T*)a.q + (long long)(o0 + i) * a.q_stride + (long long)(g * G + (r & (G - 1))) * HD + d;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = elem<T>(p + e);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) qs[(d + e) * ROWS + r] = y[e];
-  }
-}
-
-// Entries of a step: keys transposed (ks[d][slot]) or values as they lie
-// (vs[slot][d]).  Slots from `end` on, and blocks outside the pool, are zero.
-template <typename T, int HD, bool TRANSPOSE>
-__device__ __forceinline__ void load_entries(const RowsArgs& a, const void* pool, float* dst, const int* blocks, int t0,
-                                             int end, int g) {
-  for (int x = threadIdx.x; x < kRowsStep * (HD / 4); x += kRowsThreads) {
-    int t, d;
-    if (TRANSPOSE) {   // a warp takes 8 slots x 4 quads: whole sectors, two lanes a bank
-      const int w = x >> 5, l = x & 31;
-      t = (w % (kRowsStep / 8)) * 8 + (l & 7);
-      d = ((w / (kRowsStep / 8)) * 4 + (l >> 3)) * 4;
-    } else {
-      t = x / (HD / 4);
-      d = x % (HD / 4) * 4;
-    }
-    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int blk = blocks[t >> 4];
-    if (t0 + t < end && blk >= 0) {
-      const T* p = (const T*)pool + (((long long)blk * a.n_kv + g) * kBlk + (t & 15)) * HD + d;
-      if constexpr (sizeof(T) == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(p);
-        y[0] = u.x; y[1] = u.y; y[2] = u.z; y[3] = u.w;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        y[0] = bf16_lo(u.x); y[1] = bf16_hi(u.x); y[2] = bf16_lo(u.y); y[3] = bf16_hi(u.y);
-      }
-    }
-    if (TRANSPOSE) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dst[(d + e) * kRowsPitch + t] = y[e];
-    } else {
-      *reinterpret_cast<float4*>(dst + t * HD + d) = make_float4(y[0], y[1], y[2], y[3]);
-    }
-  }
-}
-
-// The step's block ids (-1: outside the pool).
-__device__ __forceinline__ void load_blocks(const RowsArgs& a, int* blocks, int b, int t0, int end) {
-  if (threadIdx.x < kRowsStep / kBlk) {
-    const int t = t0 + threadIdx.x * kBlk;
-    int blk = -1;
-    if (t < end) {
-      blk = a.kv.block_table[(long long)b * a.kv.max_blocks + (t >> 4)];
-      if (blk < 0 || blk >= a.kv.num_blocks) {
-        set_error(a.err, MTP_ERR_CAPACITY);
-        blk = -1;
-      }
-    }
-    blocks[threadIdx.x] = blk;
-  }
-}
-
-// Scores of pairs RT ty .. and slots 4 tx ..
-template <int HD, int RT>
-__device__ __forceinline__ void tile_scores(const float* qs, const float* ks, int ty, int tx, float (&s)[RT][4]) {
-  constexpr int ROWS = 16 * RT;
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
-#pragma unroll 8
-  for (int d = 0; d < HD; ++d) {
-    float q[RT];
-    if constexpr (RT == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(qs + d * ROWS + 4 * ty);
-      q[0] = u.x; q[1] = u.y; q[2] = u.z; q[3] = u.w;
-    } else {
-      q[0] = qs[d * ROWS + ty];
-    }
-    const float4 k = *reinterpret_cast<const float4*>(ks + d * kRowsPitch + 4 * tx);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      s[i][0] = fmaf(q[i], k.x, s[i][0]);
-      s[i][1] = fmaf(q[i], k.y, s[i][1]);
-      s[i][2] = fmaf(q[i], k.z, s[i][2]);
-      s[i][3] = fmaf(q[i], k.w, s[i][3]);
-    }
-  }
-}
-
-// 16 bytes global -> shared; none of them (zeros) for bytes = 0.
+// 16 bytes global -> shared; none of them (zeros) unless `there`.
 __device__ __forceinline__ void rows_cp(float* dst, const float* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// Staged rows of HD floats: 16-byte chunk c of row r lies at chunk c ^ (r & 7),
-// so that eight lanes that read one chunk of eight rows meet no bank twice.
+// Staged rows of HD floats: 16-byte chunk c of row r lies at chunk c ^ (r & 7).
 template <int HD>
 __device__ __forceinline__ int rows_at(int r, int c) {
   return r * HD + ((c ^ (r & 7)) << 2);
 }
 
-template <int HD, int RT>
-__global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs a, const SegShape sh) {
-  using S = AttnShape<HD, RT>;
-  constexpr int ROWS = S::kRows, CH = HD / 4, PASS = kRowsThreads / CH;   // rows that the block copies at a time
+// Queries of a tile, a pair's row at a time; pairs past the request's rows are zero.
+// (SPREAD: four rows by four, 16-byte chunk c lies at chunk c ^ (r / 4 & 7).)
+template <int HD, int PAIRS, int THREADS, bool SPREAD>
+__device__ __forceinline__ void load_queries(const RowsArgs& a, float* qs, int o0, int i0, int n, int g) {
+  constexpr int CH = HD / 4;
+  const int G = 1 << a.g_shift;
+  for (int x = threadIdx.x; x < PAIRS * CH; x += THREADS) {
+    const int r = x / CH, c = x % CH, i = i0 + (r >> a.g_shift);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < n) {
+      const float* src = (const float*)a.q + (long long)(o0 + i) * a.q_stride + (long long)(g * G + (r & (G - 1))) * HD + c * 4;
+      if (a.q_vec) v = *reinterpret_cast<const float4*>(src);
+      else v = make_float4(src[0], src[1], src[2], src[3]);
+    }
+    *reinterpret_cast<float4*>(qs + r * HD + ((SPREAD ? c ^ (r / 4 & 7) : c) << 2)) = v;
+  }
+}
+
+// The slot of eight that a lane takes, together with three lanes beside it (chunks lane % 4, + 4, ...): lanes 8 j ..
+// 8 j + 7 read rows j and j + 4 of a stage, whose chunks lie in different banks.
+__device__ __forceinline__ int lane_slot(int lane) { return (lane >> 2 & 1) * 4 + (lane >> 3); }
+
+// Scores of four pairs (rows of qs from `q` on) and the NS keys of which this lane and the three beside it hold the
+// parts: lane % 4 = j gets pair j's.  Three exchanges sum four pairs over four lanes.
+template <int HD, int NS>
+__device__ __forceinline__ void four_scores(const float* q, const float4 (&k)[NS][HD / 16], int lane, float (&s)[NS]) {
+  uint64_t acc[NS][4];
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[n][j] = 0;   // two zeros
+#pragma unroll
+  for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = *reinterpret_cast<const float4*>(q + j * HD + ((lane & 3) + 4 * i) * 4);
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        acc[n][j] = fma2(two(x.x, x.y), two(k[n][i].x, k[n][i].y), acc[n][j]);
+        acc[n][j] = fma2(two(x.z, x.w), two(k[n][i].z, k[n][i].w), acc[n][j]);
+      }
+    }
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      untwo(acc[n][j], lo, hi);
+      y[j] = lo + hi;
+    }
+    const bool b0 = lane & 1, b1 = lane & 2;
+    const float e = (b0 ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1);
+    const float f = (b0 ? y[3] : y[2]) + __shfl_xor_sync(0xffffffffu, b0 ? y[2] : y[3], 1);
+    s[n] = (b1 ? f : e) + __shfl_xor_sync(0xffffffffu, b1 ? e : f, 2);
+  }
+}
+
+template <int HD, int PAIRS>
+__global__ void __launch_bounds__(FewShape<HD, PAIRS>::kThreads, 1) rows_few_kernel(const RowsArgs a, const SegShape sh) {
+  using S = FewShape<HD, PAIRS>;
+  constexpr int CH = HD / 4, NG = PAIRS / 4, RING = S::kRing, PASS = 32 / CH, STEP = S::kStep;
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int pre[kKvMaxB + 1];
+  __shared__ long long wsum[S::kWarps];
+  float* qs = smem;                       // [pairs][HD]
+  float* kv = qs + S::kQ + S::kP;         // [RING][STEP][HD]
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, G = 1 << a.g_shift;
+  float* ps = qs + S::kQ + w * (PAIRS * 8);   // this warp's, [pair][8 slots]
+  if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  Split sp;
+  if (!rows_split<S::kThreads>(a, SegUnits{a, sh}, sh.lead + 1, pre, wsum, sp)) return;
+  for (uint32_t u = sp.u0; u < sp.u1;) {
+    Piece p;
+    find_piece(a, sh, pre, sp, u, p);
+    u = p.next;
+    if (p.s_lo >= p.s_hi) continue;
+    const int i0 = p.tile << sh.rows, valid = min(PAIRS, (p.n - i0) << a.g_shift);
+    const int32_t* table = a.kv.block_table + (long long)p.b * a.kv.max_blocks;
+    // a warp copies its own eight slots, which lie in one block; its id is looked up a step ahead
+    int id = 0, id_v = 0;
+    auto look = [&](int step) {
+      const int t = step * STEP + w * 8;
+      id = step < p.s_hi && t < p.end ? table[t >> 4] : 0;
+    };
+    // unit h: the keys (h even) or values of step s_lo + h / 2
+    auto copy = [&](int h, int at) {
+      const int step = p.s_lo + (h >> 1);
+      if (step < p.s_hi) {
+        if (!(h & 1)) id_v = id;
+        const int t0 = step * STEP + w * 8;
+        const bool good = id_v >= 0 && id_v < a.kv.num_blocks;
+        const int live = good ? p.end - t0 : 0;
+        const int r0 = lane / CH, c = lane % CH;
+        float* dst = kv + at * S::kHalf + w * 8 * HD;
+        const float* src = (const float*)(h & 1 ? a.kv.v_pool : a.kv.k_pool) +
+                           (((long long)(good ? id_v : 0) * a.n_kv + p.g) * kBlk + (t0 & 15) + r0) * HD + c * 4;
+#pragma unroll
+        for (int x = 0; x < 8 / PASS; ++x) {
+          const int t = r0 + x * PASS;
+          rows_cp(dst + rows_at<HD>(t, c), src + x * PASS * HD, t < live);
+        }
+        if (!good && t0 < p.end && lane == 0) set_error(a.err, MTP_ERR_CAPACITY);
+        if (!(h & 1)) look(step + 1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look(p.s_lo);
+    __syncthreads();              // the last piece's results are read
+#pragma unroll
+    for (int x = 0; x < RING - 1; ++x) copy(x, x);
+    load_queries<HD, PAIRS, S::kThreads, false>(a, qs, p.o0, i0, p.n, p.g);
+    __syncthreads();
+    // o: four columns of every pair; m and l: lane % 4 = j has the maximum of pair 4 x + j, and its slot's share of the sum
+    float o[PAIRS][4], m[NG], l[NG];
+#pragma unroll
+    for (int x = 0; x < NG; ++x) {
+      m[x] = kKvLeast;
+      l[x] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    int at = 0;     // where unit h lies
+    // the next unit's place, which the last one leaves, is filled; then unit h is there
+    auto next = [&](int h) -> const float* {
+      __syncwarp();
+      copy(h + RING - 1, at == 0 ? RING - 1 : at - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+      __syncwarp();
+      const float* here = kv + at * S::kHalf + w * 8 * HD;
+      at = at == RING - 1 ? 0 : at + 1;
+      return here;
+    };
+    for (int step = p.s_lo; step < p.s_hi; ++step) {
+      const int t0 = step * STEP, h = 2 * (step - p.s_lo);
+      // slots that some row of the tile does not see: from the first new one that its first row may not see
+      const bool edge = t0 + STEP > p.base + (a.mask ? 0 : i0 + 1);
+      const float* ks = next(h);
+      const int sl = lane_slot(lane), t = t0 + w * 8 + sl;
+      float4 k[1][HD / 16];
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) k[0][i] = *reinterpret_cast<const float4*>(ks + rows_at<HD>(sl, (lane & 3) + 4 * i));
+#pragma unroll
+      for (int x = 0; x < NG; ++x) {
+        if (4 * x >= valid) break;
+        float s[1];
+        four_scores<HD, 1>(qs + 4 * x * HD, k, lane, s);
+        s[0] *= a.c;
+        bool seen = true;
+        if (edge) {
+          const int row = i0 + ((4 * x + (lane & 3)) >> a.g_shift);
+          const int32_t* words = a.mask && row < p.n ? a.mask + (long long)(p.o0 + row) * a.mask_words : nullptr;
+          seen = row < p.n && t < p.end && row_sees(words, row, t, p.base, p.n);
+        }
+        if (__any_sync(0xffffffffu, seen && s[0] > m[x])) {
+          float mx = seen ? s[0] : kKvLeast;
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          mx = fmaxf(m[x], mx);
+          const float alpha = exp2f(m[x] - mx);
+          m[x] = mx;
+          l[x] *= alpha;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f = __shfl_sync(0xffffffffu, alpha, j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * x + j][e] *= f;
+          }
+        }
+        const float e = seen ? exp2f(s[0] - m[x]) : 0.0f;
+        l[x] += e;
+        // (-1: unseen, so that 0 times an entry that is not finite is left out)
+        ps[(4 * x + (lane & 3)) * 8 + sl] = seen ? e : -1.0f;
+      }
+      const float* vs = next(h + 1);
+      auto values = [&](auto checked) {
+        // heads of 64 take four slots a half warp
+#pragma unroll
+        for (int h = 0; h < CH / 16; ++h) {
+          const int first = HD == 128 ? 4 * h : lane / CH * 4;
+          float4 v[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const float4*>(vs + rows_at<HD>(first + y, lane % CH));
+#pragma unroll
+          for (int x = 0; x < NG; ++x) {
+            if (4 * x >= valid) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float e[4];
+              *reinterpret_cast<float4*>(e) = *reinterpret_cast<const float4*>(ps + (4 * x + j) * 8 + first);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if (decltype(checked)::value && e[y] == -1.0f) continue;
+                o[4 * x + j][0] = fmaf(e[y], v[y].x, o[4 * x + j][0]);
+                o[4 * x + j][1] = fmaf(e[y], v[y].y, o[4 * x + j][1]);
+                o[4 * x + j][2] = fmaf(e[y], v[y].z, o[4 * x + j][2]);
+                o[4 * x + j][3] = fmaf(e[y], v[y].w, o[4 * x + j][3]);
+              }
+            }
+          }
+        }
+      };
+      if (edge) values(Flag<true>{});
+      else values(Flag<false>{});
+    }
+    // ---- the warps' results joined, in the ring's place
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* os = kv;                                        // [warp][pair][HD]
+    float* ml = kv + S::kWarps * PAIRS * HD;         // [warp][pair][2]
+#pragma unroll
+    for (int x = 0; x < NG; ++x) {
+      if (4 * x >= valid) break;
+      float sum = l[x];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane < 4) *reinterpret_cast<float2*>(ml + (w * PAIRS + 4 * x + lane) * 2) = make_float2(m[x], sum);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float4 y = make_float4(o[4 * x + j][0], o[4 * x + j][1], o[4 * x + j][2], o[4 * x + j][3]);
+        if (HD == 64) {
+          y.x += __shfl_xor_sync(0xffffffffu, y.x, 16);
+          y.y += __shfl_xor_sync(0xffffffffu, y.y, 16);
+          y.z += __shfl_xor_sync(0xffffffffu, y.z, 16);
+          y.w += __shfl_xor_sync(0xffffffffu, y.w, 16);
+        }
+        if (lane < CH) *reinterpret_cast<float4*>(os + (w * PAIRS + 4 * x + j) * HD + lane * 4) = y;
+      }
+    }
+    __syncthreads();
+    const bool whole = p.c_first == p.c_last;
+    const int slot = (int)blockIdx.x == p.c_first ? 1 : 0;
+    for (int x = tid; x < valid * CH; x += S::kThreads) {
+      const int r = x / CH, c = x % CH;
+      float M = kKvLeast, L = 0.0f;
+#pragma unroll
+      for (int y = 0; y < S::kWarps; ++y) M = fmaxf(M, ml[(y * PAIRS + r) * 2]);
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int y = 0; y < S::kWarps; ++y) {
+        const float2 z = *reinterpret_cast<const float2*>(ml + (y * PAIRS + r) * 2);
+        const float4 v = *reinterpret_cast<const float4*>(os + (y * PAIRS + r) * HD + c * 4);
+        const float f = exp2f(z.x - M);
+        L = fmaf(z.y, f, L);
+        sum.x = fmaf(v.x, f, sum.x);
+        sum.y = fmaf(v.y, f, sum.y);
+        sum.z = fmaf(v.z, f, sum.z);
+        sum.w = fmaf(v.w, f, sum.w);
+      }
+      if (whole) {
+        const long long row = (long long)(p.o0 + i0 + (r >> a.g_shift)) * (a.n_kv << a.g_shift) + p.g * G + (r & (G - 1));
+        rows_finish<float, HD>(a, row, c, sum, M, L);
+      } else {
+        float* pr = a.part + ((2ll * blockIdx.x + slot) * PAIRS + r) * (HD + 4);
+        *reinterpret_cast<float4*>(pr + 4 * c) = sum;
+        if (c == 0) *reinterpret_cast<float2*>(pr + HD) = make_float2(M, L);
+      }
+    }
+    if (tid == 0 && slot == 1 && !whole) {
+      a.meta[2 * blockIdx.x] = make_int4(p.c_last - p.c_first + 1, p.c_first, valid, p.g);
+      a.meta[2 * blockIdx.x + 1] = make_int4(p.o0 + i0, 0, 0, 0);
+    }
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kRowsThreads) rows_many_kernel(const RowsArgs a, const SegShape sh) {
+  using S = ManyShape<HD>;
+  constexpr int RT = 4, ROWS = kRowsPairs, CH = HD / 4, PASS = kRowsThreads / CH;   // rows that the block copies at a time
   constexpr int OC = HD / 64;     // float4 columns of the result per thread and pair
   constexpr int PP = kRowsStep + 4;
   extern __shared__ __align__(16) float smem[];
@@ -198,17 +391,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_attn_kernel(const RowsArgs 
     __syncthreads();              // the last piece's tiles are done with
     copy(p.s_lo, 0);
     look(p.s_lo + 1);
-    // queries, a pair's row at a time; pairs past the request's rows are zero
-    for (int x = tid; x < ROWS * CH; x += kRowsThreads) {
-      const int r = x / CH, c = x % CH, i = i0 + (r >> a.g_shift);
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (i < p.n) {
-        const float* src = (const float*)a.q + (long long)(p.o0 + i) * a.q_stride + (long long)(p.g * G + (r & (G - 1))) * HD + c * 4;
-        if (a.q_vec) v = *reinterpret_cast<const float4*>(src);
-        else v = make_float4(src[0], src[1], src[2], src[3]);
-      }
-      *reinterpret_cast<float4*>(qs + r * HD + ((c ^ (r / RT & 7)) << 2)) = v;
-    }
+    load_queries<HD, ROWS, kRowsThreads, true>(a, qs, p.o0, i0, p.n, p.g);
     float o[RT][OC][4], m[RT], l[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -384,22 +567,16 @@ __global__ void __launch_bounds__(kRowsJoinThreads) rows_join_kernel(const RowsA
   }
 }
 
-// Thread block (step of slots, kv head, request): the weights of 64 entries, its
-// keys kept in shared memory, all rows that may see them in tiles of 64 pairs.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kRowsThreads) rows_weights_kernel(const RowsArgs a) {
-  constexpr int RT = 4, ROWS = 64;
-  using S = RowsShape<HD, RT>;
-  extern __shared__ __align__(16) float smem[];
-  __shared__ int blocks[kRowsStep / kBlk];
-  __shared__ float lse_s[ROWS];
-  __shared__ float sums[16][kRowsStep + 1];
-  float* qs = smem;
-  float* ks = qs + S::kQ;
+// Thread block (128 slots, kv head, request): the weights of its entries, whose
+// keys stay in registers; all rows that may see them pass in tiles of 64 pairs.
+template <int HD>
+__global__ void __launch_bounds__(kRowsThreads, 2) rows_weights_kernel(const RowsArgs a) {
+  extern __shared__ __align__(16) float qs[];   // [pairs][HD]
+  __shared__ float lse_s[kWeightPairs];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int t0 = blockIdx.x * kRowsStep, g = blockIdx.y, b = blockIdx.z, G = 1 << a.g_shift;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int t0 = blockIdx.x * kWeightSlots, g = blockIdx.y, b = blockIdx.z, G = 1 << a.g_shift;
   int bad = 0;
   for (int x = tid; x < a.B; x += kRowsThreads) {
     const int r0 = a.row_offsets[x], r1 = a.row_offsets[x + 1];
@@ -418,47 +595,62 @@ __global__ void __launch_bounds__(kRowsThreads) rows_weights_kernel(const RowsAr
     return;
   }
   if (t0 >= L) return;
-  load_blocks(a, blocks, b, t0, L);
-  __syncthreads();
-  load_entries<T, HD, true>(a, a.kv.k_pool, ks, blocks, t0, L, g);
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // a warp's sixteen slots are a block; a lane has parts of two of them
+  const int tw = t0 + w * kBlk, sl = lane_slot(lane);
+  int blk = -1;
+  if (tw < L) {
+    blk = a.kv.block_table[(long long)b * a.kv.max_blocks + tw / kBlk];
+    if (blk < 0 || blk >= a.kv.num_blocks) {
+      if (lane == 0) set_error(a.err, MTP_ERR_CAPACITY);
+      blk = -1;
+    }
+  }
+  float4 k[2][HD / 16];
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i) {
+      k[x][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (blk >= 0)   // (slots from L on are read and not used)
+        k[x][i] = reinterpret_cast<const float4*>((const float*)a.kv.k_pool + (((long long)blk * a.n_kv + g) * kBlk + sl + 8 * x) * HD)[(lane & 3) + 4 * i];
+    }
+  float acc[2] = {0.0f, 0.0f};
   const int row0 = a.mask ? 0 : max(0, t0 - base);   // rows before it see none of these slots
-  const int tile_rows = ROWS >> a.g_shift;
+  const int tile_rows = kWeightPairs >> a.g_shift;
   for (int i0 = row0; i0 < n; i0 += tile_rows) {
+    const int valid = min(kWeightPairs, (n - i0) << a.g_shift);
     __syncthreads();
-    load_queries<T, HD, ROWS>(a, qs, o0, i0, n, g);
-    if (tid < ROWS) {
+    load_queries<HD, kWeightPairs, kRowsThreads, false>(a, qs, o0, i0, n, g);
+    if (tid < kWeightPairs) {
       const int i = i0 + (tid >> a.g_shift);
       const float l = i < n ? a.lse[(long long)(o0 + i) * (a.n_kv << a.g_shift) + g * G + (tid & (G - 1))] : -INFINITY;
       lse_s[tid] = l == -INFINITY ? INFINITY : l * kLog2e;   // a row that sees nothing weighs nothing
     }
     __syncthreads();
-    float s[RT][4];
-    tile_scores<HD, RT>(qs, ks, ty, tx, s);
-    const bool edge = t0 + kRowsStep > base + (a.mask ? 0 : i0 + 1) || i0 + tile_rows > n;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int r = ty * RT + i, row = i0 + (r >> a.g_shift);
+    const bool edge = t0 + kWeightSlots > base + (a.mask ? 0 : i0 + 1) || valid % 4;
+    for (int x = 0; x < valid; x += 4) {
+      float s[2];
+      four_scores<HD, 2>(qs + x * HD, k, lane, s);
+      const int r = x + (lane & 3), row = i0 + (r >> a.g_shift);
+      const float l = lse_s[r];
       const int32_t* words = a.mask && row < n ? a.mask + (long long)(o0 + row) * a.mask_words : nullptr;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t0 + 4 * tx + j;
-        if (!edge || (row < n && t < L && row_sees(words, row, t, base, n)))
-          acc[j] += exp2f(fmaf(s[i][j], a.c, -lse_s[r]));
+      for (int y = 0; y < 2; ++y) {
+        const int t = tw + sl + 8 * y;
+        if (!edge || (row < n && t < L && row_sees(words, row, t, base, n))) acc[y] += exp2f(fmaf(s[y], a.c, -l));
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) sums[ty][4 * tx + j] = acc[j];
-  __syncthreads();
-  const int t = t0 + tid;
-  if (tid < kRowsStep && t < L && blocks[tid >> 4] >= 0) {
-    float x = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x += sums[i][tid];
-    const long long at = ((long long)blocks[tid >> 4] * a.n_kv + g) * kBlk + (t & 15);
+  for (int y = 0; y < 2; ++y) {
+    acc[y] += __shfl_xor_sync(0xffffffffu, acc[y], 1);
+    acc[y] += __shfl_xor_sync(0xffffffffu, acc[y], 2);
+  }
+  const int t = tw + sl + 8 * (lane & 1);
+  if ((lane & 2) == 0 && t < L && blk >= 0) {
+    const long long at = ((long long)blk * a.n_kv + g) * kBlk + (t & 15);
     if (MTP_IN_BOUNDS(a.err, at, (long long)a.kv.num_blocks * a.n_kv * kBlk))
-      a.weights[at] = (t < first ? a.weights[at] : 0.0f) + x;
+      a.weights[at] = (t < first ? a.weights[at] : 0.0f) + (lane & 1 ? acc[1] : acc[0]);
   }
 }
 
@@ -470,16 +662,22 @@ static cudaError_t rows_join_launch(cudaStream_t s, const RowsArgs& a, int grid,
   return launch_pdl(rows_join_kernel<T, HD>, dim3(grid, groups), dim3(kRowsJoinThreads), 0, s, a, pairs);
 }
 
-template <int HD, int RT>
+template <int HD>
 static cudaError_t rows_attn_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
-  using S = AttnShape<HD, RT>;
-  cudaError_t e = ensure_smem((const void*)rows_attn_kernel<HD, RT>, S::kBytes);
-  if (e != cudaSuccess) return e;
-  const SegShape sh{(RT == 1 ? 4 : 6) - a.g_shift, 6, 2};   // 16 or 64 pairs, 64 slots
-  static_assert(S::kRows == (RT == 1 ? 16 : 64) && kRowsStep == 64, "shifts");
-  const int grid = (HD == 64 ? 2 : 1) * ctx->num_sms;   // what shared memory holds
-  e = launch_pdl(rows_attn_kernel<HD, RT>, dim3(grid), dim3(kRowsThreads), S::kBytes, s, a, sh);
-  return e != cudaSuccess ? e : rows_join_launch<float, HD>(s, a, grid, S::kRows);
+  const int pairs = (int)((long long)a.max_rows << a.g_shift < kRowsPairs ? a.max_rows << a.g_shift : kRowsPairs);
+  const int tile = pairs <= 8 ? 8 : pairs <= 32 ? 32 : kRowsPairs;
+  const int grid = (tile == kRowsPairs && HD == 64 ? 2 : 1) * ctx->num_sms;   // what shared memory holds
+  const auto go = [&](auto kernel, int threads, int bytes, int step) {
+    const cudaError_t e = ensure_smem((const void*)kernel, bytes);
+    const SegShape sh{(tile == 8 ? 3 : tile == 32 ? 5 : 6) - a.g_shift, step, 2};
+    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(threads), bytes, s, a, sh);
+  };
+  static_assert(FewShape<HD, 8>::kStep == 128 && FewShape<HD, 32>::kStep == 64 && kRowsStep == 64 && kRowsPairs == 64, "shifts");
+  cudaError_t e;
+  if (tile == 8) e = go(rows_few_kernel<HD, 8>, FewShape<HD, 8>::kThreads, FewShape<HD, 8>::kBytes, 7);
+  else if (tile == 32) e = go(rows_few_kernel<HD, 32>, FewShape<HD, 32>::kThreads, FewShape<HD, 32>::kBytes, 6);
+  else e = go(rows_many_kernel<HD>, kRowsThreads, ManyShape<HD>::kBytes, 6);
+  return e != cudaSuccess ? e : rows_join_launch<float, HD>(s, a, grid, tile);
 }
 static cudaError_t launch_rows_attn(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
   ctx->launches += 2;
@@ -489,18 +687,16 @@ static cudaError_t launch_rows_attn(mtp_ctx* ctx, cudaStream_t s, const RowsArgs
     return ctx->cfg.head_dim == 128 ? rows_join_launch<uint16_t, 128>(s, a, ctx->num_sms, kAtPairs)
                                     : rows_join_launch<uint16_t, 64>(s, a, ctx->num_sms, kAtPairs);
   }
-  const bool few = (a.max_rows << a.g_shift) <= 16;
-  if (ctx->cfg.head_dim == 128) return few ? rows_attn_launch<128, 1>(ctx, s, a) : rows_attn_launch<128, 4>(ctx, s, a);
-  return few ? rows_attn_launch<64, 1>(ctx, s, a) : rows_attn_launch<64, 4>(ctx, s, a);
+  return ctx->cfg.head_dim == 128 ? rows_attn_launch<128>(ctx, s, a) : rows_attn_launch<64>(ctx, s, a);
 }
 
 template <int HD>
 static cudaError_t rows_weights_launch(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
-  const int smem = RowsShape<HD, 4>::kWeightBytes;
-  const cudaError_t e = ensure_smem((const void*)rows_weights_kernel<float, HD>, smem);
+  const int smem = kWeightPairs * HD * 4;
+  const cudaError_t e = ensure_smem((const void*)rows_weights_kernel<HD>, smem);
   if (e != cudaSuccess) return e;
-  const int tiles = (int)(((long long)a.kv.max_blocks * kBlk + kRowsStep - 1) / kRowsStep);
-  return launch_pdl(rows_weights_kernel<float, HD>, dim3(tiles, a.n_kv, a.B), dim3(kRowsThreads), smem, s, a);
+  const int tiles = (int)(((long long)a.kv.max_blocks * kBlk + kWeightSlots - 1) / kWeightSlots);
+  return launch_pdl(rows_weights_kernel<HD>, dim3(tiles, a.n_kv, a.B), dim3(kRowsThreads), smem, s, a);
 }
 static cudaError_t launch_rows_weights(mtp_ctx* ctx, cudaStream_t s, const RowsArgs& a) {
   ctx->launches++;
@@ -553,7 +749,7 @@ extern "C" {
 
 size_t mtp_kv_attention_workspace_bytes(const mtp_ctx* ctx) {
   if (!ctx) return 0;
-  const int pairs = ctx->cfg.dtype == MTP_DTYPE_BF16 ? kAtPairs : kRowsMaxBlocks * 64;   // of an SM's thread blocks
+  const int pairs = ctx->cfg.dtype == MTP_DTYPE_BF16 ? kAtPairs : kRowsMaxBlocks * kRowsPairs;   // of an SM's thread blocks
   return rows_meta_bytes(ctx) + rows_pre_bytes(ctx) + kPlanBytes + (size_t)2 * ctx->num_sms * pairs * (ctx->cfg.head_dim + 4) * sizeof(float);
 }
 
