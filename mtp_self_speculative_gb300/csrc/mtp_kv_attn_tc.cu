@@ -29,19 +29,19 @@
 // equal shares, found on the device from the lengths; a segment that spans
 // thread blocks leaves its pieces in the workspace for rows_join_kernel.
 //
-// What bounds it: for few rows the cache's bytes (64 requests of 4096 entries: 170
-// us, 6.3 TB/s).  For many the chain of a group's step: its products (two of 512
-// cycles at the pipe's peak) and its softmax (1150 cycles for 128 scores a
+// What bounds it: for few rows the cache's bytes (64 requests of 4096 entries: 167
+// us, 6.4 TB/s).  For many the chain of a group's step: its products (two of 512
+// cycles at the pipe's peak) and its softmax (1000 cycles for 128 scores a
 // thread) follow one another, and the other group fills no more than its own two
-// products of the pipe meanwhile; a step of both takes 3150 cycles against 2048
-// of products.  8192 rows, 32 query heads of 128: 350 us, 1570 TFLOP/s; 1024 rows
-// on 32768 entries 1530 TFLOP/s.  A segment costs some 8000 cycles besides its
-// steps (the last products, 128 x 128 results a group to be scaled and written,
-// the step that is partly seen), so short contexts pay more: 16 chunks of 512
-// rows on up to 1500 entries take 141 us.  Tried and not kept: results staged and
-// stored by the copy engine (the end of a segment 4000 -> 3100 cycles, but a step
-// slower, 357 us), first and partly seen steps in one pass as well (short
-// contexts 141 -> 138 us, long ones 359 -> 367 us).
+// products of the pipe meanwhile; a step of both takes 3100 cycles against 2048
+// of products.  8192 rows, 32 query heads of 128: 335 us, 1640 TFLOP/s; 1024 rows
+// on 32768 entries 361 us, 1550 TFLOP/s.  A segment costs some 6500 cycles besides
+// its steps (the last products, 128 x 128 results a group to be scaled and
+// written, the first step and the one that is partly seen), so short contexts pay
+// more: 16 chunks of 512 rows on up to 1500 entries take 128 to 138 us.  Tried and
+// not kept: results staged in a fifth tile's place and stored by the copy engine
+// (the same times, long contexts 361 -> 370 us), first and partly seen steps in
+// the pass of the others (its code then runs slower, 350 -> 357 us at the time).
 #include <cuda.h>
 #include <math.h>
 
@@ -57,8 +57,8 @@ template <int HD>
 struct AtShape {
   static constexpr int kHalves = HD / 64;
   static constexpr int kTile = kAtStep * HD * 2;              // bytes of a K or V tile, and of 128 pairs' queries
-  // Five tiles of 32 KB are what fits (four would do: a prompt of 8192 takes 350
-  // us with either).
+  // Five tiles of 32 KB are what fits.  (Four: 1024 rows on 32768 entries 370 instead
+  // of 361 us, a prompt of 8192 338 instead of 335.)
   static constexpr int kStages = HD == 128 ? 5 : 8;
   static constexpr int kBytes = 2 * kTile + kStages * kTile;
 };
@@ -558,71 +558,78 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
           }
         }
         if (!done) {
+          sum[0] = sum[1] = 0ull;
           // The first step, steps that some row sees only part of, and those that
-          // move the reference: the maximum first, then the weights, in little
-          // code.  The weights of columns 32 c .. go, two a word, over columns
-          // 16 c .., which are done with.
-          uint32_t v[32], v2[32];
-          auto hide = [&](uint32_t (&v)[32], int c) {
-            const uint32_t bits = at_seen(words, last, t0 + 32 * c, base, rows);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : 0xFF800000u;
-          };
-          auto load = [&](int c) {   // columns 32 c .. 32 c + 63
-            tmem_ld(s_at + 32 * c, v);
-            tmem_ld(s_at + 32 * c + 32, v2);
-            tmem_wait_ld();
-            tmem_ready(v);
-            tmem_ready(v2);
-            if (part) {
-              hide(v, c);
-              hide(v2, c + 1);
-            }
-          };
+          // move the reference: 32 columns at a time in little code (fetching
+          // instructions that a segment runs once or twice costs more than running
+          // them), the maximum before the weights, which go, two a word, over columns
+          // 16 c .. that are done with.  Where a later quarter moves the reference, the
+          // weights written before move with it: by whole powers of two, so
+          // that they are not rounded again.
           mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            load(c);
-            most(v);
-            most(v2);
-          }
-          const float t = top();
-          if (x == 0) {
-            m = t;
-          } else if (__any_sync(0xffffffffu, t > m + kAtSlack)) {
-            const float mn = t > m + kAtSlack ? t : m, alpha = exp2_fast(m - mn);
-            m = mn;
-            l *= alpha;
-            // (S_w full: the products into O_w before it have ended)
-#pragma unroll 1
-            for (int c0 = 0; c0 < HD; c0 += 32) {
-              tmem_ld(o_at + w * HD + c0, v);
-              tmem_wait_ld();
-              tmem_ready(v);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld(s_at + 32 * c, v);
+            tmem_wait_ld();
+            tmem_ready(v);
+            if (part) {
+              const uint32_t bits = at_seen(words, last, t0 + 32 * c, base, rows);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tmem_st(o_at + w * HD + c0, v);
+              for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : 0xFF800000u;
             }
-          }
-          // from kAtCoarse on the reference is rounded to whole units: scores are
-          // then rounded like it before it is taken off
-          coarse = __any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast);
-          sum[0] = sum[1] = 0ull;
-          const float f = coarse ? 1.0f : a.c;
+            most(v);
+            const float t = top();
+            if (x == 0 && c == 0) {
+              m = t;
+            } else if (__any_sync(0xffffffffu, t > m + kAtSlack)) {
+              const float up = fmaxf(fabsf(m), fabsf(t)) < 1048576.0f ? m + ceilf(t - m) : t;   // (2^20: little rounding)
+              const float mn = t > m + kAtSlack ? up : m;
+              const float alpha = exp2_fast(m - mn);
+              const uint32_t f = pack2_bf16(alpha, alpha);
+              m = mn;
+              l *= alpha;
+              sum[0] = mul2(sum[0], two(alpha, alpha));
+              sum[1] = mul2(sum[1], two(alpha, alpha));
+              tmem_wait_st();
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            load(c);
-            if (coarse) {
+              for (int d = 0; d < c; ++d) {
+                uint32_t o[16];
+                tmem_ld16(s_at + 16 * d, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c));
-                v2[e] = __float_as_uint(__fmul_rn(__uint_as_float(v2[e]), a.c));
+                for (int e = 0; e < 16; ++e) o[e] = mul_bf16x2(o[e], f);
+                tmem_st16(s_at + 16 * d, o);
+              }
+              // (S_w full: the products into O_w before it have ended)
+#pragma unroll 1
+              for (int c0 = 0; c0 < HD && x > 0; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_at + w * HD + c0, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16(o_at + w * HD + c0, o);
               }
             }
-            uint32_t pw[32];
-            weights(v, pw, two(f, f), two(-m, -m));
-            weights(v2, pw + 16, two(f, f), two(-m, -m));
-            tmem_st(s_at + 16 * c, pw);
+            // from kAtCoarse on the reference is rounded to whole units: scores are
+            // then rounded like it before it is taken off
+            coarse = __any_sync(0xffffffffu, fabsf(m) > kAtCoarse && m != kKvLeast);
+            const float f = coarse ? 1.0f : a.c;
+            if (coarse) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a.c));
+            }
+            const uint64_t cc = two(f, f), mm = two(-m, -m);
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float x0, x1;
+              untwo(fma2(two(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, mm), x0, x1);
+              x0 = exp2_fast(x0);
+              x1 = exp2_fast(x1);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(x0, x1));
+              pw[e / 2] = pack2_bf16(x0, x1);
+            }
+            tmem_st16(s_at + 16 * c, pw);
           }
         }
         float l0, l1;
@@ -672,11 +679,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       uint16_t* out = (uint16_t*)a.out + row * HD;
       const bool out32 = !((uintptr_t)a.out & 31);
       float* piece = p.slot < 0 ? nullptr : a.part + ((2ll * blockIdx.x + p.slot) * kAtPairs + pr) * (HD + 4);
+      uint32_t v[32];
+      tmem_ld(o_mine + c_lo, v);
 #pragma unroll 1
       for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-        uint32_t v[32];
         float y[32];
-        tmem_ld(o_mine + c0, v);
         tmem_wait_ld();
         tmem_ready(v);
 #pragma unroll
@@ -688,6 +695,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = y[e] * f0 + __uint_as_float(v[e]) * f1;
         }
+        if (c0 + 32 < c_hi) tmem_ld(o_mine + c0 + 32, v);
         if (dirty && live) {
           // what the row sees of the entries that were taken out
           for (int t = max(s_lo, p.edge) * kAtStep; t < min(p.end, (s_lo + n) * kAtStep); ++t) {
@@ -700,21 +708,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
               if ((vr[e] & 0x7F80u) == 0x7F80u) y[e] += elem<uint16_t>(vr + e);
           }
         }
-        if (!live) continue;
         if (piece) {   // (rows of HD + 4 floats: on 16 bytes)
+          if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(piece + c0 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(piece + c0 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          }
           continue;
         }
-        if (!MTP_IN_BOUNDS(a.err, row * HD + c0 + 31, (long long)a.T * (a.n_kv << a.g_shift) * HD)) continue;
+        uint32_t z[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = pack2_bf16(y[2 * e] * inv, y[2 * e + 1] * inv);
-        if (out32) {
-          st_global32(out + c0, v);
-          st_global32(out + c0 + 16, v + 8);
-        } else {
+        for (int e = 0; e < 16; ++e) z[e] = pack2_bf16(y[2 * e] * inv, y[2 * e + 1] * inv);
+        if (live && MTP_IN_BOUNDS(a.err, row * HD + c0 + 31, (long long)a.T * (a.n_kv << a.g_shift) * HD)) {
+          if (out32) {
+            st_global32(out + c0, z);
+            st_global32(out + c0 + 16, z + 8);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(out + c0 + 2 * e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(out + c0 + 2 * e) = make_uint4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+          }
         }
       }
       if (live && c_lo == 0 && piece) *reinterpret_cast<float2*>(piece + HD) = make_float2(m, l);
