@@ -98,7 +98,9 @@ __device__ __forceinline__ uint32_t ring_v(int j, int n) { return j == n - 1 ? 2
 template <int HD>
 struct AtShared {
   uint64_t full[AtShape<HD>::kStages], empty[AtShape<HD>::kStages];
-  uint64_t s_full[2], p_ready[2], q_full[2], q_empty[2], q_ready[2], scan, clean, merged, piece_full[2], piece_empty[2];
+  // (o_full: results of a segment.  Not a phase of s_full, as the next segment's scores are not waited for by anyone
+  // and could complete the next phase before a slow warp has seen that one.)
+  uint64_t s_full[2], o_full[2], p_ready[2], q_full[2], q_empty[2], q_ready[2], scan, clean, merged, piece_full[2], piece_empty[2];
   AtPiece piece[2];
   float ml[2][128][2];
   uint32_t tmem;
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sm.s_full[w], 1);
+      mbar_init(&sm.o_full[w], 1);
       mbar_init(&sm.p_ready[w], 4);
       mbar_init(&sm.q_ready[w], 4);
       mbar_init(&sm.q_full[w], 1);
@@ -362,12 +365,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
             if (!wait_ring(ring_k(j + 1))) break;
             scores(0, j + 1);
           }
-          mma_commit(&sm.s_full[0]);
+          mma_commit(more ? &sm.s_full[0] : &sm.o_full[0]);
           if (!wait_p(1)) break;
           values(1, j, j == 0);
           free_ring(ring_v(j, n));
           if (more) scores(1, j + 1);
-          mma_commit(&sm.s_full[1]);
+          mma_commit(more ? &sm.s_full[1] : &sm.o_full[1]);
           if (more) {
             free_ring(ring_k(j + 1));
             if (!wait_v(j + 1)) break;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
             scores(w, j + 2);
             free_ring(ring_k(j + 2));
           }
-          mma_commit(&sm.s_full[w]);
+          mma_commit(j + 2 < n ? &sm.s_full[w] : &sm.o_full[w]);
         }
       }
       if (!ok) break;
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256;
-    uint32_t s_count = 0, merges = 0;   // phases of s_full[w] and of merged
+    uint32_t s_count = 0, o_count = 0, merges = 0;   // phases of s_full[w], o_full[w] and merged
     bool ok = true;
     // Queries whose rows do not lie on 16 bytes: fetched by the groups themselves,
     // between two segments.
@@ -643,9 +646,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
       if (!ok) break;
       // ---- results: O_w of 128 pairs, or both groups' parts of the same pairs, half of the columns each
       if (mine > 0) {
-        ok = __all_sync(0xffffffffu, at_wait(&sm.s_full[w], s_count & 1, &sm.abort_flag));
+        ok = __all_sync(0xffffffffu, at_wait(&sm.o_full[w], o_count & 1, &sm.abort_flag));
         if (!ok) break;
-        ++s_count;
+        ++o_count;
       }
       float f0 = 1.0f, f1 = 0.0f;
       const bool both = split && n > 1;

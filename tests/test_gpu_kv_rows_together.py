@@ -339,3 +339,21 @@ def test_results_off_32_bytes_and_reused_workspaces(dtype):
     with pytest.raises(M.MTPError):
         M.mtp_kv_attention(ctx, kv, q, i32(off), bad, ws, 200)
     clean(ctx)
+
+
+@pytest.mark.parametrize("lens,new", [([30000], [1000]), ([900] * 8, [64] * 8), ([200] * 64, [1] * 64)])
+def test_many_calls_without_a_wait_between(lens, new):
+    """Calls queued one behind another, long and short segments: every wait in them ends, the results stay."""
+    M = M_()
+    rng = np.random.default_rng(12)
+    ctx = context(32, 8, 128, "bf16", max_batch=len(lens))
+    kv = pooled(ctx, lens, new, rng)
+    off = np.concatenate([[0], np.cumsum(new)])
+    q = torch.randn((int(off[-1]), 32, 128), device="cuda").bfloat16()
+    ws = M.AttentionWorkspace(ctx)
+    want, want_lse = attend(ctx, kv, q, off, max(new), ws=ws)
+    for _ in range(40):
+        M.mtp_kv_attention(ctx, kv, q, i32(off), want, ws, max(new), lse=want_lse)
+    out, lse = attend(ctx, kv, q, off, max(new), ws=ws)
+    clean(ctx)
+    assert same_bits(out, want) and same_bits(lse, want_lse)
