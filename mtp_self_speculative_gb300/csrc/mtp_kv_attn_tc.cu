@@ -41,7 +41,11 @@
 // more: 16 chunks of 512 rows on up to 1500 entries take 128 to 138 us.  Tried and
 // not kept: results staged in a fifth tile's place and stored by the copy engine
 // (the same times, long contexts 361 -> 370 us), first and partly seen steps in
-// the pass of the others (its code then runs slower, 350 -> 357 us at the time).
+// the pass of the others (its code then runs slower, 350 -> 357 us at the time),
+// every sixth, fourth or third pair of exponentials as a polynomial on the
+// multiply-add pipe (358, 377 and 376 us: the softmax is bound by issuing, not by
+// the exponentials).  With the softmax left out the products and copies alone
+// take 302 us of the prompt's 335.
 #include <cuda.h>
 #include <math.h>
 

@@ -357,3 +357,28 @@ def test_many_calls_without_a_wait_between(lens, new):
     out, lse = attend(ctx, kv, q, off, max(new), ws=ws)
     clean(ctx)
     assert same_bits(out, want) and same_bits(lse, want_lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("slope", [0.5, 4.0, 30.0, -0.5, -30.0])
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_scores_that_rise_or_fall_along_the_context(dtype, slope, rows):
+    """Each 32 entries' largest score lies powers of two above (below) the ones before: the softmax's reference moves
+    within steps and between them, from the first step to the ones that rows see only part of."""
+    rng = np.random.default_rng(rows)
+    ctx = context(8, 2, 128, dtype, max_batch=2)
+    lens, new = [500, 0], [rows, rows]
+    kv = pooled(ctx, lens, new, rng)
+    for b in range(2):
+        for i in range((lens[b] + new[b] + 15) // 16):
+            t = torch.arange(16 * i, 16 * i + 16, device="cuda")
+            kv.k_pool[int(kv.block_table[b, i]), :, :, 0] = (t * slope / 16).to(ctx.dtype)
+    q = torch.randn((2 * rows, 8, 128), device="cuda").to(ctx.dtype)
+    q[..., 0] = 11.0
+    off = [0, rows, 2 * rows]
+    out, lse = attend(ctx, kv, q, off, rows)
+    clean(ctx)
+    for b in range(2):
+        want, wl, mass, size = exact_on_gpu(q, kv, b, off[b], off[b + 1], 128 ** -0.5, 4)
+        close(host(out[off[b]:off[b + 1]]), want, out_tol(want, mass, size, dtype), "out")
+        close(host(lse[off[b]:off[b + 1]]), wl, 2.0 ** -20 + 2.0 ** -17 * size + 2.0 ** -22 * np.abs(wl), "lse")
