@@ -36,6 +36,7 @@ namespace mtp {
 constexpr int kRowsThreads = 256;
 constexpr int kRowsStep = 64;       // slots of a step
 constexpr int kRowsPairs = 64;      // pairs of a tile
+constexpr int kRowsShare = 2;       // units of a thread block at least: trees of 33 rows 21.7 us (three: 26.2, one: 22.2)
 constexpr int kWeightSlots = 128;   // slots of a thread block of the weights' kernel, sixteen a warp
 constexpr int kWeightPairs = 64;
 
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(FewShape<HD, PAIRS>::kThreads, 1) rows_few_ker
   float* ps = qs + S::kQ + w * (PAIRS * 8);   // this warp's, [pair][8 slots]
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   Split sp;
-  if (!rows_split<S::kThreads>(a, SegUnits{a, sh}, sh.lead + 1, pre, wsum, sp)) return;
+  if (!rows_split<S::kThreads>(a, SegUnits{a, sh}, kRowsShare, pre, wsum, sp)) return;
   for (uint32_t u = sp.u0; u < sp.u1;) {
     Piece p;
     find_piece(a, sh, pre, sp, u, p);
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_many_kernel(const RowsArgs 
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = 1 << a.g_shift;
   if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   Split sp;
-  if (!rows_split<kRowsThreads>(a, SegUnits{a, sh}, sh.lead + 1, pre, wsum, sp)) return;
+  if (!rows_split<kRowsThreads>(a, SegUnits{a, sh}, kRowsShare, pre, wsum, sp)) return;
   for (uint32_t u = sp.u0; u < sp.u1;) {
     Piece p;
     find_piece(a, sh, pre, sp, u, p);
