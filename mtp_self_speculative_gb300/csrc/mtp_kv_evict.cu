@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include "mtp_kv16.cuh"
+#include "mtp_kv_evict_range.h"
 
 namespace mtp {
 
@@ -78,7 +79,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warps) {
   return x - v + y;
 }
 
-// Cluster (kv head, request); its block c has the slots [c * share, (c + 1) * share).
+// Cluster (kv head, request); its blocks share the slots (mtp_kv_evict_range.h).
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t keys[];
@@ -108,8 +109,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   // candidates: the slots [lo, hi); `want` of them stay (budget - sink - recent >= 0)
   const int lo = a.sink, hi = L - a.recent, want = n - a.sink - a.recent;
-  const int share = ((L + C - 1) / C + 127) & ~127, s0 = min(L, c * share), s1 = min(L, s0 + share);
-  const int c0 = max(lo, s0), c1 = min(hi, s1);      // this block's candidates
+  const EvictRange own = evict_range(L, a.sink, a.recent, C, c);   // a short request leaves blocks without slots
+  const int s0 = own.s0, s1 = own.s1, c0 = own.c0, c1 = own.c1, f0 = own.f0;
   const int32_t* row = a.from.block_table + (long long)b * a.from.max_blocks;
   int lost = 0;
   // slots go in fours, which lie in one cache block
@@ -140,7 +141,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     load4(t & ~3, k);
     return t & 2 ? (t & 1 ? k[3] : k[2]) : (t & 1 ? k[1] : k[0]);
   };
-  const int f0 = c0 & ~3;                            // the first four with a candidate
 #pragma unroll 2
   for (int t = f0 + 4 * tid; t < min(c1, s0 + a.cached); t += 4 * kSelThreads) {
     uint32_t k[4];
@@ -372,7 +372,7 @@ mtp_status mtp_kv_evict(mtp_ctx* ctx, void* stream, int B, const mtp_kv* from, c
   const long long most = (long long)from->max_blocks * kBlk, heads = (long long)B * c.n_kv_heads;
   int C = 1;
   while (C < kSelCluster && most > 2048ll * C && heads * 2 * C <= ctx->num_sms) C *= 2;
-  const long long part = (((most + C - 1) / C + 127) & ~127ll) + 4;
+  const long long part = evict_share(most, C) + 4;
   a.cached = (int)(part < 49152 ? part : 49152) & ~3;
   a.vec = !((uintptr_t)weights & 15);
   cudaStream_t s = (cudaStream_t)stream;
