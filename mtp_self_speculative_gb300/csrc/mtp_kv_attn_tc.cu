@@ -56,6 +56,7 @@ namespace mtp {
 constexpr int kAtThreads = 384;
 constexpr float kAtSlack = 8.0f;    // how far (powers of two) a maximum may pass its reference
 constexpr float kAtCoarse = 67108864.0f;   // from 2^26 on the reference's rounding is some units
+constexpr float kAtWhole = 4096.0f;        // from 2^12 on references are whole numbers
 
 template <int HD>
 struct AtShape {
@@ -572,7 +573,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
           // them), the maximum before the weights, which go, two a word, over columns
           // 16 c .. that are done with.  Where a later quarter moves the reference, the
           // weights written before move with it: by whole powers of two, so
-          // that they are not rounded again.
+          // that they are not rounded again.  A reference plus a whole number is a
+          // float to 2^-12 while it is small; larger references are whole numbers
+          // themselves, so that their sums are exact.
           mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -587,10 +590,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) kv_attn_tc_kernel(const __grid_
             }
             most(v);
             const float t = top();
+            const float whole = fabsf(t) < kAtWhole ? t : ceilf(t);
             if (x == 0 && c == 0) {
-              m = t;
+              m = whole;
             } else if (__any_sync(0xffffffffu, t > m + kAtSlack)) {
-              const float up = fmaxf(fabsf(m), fabsf(t)) < 1048576.0f ? m + ceilf(t - m) : t;   // (2^20: little rounding)
+              // (2^-256 is zero: then, and where nothing is written yet, any distance does)
+              const float up = t - m < 256.0f && (c > 0 || fabsf(t) < kAtWhole) ? m + ceilf(t - m) : whole;
               const float mn = t > m + kAtSlack ? up : m;
               const float alpha = exp2_fast(m - mn);
               const uint32_t f = pack2_bf16(alpha, alpha);
