@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
       wb[i] = s.w ? two(w[8 + 2 * i], w[9 + 2 * i]) : 0ull;
     }
   }
-  const bool turns = 8 * u < rd / 2;      // (a unit that turns in part has pairs with cosine 1 and sine 0)
+  const int turns = rd / 2 - 8 * u;       // pairs of the unit that turn: all from 8 on (VEC: 8 or none)
   // Each thread has its next head on its way.  (out may be x, so the compiler may
   // not fetch it ahead of the store by itself; two or three heads ahead cost
   // more in registers than they gain.)
@@ -294,12 +294,16 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
       }
     }
     if (!live) continue;
-    if (turns) {
+    if (turns > 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t p = fma2(A[i], cc[i], mul2(B[i], ss[i]) ^ 0x8000000080000000ull);   // minus
-        B[i] = fma2(B[i], cc[i], mul2(A[i], ss[i]));
-        A[i] = p;
+        const uint64_t q = fma2(B[i], cc[i], mul2(A[i], ss[i]));
+        // pairs behind the rotated part stay as they are (0 times an infinite partner
+        // is not 0); the lower half of A[i] and B[i] is the first of their two pairs
+        const uint64_t stay = VEC || turns >= 2 * i + 2 ? 0ull : turns == 2 * i + 1 ? 0xFFFFFFFF00000000ull : ~0ull;
+        A[i] = (A[i] & stay) | (p & ~stay);
+        B[i] = (B[i] & stay) | (q & ~stay);
       }
     }
 #pragma unroll
