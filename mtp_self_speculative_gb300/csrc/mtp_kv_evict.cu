@@ -122,10 +122,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (a.vec) w = *reinterpret_cast<const float4*>(p);
     else w = make_float4(p[0], p[1], p[2], p[3]);
     if (!good) lost = 1;
-    k[0] = good ? weight_key(w.x) : 0u;
-    k[1] = good ? weight_key(w.y) : 0u;
-    k[2] = good ? weight_key(w.z) : 0u;
-    k[3] = good ? weight_key(w.w) : 0u;
+    if (!good) w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // (as its entries are copied)
+    k[0] = weight_key(w.x);
+    k[1] = weight_key(w.y);
+    k[2] = weight_key(w.z);
+    k[3] = weight_key(w.w);
   };
   auto keys4 = [&](int t, uint32_t (&k)[4]) {
     if (t - s0 < a.cached) {

@@ -77,3 +77,34 @@ def test_every_length_up_to_a_cluster_of_full_shares():
     for first in range(1, 1160, 110):
         lens = [first + 11 * i for i in range(10)]
         evict_wide(ctx, 300, lens, [L // 2 for L in lens], rng)
+
+
+@pytest.mark.parametrize("max_blocks", [40, 257])
+@pytest.mark.parametrize("bad", [-1, 38])
+def test_entries_of_a_block_outside_the_pool_count_as_zeros(max_blocks, bad):
+    """Their weight too: above negative ones and NaN, equal to zeros, below the rest."""
+    M = M_()
+    ctx = context(1, 1, 64, "bf16", max_batch=1)
+    nb, L = 38, 600
+    rng = np.random.default_rng(max_blocks)
+    table = np.concatenate([np.arange(nb), np.full(max_blocks - nb, -1)])[None]
+    table[0, [1, 20]] = bad
+    kv, to = M.KVCache.empty(ctx, nb, i32(table)), M.KVCache.empty(ctx, nb, i32(np.arange(nb)[None]))
+    kv.k_pool.fill_(1.0), kv.v_pool.fill_(2.0)
+    kv.seq_len.fill_(L)
+    w = torch.from_numpy(rng.choice(np.array([-1.0, 0.0, np.nan, 1.0], np.float32), (nb, 1, 16))).cuda()
+    flat = w.flatten().cpu().numpy()[:L].copy()
+    for x in (1, 20):
+        flat[16 * x:16 * x + 16] = 0.0
+    for budget in (50, 180, 300, 599):
+        kept = torch.zeros((1, 1, 600), dtype=torch.int32, device="cuda")
+        to_w = torch.full((nb, 1, 16), 5.0, device="cuda")
+        M.mtp_kv_evict(ctx, kv, w, i32([budget]), to, to_w, kept, sink=1, recent=3)
+        assert M.mtp_get_device_error(ctx) == M.MTP_ERR_CAPACITY
+        want = P.kept(flat, budget, 1, 3)
+        np.testing.assert_array_equal(kept[0, 0, :budget].cpu().numpy(), want)
+        lost = torch.as_tensor(np.isin(want // 16, (1, 20))).cuda()
+        assert bool(lost.any()) or budget == 50
+        got = to.k_pool[:, 0].flatten(0, 1)[:budget]
+        assert bool((got[lost] == 0).all()) and bool((got[~lost] == 1).all())
+        np.testing.assert_array_equal(to_w.flatten()[:budget].cpu().numpy(), flat[want])
