@@ -686,8 +686,8 @@ mtp_status mtp_qk_norm_rope(mtp_ctx* ctx, void* stream, int T, const void* q, in
  * need one each.
  *   row_offsets [B+1] int32, ascending from >= 0 to <= T; rows outside are not
  * read.  Device errors as in mtp_kv8_append: MTP_ERR_DEVICE_ARGS for bad offsets
- * or lengths, MTP_ERR_CAPACITY for slots beyond max_blocks (the request's cache
- * is then left as it was) or a block id outside the pool (its rows are not
+ * or lengths, MTP_ERR_CAPACITY for slots beyond max_blocks or 2^30 (the request's
+ * cache is then left as it was) or a block id outside the pool (its rows are not
  * stored); with bad offsets the call does nothing, else q is processed whatever
  * becomes of the cache.  T = 0 is a no-op. */
 mtp_status mtp_kv_append(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, const void* k,
@@ -755,11 +755,12 @@ mtp_status mtp_kv_attention_weights(mtp_ctx* ctx, void* stream, int B, int T, co
  * longer positions, which the rows carry by themselves.
  *   Device errors, which leave the request's blocks and kept list as they were:
  * MTP_ERR_DEVICE_ARGS for pending[b] != 0 in `from`, a negative length or
- * budget, sink + recent > budget[b]; MTP_ERR_CAPACITY for n above kept_width or
- * to's max_blocks.  A block id outside its pool is MTP_ERR_CAPACITY too: entries
- * of such a block of `from` count as zeros, those for one of `to` are dropped.
- * Host errors: NULL pointers, sink or recent < 0, lengths or tables shared by
- * `from` and `to`. */
+ * budget, sink + recent > budget[b]; MTP_ERR_CAPACITY for L above 2^30, n above
+ * kept_width or to's max_blocks.  A block id outside its pool is
+ * MTP_ERR_CAPACITY too: entries of such a block of `from` count as zeros (their
+ * weights as well), those for one of `to` are dropped.
+ * Host errors: NULL pointers, sink or recent < 0, kept_width above 2^30, lengths
+ * or tables shared by `from` and `to`. */
 mtp_status mtp_kv_evict(mtp_ctx* ctx, void* stream, int B, const mtp_kv* from, const float* weights,
                         const int32_t* budget, int sink, int recent, const mtp_kv* to, float* to_weights,
                         int32_t* kept, int kept_width);

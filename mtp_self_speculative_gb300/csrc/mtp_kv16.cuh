@@ -8,6 +8,7 @@
 namespace mtp {
 
 constexpr int kKvMaxB = 1024;                 // requests of a call (prefix sums in shared memory)
+constexpr int kKvMaxSlots = 1 << 30;          // entries of a request: slots and the ends of tiles are ints
 constexpr float kKvLeast = -3.4028235e38f;    // the softmax reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -127,8 +128,7 @@ __device__ __forceinline__ int rows_request(const RowsArgs& a, int b, int& o0, i
   const long long len = (long long)sl + pe;
   L = (int)len;
   if (n > a.max_rows || sl < 0 || pe < 0 || len < n) return MTP_ERR_DEVICE_ARGS;
-  // (2^30 entries: slots and the ends of tiles are ints)
-  if (len > (long long)a.kv.max_blocks * kBlk || len > (1 << 30)) return MTP_ERR_CAPACITY;
+  if (len > (long long)a.kv.max_blocks * kBlk || len > kKvMaxSlots) return MTP_ERR_CAPACITY;
   return MTP_OK;
 }
 

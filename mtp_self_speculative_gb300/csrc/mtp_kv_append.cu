@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
       const int sl = b == tid ? sl0 : a.kv.seq_len[b], pe = b == tid ? pe0 : a.kv.pending[b];
       int e = MTP_OK;
       if (sl < 0 || pe < 0 || sl > INT32_MAX - pe) e = MTP_ERR_DEVICE_ARGS;
-      else if ((long long)sl + pe + (o1 - o0) > (long long)a.kv.max_blocks * kBlk) e = MTP_ERR_CAPACITY;
+      else if ((long long)sl + pe + (o1 - o0) > min((long long)a.kv.max_blocks * kBlk, (long long)kKvMaxSlots)) e = MTP_ERR_CAPACITY;
       if (e != MTP_OK) {
         set_error(a.err, e);
         continue;

@@ -47,7 +47,7 @@ __device__ __forceinline__ bool evict_request(const EvictArgs& a, int b, int& L,
   const int budget = a.budget[b];
   int e = MTP_OK;
   if (L < 0 || a.from.pending[b] != 0 || budget < 0 || (long long)a.sink + a.recent > budget) e = MTP_ERR_DEVICE_ARGS;
-  else if ((long long)L > (long long)a.from.max_blocks * kBlk) e = MTP_ERR_CAPACITY;
+  else if ((long long)L > (long long)a.from.max_blocks * kBlk || L > kKvMaxSlots) e = MTP_ERR_CAPACITY;
   n = min(L, budget);
   if (e == MTP_OK && (n > a.width || (long long)n > (long long)a.to.max_blocks * kBlk)) e = MTP_ERR_CAPACITY;
   if (e != MTP_OK && report) set_error(a.err, e);
@@ -343,7 +343,7 @@ mtp_status mtp_kv_evict(mtp_ctx* ctx, void* stream, int B, const mtp_kv* from, c
                         const int32_t* budget, int sink, int recent, const mtp_kv* to, float* to_weights,
                         int32_t* kept, int kept_width) {
   if (!ctx || B < 1 || B > ctx->cfg.max_batch || B > 65535 || !kv16_ok(from) || !kv16_ok(to) || !weights || !budget ||
-      !kept || kept_width < 1 || sink < 0 || recent < 0)
+      !kept || kept_width < 1 || kept_width > kKvMaxSlots || sink < 0 || recent < 0)
     return MTP_ERR_INVALID;
   // the new cache's lengths are written while the old ones are read
   if (from->seq_len == to->seq_len || from->pending == to->pending || from->block_table == to->block_table)
