@@ -710,7 +710,7 @@ size_t mtp_kv_attention_workspace_bytes(const mtp_ctx* ctx);
  * row does not see, do not reach its result, whatever they hold (an entry that
  * is not finite makes the results of the rows that see it not finite).
  *   Scores, maxima and sums are held in float32.  bf16 heads: the products'
- * operands are bf16, the softmax weights rounded to it (8 bits; the normalising
+ * operands are bf16, the softmax weights rounded to it once (8 bits; the normalising
  * sum takes them unrounded).  float32 heads: float32 throughout.  out: 16-byte
  * aligned.  B: at most 1024; entries of a request: at most 2^30. */
 mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,
@@ -730,6 +730,7 @@ mtp_status mtp_kv_attention(mtp_ctx* ctx, void* stream, int B, int T, const int3
  *   first:   [B] int32 >= 0: from that slot on entries have no weight yet (what
  *            is stored there is not read); NULL: base_b, the first new entry.
  * Requests without rows, and slots that hold no entry, are left as they were.
+ * Requests of a call must not share blocks: their sums would go to one place.
  * The sums are in float32, their order depends on nothing but the lengths.
  * Other arguments and device errors as in mtp_kv_attention. */
 mtp_status mtp_kv_attention_weights(mtp_ctx* ctx, void* stream, int B, int T, const int32_t* row_offsets, int max_rows,

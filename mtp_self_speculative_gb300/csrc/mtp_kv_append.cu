@@ -11,7 +11,8 @@
 // next head's elements on their way.  8192 tokens of 32 query and 8 key heads of
 // 128, bf16: 33 us, 5.0 TB/s; with values appended to a cache (four prompts,
 // 8192 rows) 42 us, 4.3 TB/s.  A batch of 32 tokens is bound by the chain of loads:
-// 3.1 us, appended 6.8 us (offsets, lengths and blocks first).
+// 3.1 us, appended 6.8 us (offsets, lengths and blocks first).  float32, 8192 tokens: 59
+// us, 5.7 TB/s, appended 82 us, 4.9 TB/s.
 #include <math.h>
 
 #include "mtp_kv16.cuh"

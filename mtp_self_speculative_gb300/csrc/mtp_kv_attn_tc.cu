@@ -29,16 +29,23 @@
 // equal shares, found on the device from the lengths; a segment that spans
 // thread blocks leaves its pieces in the workspace for rows_join_kernel.
 //
+// The weights' rounding to bf16 (once, half a step of 2^-8; the normalising sum takes
+// them unrounded) is the second product's: its operands have one type, and V is bf16.  A
+// second operand for the rounding's rest would make three products of two.  Results are
+// off by 0.0021 to 0.0023 of themselves against 64 bits, where weights held in float32
+// and results rounded once give 0.0016 to 0.0017.
+//
 // What bounds it: for few rows the cache's bytes (64 requests of 4096 entries: 167
 // us, 6.4 TB/s).  For many the chain of a group's step: its products (two of 512
 // cycles at the pipe's peak) and its softmax (1000 cycles for 128 scores a
 // thread) follow one another, and the other group fills no more than its own two
 // products of the pipe meanwhile; a step of both takes 3100 cycles against 2048
-// of products.  8192 rows, 32 query heads of 128: 335 us, 1640 TFLOP/s; 1024 rows
-// on 32768 entries 361 us, 1550 TFLOP/s.  A segment costs some 6500 cycles besides
+// of products.  8192 rows, 32 query heads of 128: 335 to 342 us, 1610 to 1640 TFLOP/s, and
+// 366 us, 1500 TFLOP/s, once thousands of calls have brought the GPU to its power cap
+// (1905 MHz); 1024 rows on 32768 entries 340 to 365 us, 1530 to 1650 TFLOP/s.  A segment costs some 6500 cycles besides
 // its steps (the last products, 128 x 128 results a group to be scaled and
 // written, the first step and the one that is partly seen), so short contexts pay
-// more: 16 chunks of 512 rows on up to 1500 entries take 128 to 138 us.  Tried and
+// more: 16 chunks of 512 rows on up to 1500 entries take 130 to 140 us.  Tried and
 // not kept: results staged in a fifth tile's place and stored by the copy engine
 // (the same times, long contexts 361 -> 370 us), first and partly seen steps in
 // the pass of the others (its code then runs slower, 350 -> 357 us at the time),
@@ -63,7 +70,7 @@ struct AtShape {
   static constexpr int kHalves = HD / 64;
   static constexpr int kTile = kAtStep * HD * 2;              // bytes of a K or V tile, and of 128 pairs' queries
   // Five tiles of 32 KB are what fits.  (Four: 1024 rows on 32768 entries 370 instead
-  // of 361 us, a prompt of 8192 338 instead of 335.)
+  // of 361 us at the time, a prompt of 8192 338 instead of 335.)
   static constexpr int kStages = HD == 128 ? 5 : 8;
   static constexpr int kBytes = 2 * kTile + kStages * kTile;
 };

@@ -16,6 +16,8 @@
 // The copy is bound by memory; the selection by its chain of steps, each a pass
 // over a few entries a thread and a barrier.  Four requests of 16384 entries to
 // 2048, 8 heads of 128: 27 us, 10 of them the copy's bytes; 24 short ones 11 us.
+// Clusters and shared memory are sized by the table, whose width the host knows, and
+// not by the lengths: a short request leaves blocks of its clusters without slots.
 #include <cooperative_groups.h>
 
 #include "mtp_kv16.cuh"
